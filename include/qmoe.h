@@ -336,6 +336,106 @@ int qmoe_block_forward(const qmoe_block_desc *b, const float *X, float *out, int
                        uint16_t *k_cache, uint16_t *v_cache, int pos0, int ctx_cap, void *ws,
                        size_t ws_bytes, qmoe_stream_t stream);
 
+/*
+ * A paged key-value cache for many sequences, bounded by eviction (the pages
+ * have no counterpart in the sources; the keys, values and heads are those of
+ * the block above). Entry j of sequence b (its slot j, 0 <= j < lens[b]) lies in
+ * page table[b][j / page], row j % page:
+ *   key of KV head g    k + table[b][j / page] * page_stride
+ *                         + (j % page) * slot_stride + g * head_stride, head_dim
+ *                       bf16 bit patterns in a row; the value likewise in v.
+ *   n_seqs     sequences (>= 1);  n_kv KV heads (1..65535);
+ *   head_dim   a multiple of 8, 8..256;
+ *   page       slots of a page, a power of two, 8..4096;
+ *   n_pages    pages of the pools k and v;
+ *   max_pages  table width, max_pages * page <= 2^30; a sequence's capacity is
+ *              max_pages * page slots;
+ *   strides    in elements, multiples of 8 (the pools k and v have the same);
+ *              entries must not overlap, which is not checked. A contiguous
+ *              cache [ctx][n_kv][hd] is a pool of ctx / page pages.
+ *   table      [n_seqs][max_pages] int32; entries behind a sequence's last page
+ *              are not read. A page number outside 0..n_pages-1 that a call
+ *              needs is recorded as QMOE_ERR_DEVICE_ARG, and the call goes on
+ *              as if its slots held nothing.
+ *   lens       [n_seqs] int32; taken as 0 below 0, as the capacity above it.
+ *   weight     [n_seqs][n_kv][max_pages * page] fp32, the attention weight each
+ *              entry has received so far, or NULL (then nothing accumulates and
+ *              nothing can be evicted);
+ *   pos        [n_seqs][n_kv][max_pages * page] int32, the position of each
+ *              entry, or NULL (then eviction protects none by position). KV
+ *              heads evict apart, so a slot's entries differ between them.
+ * An entry's slot is not its position once something was evicted; keys carry
+ * their rotation with them, and attention does not depend on the slots' order.
+ */
+typedef enum { QMOE_F32 = 0, QMOE_BF16 = 1 } qmoe_dtype;
+
+typedef struct {
+  int n_seqs, n_kv, head_dim, page, n_pages, max_pages;
+  long long page_stride, slot_stride, head_stride;
+  uint16_t *k, *v;
+  const int32_t *table;
+  int32_t *lens;
+  float *weight;
+  int32_t *pos;
+} qmoe_paged_cache;
+
+/*
+ * New rows into the cache. Row n goes to sequence seq[n], slot slot[n], at
+ * position pos[n]:
+ *   k row = bf16(rot(k_n, pos[n])), v row = bf16(v_n), q_out_n = rot(q_n, pos[n]),
+ *   pos[seq][g][slot] = pos[n], weight[seq][g][slot] = 0,
+ *   lens[seq] = max(lens[seq], slot + 1).
+ *   q, q_out [n_rows][n_heads][hd] (q_out may be q), or both NULL; k, v
+ *   [n_rows][n_kv][hd]; all four of type dtype (qmoe_dtype).
+ *   rope_theta > 0: rot turns pairs (i, i + hd/2) by pos * theta^(-2i/hd) (the
+ *   angle in double); 0: rot leaves the values as they are.
+ *   seq, slot, pos [n_rows] int32. seq and slot NULL: n_rows == n_seqs, row n is
+ *   the next entry of sequence n (slot lens[n]). slot < 0: a padding row, which
+ *   is not cached (its q is still turned). Two rows of one call must not have the
+ *   same (seq, slot). A seq or slot out of range is recorded as
+ *   QMOE_ERR_DEVICE_ARG and its row is not cached.
+ */
+int qmoe_paged_append(const qmoe_paged_cache *c, const void *q, void *q_out, const void *k, const void *v,
+                      int dtype, const int32_t *seq, const int32_t *slot, const int32_t *pos, int n_rows,
+                      int n_heads, float rope_theta, qmoe_stream_t stream);
+
+/*
+ * Attention of one new token for each sequence: for query head h of sequence b,
+ * g = h / (n_heads / n_kv), over the slots j < lens[b]
+ *   s_j = scale * q . k_j,  p = softmax(s),  out = sum_j p_j v_j,
+ * with accumulate != 0 also weight[b][g][j] += sum over the heads h of g of p_j.
+ *   q, out [n_seqs][n_heads][hd] of type dtype (fp32 rows are taken with all
+ *   their bits, bf16 rows are exact as they are); out may be q. A sequence
+ *   without entries gives zeros. What the cache holds outside the entries is
+ *   never used (it may be NaN).
+ *   scale: finite; 0 takes 1 / sqrt(head_dim).
+ *   ws: qmoe_paged_attention_workspace_bytes(c, n_heads, accumulate) bytes,
+ *   256-byte aligned. The sums are taken in a fixed order: the same call gives
+ *   the same bits.
+ */
+size_t qmoe_paged_attention_workspace_bytes(const qmoe_paged_cache *c, int n_heads, int accumulate);
+int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, int dtype, int n_heads,
+                         float scale, int accumulate, void *ws, size_t ws_bytes, qmoe_stream_t stream);
+
+/*
+ * Brings every (sequence, KV head) to at most ``budget`` entries. Those that
+ * stay are the first m = min(lens[b], budget) in the order
+ *   pos >= next_pos[b] - recent first (the newest; recent 0: none),
+ *   then larger weight (NaN as -infinity), then lower slot.
+ * An entry that stays in a slot below m stays where it is; the i-th staying
+ * entry of the slots from m on moves to the i-th slot below m whose entry
+ * goes, with its key, value, weight and position. lens_out[b] = m.
+ *   weight_out, pos_out: as the cache's weight and pos; slots below m are
+ *   written, the others are not touched. Each _out may be the cache's own array
+ *   (nothing else of it); pos_out is NULL where the cache has no pos.
+ *   0 <= recent <= budget; next_pos [n_seqs] int32 is read where recent > 0.
+ *   ws: qmoe_cache_evict_workspace_bytes(c) bytes, 256-byte aligned.
+ */
+size_t qmoe_cache_evict_workspace_bytes(const qmoe_paged_cache *c);
+int qmoe_cache_evict(const qmoe_paged_cache *c, const int32_t *next_pos, int budget, int recent,
+                     int32_t *lens_out, float *weight_out, int32_t *pos_out, void *ws, size_t ws_bytes,
+                     qmoe_stream_t stream);
+
 /* The CUDA runtime error code (cudaError_t) behind the last QMOE_ERR_LAUNCH
  * returned on this thread, 0 if none. */
 int qmoe_last_cuda_error(void);

@@ -93,7 +93,9 @@ def exported_symbols() -> list[str]:
             "qmoe_launch_count", "qmoe_profile_start", "qmoe_profile_stop", "qmoe_profile_read",
             "qmoe_moe_forward_noalloc", "qmoe_get_decode_max_rows", "qmoe_set_decode_max_rows",
             "qmoe_last_cuda_error", "qmoe_rmsnorm", "qmoe_attn_workspace_bytes", "qmoe_attn_forward", "qmoe_block_workspace_bytes",
-            "qmoe_block_forward", "qmoe_test_inject"]
+            "qmoe_block_forward", "qmoe_test_inject",
+            "qmoe_paged_append", "qmoe_paged_attention_workspace_bytes", "qmoe_paged_attention",
+            "qmoe_cache_evict_workspace_bytes", "qmoe_cache_evict"]
 
 
 def _check(status: int):
@@ -384,3 +386,184 @@ def block_forward(block: Block, X: torch.Tensor, k_cache: torch.Tensor, v_cache:
                                            _ptr(v_cache), pos0, k_cache.shape[0], _ptr(ws), ws.numel(),
                                            _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- paged cache
+
+class PagedCacheDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", _c_int), ("n_kv", _c_int), ("head_dim", _c_int), ("page", _c_int), ("n_pages", _c_int),
+                ("max_pages", _c_int), ("page_stride", ctypes.c_longlong), ("slot_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("k", _vp), ("v", _vp), ("table", _vp), ("lens", _vp),
+                ("weight", _vp), ("pos", _vp)]
+
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _paged_lib():
+    L = lib()
+    if not getattr(L, "_paged_declared", False):
+        P = ctypes.POINTER(PagedCacheDesc)
+        L.qmoe_paged_append.argtypes = [P, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int, ctypes.c_float,
+                                        _vp]
+        L.qmoe_paged_attention_workspace_bytes.restype = _c_size
+        L.qmoe_paged_attention_workspace_bytes.argtypes = [P, _c_int, _c_int]
+        L.qmoe_paged_attention.argtypes = [P, _vp, _vp, _c_int, _c_int, ctypes.c_float, _c_int, _vp, _c_size, _vp]
+        L.qmoe_cache_evict_workspace_bytes.restype = _c_size
+        L.qmoe_cache_evict_workspace_bytes.argtypes = [P]
+        L.qmoe_cache_evict.argtypes = [P, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_size, _vp]
+        L._paged_declared = True
+    return L
+
+
+def _need(t, what, shape=None, dtype=None):
+    """Checks one tensor argument: on a CUDA device, contiguous, shape and type."""
+    if not t.is_cuda:
+        raise QmoeError(f"{what} must be on a CUDA device")
+    if not t.is_contiguous():
+        raise QmoeError(f"{what} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise QmoeError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise QmoeError(f"{what} has type {t.dtype}, not {dtype}")
+    return t.data_ptr()
+
+
+class PagedCache:
+    """Keys and values of many sequences in pages, and what eviction goes by.
+
+    k, v [pages][page][kv heads][head dim] bf16 (any strides but the last, the
+    same for both), table [sequences][pages of a sequence] int32, lens
+    [sequences] int32, weight (fp32) and pos (int32) [sequences][kv heads][slots]
+    or None. The cache refers to these tensors; the calls below write them.
+    """
+
+    def __init__(self, k, v, table, lens, weight=None, pos=None):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise QmoeError("k and v must be [pages][page][kv heads][head dim] with the same strides, the last 1")
+        for t, what in ((k, "k"), (v, "v")):
+            if not t.is_cuda:
+                raise QmoeError(f"{what} must be on a CUDA device")
+            if t.dtype != torch.bfloat16:
+                raise QmoeError(f"{what} has type {t.dtype}, not {torch.bfloat16}")
+        self.n_pages, self.page, self.n_kv, self.head_dim = k.shape
+        if table.dim() != 2:
+            raise QmoeError("the table must be [sequences][pages of a sequence]")
+        self.n_seqs, self.max_pages = table.shape
+        self.slots = self.max_pages * self.page
+        per_slot = (self.n_seqs, self.n_kv, self.slots)
+        self.k, self.v, self.table, self.lens, self.weight, self.pos = k, v, table, lens, weight, pos
+        self._desc = PagedCacheDesc(
+            self.n_seqs, self.n_kv, self.head_dim, self.page, self.n_pages, self.max_pages, k.stride(0), k.stride(1),
+            k.stride(2), k.data_ptr(), v.data_ptr(), _need(table, "table", dtype=torch.int32),
+            _need(lens, "lens", (self.n_seqs,), torch.int32),
+            None if weight is None else _need(weight, "weight", per_slot, torch.float32),
+            None if pos is None else _need(pos, "pos", per_slot, torch.int32))
+        self._desc_ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, n_seqs, max_len, n_kv, head_dim, page=64, n_pages=None, device="cuda"):
+        """An empty cache. Without ``n_pages`` every sequence owns the pages of
+        ``max_len`` entries; with it the pool has that many and the table is
+        filled with -1 for the caller to hand pages out."""
+        width = -(-max_len // page)
+        if n_pages is None:
+            table = torch.arange(n_seqs * width, dtype=torch.int32, device=device).view(n_seqs, width)
+            n_pages = n_seqs * width
+        else:
+            table = torch.full((n_seqs, width), -1, dtype=torch.int32, device=device)
+        k = torch.zeros((n_pages, page, n_kv, head_dim), dtype=torch.bfloat16, device=device)
+        return cls(k, torch.zeros_like(k), table, torch.zeros(n_seqs, dtype=torch.int32, device=device),
+                   torch.zeros((n_seqs, n_kv, width * page), dtype=torch.float32, device=device),
+                   torch.zeros((n_seqs, n_kv, width * page), dtype=torch.int32, device=device))
+
+    @property
+    def desc(self) -> PagedCacheDesc:
+        return self._desc
+
+
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slot=None, rope_theta: float = 0.0,
+                 stream=None):
+    """Rows k, v [rows][kv heads][hd] (fp32 or bf16) into the cache: row n to
+    slot ``slot[n]`` of sequence ``seq[n]`` (both None: row n is the next entry
+    of sequence n; a slot below 0: not cached), at position ``pos[n]``, keys (and
+    the queries q [rows][heads][hd], returned) rotated when ``rope_theta`` > 0."""
+    rows = k.shape[0]
+    dtype = k.dtype
+    if dtype not in _DTYPE:
+        raise QmoeError(f"k has type {dtype}, not fp32 or bf16")
+    kv_shape = (rows, cache.n_kv, cache.head_dim)
+    heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        q_shape = (rows, heads, cache.head_dim)
+        qp, qo = _need(q, "q", q_shape, dtype), _need(q_out, "q_out", q_shape, dtype)
+    elif q_out is not None:
+        raise QmoeError("q_out without q")
+    else:
+        qp = qo = None
+    _check(_paged_lib().qmoe_paged_append(
+        cache._desc_ref, qp, qo, _need(k, "k", kv_shape), _need(v, "v", kv_shape, dtype), _DTYPE[dtype],
+        None if seq is None else _need(seq, "seq", (rows,), torch.int32),
+        None if slot is None else _need(slot, "slot", (rows,), torch.int32), _need(pos, "pos", (rows,), torch.int32),
+        rows, heads, rope_theta, _raw_stream(stream)))
+    return q_out
+
+
+def paged_attention_workspace(cache: PagedCache, n_heads: int, accumulate: bool = False) -> torch.Tensor:
+    n = int(_paged_lib().qmoe_paged_attention_workspace_bytes(cache._desc_ref, n_heads, int(accumulate)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def paged_attention(cache: PagedCache, q, out=None, scale: float = 0.0, accumulate: bool = False, ws=None,
+                    stream=None):
+    """Attention of one new token q [sequences][heads][hd] (fp32 or bf16) for
+    each sequence over its cached entries; with ``accumulate`` every entry's
+    weight grows by the attention it received. scale 0: 1/sqrt(hd)."""
+    dtype = q.dtype
+    if dtype not in _DTYPE:
+        raise QmoeError(f"q has type {dtype}, not fp32 or bf16")
+    heads = q.shape[1]
+    shape = (cache.n_seqs, heads, cache.head_dim)
+    if out is None:
+        out = torch.empty_like(q)
+    if ws is None:
+        ws = paged_attention_workspace(cache, heads, accumulate)
+    _check(_paged_lib().qmoe_paged_attention(
+        cache._desc_ref, _need(q, "q", shape), _need(out, "out", shape, dtype), _DTYPE[dtype], heads, scale,
+        int(accumulate), _need(ws, "ws"), ws.numel(), _raw_stream(stream)))
+    return out
+
+
+def cache_evict_workspace(cache: PagedCache) -> torch.Tensor:
+    n = int(_paged_lib().qmoe_cache_evict_workspace_bytes(cache._desc_ref))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def cache_evict(cache: PagedCache, next_pos, budget: int, recent: int = 0, lens_out=None, weight_out=None,
+                pos_out=None, ws=None, stream=None):
+    """Brings every sequence to at most ``budget`` entries for each KV head: those
+    at positions >= next_pos - recent and the heaviest of the others. Without
+    outputs the cache's own lens, weight and pos are updated; (lens, weight, pos)
+    are returned."""
+    lens_out = cache.lens if lens_out is None else lens_out
+    weight_out = cache.weight if weight_out is None else weight_out
+    pos_out = cache.pos if pos_out is None else pos_out
+    if weight_out is None:
+        raise QmoeError("the cache has no weights to evict by")
+    per_slot = (cache.n_seqs, cache.n_kv, cache.slots)
+    if ws is None:
+        ws = cache_evict_workspace(cache)
+    _check(_paged_lib().qmoe_cache_evict(
+        cache._desc_ref, None if next_pos is None else _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),
+        budget, recent, _need(lens_out, "lens_out", (cache.n_seqs,), torch.int32),
+        _need(weight_out, "weight_out", per_slot, torch.float32),
+        None if pos_out is None else _need(pos_out, "pos_out", per_slot, torch.int32), _need(ws, "ws"), ws.numel(),
+        _raw_stream(stream)))
+    return lens_out, weight_out, pos_out

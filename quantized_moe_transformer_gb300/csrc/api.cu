@@ -2,11 +2,13 @@
 // The operations are defined in include/qmoe.h.
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <cstdio>
 
 #include "kernels.cuh"
+#include "paged.cuh"
 
 using namespace qmoe;
 
@@ -422,6 +424,44 @@ int attn_impl(const qmoe_block_desc* b, const float* X, const float* R, float* o
   return launch_status(e);
 }
 
+
+// ---------------------------------------------------------------- paged cache
+// Checks a cache descriptor and makes the kernels' view of it.
+int paged_view(const qmoe_paged_cache* c, PagedView* out) {
+  if (!c) return QMOE_ERR_NULL;
+  if (c->n_seqs < 1 || c->n_kv < 1 || c->n_kv > 65535 || c->n_pages < 1 || c->max_pages < 1) return QMOE_ERR_ARG;
+  if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0) return QMOE_ERR_ARG;
+  if (c->page < 8 || c->page > 4096 || (c->page & (c->page - 1)) != 0) return QMOE_ERR_ARG;
+  if ((long long)c->max_pages * c->page > (1ll << 30)) return QMOE_ERR_ARG;
+  const long long strides[] = {c->page_stride, c->slot_stride, c->head_stride};
+  for (long long s : strides)
+    if (s < 0 || s % 8 != 0) return QMOE_ERR_ARG;
+  if (!c->k || !c->v || !c->table || !c->lens) return QMOE_ERR_NULL;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4) || !aligned(c->lens, 4) ||
+      !aligned(c->weight, 16) || !aligned(c->pos, 16))
+    return QMOE_ERR_ALIGN;
+  PagedView v{};
+  v.k = reinterpret_cast<__nv_bfloat16*>(c->k);
+  v.v = reinterpret_cast<__nv_bfloat16*>(c->v);
+  v.table = c->table;
+  v.lens = c->lens;
+  v.weight = c->weight;
+  v.pos = c->pos;
+  v.page_stride = c->page_stride;
+  v.slot_stride = c->slot_stride;
+  v.head_stride = c->head_stride;
+  v.n_seqs = c->n_seqs;
+  v.n_kv = c->n_kv;
+  v.head_dim = c->head_dim;
+  while ((1 << v.page_log2) < c->page) ++v.page_log2;
+  v.n_pages = c->n_pages;
+  v.max_pages = c->max_pages;
+  *out = v;
+  return QMOE_OK;
+}
+
+bool dtype_ok(int dtype) { return dtype == QMOE_F32 || dtype == QMOE_BF16; }
+
 }  // namespace
 
 extern "C" {
@@ -483,6 +523,103 @@ int qmoe_block_forward(const qmoe_block_desc* b, const float* X, float* out, int
   if (launch_rmsnorm(h1, b->g2, b->eps, r2, T, b->H, st) != cudaSuccess) return QMOE_ERR_LAUNCH;
   return qmoe_moe_forward(&b->moe, r2, h1, nullptr, nullptr, out, T, moe_ws, ws_bytes - a_bytes - 2 * row_bytes,
                           stream);
+}
+
+
+int qmoe_paged_append(const qmoe_paged_cache* c, const void* q, void* q_out, const void* k, const void* v, int dtype,
+                      const int32_t* seq, const int32_t* slot, const int32_t* pos, int n_rows, int n_heads,
+                      float rope_theta, qmoe_stream_t stream) {
+  PagedView view;
+  int r = paged_view(c, &view);
+  if (r != QMOE_OK) return r;
+  if (!dtype_ok(dtype) || n_rows < 0 || !(rope_theta >= 0.f) || rope_theta > 1e30f) return QMOE_ERR_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (seq == nullptr) != (slot == nullptr)) return QMOE_ERR_NULL;
+  if (q && (n_heads < 1 || n_heads > 65535)) return QMOE_ERR_ARG;
+  if (n_rows == 0) return QMOE_OK;
+  if (!seq && n_rows != c->n_seqs) return QMOE_ERR_ARG;
+  if (!k || !v || !pos) return QMOE_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(seq, 4) ||
+      !aligned(slot, 4) || !aligned(pos, 4))
+    return QMOE_ERR_ALIGN;
+  AppendArgs a{};
+  r = device_ready(&a.status);
+  if (r != QMOE_OK) return r;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.seq = seq;
+  a.slot = slot;
+  a.pos = pos;
+  a.n_rows = n_rows;
+  a.n_heads = q ? n_heads : 0;
+  a.f32 = dtype == QMOE_F32;
+  a.rotate = rope_theta > 0.f;
+  a.theta = (double)rope_theta;
+  g_launches.fetch_add(1);
+  return launch_status(launch_paged_append(view, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qmoe_paged_attention_workspace_bytes(const qmoe_paged_cache* c, int n_heads, int accumulate) {
+  PagedView view;
+  if (paged_view(c, &view) != QMOE_OK || n_heads < 1 || n_heads > 65535 || n_heads % c->n_kv != 0) return 0;
+  return paged_attention_ws_bytes(view, n_heads, accumulate != 0);
+}
+
+int qmoe_paged_attention(const qmoe_paged_cache* c, const void* q, void* out, int dtype, int n_heads, float scale,
+                         int accumulate, void* ws, size_t ws_bytes, qmoe_stream_t stream) {
+  PagedView view;
+  int r = paged_view(c, &view);
+  if (r != QMOE_OK) return r;
+  if (!dtype_ok(dtype) || n_heads < 1 || n_heads > 65535 || n_heads % c->n_kv != 0 || !std::isfinite(scale))
+    return QMOE_ERR_ARG;
+  if (!q || !out || !ws || (accumulate && !c->weight)) return QMOE_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return QMOE_ERR_ALIGN;
+  if (ws_bytes < paged_attention_ws_bytes(view, n_heads, accumulate != 0)) return QMOE_ERR_WORKSPACE;
+  PagedAttnArgs a{};
+  r = device_ready(&a.status);
+  if (r != QMOE_OK) return r;
+  a.q = q;
+  a.out = out;
+  a.n_heads = n_heads;
+  a.f32 = dtype == QMOE_F32;
+  a.accumulate = accumulate != 0;
+  a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)c->head_dim);
+  a.ws = ws;
+  g_launches.fetch_add(paged_attention_launches(view, n_heads, a.accumulate));
+  return launch_status(launch_paged_attention(view, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qmoe_cache_evict_workspace_bytes(const qmoe_paged_cache* c) {
+  PagedView view;
+  if (paged_view(c, &view) != QMOE_OK) return 0;
+  return cache_evict_ws_bytes(view);
+}
+
+int qmoe_cache_evict(const qmoe_paged_cache* c, const int32_t* next_pos, int budget, int recent, int32_t* lens_out,
+                     float* weight_out, int32_t* pos_out, void* ws, size_t ws_bytes, qmoe_stream_t stream) {
+  PagedView view;
+  int r = paged_view(c, &view);
+  if (r != QMOE_OK) return r;
+  if (budget < 0 || recent < 0 || recent > budget) return QMOE_ERR_ARG;
+  if (!c->weight || !lens_out || !weight_out || !ws || (c->pos && !pos_out)) return QMOE_ERR_NULL;
+  if (recent > 0 && (!c->pos || !next_pos)) return QMOE_ERR_NULL;
+  if (!aligned(next_pos, 4) || !aligned(lens_out, 4) || !aligned(weight_out, 16) || !aligned(pos_out, 16) ||
+      !aligned(ws, 256))
+    return QMOE_ERR_ALIGN;
+  if (ws_bytes < cache_evict_ws_bytes(view)) return QMOE_ERR_WORKSPACE;
+  EvictArgs a{};
+  r = device_ready(&a.status);
+  if (r != QMOE_OK) return r;
+  a.next_pos = next_pos;
+  a.budget = budget;
+  a.recent = recent;
+  a.lens_out = lens_out;
+  a.weight_out = weight_out;
+  a.pos_out = pos_out;
+  a.ws = ws;
+  g_launches.fetch_add(cache_evict_launches());
+  return launch_status(launch_cache_evict(view, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 
