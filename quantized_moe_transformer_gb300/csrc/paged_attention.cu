@@ -4,111 +4,796 @@
 // Now Splits": 16 query heads over 2 KV heads, query head h reads KV head
 // h / 8. "Distributed CPU: Zip Fusion Beyond Tensor Parallelism",
 // "Two-Dimensional Attention at Long Context": the softmax over parts of the
-// context carried by (max, normaliser, weighted output).
+// context carried by (max, normaliser, weighted output) and joined exactly.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace qmoe {
 
 namespace {
 
-constexpr int PA_CHUNK = 256;
+// What bounds it: each cached byte is read once and serves the G query heads of
+// its KV head, 8 flops a byte at G = 8, so HBM bounds it.
+//
+// Work. A row is (sequence, KV head, tile of at most 8 NT query heads); its
+// slots are cut into tiles of KT. The tiles of all rows in order are dealt out
+// evenly, a contiguous range to each CTA (one CTA per SM), so that a batch of
+// unequal sequences and one long sequence both keep every SM busy. The part of
+// a row inside a CTA is a segment; the CTA's warps take its tiles in turn, each
+// with its own running (maximum, sum, output), and merge them through shared
+// memory at the segment's end. A row inside one CTA is finished there; of a
+// row over several CTAs each writes a partial, and the join kernel finishes it.
+// A CTA has at most one partial of a row that began earlier (slot 0) and one
+// of a row that begins in it (slot 1).
+//
+// Loads. Every warp feeds itself: its lanes look pages up one tile ahead and
+// issue tensor copies (boxes of 64 head dims x up to KT slots of a page, 128-byte
+// swizzled) into the warp's own ring of STAGES tiles; no warp waits for
+// another inside a segment, and the copies of the next segment are in flight
+// while one is merged.
+//
+// Products. Scores are S^T = K Q^T with the slots as the rows of a 16 x 8
+// fragment and the G heads as its 8 columns, so that a group of 8 heads fills
+// the instruction; the output is O^T = V^T P^T with the head dims as rows. The
+// instructions are mma.sync: at 8 flops a byte the whole cache needs a tenth of
+// their rate, and a fragment's scores are in registers at once.
+// fp32 queries are split into three bf16 parts (exact), probabilities into two
+// (2^-17 of each), so fp32 rows come out at fp32 accuracy; sums are fp32.
+template <int HDP_, int NT_, bool F32_>
+struct PaCfg {
+  static constexpr int HDP = HDP_, NT = NT_, QP = F32_ ? 3 : 1;
+  static constexpr bool F32 = F32_;
+  static constexpr int KT = HDP == 64 ? 32 : 16;           // slots of a tile: 4 or 8 KB of keys
+  static constexpr int WARPS = HDP == 256 ? 4 : 8;
+  static constexpr int STAGES = NT == 1 ? 3 : 2;           // 192 KB (128 KB) in flight an SM
+  static constexpr int HALF = KT * 128;                    // 64 head dims of a tile
+  static constexpr int KBYTES = HALF * (HDP / 64);
+  static constexpr int RING = WARPS * STAGES * 2 * KBYTES;
+  static constexpr int HT = 8 * NT;                        // heads of a row
+  static constexpr int MERGE = WARPS * HT * HDP * 4;
+  static constexpr int SMEM = 1024 + RING + MERGE + WARPS * HT * 8 + WARPS * STAGES * 16 + 128;
+};
 
-__device__ __forceinline__ float block_reduce(float v, bool is_max, float* red) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, v, off);
-    v = is_max ? fmaxf(v, o) : v + o;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-  for (int w = 1; w < PA_CHUNK / 32; ++w) v = is_max ? fmaxf(v, red[w]) : v + red[w];
-  return v;
+struct PaSplit {
+  PagedView c;
+  const void* q;
+  void* out;
+  float scale_log2;  // scores in units of log2(e)
+  int n_heads, group, head_tiles, box_rows;
+  int min_tiles;     // a CTA's share is at least this
+  int4* desc;        // [CTAs] the row that begins there and is joined: (sequence, row, CTAs, -), or -1
+  float2* part_ml;   // [CTAs][2][heads]
+  float* part_o;     // [CTAs][2][heads][HDP]
+  float* lse;        // [sequences][heads] log2 of the softmax's denominator, with accumulate
+  float* scores;     // [sequences][KV heads][slots][group], with accumulate
+  int* status;
+};
+
+__device__ __forceinline__ void pa_tma(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(page), "r"(tc::smem_u32(bar))
+      : "memory");
 }
 
-// One CTA per (sequence, KV head), its query heads one after the other: scores
-// of 256 slots at a time (a thread per slot), running maximum and sum, then a
-// second walk adds the probabilities to the slots' weights.
-template <typename T>
-__global__ void __launch_bounds__(PA_CHUNK) paged_attention_simple_kernel(const PagedView c, const PagedAttnArgs a) {
-  __shared__ float qs[256], ps[PA_CHUNK], red[PA_CHUNK / 32];
-  __shared__ long long offs[PA_CHUNK];
-  const int b = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, hd = c.head_dim;
-  const int group = a.n_heads / c.n_kv, n = paged_len(c, b);
-  float* stat = static_cast<float*>(a.ws);  // (maximum, sum) of every query head
-  for (int h = g * group; h < (g + 1) * group; ++h) {
-    const long long qoff = ((long long)b * a.n_heads + h) * hd;
-    __syncthreads();
-    if (tid < hd)
-      qs[tid] = a.f32 ? static_cast<const float*>(a.q)[qoff + tid]
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qoff + tid]);
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int j0 = 0; j0 < n; j0 += PA_CHUNK) {
-      const int j = j0 + tid;
-      float s = -INFINITY;
-      __syncthreads();
-      offs[tid] = j < n ? paged_offset(c, b, j) : -1;
-      if (j < n && offs[tid] < 0) record_status(a.status, QMOE_ERR_DEVICE_ARG);
-      __syncthreads();
-      if (offs[tid] >= 0) {
-        const __nv_bfloat16* kr = c.k + offs[tid] + (long long)g * c.head_stride;
-        s = 0.f;
-        for (int i = 0; i < hd; ++i) s = fmaf(qs[i], __bfloat162float(kr[i]), s);
-        s *= a.scale;
+__device__ __forceinline__ void pa_ldsm(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void pa_ldsm_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pa_transpose(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void pa_mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+__device__ __forceinline__ int pa_tiles(const PagedView& c, int b, int kt) {
+  const int n = (paged_len(c, b) + kt - 1) / kt;
+  return n > 0 ? n : 1;  // an empty sequence has one tile without entries, which writes its zeros
+}
+
+// A walk over tiles: row ``vh`` of sequence ``b``, its tile ``t`` of ``nt``.
+struct PaWalk {
+  int b, vh, t, nt, len;
+};
+
+template <int KT>
+__device__ __forceinline__ void pa_step(const PagedView& c, int rows, int by, PaWalk& w) {
+  w.t += by;
+  while (w.t >= w.nt) {
+    w.t -= w.nt;
+    if (++w.vh == rows) {
+      w.vh = 0;
+      if (++w.b >= c.n_seqs) {  // behind the last tile; never used
+        w.nt = 1 << 30;
+        return;
       }
-      const float mn = fmaxf(m, block_reduce(s, true, red));
-      const float p = s > -INFINITY ? __expf(s - mn) : 0.f;
-      const float alpha = m > -INFINITY ? __expf(m - mn) : 0.f;
-      ps[tid] = p;
-      l = l * alpha + block_reduce(p, false, red);
-      m = mn;
-      if (tid < hd) {
-        o *= alpha;
-        for (int i = 0; i < min(PA_CHUNK, n - j0); ++i)
-          if (offs[i] >= 0) o = fmaf(ps[i], __bfloat162float(c.v[offs[i] + (long long)g * c.head_stride + tid]), o);
-      }
-    }
-    if (tid == 0) {
-      stat[2 * ((long long)b * a.n_heads + h)] = m;
-      stat[2 * ((long long)b * a.n_heads + h) + 1] = l;
-    }
-    if (tid < hd) {
-      const float r = l > 0.f ? o / l : 0.f;
-      if (a.f32)
-        static_cast<float*>(a.out)[qoff + tid] = r;
-      else
-        static_cast<__nv_bfloat16*>(a.out)[qoff + tid] = __float2bfloat16_rn(r);
+      w.len = paged_len(c, w.b);
+      w.nt = w.len > 0 ? (w.len + KT - 1) / KT : 1;
     }
   }
-  if (!a.accumulate) return;
+}
+
+template <class C>
+__global__ void __launch_bounds__(32 * C::WARPS, 1)
+    paged_split_kernel(const PaSplit p, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap) {
+  constexpr int KT = C::KT, W = C::WARPS, ST = C::STAGES, NT = C::NT, HDP = C::HDP, KS = HDP / 16, HT = C::HT;
+  constexpr int THREADS = 32 * W, KB = KT / 16;
+  extern __shared__ uint8_t pa_smem_raw[];
+  __shared__ long long s_scan[W + 1], s_start[2];
+  __shared__ int s_seq, s_abort;
+  const uint32_t s0 = tc::smem_u32(pa_smem_raw);
+  uint8_t* smem = pa_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
+  float* merge_o = reinterpret_cast<float*>(smem + C::RING);                    // [W][HT][HDP]
+  float2* merge_ml = reinterpret_cast<float2*>(smem + C::RING + C::MERGE);      // [W][HT]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + W * HT);              // [W][ST]
+  uint32_t* masks = reinterpret_cast<uint32_t*>(bars + W * ST);                 // [W][ST]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const PagedView& c = p.c;
+  const int rows = c.n_kv * p.head_tiles;
+  tc::grid_dep_launch();
+
+  if (tid < W * ST) tc::mbar_init(&bars[tid], 1);
+  if (tid == 0) {
+    s_abort = 0;
+    tc::fence_barrier_init();
+  }
+
+  // ---- this CTA's share of the tiles
+  long long mine = 0;
+  for (int b = tid; b < c.n_seqs; b += THREADS) mine += pa_tiles(c, b, KT);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+  if (lane == 0) s_scan[warp] = mine;
   __syncthreads();
-  for (int j = tid; j < n; j += PA_CHUNK) {
-    const long long off = paged_offset(c, b, j);
-    if (off < 0) continue;
-    const __nv_bfloat16* kr = c.k + off + (long long)g * c.head_stride;
-    float w = 0.f;
-    for (int h = g * group; h < (g + 1) * group; ++h) {
-      const long long at = (long long)b * a.n_heads + h;
-      float s = 0.f;
-      for (int i = 0; i < hd; ++i)
-        s = fmaf(a.f32 ? static_cast<const float*>(a.q)[at * hd + i]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at * hd + i]),
-                 __bfloat162float(kr[i]), s);
-      w += __expf(s * a.scale - stat[2 * at]) / stat[2 * at + 1];
-    }
-    c.weight[((long long)b * c.n_kv + g) * paged_slots(c) + j] += w;
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) total += s_scan[w];
+  total *= rows;
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < p.min_tiles) per = p.min_tiles;
+  const long long T0 = (long long)blockIdx.x * per;
+  const long long T1 = T0 + per < total ? T0 + per : total;
+  if (T0 >= T1) {
+    if (tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
   }
+  // the sequence in which it begins
+  long long before = 0;
+  for (int b0 = 0; b0 < c.n_seqs; b0 += THREADS) {
+    const int b = b0 + tid;
+    const long long own = b < c.n_seqs ? (long long)pa_tiles(c, b, KT) * rows : 0;
+    long long incl = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long base = before, all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) base += s_scan[w];
+      all += s_scan[w];
+    }
+    if (T0 >= base + incl - own && T0 < base + incl) {
+      s_seq = b;
+      s_start[0] = base + incl - own;
+    }
+    before += all;
+    if (T0 < before) break;
+  }
+  __syncthreads();
+  PaWalk first;
+  first.b = s_seq;
+  first.len = paged_len(c, first.b);
+  first.nt = first.len > 0 ? (first.len + KT - 1) / KT : 1;
+  first.vh = (int)((T0 - s_start[0]) / first.nt);
+  first.t = (int)((T0 - s_start[0]) % first.nt);
+  if (tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+
+  // ---- loads: this warp's tiles are T0 + warp, T0 + warp + W, ...
+  uint8_t* ring = smem + warp * ST * 2 * C::KBYTES;
+  uint64_t* full = bars + warp * ST;
+  uint32_t* mask_of = masks + warp * ST;
+  const int pieces = KT / p.box_rows, page_mask = (1 << c.page_log2) - 1;
+  long long left = T1 - T0 - warp;  // tiles of this warp still to look up: ceil(left / W)
+  PaWalk ahead = first;
+  pa_step<KT>(c, rows, warp, ahead);
+  // page of this lane's piece of the tile at ``ahead``; -1: holds nothing
+  auto look_up = [&](int& page) {
+    page = -1;
+    const int slot = ahead.t * KT + lane * p.box_rows;
+    if (left > 0 && lane < pieces && slot < ahead.len)
+      page = __ldg(c.table + (long long)ahead.b * c.max_pages + (slot >> c.page_log2));
+  };
+  auto issue = [&](int st, const PaWalk& w, int page) {
+    const int slot = w.t * KT + lane * p.box_rows;
+    const bool want = lane < pieces && slot < w.len;
+    const bool there = want && (unsigned)page < (unsigned)c.n_pages;
+    if (want && !there) record_status(p.status, QMOE_ERR_DEVICE_ARG);
+    const unsigned ok = __ballot_sync(0xffffffffu, there);
+    // slots of the tile that hold entries: their piece has a page and they lie below the length
+    const int key = w.t * KT + lane;
+    const bool held = lane < KT && key < w.len && ((ok >> (lane / p.box_rows)) & 1u);
+    const unsigned m = __ballot_sync(0xffffffffu, held);
+    if (lane == 0) {
+      mask_of[st] = m;
+      tc::mbar_expect_tx(&full[st], (uint32_t)__popc(ok) * (uint32_t)p.box_rows * 2u * HDP * 2u);
+    }
+    __syncwarp();
+    if (there) {
+      const uint32_t dst = tc::smem_u32(ring + st * 2 * C::KBYTES) + (uint32_t)(lane * p.box_rows) * 128u;
+      const int g = w.vh / p.head_tiles;
+#pragma unroll
+      for (int h = 0; h < HDP / 64; ++h) pa_tma(dst + h * C::HALF, &kmap, 64 * h, slot & page_mask, g, page, &full[st]);
+#pragma unroll
+      for (int h = 0; h < HDP / 64; ++h)
+        pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, 64 * h, slot & page_mask, g, page, &full[st]);
+    }
+  };
+  {
+    int pages[ST];
+    PaWalk at[ST];
+    bool some[ST];
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      look_up(pages[s]);
+      at[s] = ahead;
+      some[s] = left > 0;
+      left -= W;
+      if (left > 0) pa_step<KT>(c, rows, W, ahead);
+    }
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+      if (some[s]) issue(s, at[s], pages[s]);
+  }
+  int next_page;
+  look_up(next_page);
+
+  // ---- segments
+  PaWalk seg = first;
+  long long pos = T0;
+  int turn = warp;  // tiles until this warp's next one
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  while (pos < T1) {
+    const long long rest = T1 - pos;
+    const int n_tiles = (int)(rest < seg.nt - seg.t ? rest : seg.nt - seg.t);
+    const bool whole = seg.t == 0 && n_tiles == seg.nt;
+    const int g = seg.vh / p.head_tiles, h0 = g * p.group + (seg.vh % p.head_tiles) * HT;
+    const int n_h = min(HT, (g + 1) * p.group - h0);  // heads of this row
+    float m[NT][2], l[NT][2], o[KS][NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    }
+    if (turn < n_tiles) {
+      // the row's queries as B fragments: head lane / 4, dims 2 (lane % 4) + {0, 1, 8, 9} of each 16
+      uint32_t qf[KS][NT][C::QP][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int hh = 8 * n + (lane >> 2);
+        const long long qo = ((long long)seg.b * p.n_heads + h0 + hh) * c.head_dim;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int d = 16 * i + 8 * half + 2 * (lane & 3);
+            const bool in = hh < n_h && d < c.head_dim;
+            if (C::F32) {
+              const float2 x = in ? *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + qo + d)
+                                  : make_float2(0.f, 0.f);
+              float x0 = x.x, x1 = x.y;
+#pragma unroll
+              for (int part = 0; part < C::QP; ++part) {
+                const uint32_t u = tc::pack_bf16x2(x0, x1);
+                qf[i][n][part][half] = u;
+                x0 -= bf_lo(u);
+                x1 -= bf_hi(u);
+              }
+            } else {
+              qf[i][n][0][half] =
+                  in ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + qo + d) : 0u;
+            }
+          }
+        }
+      }
+      for (; turn < n_tiles; turn += W) {
+        if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &s_abort))) {
+          ok = false;
+          if (lane == 0) record_status(p.status, QMOE_ERR_TIMEOUT);
+        }
+        if (!ok) continue;
+        const uint32_t held = mask_of[stage];
+        uint8_t* tile = ring + stage * 2 * C::KBYTES;
+        const uint32_t kt = tc::smem_u32(tile), vt = kt + C::KBYTES;
+        constexpr uint32_t FULL = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
+        if (held != FULL) {
+          // values of slots that hold nothing are set to zero: 0 times whatever lay there need not be 0
+          for (int i = lane; i < KT * (HDP / 8); i += 32) {
+            const int r = i / (HDP / 8), ch = i % (HDP / 8);
+            if (!((held >> r) & 1u))
+              *reinterpret_cast<uint4*>(tile + C::KBYTES + (ch >> 3) * C::HALF + r * 128 + (ch & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();  // before a later copy into the same bytes
+          __syncwarp();
+        }
+        // S^T: slots x heads
+        float s[KB][NT][4];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          float s2[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[kb][n][e] = s2[n][e] = 0.f;
+          const int r = 16 * kb + (lane & 15);
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t a[4];
+            const int ch = 2 * (i & 3) + (lane >> 4);
+            pa_ldsm(a, kt + (i >> 2) * C::HALF + tc::sw128_offset(r, ch));
+#pragma unroll
+            for (int part = C::QP - 1; part >= 0; --part)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                pa_mma((i & 1) ? s2[n] : s[kb][n], a, qf[i][n][part][0], qf[i][n][part][1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[kb][n][e] = (s[kb][n][e] + s2[n][e]) * p.scale_log2;
+          if (held != FULL) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+              if (!((held >> (16 * kb + (lane >> 2) + 4 * e)) & 1u))
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[kb][n][e] = s[kb][n][e + 1] = -INFINITY;
+          }
+        }
+        if (p.scores != nullptr) {
+          // kept until the denominators are known
+          const int t0 = (seg.t + turn) * KT;
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = t0 + 16 * kb + (lane >> 2) + 4 * (e & 2);
+              const long long at = (((long long)seg.b * c.n_kv + g) * paged_slots(c) + j) * p.group + (h0 - g * p.group);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const int hh = 8 * n + 2 * (lane & 3) + (e & 1);
+                if (j < seg.len && hh < n_h) p.scores[at + hh] = s[kb][n][e];
+              }
+            }
+        }
+        // running maximum; the output is rescaled where one grew
+        uint32_t pf[KB][NT][2][2];  // P^T as B fragments: two bf16 parts, slots 0-7 and 8-15
+        bool grew = false;
+        float mn[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[0][n][e], s[0][n][e + 2]);
+#pragma unroll
+            for (int kb = 1; kb < KB; ++kb) x = fmaxf(x, fmaxf(s[kb][n][e], s[kb][n][e + 2]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            mn[n][e] = fmaxf(m[n][e], x);
+            grew |= mn[n][e] > m[n][e];
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float al[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              al[e] = m[n][e] == mn[n][e] ? 1.f : exp2f(m[n][e] - mn[n][e]);
+              m[n][e] = mn[n][e];
+              l[n][e] *= al[e];
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              o[i][n][0] *= al[0];
+              o[i][n][1] *= al[1];
+              o[i][n][2] *= al[0];
+              o[i][n][3] *= al[1];
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            const float p0 = exp2f(s[kb][n][0] - r0), p1 = exp2f(s[kb][n][1] - r1);
+            const float p2 = exp2f(s[kb][n][2] - r0), p3 = exp2f(s[kb][n][3] - r1);
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            const uint32_t ua = tc::pack_bf16x2(p0, p1), ub = tc::pack_bf16x2(p2, p3);
+            pf[kb][n][0][0] = pa_transpose(ua);
+            pf[kb][n][0][1] = pa_transpose(ub);
+            pf[kb][n][1][0] = pa_transpose(tc::pack_bf16x2(p0 - bf_lo(ua), p1 - bf_hi(ua)));
+            pf[kb][n][1][1] = pa_transpose(tc::pack_bf16x2(p2 - bf_lo(ub), p3 - bf_hi(ub)));
+          }
+        }
+        // O^T += V^T P^T: head dims x heads
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const int r = 16 * kb + (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t a[4];
+            const int ch = 2 * (i & 3) + ((lane >> 3) & 1);
+            pa_ldsm_t(a, vt + (i >> 2) * C::HALF + tc::sw128_offset(r, ch));
+#pragma unroll
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) pa_mma(o[i][n], a, pf[kb][n][part][0], pf[kb][n][part][1]);
+          }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (left > 0) {
+          issue(stage, ahead, next_page);
+          left -= W;
+          if (left > 0) pa_step<KT>(c, rows, W, ahead);
+          look_up(next_page);
+        }
+        if (++stage == ST) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    turn -= n_tiles;
+
+    // ---- this warp's (m, l, O) of the segment
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[n][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        l[n][e] = x;
+        const int hh = 8 * n + 2 * (lane & 3) + e;
+        if (lane < 4) merge_ml[warp * HT + hh] = make_float2(m[n][e], x);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          merge_o[(warp * HT + hh) * HDP + 16 * i + (lane >> 2)] = o[i][n][e];
+          merge_o[(warp * HT + hh) * HDP + 16 * i + 8 + (lane >> 2)] = o[i][n][e + 2];
+        }
+      }
+    __syncthreads();
+    // ---- merged over the warps: the result, or a partial for the join
+    const long long part = ((long long)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0)) * HT;
+    for (int i = tid; i < n_h * (HDP / 4); i += THREADS) {
+      const int hh = i / (HDP / 4), d = 4 * (i % (HDP / 4));
+      float M = -INFINITY, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) M = fmaxf(M, merge_ml[w * HT + hh].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 ml = merge_ml[w * HT + hh];
+        const float f = exp2f(ml.x - ref);
+        const float4 x = *reinterpret_cast<const float4*>(&merge_o[(w * HT + hh) * HDP + d]);
+        L = fmaf(ml.y, f, L);
+        acc.x = fmaf(x.x, f, acc.x);
+        acc.y = fmaf(x.y, f, acc.y);
+        acc.z = fmaf(x.z, f, acc.z);
+        acc.w = fmaf(x.w, f, acc.w);
+      }
+      if (!whole) {
+        if (d == 0) p.part_ml[part + hh] = make_float2(M, L);
+        *reinterpret_cast<float4*>(&p.part_o[(part + hh) * HDP + d]) = acc;
+        continue;
+      }
+      const float il = L == 0.f ? 0.f : 1.f / L;
+      const long long head = (long long)seg.b * p.n_heads + h0 + hh;
+      if (d == 0 && p.lse != nullptr) p.lse[head] = L == 0.f ? 0.f : M + log2f(L);
+      if (d < c.head_dim) {
+        if (C::F32)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + head * c.head_dim + d) =
+              make_float4(acc.x * il, acc.y * il, acc.z * il, acc.w * il);
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + head * c.head_dim + d) =
+              make_uint2(tc::pack_bf16x2(acc.x * il, acc.y * il), tc::pack_bf16x2(acc.z * il, acc.w * il));
+      }
+    }
+    if (tid == 0 && !whole && seg.t == 0) {
+      // tiles of the row behind this CTA's range, ``per`` to a CTA
+      const long long more = (long long)seg.nt - n_tiles;
+      p.desc[blockIdx.x] = make_int4(seg.b, seg.vh, 1 + (int)((more + per - 1) / per), 0);
+    }
+    __syncthreads();
+    pos += n_tiles;
+    if (pos < T1) pa_step<KT>(c, rows, n_tiles, seg);
+  }
+}
+
+// Joins the partials of a row over several CTAs: one CTA per (CTA in which a
+// row may begin, head of the row). out = sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M).
+struct PaJoin {
+  const int4* desc;
+  const float2* part_ml;
+  const float* part_o;
+  void* out;
+  float* lse;
+  int n_heads, group, head_tiles, head_tile, head_dim, hdp;
+  bool f32;
+};
+
+constexpr int PJ_THREADS = 256;
+
+__global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PaJoin p) {
+  __shared__ float fs[PJ_THREADS], red[PJ_THREADS / 32], acc_s[PJ_THREADS * 4];
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  const int4 d = p.desc[blockIdx.x];
+  if (d.x < 0) return;
+  const int hh = blockIdx.y, tid = threadIdx.x, g = d.y / p.head_tiles;
+  const int h0 = g * p.group + (d.y % p.head_tiles) * p.head_tile;
+  if (h0 + hh >= (g + 1) * p.group) return;
+  // partial i: the beginning in slot 1 of the first CTA, then slot 0 of the next ones
+  auto at = [&](int i) { return ((long long)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * p.head_tile + hh; };
+  const int lanes = p.hdp / 4, groups = PJ_THREADS / lanes;  // lanes over the head dims, groups over the partials
+  const int grp = tid / lanes, col = 4 * (tid % lanes);
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < d.z; i0 += PJ_THREADS) {
+    const int n = min(PJ_THREADS, d.z - i0);
+    const float2 ml = tid < n ? p.part_ml[at(i0 + tid)] : make_float2(-INFINITY, 0.f);
+    float mx = ml.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = mx;
+    __syncthreads();
+    mx = M;
+#pragma unroll
+    for (int w = 0; w < PJ_THREADS / 32; ++w) mx = fmaxf(mx, red[w]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float old = exp2f(M - ref), f = exp2f(ml.x - ref);
+    M = mx;
+    fs[tid] = f;
+    float sum = ml.y * f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = sum;
+    __syncthreads();
+    L *= old;
+#pragma unroll
+    for (int w = 0; w < PJ_THREADS / 32; ++w) L += red[w];
+    acc.x *= old;
+    acc.y *= old;
+    acc.z *= old;
+    acc.w *= old;
+#pragma unroll 8
+    for (int i = grp; i < n; i += groups) {
+      const float4 x = *reinterpret_cast<const float4*>(&p.part_o[at(i0 + i) * p.hdp + col]);
+      const float fi = fs[i];
+      acc.x = fmaf(x.x, fi, acc.x);
+      acc.y = fmaf(x.y, fi, acc.y);
+      acc.z = fmaf(x.z, fi, acc.z);
+      acc.w = fmaf(x.w, fi, acc.w);
+    }
+  }
+  __syncthreads();
+  *reinterpret_cast<float4*>(&acc_s[4 * tid]) = acc;
+  __syncthreads();
+  const long long head = (long long)d.x * p.n_heads + h0 + hh;
+  const float il = L == 0.f ? 0.f : 1.f / L;
+  if (tid == 0 && p.lse != nullptr) p.lse[head] = L == 0.f ? 0.f : M + log2f(L);
+  if (tid < p.head_dim) {
+    float x = 0.f;
+    for (int k = 0; k < groups; ++k) x += acc_s[k * p.hdp + tid];
+    if (p.f32)
+      static_cast<float*>(p.out)[head * p.head_dim + tid] = x * il;
+    else
+      static_cast<__nv_bfloat16*>(p.out)[head * p.head_dim + tid] = __float2bfloat16_rn(x * il);
+  }
+}
+
+// weight[b][g][j] += sum over the group's heads of 2^(score - lse).
+__global__ void __launch_bounds__(256) paged_weight_kernel(const PagedView c, const float* __restrict__ scores,
+                                                           const float* __restrict__ lse, int n_heads, int group) {
+  tc::grid_dep_wait();
+  const int pair = blockIdx.x, b = pair / c.n_kv, g = pair % c.n_kv;
+  const int n = paged_len(c, b);
+  const long long base = (long long)pair * paged_slots(c);
+  const float* ls = lse + (long long)b * n_heads + (long long)g * group;
+  for (int j = blockIdx.y * 256 + threadIdx.x; j < n; j += gridDim.y * 256) {
+    const float* s = scores + (base + j) * group;
+    float w = 0.f;
+    if (group == 8) {
+      const float4 x = *reinterpret_cast<const float4*>(s), y = *reinterpret_cast<const float4*>(s + 4);
+      w = ((exp2f(x.x - ls[0]) + exp2f(x.y - ls[1])) + (exp2f(x.z - ls[2]) + exp2f(x.w - ls[3]))) +
+          ((exp2f(y.x - ls[4]) + exp2f(y.y - ls[5])) + (exp2f(y.z - ls[6]) + exp2f(y.w - ls[7])));
+    } else {
+      for (int h = 0; h < group; ++h) w += exp2f(s[h] - ls[h]);
+    }
+    c.weight[base + j] += w;
+  }
+}
+
+struct PaPlan {
+  int hdp, nt, head_tile, head_tiles, ctas;
+  size_t desc, ml, o, lse, scores, total;
+};
+
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+PaPlan pa_plan(const PagedView& c, int n_heads, bool f32, bool accumulate, int ctas) {
+  PaPlan p{};
+  const int group = n_heads / c.n_kv;
+  p.hdp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
+  // rows of 16 heads where a group has more than 8 (each byte serves them all at once); three parts of
+  // 256-wide queries for 16 heads do not fit the registers
+  p.nt = group > 8 && !(p.hdp == 256 && f32) ? 2 : 1;
+  p.head_tile = 8 * p.nt;
+  p.head_tiles = (group + p.head_tile - 1) / p.head_tile;
+  p.ctas = ctas;
+  size_t o = 0;
+  p.desc = o;   o += up256(sizeof(int4) * ctas);
+  p.ml = o;     o += up256(sizeof(float2) * ctas * 2 * 16);
+  p.o = o;      o += up256(sizeof(float) * ctas * 2 * 16 * (size_t)p.hdp);
+  p.lse = o;    o += accumulate ? up256(sizeof(float) * (size_t)c.n_seqs * n_heads) : 0;
+  p.scores = o; o += accumulate ? up256(sizeof(float) * (size_t)c.n_seqs * n_heads * (size_t)paged_slots(c)) : 0;
+  p.total = o;
+  return p;
+}
+
+constexpr int PA_MAX_CTAS = 256;  // the workspace does not depend on the device
+
+// A pool as a 4-D tensor map [head dim][slot of a page][KV head][page]; head
+// dims from hd on read as zero.
+bool pa_encode(CUtensorMap* m, const void* base, const PagedView& c, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)1 << c.page_log2, (cuuint64_t)c.n_kv,
+                              (cuuint64_t)c.n_pages};
+  // (a dimension of one element never steps: its stride may be anything that is valid)
+  const cuuint64_t strides[3] = {(cuuint64_t)c.slot_stride * 2,
+                                 (cuuint64_t)(c.n_kv > 1 ? c.head_stride : c.slot_stride) * 2,
+                                 (cuuint64_t)(c.n_pages > 1 ? c.page_stride : c.slot_stride) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t launch_split(PaSplit& s, int ctas, cudaStream_t st) {
+  s.box_rows = 1 << s.c.page_log2;
+  if (s.box_rows > C::KT) s.box_rows = C::KT;
+  s.min_tiles = C::WARPS;
+  CUtensorMap km, vm;
+  if (!pa_encode(&km, s.c.k, s.c, s.box_rows) || !pa_encode(&vm, s.c.v, s.c, s.box_rows)) return cudaErrorInvalidValue;
+  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(paged_split_kernel<C>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  paged_split_kernel<C><<<ctas, 32 * C::WARPS, C::SMEM, st>>>(s, km, vm);
+  return cudaGetLastError();
+}
+
+template <bool F32>
+cudaError_t pick_split(PaSplit& s, const PaPlan& pl, cudaStream_t st) {
+  if (pl.hdp == 64) {
+    if (pl.nt == 1) return launch_split<PaCfg<64, 1, F32>>(s, pl.ctas, st);
+    return launch_split<PaCfg<64, 2, F32>>(s, pl.ctas, st);
+  }
+  if (pl.hdp == 128) {
+    if (pl.nt == 1) return launch_split<PaCfg<128, 1, F32>>(s, pl.ctas, st);
+    return launch_split<PaCfg<128, 2, F32>>(s, pl.ctas, st);
+  }
+  if (pl.nt == 1) return launch_split<PaCfg<256, 1, F32>>(s, pl.ctas, st);
+  if constexpr (!F32) return launch_split<PaCfg<256, 2, false>>(s, pl.ctas, st);
+  return cudaErrorInvalidValue;
+}
+
+// Launches ``k`` so that it may start before the kernel ahead of it has ended
+// (it waits on the device for that kernel's memory).
+template <class Arg0, class... Args>
+cudaError_t launch_dependent(void (*k)(Arg0, Args...), dim3 grid, int threads, cudaStream_t st, Arg0 a0, Args... rest) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, a0, rest...);
 }
 
 }  // namespace
 
-size_t paged_attention_ws_bytes(const PagedView& c, int n_heads, bool) { return 8 * (size_t)c.n_seqs * n_heads; }
-int paged_attention_launches(const PagedView&, int, bool) { return 1; }
+size_t paged_attention_ws_bytes(const PagedView& c, int n_heads, bool accumulate) {
+  return pa_plan(c, n_heads, false, accumulate, PA_MAX_CTAS).total;
+}
+int paged_attention_launches(const PagedView&, int, bool accumulate) { return accumulate ? 3 : 2; }
 
 cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, cudaStream_t st) {
-  paged_attention_simple_kernel<float><<<dim3(c.n_seqs, c.n_kv), PA_CHUNK, 0, st>>>(c, a);
-  return cudaGetLastError();
+  int ctas = device_sm_count();
+  if (ctas > PA_MAX_CTAS) ctas = PA_MAX_CTAS;
+  const PaPlan pl = pa_plan(c, a.n_heads, a.f32, a.accumulate, PA_MAX_CTAS);
+  char* ws = static_cast<char*>(a.ws);
+  PaSplit s{};
+  s.c = c;
+  s.q = a.q;
+  s.out = a.out;
+  s.scale_log2 = a.scale * 1.4426950408889634f;
+  s.n_heads = a.n_heads;
+  s.group = a.n_heads / c.n_kv;
+  s.head_tiles = pl.head_tiles;
+  s.desc = reinterpret_cast<int4*>(ws + pl.desc);
+  s.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
+  s.part_o = reinterpret_cast<float*>(ws + pl.o);
+  s.lse = a.accumulate ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
+  s.scores = a.accumulate ? reinterpret_cast<float*>(ws + pl.scores) : nullptr;
+  s.status = a.status;
+  PaPlan run = pl;
+  run.ctas = ctas;
+  cudaError_t e = a.f32 ? pick_split<true>(s, run, st) : pick_split<false>(s, run, st);
+  if (e != cudaSuccess) return e;
+  PaJoin j{};
+  j.desc = s.desc;
+  j.part_ml = s.part_ml;
+  j.part_o = s.part_o;
+  j.out = a.out;
+  j.lse = s.lse;
+  j.n_heads = a.n_heads;
+  j.group = s.group;
+  j.head_tiles = pl.head_tiles;
+  j.head_tile = pl.head_tile;
+  j.head_dim = c.head_dim;
+  j.hdp = pl.hdp;
+  j.f32 = a.f32;
+  e = launch_dependent(paged_join_kernel, dim3(ctas, pl.head_tile < s.group ? pl.head_tile : s.group), PJ_THREADS, st, j);
+  if (e != cudaSuccess || !a.accumulate) return e;
+  // about 8 CTAs an SM over all (sequence, KV head) pairs
+  const long long pairs = (long long)c.n_seqs * c.n_kv;
+  long long parts = (paged_slots(c) + 255) / 256, most = (8ll * ctas + pairs - 1) / pairs;
+  if (parts > most) parts = most;
+  return launch_dependent(paged_weight_kernel, dim3((unsigned)pairs, (unsigned)parts), 256, st, c,
+                          (const float*)s.scores, (const float*)s.lse, a.n_heads, s.group);
 }
 
 }  // namespace qmoe
