@@ -618,7 +618,7 @@ int qmoe_cache_evict(const qmoe_paged_cache* c, const int32_t* next_pos, int bud
   a.weight_out = weight_out;
   a.pos_out = pos_out;
   a.ws = ws;
-  g_launches.fetch_add(cache_evict_launches());
+  g_launches.fetch_add(cache_evict_launches(view, a));
   return launch_status(launch_cache_evict(view, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

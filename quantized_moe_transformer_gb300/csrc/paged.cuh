@@ -71,7 +71,7 @@ struct EvictArgs {
   void* ws;
 };
 size_t cache_evict_ws_bytes(const PagedView& c);
-int cache_evict_launches();
+int cache_evict_launches(const PagedView& c, const EvictArgs& a);
 cudaError_t launch_cache_evict(const PagedView& c, const EvictArgs& a, cudaStream_t st);
 
 }  // namespace qmoe
