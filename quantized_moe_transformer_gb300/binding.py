@@ -460,6 +460,7 @@ class PagedCache:
             None if weight is None else _need(weight, "weight", per_slot, torch.float32),
             None if pos is None else _need(pos, "pos", per_slot, torch.int32))
         self._desc_ref = ctypes.byref(self._desc)
+        self.device = k.device.index  # the calls' default stream is this device's current one
 
     @classmethod
     def empty(cls, n_seqs, max_len, n_kv, head_dim, page=64, n_pages=None, device="cuda"):
@@ -482,8 +483,13 @@ class PagedCache:
         return self._desc
 
 
-def _raw_stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _raw_stream(stream, device):
+    """The stream's handle; without one, that of the device's current stream (by
+    PyTorch's accessor of the bare handle: 0.1 us against 2.9 us through a
+    torch.cuda.Stream object on the GB300's host)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slot=None, rope_theta: float = 0.0,
@@ -512,7 +518,7 @@ def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slo
         cache._desc_ref, qp, qo, _need(k, "k", kv_shape), _need(v, "v", kv_shape, dtype), _DTYPE[dtype],
         None if seq is None else _need(seq, "seq", (rows,), torch.int32),
         None if slot is None else _need(slot, "slot", (rows,), torch.int32), _need(pos, "pos", (rows,), torch.int32),
-        rows, heads, rope_theta, _raw_stream(stream)))
+        rows, heads, rope_theta, _raw_stream(stream, cache.device)))
     return q_out
 
 
@@ -537,7 +543,7 @@ def paged_attention(cache: PagedCache, q, out=None, scale: float = 0.0, accumula
         ws = paged_attention_workspace(cache, heads, accumulate)
     _check(_paged_lib().qmoe_paged_attention(
         cache._desc_ref, _need(q, "q", shape), _need(out, "out", shape, dtype), _DTYPE[dtype], heads, scale,
-        int(accumulate), _need(ws, "ws"), ws.numel(), _raw_stream(stream)))
+        int(accumulate), _need(ws, "ws"), ws.numel(), _raw_stream(stream, cache.device)))
     return out
 
 
@@ -565,5 +571,5 @@ def cache_evict(cache: PagedCache, next_pos, budget: int, recent: int = 0, lens_
         budget, recent, _need(lens_out, "lens_out", (cache.n_seqs,), torch.int32),
         _need(weight_out, "weight_out", per_slot, torch.float32),
         None if pos_out is None else _need(pos_out, "pos_out", per_slot, torch.int32), _need(ws, "ws"), ws.numel(),
-        _raw_stream(stream)))
+        _raw_stream(stream, cache.device)))
     return lens_out, weight_out, pos_out

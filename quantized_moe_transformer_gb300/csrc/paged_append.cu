@@ -13,89 +13,177 @@ namespace qmoe {
 
 namespace {
 
-// Inverse frequencies theta^(-2i/hd), computed on the host in double.
+constexpr int AP_THREADS = 256, AP_ROWS = 16;
+
+// theta^(-2i/hd) / (2 pi), the turns of one position, as a fraction of 2^64.
+// Whole turns drop out of the product with a position modulo 2^64, so the
+// angle of any position is reduced exactly in integers.
 struct AppendFreq {
-  double inv[128];
+  uint64_t turns[128];
 };
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// One CTA per row: pairs (i, i + hd/2) of every query and key head are turned
-// by pos * theta^(-2i/hd). The angle is formed in double and reduced to
-// [-pi, pi] by n turns, 2 pi as the double nearest to it and the remainder
-// (positions reach millions of radians), then sine and cosine are taken in
-// single precision, as the block's own rotation does.
+// Four elements in memory, as fp32, and back.
 template <typename T>
-__global__ void __launch_bounds__(256) append_kernel(const PagedView c, const AppendArgs a,
-                                                     const __grid_constant__ AppendFreq fr) {
-  __shared__ float cs[128], sn[128];
-  const int n = blockIdx.x, tid = threadIdx.x, hd = c.head_dim, half = hd / 2;
-  if (a.rotate) {
-    const int pos = a.pos[n];
-    for (int i = tid; i < half; i += 256) {
-      const double ang = (double)pos * fr.inv[i];
-      const double turns = rint(ang * 0.15915494309189535);
-      const double r = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, ang));
-      sincosf((float)r, &sn[i], &cs[i]);
+struct Four;
+template <>
+struct Four<float> {
+  using raw = float4;
+  static __device__ __forceinline__ float4 wide(raw v) { return v; }
+  static __device__ __forceinline__ raw narrow(float4 v) { return v; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  using raw = uint2;
+  static __device__ __forceinline__ float4 wide(raw u) {
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ raw narrow(float4 v) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+};
+
+// A CTA takes ``rows`` rows. A unit is four elements of a head and the four
+// half a head further on, which turn together: one thread reads a unit, turns it
+// (queries and keys) and writes it to q_out or into the page; every byte is
+// read and written once, and four units of a thread are in flight at a time.
+// Small calls are bound by the launch, large ones by HBM.
+template <typename T, bool ROT>
+__global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const PagedView c, const AppendArgs a, int rows,
+                                                            const __grid_constant__ AppendFreq fr) {
+  __shared__ float2 turn[ROT ? AP_ROWS * 128 : 1];
+  __shared__ long long off[AP_ROWS];
+  __shared__ int2 at[AP_ROWS];  // (sequence, slot), slot -1: the row is not cached
+  const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, hd = c.head_dim, half = hd / 2;
+  if (ROT) {
+    for (int i = tid; i < n * half; i += AP_THREADS) {
+      const int r = i / half, d = i - r * half;
+      const uint64_t frac = (uint64_t)(long long)a.pos[n0 + r] * fr.turns[d];
+      // the upper 32 bits as a signed part of a turn: |error| <= 2^-33 turns, then one rounding to fp32
+      const float x = (float)(int)((frac + 0x80000000ull) >> 32) * (6.283185307179586f / 4294967296.f);
+      float s, k;
+      sincosf(x, &s, &k);
+      turn[i] = make_float2(k, s);
     }
   }
-  const int seq = a.seq ? a.seq[n] : n;
-  const bool seq_ok = seq >= 0 && seq < c.n_seqs;
-  const int slot = a.slot ? a.slot[n] : seq_ok ? c.lens[seq] : -1;
-  __syncthreads();
-  if (a.q != nullptr) {
-    const T* q = static_cast<const T*>(a.q) + (long long)n * a.n_heads * hd;
-    T* qo = static_cast<T*>(a.q_out) + (long long)n * a.n_heads * hd;
-    for (int idx = tid; idx < a.n_heads * half; idx += 256) {
-      const int h = idx / half, i = idx % half;
-      const float x = load1(q + h * hd + i), y = load1(q + h * hd + i + half);
-      const float co = a.rotate ? cs[i] : 1.f, si = a.rotate ? sn[i] : 0.f;
-      store1(qo + h * hd + i, x * co - y * si);
-      store1(qo + h * hd + i + half, y * co + x * si);
+  if (tid < 32) {
+    int seq = -1, slot = -1;
+    long long o = -1;
+    if (tid < n) {
+      const int row = n0 + tid;
+      seq = a.seq ? a.seq[row] : row;
+      const bool known = seq >= 0 && seq < c.n_seqs;
+      slot = a.slot ? a.slot[row] : known ? c.lens[seq] : 0;
+      const bool padding = a.slot && slot < 0;
+      if (known && slot >= 0 && slot < paged_slots(c)) o = paged_offset(c, seq, slot);
+      if (o < 0 && !padding) record_status(a.status, QMOE_ERR_DEVICE_ARG);
+      if (o < 0) seq = slot = -1;
+      off[tid] = o;
+      at[tid] = make_int2(seq, slot);
+    }
+    // the rows of one sequence raise its length together
+    const unsigned peers = __match_any_sync(0xffffffffu, seq);
+    const int top = __reduce_max_sync(peers, slot);
+    if (seq >= 0 && (int)(threadIdx.x & 31) == __ffs(peers) - 1) atomicMax(c.lens + seq, top + 1);
+  }
+  using F = Four<T>;
+  using raw = typename F::raw;
+  const int per_head = hd / 8, units = (a.n_heads + 2 * c.n_kv) * per_head, total = n * units;
+  const T *qs = static_cast<const T*>(a.q), *ks = static_cast<const T*>(a.k), *vs = static_cast<const T*>(a.v);
+  constexpr int U = 16 / (int)sizeof(raw) * 2;  // 64 bytes of a thread in flight
+  bool looked_up = false;
+  for (int i0 = tid; i0 - tid < total; i0 += U * AP_THREADS) {
+    raw x[U], y[U];
+    int r[U], h[U], d[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * AP_THREADS;
+      h[k] = -1;
+      if (i < total) {
+        r[k] = i / units;
+        const int u = i - r[k] * units;
+        h[k] = u / per_head;
+        d[k] = 4 * (u - h[k] * per_head);
+        const int g = h[k] - a.n_heads;
+        const T* src = (g < 0 ? qs + ((long long)(n0 + r[k]) * a.n_heads + h[k]) * hd
+                              : (g < c.n_kv ? ks + ((long long)(n0 + r[k]) * c.n_kv + g) * hd
+                                            : vs + ((long long)(n0 + r[k]) * c.n_kv + g - c.n_kv) * hd)) + d[k];
+        x[k] = *reinterpret_cast<const raw*>(src);
+        y[k] = *reinterpret_cast<const raw*>(src + half);
+      }
+    }
+    if (!looked_up) __syncthreads();  // the first reads go on while the pages are looked up
+    looked_up = true;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (h[k] < 0) continue;
+      const int g = h[k] - a.n_heads;
+      const long long o = off[r[k]];
+      if (g >= 0 && o < 0) continue;
+      float4 p = F::wide(x[k]), q = F::wide(y[k]);
+      if (ROT && g < c.n_kv) {
+        const float2* t = turn + r[k] * half + d[k];
+        const float2 t0 = t[0], t1 = t[1], t2 = t[2], t3 = t[3];
+        const float4 v = p, w = q;
+        p = make_float4(v.x * t0.x - w.x * t0.y, v.y * t1.x - w.y * t1.y, v.z * t2.x - w.z * t2.y,
+                        v.w * t3.x - w.w * t3.y);
+        q = make_float4(w.x * t0.x + v.x * t0.y, w.y * t1.x + v.y * t1.y, w.z * t2.x + v.z * t2.y,
+                        w.w * t3.x + v.w * t3.y);
+      }
+      if (g < 0) {
+        T* dst = static_cast<T*>(a.q_out) + ((long long)(n0 + r[k]) * a.n_heads + h[k]) * hd + d[k];
+        *reinterpret_cast<raw*>(dst) = F::narrow(p);
+        *reinterpret_cast<raw*>(dst + half) = F::narrow(q);
+      } else {
+        using B = Four<__nv_bfloat16>;
+        __nv_bfloat16* dst = (g < c.n_kv ? c.k + o + (long long)g * c.head_stride
+                                         : c.v + o + (long long)(g - c.n_kv) * c.head_stride) + d[k];
+        *reinterpret_cast<B::raw*>(dst) = B::narrow(p);
+        *reinterpret_cast<B::raw*>(dst + half) = B::narrow(q);
+      }
     }
   }
-  if (a.slot && slot < 0) return;  // a padding row
-  long long off = -1;
-  if (seq_ok && slot >= 0 && slot < paged_slots(c)) off = paged_offset(c, seq, slot);
-  if (off < 0) {
-    if (tid == 0) record_status(a.status, QMOE_ERR_DEVICE_ARG);
-    return;
+  for (int i = tid; i < n * c.n_kv; i += AP_THREADS) {
+    const int r = i % n, g = i / n;
+    if (at[r].y < 0) continue;
+    const long long e = ((long long)at[r].x * c.n_kv + g) * paged_slots(c) + at[r].y;
+    if (c.weight) c.weight[e] = 0.f;
+    if (c.pos) c.pos[e] = a.pos[n0 + r];
   }
-  const T* k = static_cast<const T*>(a.k) + (long long)n * c.n_kv * hd;
-  const T* v = static_cast<const T*>(a.v) + (long long)n * c.n_kv * hd;
-  for (int idx = tid; idx < c.n_kv * half; idx += 256) {
-    const int g = idx / half, i = idx % half;
-    const float x = load1(k + g * hd + i), y = load1(k + g * hd + i + half);
-    const float co = a.rotate ? cs[i] : 1.f, si = a.rotate ? sn[i] : 0.f;
-    __nv_bfloat16* dst = c.k + off + (long long)g * c.head_stride;
-    dst[i] = __float2bfloat16_rn(x * co - y * si);
-    dst[i + half] = __float2bfloat16_rn(y * co + x * si);
-  }
-  for (int idx = tid; idx < c.n_kv * hd; idx += 256) {
-    const int g = idx / hd, i = idx % hd;
-    c.v[off + (long long)g * c.head_stride + i] = __float2bfloat16_rn(load1(v + idx));
-  }
-  for (int g = tid; g < c.n_kv; g += 256) {
-    const long long at = ((long long)seq * c.n_kv + g) * paged_slots(c) + slot;
-    if (c.weight) c.weight[at] = 0.f;
-    if (c.pos) c.pos[at] = a.pos[n];
-  }
-  if (tid == 0) atomicMax(c.lens + seq, slot + 1);
+}
+
+template <typename T>
+void append_rows(const PagedView& c, const AppendArgs& a, const AppendFreq& fr, cudaStream_t st) {
+  // one row a CTA until every SM has four, then up to 16 rows
+  int rows = a.n_rows / (4 * device_sm_count());
+  rows = rows < 1 ? 1 : rows > AP_ROWS ? AP_ROWS : rows;
+  const int ctas = (a.n_rows + rows - 1) / rows;
+  if (a.rotate)
+    append_kernel<T, true><<<ctas, AP_THREADS, 0, st>>>(c, a, rows, fr);
+  else
+    append_kernel<T, false><<<ctas, AP_THREADS, 0, st>>>(c, a, rows, fr);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedView& c, const AppendArgs& a, cudaStream_t st) {
-  AppendFreq fr{};
-  if (a.rotate)
-    for (int i = 0; i < c.head_dim / 2; ++i) fr.inv[i] = std::pow(a.theta, -2.0 * (double)i / (double)c.head_dim);
+  AppendFreq fr;
+  if (a.rotate) {
+    // powers of the ratio by squares and one product (an error of i half steps of a double at the i-th)
+    double inv[128];
+    const double ratio = std::pow(a.theta, -2.0 / (double)c.head_dim);
+    inv[0] = 1.0;
+    for (int i = 1; i < c.head_dim / 2; ++i) inv[i] = (i & 1) ? inv[i - 1] * ratio : inv[i / 2] * inv[i / 2];
+    for (int i = 0; i < c.head_dim / 2; ++i) {
+      const double t = inv[i] * 0.15915494309189535;
+      fr.turns[i] = (uint64_t)((t - std::floor(t)) * 18446744073709551616.0);
+    }
+  }
   if (a.f32)
-    append_kernel<float><<<a.n_rows, 256, 0, st>>>(c, a, fr);
+    append_rows<float>(c, a, fr, st);
   else
-    append_kernel<__nv_bfloat16><<<a.n_rows, 256, 0, st>>>(c, a, fr);
+    append_rows<__nv_bfloat16>(c, a, fr, st);
   return cudaGetLastError();
 }
 

@@ -16,7 +16,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
+constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32;
+static_assert(EV_WARPS == 32, "a warp adds up the warps' counts");
 constexpr int EV_MAX_KEYS = 40960;   // keys a CTA holds in shared memory (160 KB); it re-reads what is behind
 constexpr int MV_THREADS = 256, MV_MOVES = 64;
 
@@ -39,6 +40,7 @@ struct EvictLists {
 
 // Up to MV_MOVES moves from the ``i0``-th of a pair on: weights and positions,
 // then the rows in units of 16 bytes, all of a thread's loads before its stores.
+template <int U>
 __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& a, const EvictLists& ls, int b, int g,
                                            int i0, int moves, int threads, long long (*off)[2]) {
   const long long pair = (long long)b * c.n_kv + g, base = pair * paged_slots(c), lb = pair * ls.list;
@@ -58,26 +60,20 @@ __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& 
   __syncthreads();
   const int row = c.head_dim / 8, units = n * 2 * row;
   const long long hs = (long long)g * c.head_stride;
-  constexpr int U = 8;
   for (int u0 = tid; u0 < units; u0 += U * threads) {
     uint4 x[U];
-    uint4* to[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int u = u0 + k * threads;
-      to[k] = nullptr;
-      if (u < units) {
-        const int mv = u / (2 * row), r = u % (2 * row);
-        __nv_bfloat16* pool = (r < row ? c.k : c.v) + hs + 8 * (r < row ? r : r - row);
-        if (off[mv][0] >= 0) {
-          x[k] = *reinterpret_cast<const uint4*>(pool + off[mv][0]);
-          to[k] = reinterpret_cast<uint4*>(pool + off[mv][1]);
-        }
-      }
+      const int u = u0 + k * threads, mv = u / (2 * row), r = u - mv * 2 * row;
+      if (u < units && off[mv][0] >= 0)
+        x[k] = *reinterpret_cast<const uint4*>((r < row ? c.k + 8 * r : c.v + 8 * (r - row)) + hs + off[mv][0]);
     }
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (to[k] != nullptr) *to[k] = x[k];
+    for (int k = 0; k < U; ++k) {
+      const int u = u0 + k * threads, mv = u / (2 * row), r = u - mv * 2 * row;
+      if (u < units && off[mv][0] >= 0)
+        *reinterpret_cast<uint4*>((r < row ? c.k + 8 * r : c.v + 8 * (r - row)) + hs + off[mv][1]) = x[k];
+    }
   }
   __syncthreads();
 }
@@ -90,8 +86,9 @@ __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& 
 // far all stay. Then the staying entries' ranks (counts over warps and CTAs)
 // give each of them its place in the list of holes or movers. The weights are
 // read once; what bounds it is the latency of the 2 to 6 cluster barriers.
+template <bool INLINE>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedView c, const EvictArgs a,
-                                                                  const EvictLists ls, int smem_keys, int inline_moves) {
+                                                                     const EvictLists ls, int smem_keys) {
   extern __shared__ uint32_t ev_keys[];
   __shared__ int hist[2][256], warp_cnt[2][EV_WARPS], cta_cnt[2][2], scan[8], pick[3];
   __shared__ long long off[MV_MOVES][2];
@@ -112,7 +109,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
       if (copy_w) a.weight_out[base + j] = c.weight[base + j];
       if (copy_p) a.pos_out[base + j] = c.pos[base + j];
     }
-    if (inline_moves && rank == 0 && g == 0 && tid == 0) a.lens_out[b] = m;
+    if (INLINE && rank == 0 && g == 0 && tid == 0) a.lens_out[b] = m;
     return;
   }
   const int per = ((n + C - 1) / C + EV_THREADS - 1) / EV_THREADS * EV_THREADS;  // slots of a slice
@@ -153,7 +150,8 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     cluster.sync();
     int cnt = 0, incl = 0;
     if (tid < 256) {  // from the largest digit down
-      for (int r = 0; r < C; ++r) cnt += cluster.map_shared_rank(h, r)[255 - tid];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) cnt += cluster.map_shared_rank(h, r < C ? r : rank)[255 - tid] * (r < C);
       incl = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -187,14 +185,12 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) warp_cnt[0][warp] = cnt;
     __syncthreads();
-    if (tid == 0) {
-      int s = 0;
-      for (int w = 0; w < EV_WARPS; ++w) s += warp_cnt[0][w];
-      cta_cnt[0][0] = s;
-    }
+    const int v = warp_cnt[0][lane], all = __reduce_add_sync(0xffffffffu, v);
+    eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+    if (tid == 0) cta_cnt[0][0] = all;
     cluster.sync();
-    for (int r = 0; r < rank; ++r) eq_before += cluster.map_shared_rank(&cta_cnt[0][0], r)[0];
-    for (int w = 0; w < warp; ++w) eq_before += warp_cnt[0][w];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) eq_before += cluster.map_shared_rank(&cta_cnt[0][0], r < rank ? r : rank)[0] * (r < rank);
     __syncthreads();
   }
   // which of 32 entries stay; ``eq`` runs over the equal ones before them
@@ -221,25 +217,27 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     warp_cnt[1][warp] = movers;
   }
   __syncthreads();
-  if (tid < 2) {
-    int s = 0;
-    for (int w = 0; w < EV_WARPS; ++w) s += warp_cnt[tid][w];
-    cta_cnt[1][tid] = s;
+  {
+    const int h = warp_cnt[0][lane], v = warp_cnt[1][lane];
+    const int hs = __reduce_add_sync(0xffffffffu, h), vs = __reduce_add_sync(0xffffffffu, v);
+    if (tid == 0) {
+      cta_cnt[1][0] = hs;
+      cta_cnt[1][1] = vs;
+    }
+    holes = __reduce_add_sync(0xffffffffu, lane < warp ? h : 0);
+    movers = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
   }
   cluster.sync();
-  holes = movers = 0;
   int all = 0;
-  for (int r = 0; r < C; ++r) {
-    const int* x = cluster.map_shared_rank(&cta_cnt[1][0], r);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {  // (all loads at once: one after the other they cost their latency each)
+    const int* x = cluster.map_shared_rank(&cta_cnt[1][0], r < C ? r : rank);
+    const int x0 = x[0], x1 = x[1];
     if (r < rank) {
-      holes += x[0];
-      movers += x[1];
+      holes += x0;
+      movers += x1;
     }
-    all += x[1];
-  }
-  for (int w = 0; w < warp; ++w) {
-    holes += warp_cnt[0][w];
-    movers += warp_cnt[1][w];
+    if (r < C) all += x1;
   }
   eq = eq_before;
   for (int i0 = w0; i0 < w1; i0 += 32) {
@@ -260,14 +258,14 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
   }
   if (rank == 0 && tid == 0) ls.count[pair] = all;
   cluster.sync();  // the lists are written, and no CTA ends while another reads its counts
-  if (!inline_moves) return;
+  if (!INLINE) return;
   if (rank == 0 && g == 0 && tid == 0) a.lens_out[b] = m;  // (every CTA of the cluster has read the old length)
   for (int i0 = rank * MV_MOVES; i0 < all; i0 += C * MV_MOVES)
-    evict_move(c, a, ls, b, g, i0, all, EV_THREADS, off);
+    evict_move<4>(c, a, ls, b, g, i0, all, EV_THREADS, off);
 }
 
 // 64 moves a CTA.
-__global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const PagedView c, const EvictArgs a,
+__global__ void __launch_bounds__(MV_THREADS, 4) evict_move_kernel(const PagedView c, const EvictArgs a,
                                                                 const EvictLists ls) {
   __shared__ long long off[MV_MOVES][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(MV_THREADS) evict_move_kernel(const PagedView 
   const int b = (int)(pair / c.n_kv), g = (int)(pair % c.n_kv), all = ls.count[pair];
   if (blockIdx.y == 0 && g == 0 && threadIdx.x == 0) a.lens_out[b] = ls.keep[pair];
   for (long long i0 = (long long)blockIdx.y * MV_MOVES; i0 < all; i0 += (long long)gridDim.y * MV_MOVES)
-    evict_move(c, a, ls, b, g, (int)i0, all, MV_THREADS, off);
+    evict_move<8>(c, a, ls, b, g, (int)i0, all, MV_THREADS, off);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -309,14 +307,16 @@ cudaError_t launch_cache_evict(const PagedView& c, const EvictArgs& a, cudaStrea
   ls.keep = reinterpret_cast<int32_t*>(p + up256(4 * pairs));
   ls.hole = reinterpret_cast<int32_t*>(p + 2 * up256(4 * pairs));
   ls.mover = reinterpret_cast<int32_t*>(p + 2 * up256(4 * pairs) + up256(4 * pairs * ls.list));
-  // CTAs of a cluster: slices of at most 1024 slots while the CTAs fit the SMs twice
+  // CTAs of a cluster: slices of at most 8192 slots (8 keys a thread; a barrier of the cluster costs more than
+  // those), while the CTAs fit the SMs
   int C = 1;
-  while (C < 8 && slots > 1024ll * C && pairs * C * 2 <= 2ll * device_sm_count()) C *= 2;
+  while (C < 8 && slots > 8192ll * C && pairs * C * 2 <= device_sm_count()) C *= 2;
   const long long slice = ((slots + C - 1) / C + EV_THREADS - 1) / EV_THREADS * EV_THREADS;
   const int keys = slice < EV_MAX_KEYS ? (int)slice : EV_MAX_KEYS;
   const bool in = evict_inline(c, a);
   if (pairs * C > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(evict_select_kernel), sizeof(uint32_t) * keys);
+  auto* select = in ? evict_select_kernel<true> : evict_select_kernel<false>;
+  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(select), sizeof(uint32_t) * keys);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(pairs * C));
@@ -329,7 +329,7 @@ cudaError_t launch_cache_evict(const PagedView& c, const EvictArgs& a, cudaStrea
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, c, a, ls, keys, (int)in);
+  e = cudaLaunchKernelEx(&cfg, select, c, a, ls, keys);
   if (e != cudaSuccess || in) return e;
   const long long most = a.budget < slots - a.budget ? a.budget : slots - a.budget;
   long long parts = (most + MV_MOVES - 1) / MV_MOVES;
