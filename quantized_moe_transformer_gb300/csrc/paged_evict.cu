@@ -16,9 +16,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32;
-static_assert(EV_WARPS == 32, "a warp adds up the warps' counts");
-constexpr int EV_MAX_KEYS = 40960;   // keys a CTA holds in shared memory (160 KB); it re-reads what is behind
+constexpr int EV_THREADS = 1024, EV_WARPS = 32, EV_CLUSTER = 8;
+constexpr int EV_MAX_KEYS = 40960;  // 160 KB
 constexpr int MV_THREADS = 256, MV_MOVES = 64;
 
 // Order of an entry as an unsigned key: 0xFFFFFFFF for the protected newest
@@ -34,64 +33,86 @@ __device__ __forceinline__ uint32_t evict_key(float w, bool young) {
 
 struct EvictLists {
   int32_t *count, *keep;  // [pairs] entries that move, entries that stay
-  int32_t *hole, *mover;  // [pairs][list] slots, in order
+  int2 *hole, *mover;     // [pairs][list] (slot, page), in the slots' order
   long long list;
 };
 
+__device__ __forceinline__ long long row_offset(const PagedView& c, int2 at) {
+  if ((unsigned)at.y >= (unsigned)c.n_pages) return -1;
+  return (long long)at.y * c.page_stride + (long long)(at.x & ((1 << c.page_log2) - 1)) * c.slot_stride;
+}
+
 // Up to MV_MOVES moves from the ``i0``-th of a pair on: weights and positions,
-// then the rows in units of 16 bytes, all of a thread's loads before its stores.
+// then the rows in units of 16 bytes, U loads of a thread before their stores.
+// (``count``: the pair's moves; the lists are read while it is still on its way.)
 template <int U>
 __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& a, const EvictLists& ls, int b, int g,
-                                           int i0, int moves, int threads, long long (*off)[2]) {
-  const long long pair = (long long)b * c.n_kv + g, base = pair * paged_slots(c), lb = pair * ls.list;
-  const int tid = threadIdx.x, n = min(MV_MOVES, moves - i0);
+                                           int i0, const int32_t* count, int threads, long long (*off)[2]) {
+  const long long pair = (long long)b * c.n_kv + g, base = pair * paged_slots(c), at = pair * ls.list + i0;
+  const int tid = threadIdx.x;
+  int2 src = make_int2(0, 0), dst = src;
+  if (tid < MV_MOVES && i0 + tid < ls.list) {
+    src = ls.mover[at + tid];
+    dst = ls.hole[at + tid];
+  }
+  const int n = min(MV_MOVES, *count - i0);
   if (tid < n) {
-    const int src = ls.mover[lb + i0 + tid], dst = ls.hole[lb + i0 + tid];
-    long long so = paged_offset(c, b, src), to = paged_offset(c, b, dst);
-    a.weight_out[base + dst] = c.weight[base + src];
-    if (c.pos) a.pos_out[base + dst] = c.pos[base + src];
+    long long so = row_offset(c, src);
+    const long long to = row_offset(c, dst);
     if (so < 0 || to < 0) {
       record_status(a.status, QMOE_ERR_DEVICE_ARG);
       so = -1;
     }
     off[tid][0] = so;
     off[tid][1] = to;
+    a.weight_out[base + dst.x] = c.weight[base + src.x];
+    if (c.pos) a.pos_out[base + dst.x] = c.pos[base + src.x];
   }
   __syncthreads();
-  const int row = c.head_dim / 8, units = n * 2 * row;
+  // a lane keeps its place r in a row pair (the key's units, then the value's); a warp has 32 / (2 row) moves at once
+  // where a pair fits it, else it walks one pair
+  const int row = c.head_dim / 8, pair_units = 2 * row, lane = tid & 31, warp = tid >> 5, warps = threads / 32;
+  const int at_once = pair_units <= 32 ? 32 / pair_units : 1, sub = pair_units <= 32 ? lane / pair_units : 0;
   const long long hs = (long long)g * c.head_stride;
-  for (int u0 = tid; u0 < units; u0 += U * threads) {
-    uint4 x[U];
+  for (int r = lane - sub * pair_units; r < pair_units && sub < at_once; r += 32) {
+    __nv_bfloat16* pool = (r < row ? c.k + 8 * r : c.v + 8 * (r - row)) + hs;
+    for (int mv = warp * at_once + sub; mv < n; mv += U * warps * at_once) {
+      uint4 x[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + k * threads, mv = u / (2 * row), r = u - mv * 2 * row;
-      if (u < units && off[mv][0] >= 0)
-        x[k] = *reinterpret_cast<const uint4*>((r < row ? c.k + 8 * r : c.v + 8 * (r - row)) + hs + off[mv][0]);
-    }
+      for (int k = 0; k < U; ++k) {
+        const int i = mv + k * warps * at_once;
+        if (i < n && off[i][0] >= 0) x[k] = *reinterpret_cast<const uint4*>(pool + off[i][0]);
+      }
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + k * threads, mv = u / (2 * row), r = u - mv * 2 * row;
-      if (u < units && off[mv][0] >= 0)
-        *reinterpret_cast<uint4*>((r < row ? c.k + 8 * r : c.v + 8 * (r - row)) + hs + off[mv][1]) = x[k];
+      for (int k = 0; k < U; ++k) {
+        const int i = mv + k * warps * at_once;
+        if (i < n && off[i][0] >= 0) *reinterpret_cast<uint4*>(pool + off[i][1]) = x[k];
+      }
     }
   }
   __syncthreads();
 }
 
-// One cluster per (sequence, KV head); CTA r of it holds the keys of the r-th
-// slice of the slots in shared memory, warp w the w-th part of the slice. The m-th
-// largest key is found 8 bits at a time from the top: each CTA counts its keys by
-// digit, every CTA adds the counts up over the cluster through distributed
-// shared memory and picks the digit, until the entries that share the digits so
-// far all stay. Then the staying entries' ranks (counts over warps and CTAs)
-// give each of them its place in the list of holes or movers. The weights are
-// read once; what bounds it is the latency of the 2 to 6 cluster barriers.
-template <bool INLINE>
+// One cluster of C CTAs per (sequence, KV head). CTA r takes the r-th slice of
+// the slots, warp w the w-th part of the slice, 32 slots at a time; the keys
+// stay in shared memory (slices beyond EV_MAX_KEYS are read again for each step). The m-th largest key is
+// found 8 bits at a time from the top: the keys that share the digits so far
+// are counted by their next digit in shared memory, over the cluster through
+// distributed shared memory, until all that share the digits stay. The staying
+// entries' ranks (counts over warps and CTAs) give each its place in the list
+// of holes or movers. Weights and positions are read once; what bounds it is a
+// chain of short steps: barriers (0.1 us in a CTA, 0.8 us in a cluster, so a
+// cluster is only taken where a CTA would have more than 8 keys a thread) and code
+// that runs once, whose fetch shows (loops unrolled to 8 keys a thread in
+// registers ran longer than these).
+template <bool LONG, bool INLINE>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedView c, const EvictArgs a,
-                                                                     const EvictLists ls, int smem_keys) {
+                                                                  const EvictLists ls) {
   extern __shared__ uint32_t ev_keys[];
-  __shared__ int hist[2][256], warp_cnt[2][EV_WARPS], cta_cnt[2][2], scan[8], pick[3];
-  __shared__ long long off[MV_MOVES][2];
+  __shared__ __align__(16) int hist[3][256];
+  __shared__ __align__(16) int sum[256];
+  __shared__ int warp_cnt[3][EV_WARPS], cta_cnt[3], pick[3];
+  __shared__ long long off[INLINE ? MV_MOVES : 1][2];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -112,61 +133,93 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     if (INLINE && rank == 0 && g == 0 && tid == 0) a.lens_out[b] = m;
     return;
   }
-  const int per = ((n + C - 1) / C + EV_THREADS - 1) / EV_THREADS * EV_THREADS;  // slots of a slice
-  const long long lo = (long long)rank * per;
-  const int size = lo < n ? (int)(n - lo < per ? n - lo : per) : 0;
-  const int w0 = warp * (per / EV_WARPS), w1 = min(size, w0 + per / EV_WARPS);    // this warp's part of it
-  auto fresh = [&](int i) {
-    return evict_key(c.weight[base + lo + i], a.recent > 0 && c.pos[base + lo + i] >= young_from);
+  auto all_sync = [&]() {
+    if (C > 1)
+      cluster.sync();
+    else
+      __syncthreads();
   };
-  auto key = [&](int i) { return i < smem_keys ? ev_keys[i] : fresh(i); };
-#pragma unroll 4
-  for (int i = w0 + lane; i < min(w1, smem_keys); i += 32) ev_keys[i] = fresh(i);
+  // this CTA's slots from lo on; its warp's are [w0, w1) of them
+  const int part = ((n + C - 1) / C + EV_THREADS - 1) / EV_THREADS * 32;
+  const int lo = (int)min((long long)rank * part * EV_WARPS, (long long)n), size = min(part * EV_WARPS, n - lo);
+  const int w0 = warp * part, w1 = min(size, w0 + part);
+  const float* weights = c.weight + base + lo;
+  const int32_t* positions = c.pos + base + lo;
+  auto key = [&](int i) {
+    if (!LONG || i < EV_MAX_KEYS) return ev_keys[i];
+    return evict_key(weights[i], a.recent > 0 && positions[i] >= young_from);
+  };
+  if (tid < 256) hist[0][tid] = hist[1][tid] = hist[2][tid] = 0;
+  // read once; what stays in place goes to the outputs now (what moves into the holes is written over it later)
+  // (four loads ahead of their stores, which the compiler could not tell from the inputs)
+#pragma unroll 1
+  for (int i0 = w0 + lane; i0 < w1; i0 += 128) {
+    float w[4];
+    int p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + 32 * k;
+      w[k] = i < w1 ? weights[i] : 0.f;
+      p[k] = i < w1 && c.pos != nullptr ? positions[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + 32 * k;
+      if (i >= w1) continue;
+      if (!LONG || i < EV_MAX_KEYS) ev_keys[i] = evict_key(w[k], a.recent > 0 && p[k] >= young_from);
+      if (copy_w && lo + i < m) a.weight_out[base + lo + i] = w[k];
+      if (copy_p && lo + i < m) a.pos_out[base + lo + i] = p[k];
+    }
+  }
+  __syncthreads();
 
   // ---- the m-th largest key
   uint32_t t = 0, known = 0;  // its digits so far, and which bits those are
   int need = m, equal = 0;    // of the ``equal`` keys with these digits, ``need`` stay
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    int* h = hist[(shift >> 3) & 1];
-    if (tid < 256) h[tid] = 0;
-    __syncthreads();
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t k = i < w1 ? key(i) : 0u;
-      const bool in = i < w1 && (k & known) == t;
-      const uint32_t digit = (k >> shift) & 255u;
-      // lanes with one digit (equal weights, the first digits) add up first
-      const unsigned active = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const int lead = __ffs(active) - 1;
-        const unsigned same = __ballot_sync(active, digit == __shfl_sync(active, digit, lead));
-        if (same == active) {
-          if (lane == lead) atomicAdd(&h[digit], __popc(active));
-        } else {
-          atomicAdd(&h[digit], 1);
-        }
-      }
+#pragma unroll 1
+  for (int shift = 24, pass = 0; shift >= 0; shift -= 8, ++pass) {
+    int* h = hist[pass % 3];
+    if (pass > 0 && tid < 256) hist[(pass + 1) % 3][tid] = 0;  // (last read two barriers ago)
+#pragma unroll 2
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint32_t k = key(i);
+      if ((k & known) == t) atomicAdd(&h[(k >> shift) & 255u], 1);
     }
-    cluster.sync();
-    int cnt = 0, incl = 0;
-    if (tid < 256) {  // from the largest digit down
+    all_sync();
+    if (C > 1) {
+      if (tid < 256) {
+        int v[EV_CLUSTER], s = 0;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) cnt += cluster.map_shared_rank(h, r < C ? r : rank)[255 - tid] * (r < C);
-      incl = cnt;
+        for (int r = 0; r < EV_CLUSTER; ++r) v[r] = cluster.map_shared_rank(h, r < C ? r : rank)[tid];  // all at once
+#pragma unroll
+        for (int r = 0; r < EV_CLUSTER; ++r) s += r < C ? v[r] : 0;
+        sum[tid] = s;
+      }
+      __syncthreads();
+      h = sum;
+    }
+    if (warp == 0) {
+      // lane l holds the 8 digits from 8 l on; counts from the largest digit down
+      int d[8], own = 0;
+      *reinterpret_cast<int4*>(d) = reinterpret_cast<const int4*>(h)[2 * lane];
+      *reinterpret_cast<int4*>(d + 4) = reinterpret_cast<const int4*>(h)[2 * lane + 1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) own += d[i];
+      int above = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+        const int x = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += x;
       }
-      if (lane == 31) scan[warp] = incl;
-    }
-    __syncthreads();
-    if (tid < 256) {
-      for (int w = 0; w < warp; ++w) incl += scan[w];
-      if (incl >= need && incl - cnt < need) {
-        pick[0] = 255 - tid;
-        pick[1] = need - (incl - cnt);
-        pick[2] = cnt;
+      above -= own;  // keys with digits of higher lanes
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        if (above < need && above + d[i] >= need) {
+          pick[0] = 8 * lane + i;
+          pick[1] = need - above;
+          pick[2] = d[i];
+        }
+        above += d[i];
       }
     }
     __syncthreads();
@@ -176,104 +229,106 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     equal = pick[2];
     if (need == equal) break;
   }
-  // ---- ranks: of the equal keys the lowest slots stay
+  // ---- ranks
   int eq_before = 0;
-  const bool rank_equal = need < equal;
+  const bool rank_equal = need < equal;  // of the equal keys the lowest slots stay
   if (rank_equal) {
     int cnt = 0;
+#pragma unroll 2
     for (int i = w0 + lane; i < w1; i += 32) cnt += key(i) == t;
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) warp_cnt[0][warp] = cnt;
     __syncthreads();
-    const int v = warp_cnt[0][lane], all = __reduce_add_sync(0xffffffffu, v);
+    const int v = warp_cnt[0][lane];
     eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
-    if (tid == 0) cta_cnt[0][0] = all;
-    cluster.sync();
-#pragma unroll
-    for (int r = 0; r < 8; ++r) eq_before += cluster.map_shared_rank(&cta_cnt[0][0], r < rank ? r : rank)[0] * (r < rank);
-    __syncthreads();
+    if (C > 1) {
+      if (warp == 0) {
+        const int all = __reduce_add_sync(0xffffffffu, v);
+        if (lane == 0) cta_cnt[0] = all;
+      }
+      cluster.sync();
+      const int x = lane < rank ? *cluster.map_shared_rank(&cta_cnt[0], lane < rank ? lane : rank) : 0;
+      eq_before += __reduce_add_sync(0xffffffffu, x);
+    }
   }
-  // which of 32 entries stay; ``eq`` runs over the equal ones before them
+  // whether the entry stays (the whole warp asks for 32 in a row); ``eq`` runs over the equal ones before
+  const unsigned lower = (1u << lane) - 1u;
   auto stays = [&](int i, int& eq) {
     const uint32_t k = i < w1 ? key(i) : 0u;
-    bool kept = i < w1 && k >= t;
+    bool s = i < w1 && k >= t;
     if (rank_equal) {
-      const bool same = i < w1 && k == t;
+      const bool same = s && k == t;
       const unsigned mk = __ballot_sync(0xffffffffu, same);
-      if (same) kept = eq + __popc(mk & ((1u << lane) - 1u)) < need;
+      if (same) s = eq + __popc(mk & lower) < need;
       eq += __popc(mk);
     }
-    return kept;
+    return s;
   };
   int holes = 0, movers = 0, eq = eq_before;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const bool kept = stays(i, eq);
-    holes += __popc(__ballot_sync(0xffffffffu, i < w1 && !kept && lo + i < m));
-    movers += __popc(__ballot_sync(0xffffffffu, kept && lo + i >= m));
+#pragma unroll 2
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const bool s = stays(i, eq);
+    holes += i < w1 && !s && lo + i < m;
+    movers += s && lo + i >= m;
   }
+  holes = __reduce_add_sync(0xffffffffu, holes);
+  movers = __reduce_add_sync(0xffffffffu, movers);
   if (lane == 0) {
-    warp_cnt[0][warp] = holes;
-    warp_cnt[1][warp] = movers;
+    warp_cnt[1][warp] = holes;
+    warp_cnt[2][warp] = movers;
   }
   __syncthreads();
-  {
-    const int h = warp_cnt[0][lane], v = warp_cnt[1][lane];
-    const int hs = __reduce_add_sync(0xffffffffu, h), vs = __reduce_add_sync(0xffffffffu, v);
+  const int vh = warp_cnt[1][lane], vm = warp_cnt[2][lane];
+  int all = __reduce_add_sync(0xffffffffu, vm);
+  holes = __reduce_add_sync(0xffffffffu, lane < warp ? vh : 0);
+  movers = __reduce_add_sync(0xffffffffu, lane < warp ? vm : 0);
+  if (C > 1) {
+    const int all_h = __reduce_add_sync(0xffffffffu, vh);
     if (tid == 0) {
-      cta_cnt[1][0] = hs;
-      cta_cnt[1][1] = vs;
+      cta_cnt[1] = all_h;
+      cta_cnt[2] = all;
     }
-    holes = __reduce_add_sync(0xffffffffu, lane < warp ? h : 0);
-    movers = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
-  }
-  cluster.sync();
-  int all = 0;
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {  // (all loads at once: one after the other they cost their latency each)
-    const int* x = cluster.map_shared_rank(&cta_cnt[1][0], r < C ? r : rank);
-    const int x0 = x[0], x1 = x[1];
-    if (r < rank) {
-      holes += x0;
-      movers += x1;
-    }
-    if (r < C) all += x1;
+    cluster.sync();
+    const int* x = cluster.map_shared_rank(&cta_cnt[0], lane < C ? lane : rank);
+    const int xh = x[1], xm = x[2];
+    holes += __reduce_add_sync(0xffffffffu, lane < rank ? xh : 0);
+    movers += __reduce_add_sync(0xffffffffu, lane < rank ? xm : 0);
+    all = __reduce_add_sync(0xffffffffu, lane < C ? xm : 0);
   }
   eq = eq_before;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const bool kept = stays(i, eq);
-    const int j = (int)lo + i;
-    const bool hole = i < w1 && !kept && j < m, mover = kept && j >= m;
+  const int32_t* table = c.table + (long long)b * c.max_pages;
+#pragma unroll 2
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    const bool s = stays(i, eq);
+    const int j = lo + i;
+    const bool hole = i < w1 && !s && j < m, mover = s && j >= m;
     const unsigned mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-    const unsigned below = (1u << lane) - 1u;
-    if (hole) ls.hole[lb + holes + __popc(mh & below)] = j;
-    if (mover) ls.mover[lb + movers + __popc(mm & below)] = j;
+    if (hole || mover) {
+      int2* to = hole ? ls.hole + holes + __popc(mh & lower) : ls.mover + movers + __popc(mm & lower);
+      to[lb] = make_int2(j, __ldg(table + (j >> c.page_log2)));
+    }
     holes += __popc(mh);
     movers += __popc(mm);
-    if (kept && j < m) {
-      if (copy_w) a.weight_out[base + j] = c.weight[base + j];
-      if (copy_p) a.pos_out[base + j] = c.pos[base + j];
-    }
   }
   if (rank == 0 && tid == 0) ls.count[pair] = all;
-  cluster.sync();  // the lists are written, and no CTA ends while another reads its counts
+  all_sync();  // the lists are written, and no CTA ends while another reads its counts
   if (!INLINE) return;
   if (rank == 0 && g == 0 && tid == 0) a.lens_out[b] = m;  // (every CTA of the cluster has read the old length)
   for (int i0 = rank * MV_MOVES; i0 < all; i0 += C * MV_MOVES)
-    evict_move<4>(c, a, ls, b, g, i0, all, EV_THREADS, off);
+    evict_move<2>(c, a, ls, b, g, i0, &all, EV_THREADS, off);
 }
 
 // 64 moves a CTA.
-__global__ void __launch_bounds__(MV_THREADS, 4) evict_move_kernel(const PagedView c, const EvictArgs a,
-                                                                const EvictLists ls) {
+__global__ void __launch_bounds__(MV_THREADS, 5) evict_move_kernel(const PagedView c, const EvictArgs a,
+                                                                   const EvictLists ls) {
   __shared__ long long off[MV_MOVES][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long pair = blockIdx.x;
-  const int b = (int)(pair / c.n_kv), g = (int)(pair % c.n_kv), all = ls.count[pair];
+  const int b = (int)(pair / c.n_kv), g = (int)(pair % c.n_kv);
+  const int32_t* count = ls.count + pair;
   if (blockIdx.y == 0 && g == 0 && threadIdx.x == 0) a.lens_out[b] = ls.keep[pair];
-  for (long long i0 = (long long)blockIdx.y * MV_MOVES; i0 < all; i0 += (long long)gridDim.y * MV_MOVES)
-    evict_move<8>(c, a, ls, b, g, (int)i0, all, MV_THREADS, off);
+  for (long long i0 = (long long)blockIdx.y * MV_MOVES; i0 < *count; i0 += (long long)gridDim.y * MV_MOVES)
+    evict_move<8>(c, a, ls, b, g, (int)i0, count, MV_THREADS, off);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -285,54 +340,68 @@ size_t list_len(const PagedView& c) { return (size_t)paged_slots(c) / 2 + 1; }
 
 size_t cache_evict_ws_bytes(const PagedView& c) {
   const size_t pairs = (size_t)c.n_seqs * c.n_kv;
-  return 2 * up256(4 * pairs) + 2 * up256(4 * pairs * list_len(c));
+  return 2 * up256(4 * pairs) + 2 * up256(sizeof(int2) * pairs * list_len(c));
 }
 
-// One kernel where a CTA of the select kernel has at most 64 moves, and no
-// cluster that starts later reads a length that another has replaced: a second
-// launch costs more than the moves. Else the moves get a grid of their own.
-static bool evict_inline(const PagedView& c, const EvictArgs& a) {
-  const long long slots = paged_slots(c), most = a.budget < slots - a.budget ? a.budget : slots - a.budget;
-  return most <= MV_MOVES && (c.n_kv == 1 || a.lens_out != c.lens);
+namespace {
+
+struct EvictPlan {
+  int cluster, keys;  // CTAs of a cluster, keys of a CTA in shared memory
+  bool long_slices, inline_moves;
+  long long moves;    // of one pair, at most
+};
+
+// Clusters are taken beyond 8192 slots a CTA. The moves are made by the select
+// kernel where a CTA has at most 64 of them and no cluster that starts later
+// reads a length that another has replaced (a launch costs more than those
+// moves), else by a grid of their own.
+EvictPlan evict_plan(const PagedView& c, const EvictArgs& a) {
+  EvictPlan p{};
+  const long long slots = paged_slots(c);
+  p.cluster = 1;
+  while (p.cluster < EV_CLUSTER && slots > 8ll * EV_THREADS * p.cluster) p.cluster *= 2;
+  const long long per = ((slots + p.cluster - 1) / p.cluster + EV_THREADS - 1) / EV_THREADS * EV_THREADS;
+  p.keys = per < EV_MAX_KEYS ? (int)per : EV_MAX_KEYS;
+  p.long_slices = per > EV_MAX_KEYS;
+  p.moves = a.budget < slots - a.budget ? a.budget : slots - a.budget;
+  p.inline_moves = p.moves <= MV_MOVES * p.cluster && (c.n_kv == 1 || a.lens_out != c.lens);
+  return p;
 }
 
-int cache_evict_launches(const PagedView& c, const EvictArgs& a) { return evict_inline(c, a) ? 1 : 2; }
+}  // namespace
+
+int cache_evict_launches(const PagedView& c, const EvictArgs& a) { return evict_plan(c, a).inline_moves ? 1 : 2; }
 
 cudaError_t launch_cache_evict(const PagedView& c, const EvictArgs& a, cudaStream_t st) {
-  const long long pairs = (long long)c.n_seqs * c.n_kv, slots = paged_slots(c);
+  const long long pairs = (long long)c.n_seqs * c.n_kv;
   char* p = static_cast<char*>(a.ws);
   EvictLists ls;
   ls.list = (long long)list_len(c);
+  const size_t head = up256(4 * pairs), lists = up256(sizeof(int2) * pairs * ls.list);
   ls.count = reinterpret_cast<int32_t*>(p);
-  ls.keep = reinterpret_cast<int32_t*>(p + up256(4 * pairs));
-  ls.hole = reinterpret_cast<int32_t*>(p + 2 * up256(4 * pairs));
-  ls.mover = reinterpret_cast<int32_t*>(p + 2 * up256(4 * pairs) + up256(4 * pairs * ls.list));
-  // CTAs of a cluster: slices of at most 8192 slots (8 keys a thread; a barrier of the cluster costs more than
-  // those), while the CTAs fit the SMs
-  int C = 1;
-  while (C < 8 && slots > 8192ll * C && pairs * C * 2 <= device_sm_count()) C *= 2;
-  const long long slice = ((slots + C - 1) / C + EV_THREADS - 1) / EV_THREADS * EV_THREADS;
-  const int keys = slice < EV_MAX_KEYS ? (int)slice : EV_MAX_KEYS;
-  const bool in = evict_inline(c, a);
-  if (pairs * C > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  auto* select = in ? evict_select_kernel<true> : evict_select_kernel<false>;
-  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(select), sizeof(uint32_t) * keys);
-  if (e != cudaSuccess) return e;
+  ls.keep = reinterpret_cast<int32_t*>(p + head);
+  ls.hole = reinterpret_cast<int2*>(p + 2 * head);
+  ls.mover = reinterpret_cast<int2*>(p + 2 * head + lists);
+  const EvictPlan pl = evict_plan(c, a);
+  if (pairs * pl.cluster > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(pairs * C));
+  cfg.gridDim = dim3((unsigned)(pairs * pl.cluster));
   cfg.blockDim = dim3(EV_THREADS);
-  cfg.dynamicSmemBytes = sizeof(uint32_t) * keys;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.x = pl.cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, select, c, a, ls, keys);
-  if (e != cudaSuccess || in) return e;
-  const long long most = a.budget < slots - a.budget ? a.budget : slots - a.budget;
-  long long parts = (most + MV_MOVES - 1) / MV_MOVES;
+  auto* select = pl.long_slices ? (pl.inline_moves ? evict_select_kernel<true, true> : evict_select_kernel<true, false>)
+                                : (pl.inline_moves ? evict_select_kernel<false, true> : evict_select_kernel<false, false>);
+  cfg.dynamicSmemBytes = sizeof(uint32_t) * pl.keys;
+  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(select), cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, select, c, a, ls);
+  if (e != cudaSuccess || pl.inline_moves) return e;
+  long long parts = (pl.moves + MV_MOVES - 1) / MV_MOVES;
   if (parts < 1) parts = 1;
   if (parts > 65535) parts = 65535;
   cfg = cudaLaunchConfig_t{};

@@ -439,11 +439,24 @@ def test_evict_ties_and_special_weights(kind):
     check_evict(c, 16, 333, 20, next_pos, in_place=False)
 
 
-@pytest.mark.parametrize("n,budget", [(4097, 4096), (4100, 4096), (33000, 8192), (70001, 69000), (70001, 300)])
+@pytest.mark.parametrize("n,budget", [(4097, 4096), (4100, 4096), (33000, 8192), (70001, 69000), (70001, 300), (100001, 2000)])
 def test_evict_long(n, budget):
     c, g = ref.cache(32, [n], 1, 64, 64)
     next_pos = torch.tensor([c["pos"].shape[2]], dtype=torch.int32, device="cuda")
     check_evict(c, 64, budget, min(128, budget), next_pos, in_place=True)
+
+
+@pytest.mark.parametrize("budget", [399990, 150000])
+def test_evict_longest(budget):
+    """More slots than a cluster's shared memory holds keys of, with equal weights
+    on both sides of that border."""
+    n = 400001
+    c, g = ref.cache(37, [n], 1, 8, 64)
+    c["weight"].copy_(torch.floor(c["weight"] * 50))
+    next_pos = torch.tensor([c["pos"].shape[2]], dtype=torch.int32, device="cuda")
+    check_evict(c, 64, budget, 1000, next_pos, in_place=False)
+    c["weight"][0, 0, 100:] = 7.0
+    check_evict(c, 64, budget, 0, None, in_place=True, with_pos=False)
 
 
 @pytest.mark.parametrize("layout", ["heads", "both"])
