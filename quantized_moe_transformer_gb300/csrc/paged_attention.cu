@@ -20,20 +20,20 @@ namespace {
 //
 // Work. A row is (sequence, KV head, tile of at most 8 NT query heads); its
 // slots are cut into tiles of KT. The tiles of all rows in order are dealt out
-// evenly, a contiguous range to each CTA (one CTA per SM), so that a batch of
-// unequal sequences and one long sequence both keep every SM busy. The part of
-// a row inside a CTA is a segment; the CTA's warps take its tiles in turn, each
-// with its own running (maximum, sum, output), and merge them through shared
-// memory at the segment's end. A row inside one CTA is finished there; of a
-// row over several CTAs each writes a partial, and the join kernel finishes it.
-// A CTA has at most one partial of a row that began earlier (slot 0) and one
-// of a row that begins in it (slot 1).
+// evenly, a contiguous range to each CTA (one CTA per SM) and of that to each
+// of its warps, so that a batch of unequal sequences and one long sequence both
+// keep every SM busy. A warp finishes the rows that lie inside its range by
+// itself; what it has of others it leaves in shared memory (the end of a row
+// that began earlier in the merge area, the beginning of one that goes on in
+// its own ring), and after the CTA's only barrier these are merged. A row over
+// several CTAs leaves a partial in each, which the join kernel finishes: a CTA
+// has at most one of a row that began earlier (slot 0) and one of a row that
+// begins in it (slot 1).
 //
 // Loads. Every warp feeds itself: its lanes look pages up one tile ahead and
 // issue tensor copies (boxes of 64 head dims x up to KT slots of a page, 128-byte
 // swizzled) into the warp's own ring of STAGES tiles; no warp waits for
-// another inside a segment, and the copies of the next segment are in flight
-// while one is merged.
+// another, and copies run on across rows.
 //
 // Products. Scores are S^T = K Q^T with the slots as the rows of a 16 x 8
 // fragment and the G heads as its 8 columns, so that a group of 8 heads fills
@@ -54,7 +54,8 @@ struct PaCfg {
   static constexpr int RING = WARPS * STAGES * 2 * KBYTES;
   static constexpr int HT = 8 * NT;                        // heads of a row
   static constexpr int MERGE = WARPS * HT * HDP * 4;
-  static constexpr int SMEM = 1024 + RING + MERGE + WARPS * HT * 8 + WARPS * STAGES * 16 + 128;
+  static constexpr int SMEM = 1024 + RING + MERGE + 2 * WARPS * HT * 8 + WARPS * STAGES * 12;
+  static_assert(HT * HDP * 4 <= STAGES * 2 * KBYTES, "a warp's output fits its ring");
 };
 
 struct PaSplit {
@@ -63,7 +64,7 @@ struct PaSplit {
   void* out;
   float scale_log2;  // scores in units of log2(e)
   int n_heads, group, head_tiles, box_rows;
-  int min_tiles;     // a CTA's share is at least this
+  int whole_rows;    // CTAs begin at rows (nothing is joined)
   int4* desc;        // [CTAs] the row that begins there and is joined: (sequence, row, CTAs, -), or -1
   float2* part_ml;   // [CTAs][2][heads]
   float* part_o;     // [CTAs][2][heads][HDP]
@@ -119,20 +120,25 @@ struct PaWalk {
 };
 
 template <int KT>
+__device__ __forceinline__ void pa_seq(const PagedView& c, PaWalk& w) {
+  w.len = paged_len(c, w.b);
+  w.nt = w.len > 0 ? (w.len + KT - 1) / KT : 1;
+}
+
+template <int KT>
 __device__ __forceinline__ void pa_step(const PagedView& c, int rows, int by, PaWalk& w) {
   w.t += by;
-  while (w.t >= w.nt) {
-    w.t -= w.nt;
-    if (++w.vh == rows) {
-      w.vh = 0;
-      if (++w.b >= c.n_seqs) {  // behind the last tile; never used
-        w.nt = 1 << 30;
-        return;
-      }
-      w.len = paged_len(c, w.b);
-      w.nt = w.len > 0 ? (w.len + KT - 1) / KT : 1;
-    }
-  }
+  if (w.t < w.nt) return;
+  w.t = 0;
+  if (++w.vh < rows) return;
+  w.vh = 0;
+  if (++w.b < c.n_seqs) pa_seq<KT>(c, w);  // (behind the last tile the walk is not used)
+}
+
+// floor(a * b / d) for b <= d (a share of ``a``): 32-bit division where it does.
+__device__ __forceinline__ long long pa_share(long long a, int b, int d) {
+  const unsigned long long x = (unsigned long long)a * (unsigned)b;
+  return (x >> 32) == 0 ? (long long)((unsigned)x / (unsigned)d) : (long long)(x / (unsigned)d);
 }
 
 template <class C>
@@ -142,13 +148,14 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
   constexpr int KT = C::KT, W = C::WARPS, ST = C::STAGES, NT = C::NT, HDP = C::HDP, KS = HDP / 16, HT = C::HT;
   constexpr int THREADS = 32 * W, KB = KT / 16;
   extern __shared__ uint8_t pa_smem_raw[];
-  __shared__ long long s_scan[W + 1], s_start[2];
-  __shared__ int s_seq, s_abort;
+  __shared__ int4 s_head[W], s_tail[W];  // what a warp left: (sequence, row, 1 if there, 1 if the row goes on)
+  __shared__ long long s_last[W];      // the last tile of the row that a warp's tail begins
+  __shared__ int s_abort;
   const uint32_t s0 = tc::smem_u32(pa_smem_raw);
   uint8_t* smem = pa_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
   float* merge_o = reinterpret_cast<float*>(smem + C::RING);                    // [W][HT][HDP]
-  float2* merge_ml = reinterpret_cast<float2*>(smem + C::RING + C::MERGE);      // [W][HT]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + W * HT);              // [W][ST]
+  float2* merge_ml = reinterpret_cast<float2*>(smem + C::RING + C::MERGE);      // [2: head, tail][W][HT]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + 2 * W * HT);          // [W][ST]
   uint32_t* masks = reinterpret_cast<uint32_t*>(bars + W * ST);                 // [W][ST]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const PagedView& c = p.c;
@@ -159,71 +166,69 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
   if (tid == 0) {
     s_abort = 0;
     tc::fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
-
-  // ---- this CTA's share of the tiles
-  long long mine = 0;
-  for (int b = tid; b < c.n_seqs; b += THREADS) mine += pa_tiles(c, b, KT);
+  if (tid < W) s_head[tid] = s_tail[tid] = make_int4(0, 0, 0, 0);
+  // ---- this CTA's and this warp's share of the tiles, found by every warp for itself: a lane has the sequences
+  // lane * q .. lane * q + q - 1, and the tiles ahead of them
+  const int q = (c.n_seqs + 31) / 32;
+  long long ahead_of = 0;
+  for (int b = lane * q; b < min(c.n_seqs, (lane + 1) * q); ++b) ahead_of += pa_tiles(c, b, KT);
+  const long long own_tiles = ahead_of;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-  if (lane == 0) s_scan[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) total += s_scan[w];
-  total *= rows;
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < p.min_tiles) per = p.min_tiles;
-  const long long T0 = (long long)blockIdx.x * per;
-  const long long T1 = T0 + per < total ? T0 + per : total;
-  if (T0 >= T1) {
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, ahead_of, off);
+    if (lane >= off) ahead_of += x;
+  }
+  const long long total = __shfl_sync(0xffffffffu, ahead_of, 31) * rows;
+  ahead_of = (ahead_of - own_tiles) * rows;
+  // CTAs: one for each W tiles (a tile for each warp) as far as there are; those of a single sequence then begin at its rows
+  const long long fit = c.n_seqs == 1 ? (total / rows + W - 1) / W * rows : (total + W - 1) / W;
+  const int n_ctas = (int)(fit < gridDim.x ? fit : gridDim.x);
+  if (blockIdx.x >= n_ctas) {
     if (tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
     return;
   }
-  // the sequence in which it begins
-  long long before = 0;
-  for (int b0 = 0; b0 < c.n_seqs; b0 += THREADS) {
-    const int b = b0 + tid;
-    const long long own = b < c.n_seqs ? (long long)pa_tiles(c, b, KT) * rows : 0;
-    long long incl = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
+  // the row of tile ``x`` (below the total): sequence, row, tile, and the row's first tile
+  auto locate = [&](long long x, PaWalk& w) {
+    const int holder = __popc(__ballot_sync(0xffffffffu, ahead_of <= x)) - 1;
+    long long base = __shfl_sync(0xffffffffu, ahead_of, holder);
+    w.b = holder * q;
+    pa_seq<KT>(c, w);
+    while (x >= base + (long long)w.nt * rows) {
+      base += (long long)w.nt * rows;
+      ++w.b;
+      pa_seq<KT>(c, w);
     }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    long long base = before, all = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) base += s_scan[w];
-      all += s_scan[w];
+    x -= base;
+    w.vh = (int)((x >> 32) == 0 ? (unsigned)x / (unsigned)w.nt : x / w.nt);
+    w.t = (int)(x - (long long)w.vh * w.nt);
+  };
+  long long C0 = pa_share(total, blockIdx.x, n_ctas), C1 = pa_share(total, blockIdx.x + 1, n_ctas);
+  if (p.whole_rows) {
+    PaWalk w;
+    locate(C0, w);
+    C0 -= w.t;
+    if (C1 < total) {
+      locate(C1, w);
+      C1 -= w.t;
     }
-    if (T0 >= base + incl - own && T0 < base + incl) {
-      s_seq = b;
-      s_start[0] = base + incl - own;
-    }
-    before += all;
-    if (T0 < before) break;
   }
-  __syncthreads();
-  PaWalk first;
-  first.b = s_seq;
-  first.len = paged_len(c, first.b);
-  first.nt = first.len > 0 ? (first.len + KT - 1) / KT : 1;
-  first.vh = (int)((T0 - s_start[0]) / first.nt);
-  first.t = (int)((T0 - s_start[0]) % first.nt);
+  const long long T0 = C0 + pa_share(C1 - C0, warp, W);
+  const int count = (int)(C0 + pa_share(C1 - C0, warp + 1, W) - T0);  // this warp's tiles
+  PaWalk seg{};
+  if (count > 0) locate(T0, seg);
+  __syncthreads();  // the barriers are set up
   if (tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-  // ---- loads: this warp's tiles are T0 + warp, T0 + warp + W, ...
+  // ---- loads
   uint8_t* ring = smem + warp * ST * 2 * C::KBYTES;
   uint64_t* full = bars + warp * ST;
   uint32_t* mask_of = masks + warp * ST;
   const int pieces = KT / p.box_rows, page_mask = (1 << c.page_log2) - 1;
-  long long left = T1 - T0 - warp;  // tiles of this warp still to look up: ceil(left / W)
-  PaWalk ahead = first;
-  pa_step<KT>(c, rows, warp, ahead);
+  int left = count;  // tiles still to look up
+  PaWalk ahead = seg;
   // page of this lane's piece of the tile at ``ahead``; -1: holds nothing
   auto look_up = [&](int& page) {
     page = -1;
@@ -256,38 +261,73 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
         pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, 64 * h, slot & page_mask, g, page, &full[st]);
     }
   };
+  // a row's queries as B fragments hold them: head lane / 4, dims 2 (lane % 4) + {0, 1, 8, 9} of each 16
+  float2 qx[C::F32 ? KS : 1][NT][2];
+  uint32_t qf[KS][NT][C::QP][2];
+  auto load_q = [&](const PaWalk& w) {
+    const int g = w.vh / p.head_tiles, h0 = g * p.group + (w.vh % p.head_tiles) * HT;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int hh = 8 * n + (lane >> 2);
+      const long long qo = ((long long)w.b * p.n_heads + h0 + hh) * c.head_dim;
+      const bool head = h0 + hh < (g + 1) * p.group;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int d = 16 * i + 8 * half + 2 * (lane & 3);
+          const bool in = head && d < c.head_dim;
+          if constexpr (C::F32)
+            qx[i][n][half] = in ? *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + qo + d)
+                                : make_float2(0.f, 0.f);
+          else
+            qf[i][n][0][half] =
+                in ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + qo + d) : 0u;
+        }
+    }
+  };
+  int next_page;
   {
     int pages[ST];
     PaWalk at[ST];
-    bool some[ST];
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
       look_up(pages[s]);
       at[s] = ahead;
-      some[s] = left > 0;
-      left -= W;
-      if (left > 0) pa_step<KT>(c, rows, W, ahead);
+      if (--left > 0) pa_step<KT>(c, rows, 1, ahead);
     }
+    look_up(next_page);
+    if (count > 0) load_q(seg);
 #pragma unroll
     for (int s = 0; s < ST; ++s)
-      if (some[s]) issue(s, at[s], pages[s]);
+      if (s < count) issue(s, at[s], pages[s]);
   }
-  int next_page;
-  look_up(next_page);
 
-  // ---- segments
-  PaWalk seg = first;
-  long long pos = T0;
-  int turn = warp;  // tiles until this warp's next one
-  int stage = 0;
+  // ---- rows
+  int stage = 0, done = 0;
   uint32_t phase = 0;
   bool ok = true;
-  while (pos < T1) {
-    const long long rest = T1 - pos;
-    const int n_tiles = (int)(rest < seg.nt - seg.t ? rest : seg.nt - seg.t);
-    const bool whole = seg.t == 0 && n_tiles == seg.nt;
+  while (done < count) {
+    const int n_tiles = min(count - done, seg.nt - seg.t);
     const int g = seg.vh / p.head_tiles, h0 = g * p.group + (seg.vh % p.head_tiles) * HT;
     const int n_h = min(HT, (g + 1) * p.group - h0);  // heads of this row
+    if constexpr (C::F32) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float x0 = qx[i][n][half].x, x1 = qx[i][n][half].y;
+#pragma unroll
+            for (int part = 0; part < C::QP; ++part) {
+              const uint32_t u = tc::pack_bf16x2(x0, x1);
+              qf[i][n][part][half] = u;
+              x0 -= bf_lo(u);
+              x1 -= bf_hi(u);
+            }
+          }
+    }
     float m[NT][2], l[NT][2], o[KS][NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -296,190 +336,166 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
-    if (turn < n_tiles) {
-      // the row's queries as B fragments: head lane / 4, dims 2 (lane % 4) + {0, 1, 8, 9} of each 16
-      uint32_t qf[KS][NT][C::QP][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int hh = 8 * n + (lane >> 2);
-        const long long qo = ((long long)seg.b * p.n_heads + h0 + hh) * c.head_dim;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int d = 16 * i + 8 * half + 2 * (lane & 3);
-            const bool in = hh < n_h && d < c.head_dim;
-            if (C::F32) {
-              const float2 x = in ? *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + qo + d)
-                                  : make_float2(0.f, 0.f);
-              float x0 = x.x, x1 = x.y;
-#pragma unroll
-              for (int part = 0; part < C::QP; ++part) {
-                const uint32_t u = tc::pack_bf16x2(x0, x1);
-                qf[i][n][part][half] = u;
-                x0 -= bf_lo(u);
-                x1 -= bf_hi(u);
-              }
-            } else {
-              qf[i][n][0][half] =
-                  in ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + qo + d) : 0u;
-            }
-          }
-        }
+#pragma unroll 1
+    for (int turn = 0; turn < n_tiles; ++turn) {
+      if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &s_abort))) {
+        ok = false;
+        if (lane == 0) record_status(p.status, QMOE_ERR_TIMEOUT);
       }
-      for (; turn < n_tiles; turn += W) {
-        if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &s_abort))) {
-          ok = false;
-          if (lane == 0) record_status(p.status, QMOE_ERR_TIMEOUT);
+      if (!ok) continue;
+      const uint32_t held = mask_of[stage];
+      uint8_t* tile = ring + stage * 2 * C::KBYTES;
+      const uint32_t kt = tc::smem_u32(tile), vt = kt + C::KBYTES;
+      constexpr uint32_t FULL = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
+      if (held != FULL) {
+        // values of slots that hold nothing are set to zero: 0 times whatever lay there need not be 0
+        for (int i = lane; i < KT * (HDP / 8); i += 32) {
+          const int r = i / (HDP / 8), ch = i % (HDP / 8);
+          if (!((held >> r) & 1u))
+            *reinterpret_cast<uint4*>(tile + C::KBYTES + (ch >> 3) * C::HALF + r * 128 + (ch & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
         }
-        if (!ok) continue;
-        const uint32_t held = mask_of[stage];
-        uint8_t* tile = ring + stage * 2 * C::KBYTES;
-        const uint32_t kt = tc::smem_u32(tile), vt = kt + C::KBYTES;
-        constexpr uint32_t FULL = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u;
-        if (held != FULL) {
-          // values of slots that hold nothing are set to zero: 0 times whatever lay there need not be 0
-          for (int i = lane; i < KT * (HDP / 8); i += 32) {
-            const int r = i / (HDP / 8), ch = i % (HDP / 8);
-            if (!((held >> r) & 1u))
-              *reinterpret_cast<uint4*>(tile + C::KBYTES + (ch >> 3) * C::HALF + r * 128 + (ch & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();  // before a later copy into the same bytes
-          __syncwarp();
-        }
-        // S^T: slots x heads
-        float s[KB][NT][4];
+        tc::fence_proxy_async_smem();  // before a later copy into the same bytes
+        __syncwarp();
+      }
+      // S^T: slots x heads
+      float s[KB][NT][4];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          float s2[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[kb][n][e] = s2[n][e] = 0.f;
-          const int r = 16 * kb + (lane & 15);
-#pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            uint32_t a[4];
-            const int ch = 2 * (i & 3) + (lane >> 4);
-            pa_ldsm(a, kt + (i >> 2) * C::HALF + tc::sw128_offset(r, ch));
-#pragma unroll
-            for (int part = C::QP - 1; part >= 0; --part)
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                pa_mma((i & 1) ? s2[n] : s[kb][n], a, qf[i][n][part][0], qf[i][n][part][1]);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[kb][n][e] = (s[kb][n][e] + s2[n][e]) * p.scale_log2;
-          if (held != FULL) {
-#pragma unroll
-            for (int e = 0; e < 4; e += 2)
-              if (!((held >> (16 * kb + (lane >> 2) + 4 * e)) & 1u))
-#pragma unroll
-                for (int n = 0; n < NT; ++n) s[kb][n][e] = s[kb][n][e + 1] = -INFINITY;
-          }
-        }
-        if (p.scores != nullptr) {
-          // kept until the denominators are known
-          const int t0 = (seg.t + turn) * KT;
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = t0 + 16 * kb + (lane >> 2) + 4 * (e & 2);
-              const long long at = (((long long)seg.b * c.n_kv + g) * paged_slots(c) + j) * p.group + (h0 - g * p.group);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const int hh = 8 * n + 2 * (lane & 3) + (e & 1);
-                if (j < seg.len && hh < n_h) p.scores[at + hh] = s[kb][n][e];
-              }
-            }
-        }
-        // running maximum; the output is rescaled where one grew
-        uint32_t pf[KB][NT][2][2];  // P^T as B fragments: two bf16 parts, slots 0-7 and 8-15
-        bool grew = false;
-        float mn[NT][2];
+      for (int kb = 0; kb < KB; ++kb) {
+        float s2[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(s[0][n][e], s[0][n][e + 2]);
+          for (int e = 0; e < 4; ++e) s[kb][n][e] = s2[n][e] = 0.f;
+        const int r = 16 * kb + (lane & 15);
 #pragma unroll
-            for (int kb = 1; kb < KB; ++kb) x = fmaxf(x, fmaxf(s[kb][n][e], s[kb][n][e + 2]));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            mn[n][e] = fmaxf(m[n][e], x);
-            grew |= mn[n][e] > m[n][e];
-          }
-        if (__any_sync(0xffffffffu, grew)) {
+        for (int i = 0; i < KS; ++i) {
+          uint32_t a[4];
+          const int ch = 2 * (i & 3) + (lane >> 4);
+          pa_ldsm(a, kt + (i >> 2) * C::HALF + tc::sw128_offset(r, ch));
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float al[2];
+          for (int part = C::QP - 1; part >= 0; --part)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              al[e] = m[n][e] == mn[n][e] ? 1.f : exp2f(m[n][e] - mn[n][e]);
-              m[n][e] = mn[n][e];
-              l[n][e] *= al[e];
-            }
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-              o[i][n][0] *= al[0];
-              o[i][n][1] *= al[1];
-              o[i][n][2] *= al[0];
-              o[i][n][3] *= al[1];
-            }
-          }
+            for (int n = 0; n < NT; ++n)
+              pa_mma((i & 1) ? s2[n] : s[kb][n], a, qf[i][n][part][0], qf[i][n][part][1]);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            const float p0 = exp2f(s[kb][n][0] - r0), p1 = exp2f(s[kb][n][1] - r1);
-            const float p2 = exp2f(s[kb][n][2] - r0), p3 = exp2f(s[kb][n][3] - r1);
-            l[n][0] += p0 + p2;
-            l[n][1] += p1 + p3;
-            const uint32_t ua = tc::pack_bf16x2(p0, p1), ub = tc::pack_bf16x2(p2, p3);
-            pf[kb][n][0][0] = pa_transpose(ua);
-            pf[kb][n][0][1] = pa_transpose(ub);
-            pf[kb][n][1][0] = pa_transpose(tc::pack_bf16x2(p0 - bf_lo(ua), p1 - bf_hi(ua)));
-            pf[kb][n][1][1] = pa_transpose(tc::pack_bf16x2(p2 - bf_lo(ub), p3 - bf_hi(ub)));
-          }
-        }
-        // O^T += V^T P^T: head dims x heads
+          for (int e = 0; e < 4; ++e) s[kb][n][e] = (s[kb][n][e] + s2[n][e]) * p.scale_log2;
+        if (held != FULL) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const int r = 16 * kb + (lane & 7) + 8 * (lane >> 4);
+          for (int e = 0; e < 4; e += 2)
+            if (!((held >> (16 * kb + (lane >> 2) + 4 * e)) & 1u))
 #pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            uint32_t a[4];
-            const int ch = 2 * (i & 3) + ((lane >> 3) & 1);
-            pa_ldsm_t(a, vt + (i >> 2) * C::HALF + tc::sw128_offset(r, ch));
-#pragma unroll
-            for (int part = 1; part >= 0; --part)
-#pragma unroll
-              for (int n = 0; n < NT; ++n) pa_mma(o[i][n], a, pf[kb][n][part][0], pf[kb][n][part][1]);
-          }
-        }
-        __syncwarp();  // every lane has read the stage
-        if (left > 0) {
-          issue(stage, ahead, next_page);
-          left -= W;
-          if (left > 0) pa_step<KT>(c, rows, W, ahead);
-          look_up(next_page);
-        }
-        if (++stage == ST) {
-          stage = 0;
-          phase ^= 1u;
+              for (int n = 0; n < NT; ++n) s[kb][n][e] = s[kb][n][e + 1] = -INFINITY;
         }
       }
+      if (p.scores != nullptr) {
+        // kept until the denominators are known
+        const int t0 = (seg.t + turn) * KT;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = t0 + 16 * kb + (lane >> 2) + 4 * (e & 2);
+            const long long at = (((long long)seg.b * c.n_kv + g) * paged_slots(c) + j) * p.group + (h0 - g * p.group);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const int hh = 8 * n + 2 * (lane & 3) + (e & 1);
+              if (j < seg.len && hh < n_h) p.scores[at + hh] = s[kb][n][e];
+            }
+          }
+      }
+      // running maximum; the output is rescaled where one grew
+      uint32_t pf[KB][NT][2][2];  // P^T as B fragments: two bf16 parts, slots 0-7 and 8-15
+      bool grew = false;
+      float mn[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(s[0][n][e], s[0][n][e + 2]);
+#pragma unroll
+          for (int kb = 1; kb < KB; ++kb) x = fmaxf(x, fmaxf(s[kb][n][e], s[kb][n][e + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mn[n][e] = fmaxf(m[n][e], x);
+          grew |= mn[n][e] > m[n][e];
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float al[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            al[e] = m[n][e] == mn[n][e] ? 1.f : exp2f(m[n][e] - mn[n][e]);
+            m[n][e] = mn[n][e];
+            l[n][e] *= al[e];
+          }
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            o[i][n][0] *= al[0];
+            o[i][n][1] *= al[1];
+            o[i][n][2] *= al[0];
+            o[i][n][3] *= al[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const float p0 = exp2f(s[kb][n][0] - r0), p1 = exp2f(s[kb][n][1] - r1);
+          const float p2 = exp2f(s[kb][n][2] - r0), p3 = exp2f(s[kb][n][3] - r1);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          const uint32_t ua = tc::pack_bf16x2(p0, p1), ub = tc::pack_bf16x2(p2, p3);
+          pf[kb][n][0][0] = pa_transpose(ua);
+          pf[kb][n][0][1] = pa_transpose(ub);
+          pf[kb][n][1][0] = pa_transpose(tc::pack_bf16x2(p0 - bf_lo(ua), p1 - bf_hi(ua)));
+          pf[kb][n][1][1] = pa_transpose(tc::pack_bf16x2(p2 - bf_lo(ub), p3 - bf_hi(ub)));
+        }
+      }
+      // O^T += V^T P^T: head dims x heads
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const int r = 16 * kb + (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          uint32_t a[4];
+          const int ch = 2 * (i & 3) + ((lane >> 3) & 1);
+          pa_ldsm_t(a, vt + (i >> 2) * C::HALF + tc::sw128_offset(r, ch));
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) pa_mma(o[i][n], a, pf[kb][n][part][0], pf[kb][n][part][1]);
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (left > 0) {
+        issue(stage, ahead, next_page);
+        if (--left > 0) pa_step<KT>(c, rows, 1, ahead);
+        look_up(next_page);
+      }
+      if (++stage == ST) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
-    turn -= n_tiles;
-
-    // ---- this warp's (m, l, O) of the segment
+    const PaWalk row = seg;
+    done += n_tiles;
+    if (done < count) {
+      pa_step<KT>(c, rows, n_tiles, seg);
+      load_q(seg);
+    }
+    // ---- the row's result, or what this warp leaves of it
+    const bool begins = row.t == 0, goes_on = row.t + n_tiles < row.nt;
+    const bool whole = begins && !goes_on;
+    float* left_o = begins ? reinterpret_cast<float*>(ring) : merge_o + warp * HT * HDP;
+    float2* left_ml = merge_ml + (begins ? W + warp : warp) * HT;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -488,43 +504,88 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
-        l[n][e] = x;
         const int hh = 8 * n + 2 * (lane & 3) + e;
-        if (lane < 4) merge_ml[warp * HT + hh] = make_float2(m[n][e], x);
+        if (!whole) {
+          if (lane < 4) left_ml[hh] = make_float2(m[n][e], x);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          merge_o[(warp * HT + hh) * HDP + 16 * i + (lane >> 2)] = o[i][n][e];
-          merge_o[(warp * HT + hh) * HDP + 16 * i + 8 + (lane >> 2)] = o[i][n][e + 2];
+          for (int i = 0; i < KS; ++i) {
+            left_o[hh * HDP + 16 * i + (lane >> 2)] = o[i][n][e];
+            left_o[hh * HDP + 16 * i + 8 + (lane >> 2)] = o[i][n][e + 2];
+          }
+          continue;
         }
+        if (hh >= n_h) continue;
+        const long long head = (long long)row.b * p.n_heads + h0 + hh;
+        const float il = x == 0.f ? 0.f : 1.f / x;
+        if (lane < 4 && p.lse != nullptr) p.lse[head] = x == 0.f ? 0.f : m[n][e] + log2f(x);
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int d = 16 * i + 8 * half + (lane >> 2);
+            if (d >= c.head_dim) continue;
+            const float y = o[i][n][e + 2 * half] * il;
+            if (C::F32)
+              static_cast<float*>(p.out)[head * c.head_dim + d] = y;
+            else
+              static_cast<__nv_bfloat16*>(p.out)[head * c.head_dim + d] = __float2bfloat16_rn(y);
+          }
       }
-    __syncthreads();
-    // ---- merged over the warps: the result, or a partial for the join
-    const long long part = ((long long)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0)) * HT;
+    if (!whole && lane == 0) {
+      (begins ? s_tail : s_head)[warp] = make_int4(row.b, row.vh, 1, goes_on);
+      if (begins) s_last[warp] = T0 + done - n_tiles + row.nt - 1;
+    }
+  }
+  __syncthreads();
+
+  // ---- rows over several warps: the beginning that a warp left, then the ends that the next ones did
+  const unsigned heads = __ballot_sync(0xffffffffu, lane < W && s_head[lane & (W - 1)].z);
+  const unsigned ends = __ballot_sync(0xffffffffu, lane < W && s_head[lane & (W - 1)].z && !s_head[lane & (W - 1)].w);
+  const unsigned tails = __ballot_sync(0xffffffffu, lane < W && s_tail[lane & (W - 1)].z);
+  auto merge = [&](int first, bool began) {  // first: the warp of the row's first part; began: that is its tail
+    const unsigned after = heads & ~((1u << first) - 1u) & (began ? ~(1u << first) : ~0u);
+    const unsigned end = ends & after;
+    const bool over = end != 0;  // the row ends in this CTA
+    const unsigned mine = over ? after & ((end & (0u - end)) * 2u - 1u) : after;  // warps with another part of it
+    const int4 at = began ? s_tail[first] : s_head[first];
+    const int g = at.y / p.head_tiles, h0 = g * p.group + (at.y % p.head_tiles) * HT;
+    const int n_h = min(HT, (g + 1) * p.group - h0);
+    const long long part = ((long long)blockIdx.x * 2 + (began ? 1 : 0)) * HT;
+    const float* tail_o = reinterpret_cast<const float*>(smem + first * ST * 2 * C::KBYTES);
     for (int i = tid; i < n_h * (HDP / 4); i += THREADS) {
       const int hh = i / (HDP / 4), d = 4 * (i % (HDP / 4));
+      float2 ml[W + 1];
+      float4 x[W + 1];
+#pragma unroll
+      for (int w = 0; w <= W; ++w) {  // the tail last
+        ml[w] = make_float2(-INFINITY, 0.f);
+        x[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w < W ? (mine >> w) & 1u : began) {
+          ml[w] = merge_ml[(w < W ? w : W + first) * HT + hh];
+          x[w] = *reinterpret_cast<const float4*>((w < W ? merge_o + w * HT * HDP : tail_o) + hh * HDP + d);
+        }
+      }
       float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w <= W; ++w) M = fmaxf(M, ml[w].x);
+      const float ref = M == -INFINITY ? 0.f : M;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, merge_ml[w * HT + hh].x);
-      const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float2 ml = merge_ml[w * HT + hh];
-        const float f = exp2f(ml.x - ref);
-        const float4 x = *reinterpret_cast<const float4*>(&merge_o[(w * HT + hh) * HDP + d]);
-        L = fmaf(ml.y, f, L);
-        acc.x = fmaf(x.x, f, acc.x);
-        acc.y = fmaf(x.y, f, acc.y);
-        acc.z = fmaf(x.z, f, acc.z);
-        acc.w = fmaf(x.w, f, acc.w);
+      for (int w = 0; w <= W; ++w) {
+        const float f = exp2f(ml[w].x - ref);
+        L = fmaf(ml[w].y, f, L);
+        acc.x = fmaf(x[w].x, f, acc.x);
+        acc.y = fmaf(x[w].y, f, acc.y);
+        acc.z = fmaf(x[w].z, f, acc.z);
+        acc.w = fmaf(x[w].w, f, acc.w);
       }
-      if (!whole) {
+      if (!began || !over) {
         if (d == 0) p.part_ml[part + hh] = make_float2(M, L);
         *reinterpret_cast<float4*>(&p.part_o[(part + hh) * HDP + d]) = acc;
         continue;
       }
       const float il = L == 0.f ? 0.f : 1.f / L;
-      const long long head = (long long)seg.b * p.n_heads + h0 + hh;
+      const long long head = (long long)at.x * p.n_heads + h0 + hh;
       if (d == 0 && p.lse != nullptr) p.lse[head] = L == 0.f ? 0.f : M + log2f(L);
       if (d < c.head_dim) {
         if (C::F32)
@@ -535,14 +596,21 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
               make_uint2(tc::pack_bf16x2(acc.x * il, acc.y * il), tc::pack_bf16x2(acc.z * il, acc.w * il));
       }
     }
-    if (tid == 0 && !whole && seg.t == 0) {
-      // tiles of the row behind this CTA's range, ``per`` to a CTA
-      const long long more = (long long)seg.nt - n_tiles;
-      p.desc[blockIdx.x] = make_int4(seg.b, seg.vh, 1 + (int)((more + per - 1) / per), 0);
+    if (began && !over && tid == 0) {
+      // the last CTA whose share begins at or before the row's last tile
+      const int owner = (int)(((unsigned long long)(s_last[first] + 1) * (unsigned)n_ctas - 1) / (unsigned long long)total);
+      p.desc[blockIdx.x] = make_int4(at.x, at.y, owner - (int)blockIdx.x + 1, 0);
     }
-    __syncthreads();
-    pos += n_tiles;
-    if (pos < T1) pa_step<KT>(c, rows, n_tiles, seg);
+  };
+  // a row from the CTA before comes first (no warp ahead of its part has begun one), then each that a warp began
+  const int first_head = __ffs(heads) - 1;
+  bool from_before = heads != 0 && (tails & ((1u << (first_head & 31)) - 1u)) == 0;
+#pragma unroll 1
+  for (unsigned left_tails = tails; from_before || left_tails != 0;) {
+    const int first = from_before ? first_head : __ffs(left_tails) - 1;
+    merge(first, !from_before);
+    if (!from_before) left_tails &= left_tails - 1u;
+    from_before = false;
   }
 }
 
@@ -703,7 +771,6 @@ template <class C>
 cudaError_t launch_split(PaSplit& s, int ctas, cudaStream_t st) {
   s.box_rows = 1 << s.c.page_log2;
   if (s.box_rows > C::KT) s.box_rows = C::KT;
-  s.min_tiles = C::WARPS;
   CUtensorMap km, vm;
   if (!pa_encode(&km, s.c.k, s.c, s.box_rows) || !pa_encode(&vm, s.c.v, s.c, s.box_rows)) return cudaErrorInvalidValue;
   cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(paged_split_kernel<C>), C::SMEM);
@@ -748,7 +815,14 @@ cudaError_t launch_dependent(void (*k)(Arg0, Args...), dim3 grid, int threads, c
 size_t paged_attention_ws_bytes(const PagedView& c, int n_heads, bool accumulate) {
   return pa_plan(c, n_heads, false, accumulate, PA_MAX_CTAS).total;
 }
-int paged_attention_launches(const PagedView&, int, bool accumulate) { return accumulate ? 3 : 2; }
+
+// Rows of at most 256 slots are not cut between CTAs: a row more or less for a
+// CTA costs less than the second launch that joins.
+static bool pa_whole_rows(const PagedView& c) { return paged_slots(c) <= 256; }
+
+int paged_attention_launches(const PagedView& c, int, bool accumulate) {
+  return 1 + (pa_whole_rows(c) ? 0 : 1) + (accumulate ? 1 : 0);
+}
 
 cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, cudaStream_t st) {
   int ctas = device_sm_count();
@@ -763,6 +837,7 @@ cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, c
   s.n_heads = a.n_heads;
   s.group = a.n_heads / c.n_kv;
   s.head_tiles = pl.head_tiles;
+  s.whole_rows = pa_whole_rows(c);
   s.desc = reinterpret_cast<int4*>(ws + pl.desc);
   s.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
   s.part_o = reinterpret_cast<float*>(ws + pl.o);
@@ -786,7 +861,8 @@ cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, c
   j.head_dim = c.head_dim;
   j.hdp = pl.hdp;
   j.f32 = a.f32;
-  e = launch_dependent(paged_join_kernel, dim3(ctas, pl.head_tile < s.group ? pl.head_tile : s.group), PJ_THREADS, st, j);
+  if (!s.whole_rows)
+    e = launch_dependent(paged_join_kernel, dim3(ctas, pl.head_tile < s.group ? pl.head_tile : s.group), PJ_THREADS, st, j);
   if (e != cudaSuccess || !a.accumulate) return e;
   // about 8 CTAs an SM over all (sequence, KV head) pairs
   const long long pairs = (long long)c.n_seqs * c.n_kv;
