@@ -30,10 +30,12 @@ namespace {
 // has at most one of a row that began earlier (slot 0) and one of a row that
 // begins in it (slot 1).
 //
-// Loads. Every warp feeds itself: its lanes look pages up one tile ahead and
-// issue tensor copies (boxes of 64 head dims x up to KT slots of a page, 128-byte
-// swizzled) into the warp's own ring of STAGES tiles; no warp waits for
-// another, and copies run on across rows.
+// Loads. Every warp has its own ring of STAGES tiles. It issues its first tiles'
+// copies itself; then one more warp, whose lane w serves warp w, looks pages up
+// a tile ahead and issues tensor copies (boxes of 64 head dims x up to KT slots
+// of a page, 128-byte swizzled) as stages come free, across rows. (With every
+// warp issuing its own copies a tile took 438 instructions of a warp, and the
+// kernel stopped at 6.5 TB/s even out of L2.)
 //
 // Products. Scores are S^T = K Q^T with the slots as the rows of a 16 x 8
 // fragment and the G heads as its 8 columns, so that a group of 8 heads fills
@@ -46,15 +48,16 @@ template <int HDP_, int NT_, bool F32_>
 struct PaCfg {
   static constexpr int HDP = HDP_, NT = NT_, QP = F32_ ? 3 : 1;
   static constexpr bool F32 = F32_;
+  static constexpr int CHAINS = NT == 1 ? 4 : 2;
   static constexpr int KT = HDP == 64 ? 32 : 16;           // slots of a tile: 4 or 8 KB of keys
-  static constexpr int WARPS = HDP == 256 ? 4 : 8;
-  static constexpr int STAGES = NT == 1 ? 3 : 2;           // 192 KB (128 KB) in flight an SM
+  static constexpr int WARPS = HDP == 256 ? 4 : 7;         // and one that feeds them (8 warps: 255 registers a thread)
+  static constexpr int STAGES = NT == 1 ? 3 : 2;           // at most 192 KB in flight an SM
   static constexpr int HALF = KT * 128;                    // 64 head dims of a tile
   static constexpr int KBYTES = HALF * (HDP / 64);
   static constexpr int RING = WARPS * STAGES * 2 * KBYTES;
   static constexpr int HT = 8 * NT;                        // heads of a row
   static constexpr int MERGE = WARPS * HT * HDP * 4;
-  static constexpr int SMEM = 1024 + RING + MERGE + 2 * WARPS * HT * 8 + WARPS * STAGES * 12;
+  static constexpr int SMEM = 1024 + RING + MERGE + 2 * WARPS * HT * 8 + WARPS * STAGES * 20;
   static_assert(HT * HDP * 4 <= STAGES * 2 * KBYTES, "a warp's output fits its ring");
 };
 
@@ -64,6 +67,7 @@ struct PaSplit {
   void* out;
   float scale_log2;  // scores in units of log2(e)
   int n_heads, group, head_tiles, box_rows;
+  bool at_once;      // a copy brings all head dims (else 64)
   int whole_rows;    // CTAs begin at rows (nothing is joined)
   int4* desc;        // [CTAs] the row that begins there and is joined: (sequence, row, CTAs, -), or -1
   float2* part_ml;   // [CTAs][2][heads]
@@ -73,13 +77,21 @@ struct PaSplit {
   int* status;
 };
 
-__device__ __forceinline__ void pa_tma(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page,
-                                       uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(page), "r"(tc::smem_u32(bar))
-      : "memory");
+// ``part``: the 64 head dims from 64 part on, or with a box of all parts the first of them.
+__device__ __forceinline__ void pa_tma(uint32_t dst, const CUtensorMap* map, int row, int part, int head, int page,
+                                       bool at_once, uint64_t* bar) {
+  if (at_once)
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(part), "r"(head), "r"(page), "r"(tc::smem_u32(bar))
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(64 * part), "r"(row), "r"(head), "r"(page), "r"(tc::smem_u32(bar))
+        : "memory");
 }
 
 __device__ __forceinline__ void pa_ldsm(uint32_t* r, uint32_t addr) {
@@ -142,27 +154,29 @@ __device__ __forceinline__ long long pa_share(long long a, int b, int d) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(32 * C::WARPS, 1)
+__global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     paged_split_kernel(const PaSplit p, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
   constexpr int KT = C::KT, W = C::WARPS, ST = C::STAGES, NT = C::NT, HDP = C::HDP, KS = HDP / 16, HT = C::HT;
-  constexpr int THREADS = 32 * W, KB = KT / 16;
+  constexpr int THREADS = 32 * (W + 1), KB = KT / 16;
   extern __shared__ uint8_t pa_smem_raw[];
   __shared__ int4 s_head[W], s_tail[W];  // what a warp left: (sequence, row, 1 if there, 1 if the row goes on)
   __shared__ long long s_last[W];      // the last tile of the row that a warp's tail begins
+  __shared__ int4 s_walk[W];           // a warp's next tile to copy: (sequence, row, tile, tiles left)
   __shared__ int s_abort;
   const uint32_t s0 = tc::smem_u32(pa_smem_raw);
   uint8_t* smem = pa_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
   float* merge_o = reinterpret_cast<float*>(smem + C::RING);                    // [W][HT][HDP]
   float2* merge_ml = reinterpret_cast<float2*>(smem + C::RING + C::MERGE);      // [2: head, tail][W][HT]
   uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + 2 * W * HT);          // [W][ST]
-  uint32_t* masks = reinterpret_cast<uint32_t*>(bars + W * ST);                 // [W][ST]
+  uint64_t* empties = bars + W * ST;                                            // [W][ST]
+  uint32_t* masks = reinterpret_cast<uint32_t*>(empties + W * ST);              // [W][ST]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const PagedView& c = p.c;
   const int rows = c.n_kv * p.head_tiles;
   tc::grid_dep_launch();
 
-  if (tid < W * ST) tc::mbar_init(&bars[tid], 1);
+  if (tid < 2 * W * ST) tc::mbar_init(&bars[tid], 1);
   if (tid == 0) {
     s_abort = 0;
     tc::fence_barrier_init();
@@ -215,8 +229,8 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
       C1 -= w.t;
     }
   }
-  const long long T0 = C0 + pa_share(C1 - C0, warp, W);
-  const int count = (int)(C0 + pa_share(C1 - C0, warp + 1, W) - T0);  // this warp's tiles
+  const long long T0 = C0 + pa_share(C1 - C0, min(warp, W - 1), W);
+  const int count = warp < W ? (int)(C0 + pa_share(C1 - C0, warp + 1, W) - T0) : 0;  // this warp's tiles
   PaWalk seg{};
   if (count > 0) locate(T0, seg);
   __syncthreads();  // the barriers are set up
@@ -226,7 +240,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
   uint8_t* ring = smem + warp * ST * 2 * C::KBYTES;
   uint64_t* full = bars + warp * ST;
   uint32_t* mask_of = masks + warp * ST;
-  const int pieces = KT / p.box_rows, page_mask = (1 << c.page_log2) - 1;
+  const int boxes = p.at_once ? 1 : HDP / 64, pieces = KT / p.box_rows, page_mask = (1 << c.page_log2) - 1;
   int left = count;  // tiles still to look up
   PaWalk ahead = seg;
   // page of this lane's piece of the tile at ``ahead``; -1: holds nothing
@@ -254,11 +268,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
     if (there) {
       const uint32_t dst = tc::smem_u32(ring + st * 2 * C::KBYTES) + (uint32_t)(lane * p.box_rows) * 128u;
       const int g = w.vh / p.head_tiles;
-#pragma unroll
-      for (int h = 0; h < HDP / 64; ++h) pa_tma(dst + h * C::HALF, &kmap, 64 * h, slot & page_mask, g, page, &full[st]);
-#pragma unroll
-      for (int h = 0; h < HDP / 64; ++h)
-        pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, 64 * h, slot & page_mask, g, page, &full[st]);
+#pragma unroll 1
+      for (int h = 0; h < boxes; ++h) {
+        pa_tma(dst + h * C::HALF, &kmap, slot & page_mask, h, g, page, p.at_once, &full[st]);
+        pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, slot & page_mask, h, g, page, p.at_once, &full[st]);
+      }
     }
   };
   // a row's queries as B fragments hold them: head lane / 4, dims 2 (lane % 4) + {0, 1, 8, 9} of each 16
@@ -286,8 +300,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
         }
     }
   };
-  int next_page;
-  {
+  if (count > 0) {
     int pages[ST];
     PaWalk at[ST];
 #pragma unroll
@@ -296,11 +309,84 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
       at[s] = ahead;
       if (--left > 0) pa_step<KT>(c, rows, 1, ahead);
     }
-    look_up(next_page);
-    if (count > 0) load_q(seg);
+    load_q(seg);
 #pragma unroll
     for (int s = 0; s < ST; ++s)
       if (s < count) issue(s, at[s], pages[s]);
+  }
+  if (warp < W && lane == 0) s_walk[warp] = make_int4(ahead.b, ahead.vh, ahead.t, left);
+  __syncthreads();
+
+  if (warp == W) {
+    // ---- the copies of the other warps' later tiles: lane w feeds warp w
+    const int4 from = lane < W ? s_walk[lane] : make_int4(0, 0, 0, 0);
+    PaWalk w{};
+    w.b = from.x;
+    if (from.w > 0) pa_seq<KT>(c, w);
+    w.vh = from.y;
+    w.t = from.z;
+    left = from.w;
+    constexpr int PIECES = KT / 8;
+    int pages[PIECES];
+    auto pages_of = [&]() {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int slot = w.t * KT + i * p.box_rows;
+        pages[i] = left > 0 && i < pieces && slot < w.len
+                       ? __ldg(c.table + (long long)w.b * c.max_pages + (slot >> c.page_log2)) : -1;
+      }
+    };
+    pages_of();
+    uint8_t* to = smem + (lane < W ? lane : 0) * ST * 2 * C::KBYTES;
+    const int bar0 = (lane < W ? lane : 0) * ST;
+    int st = 0;
+    uint32_t ph = 0;
+    uint64_t since = tc::global_ns();
+    for (int spin = 0; __any_sync(0xffffffffu, left > 0); ++spin) {
+      const bool ready = left > 0 && tc::mbar_test_wait(&empties[bar0 + st], ph);
+      if (ready) {
+        const int n_in = min(KT, w.len - w.t * KT);
+        uint32_t held = 0, bytes = 0;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const bool want = i < pieces && i * p.box_rows < n_in;
+          const bool there = want && (unsigned)pages[i] < (unsigned)c.n_pages;
+          if (want && !there) record_status(p.status, QMOE_ERR_DEVICE_ARG);
+          if (there) {
+            held |= (p.box_rows == 32 ? 0xffffffffu : (1u << p.box_rows) - 1u) << (i * p.box_rows);
+            bytes += (uint32_t)p.box_rows * 4u * HDP;
+          }
+        }
+        if (n_in < 32) held &= n_in > 0 ? (1u << n_in) - 1u : 0u;
+        masks[bar0 + st] = held;
+        uint64_t* bar = &bars[bar0 + st];
+        tc::mbar_expect_tx(bar, bytes);
+        const int g = w.vh / p.head_tiles;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          if (i >= pieces || i * p.box_rows >= n_in || (unsigned)pages[i] >= (unsigned)c.n_pages) continue;
+          const uint32_t dst = tc::smem_u32(to + st * 2 * C::KBYTES) + (uint32_t)(i * p.box_rows) * 128u;
+          const int row = (w.t * KT + i * p.box_rows) & page_mask;
+#pragma unroll 1
+          for (int h = 0; h < boxes; ++h) {
+            pa_tma(dst + h * C::HALF, &kmap, row, h, g, pages[i], p.at_once, bar);
+            pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, row, h, g, pages[i], p.at_once, bar);
+          }
+        }
+        if (--left > 0) pa_step<KT>(c, rows, 1, w);
+        pages_of();
+        if (++st == ST) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+      if (__any_sync(0xffffffffu, ready)) {
+        since = tc::global_ns();
+      } else if ((spin & 255) == 0 && (*(volatile int*)&s_abort || tc::global_ns() - since > tc::kWaitLimitNs)) {
+        if (lane == 0) record_status(p.status, QMOE_ERR_TIMEOUT);
+        break;
+      }
+    }
   }
 
   // ---- rows
@@ -362,11 +448,13 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
       float s[KB][NT][4];
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        float s2[NT][4];
+        float sc[C::CHAINS][NT][4];  // sums over every CHAINS-th 16 head dims: dependent products would wait for one another
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int h = 0; h < C::CHAINS; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[kb][n][e] = s2[n][e] = 0.f;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[h][n][e] = 0.f;
         const int r = 16 * kb + (lane & 15);
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
@@ -377,12 +465,17 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
           for (int part = C::QP - 1; part >= 0; --part)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              pa_mma((i & 1) ? s2[n] : s[kb][n], a, qf[i][n][part][0], qf[i][n][part][1]);
+              pa_mma(sc[i % C::CHAINS][n], a, qf[i][n][part][0], qf[i][n][part][1]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[kb][n][e] = (s[kb][n][e] + s2[n][e]) * p.scale_log2;
+          for (int e = 0; e < 4; ++e) {
+            float x = sc[0][n][e];
+#pragma unroll
+            for (int h = 1; h < C::CHAINS; ++h) x += sc[h][n][e];
+            s[kb][n][e] = x * p.scale_log2;
+          }
         if (held != FULL) {
 #pragma unroll
           for (int e = 0; e < 4; e += 2)
@@ -475,11 +568,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
         }
       }
       __syncwarp();  // every lane has read the stage
-      if (left > 0) {
-        issue(stage, ahead, next_page);
-        if (--left > 0) pa_step<KT>(c, rows, 1, ahead);
-        look_up(next_page);
-      }
+      if (lane == 0) tc::mbar_arrive(&empties[warp * ST + stage]);
       if (++stage == ST) {
         stage = 0;
         phase ^= 1u;
@@ -539,9 +628,9 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1)
   __syncthreads();
 
   // ---- rows over several warps: the beginning that a warp left, then the ends that the next ones did
-  const unsigned heads = __ballot_sync(0xffffffffu, lane < W && s_head[lane & (W - 1)].z);
-  const unsigned ends = __ballot_sync(0xffffffffu, lane < W && s_head[lane & (W - 1)].z && !s_head[lane & (W - 1)].w);
-  const unsigned tails = __ballot_sync(0xffffffffu, lane < W && s_tail[lane & (W - 1)].z);
+  const unsigned heads = __ballot_sync(0xffffffffu, lane < W && s_head[lane < W ? lane : 0].z);
+  const unsigned ends = __ballot_sync(0xffffffffu, lane < W && s_head[lane < W ? lane : 0].z && !s_head[lane < W ? lane : 0].w);
+  const unsigned tails = __ballot_sync(0xffffffffu, lane < W && s_tail[lane < W ? lane : 0].z);
   auto merge = [&](int first, bool began) {  // first: the warp of the row's first part; began: that is its tail
     const unsigned after = heads & ~((1u << first) - 1u) & (began ? ~(1u << first) : ~0u);
     const unsigned end = ends & after;
@@ -749,22 +838,25 @@ PaPlan pa_plan(const PagedView& c, int n_heads, bool f32, bool accumulate, int c
 
 constexpr int PA_MAX_CTAS = 256;  // the workspace does not depend on the device
 
-// A pool as a 4-D tensor map [head dim][slot of a page][KV head][page]; head
-// dims from hd on read as zero.
-bool pa_encode(CUtensorMap* m, const void* base, const PagedView& c, int box_rows) {
+// A pool as a tensor map. With ``hdp`` == hd, [64 head dims][slot of a page][hd /
+// 64][KV head][page] and boxes of all head dims, 64 by 64; else [head dim][slot
+// of a page][KV head][page] and boxes of 64, where head dims from hd on read as
+// zero (split in 64s, the last box would read what lies behind the head).
+bool pa_encode(CUtensorMap* m, const void* base, const PagedView& c, int box_rows, int hdp) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (fn == nullptr) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)1 << c.page_log2, (cuuint64_t)c.n_kv,
-                              (cuuint64_t)c.n_pages};
+  const bool at_once = hdp == c.head_dim;
+  const cuuint64_t page = (cuuint64_t)1 << c.page_log2, kv = (cuuint64_t)c.n_kv, pages = (cuuint64_t)c.n_pages;
   // (a dimension of one element never steps: its stride may be anything that is valid)
-  const cuuint64_t strides[3] = {(cuuint64_t)c.slot_stride * 2,
-                                 (cuuint64_t)(c.n_kv > 1 ? c.head_stride : c.slot_stride) * 2,
-                                 (cuuint64_t)(c.n_pages > 1 ? c.page_stride : c.slot_stride) * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t ss = (cuuint64_t)c.slot_stride * 2, hs = (cuuint64_t)(c.n_kv > 1 ? c.head_stride : c.slot_stride) * 2,
+                   ps = (cuuint64_t)(c.n_pages > 1 ? c.page_stride : c.slot_stride) * 2;
+  const cuuint64_t dims5[5] = {64, page, (cuuint64_t)hdp / 64, kv, pages}, dims4[4] = {(cuuint64_t)c.head_dim, page, kv, pages};
+  const cuuint64_t strides5[4] = {ss, 128, hs, ps}, strides4[3] = {ss, hs, ps};
+  const cuuint32_t box5[5] = {64, (cuuint32_t)box_rows, (cuuint32_t)hdp / 64, 1, 1}, box4[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, at_once ? 5 : 4, const_cast<void*>(base), at_once ? dims5 : dims4,
+            at_once ? strides5 : strides4, at_once ? box5 : box4, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <class C>
@@ -772,10 +864,14 @@ cudaError_t launch_split(PaSplit& s, int ctas, cudaStream_t st) {
   s.box_rows = 1 << s.c.page_log2;
   if (s.box_rows > C::KT) s.box_rows = C::KT;
   CUtensorMap km, vm;
-  if (!pa_encode(&km, s.c.k, s.c, s.box_rows) || !pa_encode(&vm, s.c.v, s.c, s.box_rows)) return cudaErrorInvalidValue;
+  // (with a page smaller than a tile the parts of a box would not land where the tile has them)
+  s.at_once = s.c.head_dim == C::HDP && s.box_rows == C::KT;
+  const int parts = s.at_once ? C::HDP : 0;
+  if (!pa_encode(&km, s.c.k, s.c, s.box_rows, parts) || !pa_encode(&vm, s.c.v, s.c, s.box_rows, parts))
+    return cudaErrorInvalidValue;
   cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(paged_split_kernel<C>), C::SMEM);
   if (e != cudaSuccess) return e;
-  paged_split_kernel<C><<<ctas, 32 * C::WARPS, C::SMEM, st>>>(s, km, vm);
+  paged_split_kernel<C><<<ctas, 32 * (C::WARPS + 1), C::SMEM, st>>>(s, km, vm);
   return cudaGetLastError();
 }
 
