@@ -37,6 +37,28 @@ __device__ __forceinline__ int paged_len(const PagedView& c, int b) {
   return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
 
+// Launches ``k`` so that it may start while the kernel ahead of it on the stream
+// ends: every kernel launched so waits on the device (griddepcontrol.wait) before
+// it touches memory, and allows the next one to start when it starts itself.
+template <class... Params, class... Args>
+cudaError_t launch_overlapped(void (*k)(Params...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                              Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, static_cast<Params>(args)...);
+}
+
 struct AppendArgs {
   const void *q, *k, *v;
   void* q_out;

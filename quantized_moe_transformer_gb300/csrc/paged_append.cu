@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace qmoe {
 
@@ -55,6 +56,8 @@ __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const PagedView c
   __shared__ float2 turn[ROT ? AP_ROWS * 128 : 1];
   __shared__ long long off[AP_ROWS];
   __shared__ int2 at[AP_ROWS];  // (sequence, slot), slot -1: the row is not cached
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
   const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, hd = c.head_dim, half = hd / 2;
   if (ROT) {
     for (int i = tid; i < n * half; i += AP_THREADS) {
@@ -154,15 +157,14 @@ __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const PagedView c
 }
 
 template <typename T>
-void append_rows(const PagedView& c, const AppendArgs& a, const AppendFreq& fr, cudaStream_t st) {
+cudaError_t append_rows(const PagedView& c, const AppendArgs& a, const AppendFreq& fr, cudaStream_t st) {
   // one row a CTA until every SM has four, then up to 16 rows
   int rows = a.n_rows / (4 * device_sm_count());
   rows = rows < 1 ? 1 : rows > AP_ROWS ? AP_ROWS : rows;
   const int ctas = (a.n_rows + rows - 1) / rows;
   if (a.rotate)
-    append_kernel<T, true><<<ctas, AP_THREADS, 0, st>>>(c, a, rows, fr);
-  else
-    append_kernel<T, false><<<ctas, AP_THREADS, 0, st>>>(c, a, rows, fr);
+    return launch_overlapped(append_kernel<T, true>, dim3(ctas), AP_THREADS, 0, 0, st, c, a, rows, fr);
+  return launch_overlapped(append_kernel<T, false>, dim3(ctas), AP_THREADS, 0, 0, st, c, a, rows, fr);
 }
 
 }  // namespace
@@ -180,11 +182,7 @@ cudaError_t launch_paged_append(const PagedView& c, const AppendArgs& a, cudaStr
       fr.turns[i] = (uint64_t)((t - std::floor(t)) * 18446744073709551616.0);
     }
   }
-  if (a.f32)
-    append_rows<float>(c, a, fr, st);
-  else
-    append_rows<__nv_bfloat16>(c, a, fr, st);
-  return cudaGetLastError();
+  return a.f32 ? append_rows<float>(c, a, fr, st) : append_rows<__nv_bfloat16>(c, a, fr, st);
 }
 
 }  // namespace qmoe

@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   if (tid < W) s_head[tid] = s_tail[tid] = make_int4(0, 0, 0, 0);
+  tc::grid_dep_wait();
   // ---- this CTA's and this warp's share of the tiles, found by every warp for itself: a lane has the sequences
   // lane * q .. lane * q + q - 1, and the tiles ahead of them
   const int q = (c.n_seqs + 31) / 32;
@@ -422,6 +423,8 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
+    const int row_t = seg.t;
+    float* row_scores = p.scores + ((long long)seg.b * c.n_kv + g) * paged_slots(c) * p.group + (h0 - g * p.group);
 #pragma unroll 1
     for (int turn = 0; turn < n_tiles; ++turn) {
       if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &s_abort))) {
@@ -486,17 +489,24 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
       }
       if (p.scores != nullptr) {
         // kept until the denominators are known
-        const int t0 = (seg.t + turn) * KT;
+        const int j0 = (row_t + turn) * KT + (lane >> 2);
+        float* at = row_scores + (long long)j0 * p.group + 2 * (lane & 3);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = t0 + 16 * kb + (lane >> 2) + 4 * (e & 2);
-            const long long at = (((long long)seg.b * c.n_kv + g) * paged_slots(c) + j) * p.group + (h0 - g * p.group);
+          for (int e = 0; e < 4; e += 2) {
+            const int j = 16 * kb + 4 * e;
+            if (j0 + j >= seg.len) continue;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const int hh = 8 * n + 2 * (lane & 3) + (e & 1);
-              if (j < seg.len && hh < n_h) p.scores[at + hh] = s[kb][n][e];
+              const int hh = 8 * n + 2 * (lane & 3);
+              float* to = at + (long long)j * p.group + 8 * n;
+              if ((p.group & 1) == 0) {
+                if (hh < n_h) *reinterpret_cast<float2*>(to) = make_float2(s[kb][n][e], s[kb][n][e + 1]);
+              } else {
+                if (hh < n_h) to[0] = s[kb][n][e];
+                if (hh + 1 < n_h) to[1] = s[kb][n][e + 1];
+              }
             }
           }
       }
@@ -790,6 +800,7 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PaJoin p) 
 // weight[b][g][j] += sum over the group's heads of 2^(score - lse).
 __global__ void __launch_bounds__(256) paged_weight_kernel(const PagedView c, const float* __restrict__ scores,
                                                            const float* __restrict__ lse, int n_heads, int group) {
+  tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int pair = blockIdx.x, b = pair / c.n_kv, g = pair % c.n_kv;
   const int n = paged_len(c, b);
@@ -871,8 +882,7 @@ cudaError_t launch_split(PaSplit& s, int ctas, cudaStream_t st) {
     return cudaErrorInvalidValue;
   cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(paged_split_kernel<C>), C::SMEM);
   if (e != cudaSuccess) return e;
-  paged_split_kernel<C><<<ctas, 32 * (C::WARPS + 1), C::SMEM, st>>>(s, km, vm);
-  return cudaGetLastError();
+  return launch_overlapped(paged_split_kernel<C>, dim3(ctas), 32 * (C::WARPS + 1), C::SMEM, 0, st, s, km, vm);
 }
 
 template <bool F32>
@@ -888,22 +898,6 @@ cudaError_t pick_split(PaSplit& s, const PaPlan& pl, cudaStream_t st) {
   if (pl.nt == 1) return launch_split<PaCfg<256, 1, F32>>(s, pl.ctas, st);
   if constexpr (!F32) return launch_split<PaCfg<256, 2, false>>(s, pl.ctas, st);
   return cudaErrorInvalidValue;
-}
-
-// Launches ``k`` so that it may start before the kernel ahead of it has ended
-// (it waits on the device for that kernel's memory).
-template <class Arg0, class... Args>
-cudaError_t launch_dependent(void (*k)(Arg0, Args...), dim3 grid, int threads, cudaStream_t st, Arg0 a0, Args... rest) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, a0, rest...);
 }
 
 }  // namespace
@@ -958,14 +952,15 @@ cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, c
   j.hdp = pl.hdp;
   j.f32 = a.f32;
   if (!s.whole_rows)
-    e = launch_dependent(paged_join_kernel, dim3(ctas, pl.head_tile < s.group ? pl.head_tile : s.group), PJ_THREADS, st, j);
+    e = launch_overlapped(paged_join_kernel, dim3(ctas, pl.head_tile < s.group ? pl.head_tile : s.group), PJ_THREADS, 0,
+                          0, st, j);
   if (e != cudaSuccess || !a.accumulate) return e;
   // about 8 CTAs an SM over all (sequence, KV head) pairs
   const long long pairs = (long long)c.n_seqs * c.n_kv;
   long long parts = (paged_slots(c) + 255) / 256, most = (8ll * ctas + pairs - 1) / pairs;
   if (parts > most) parts = most;
-  return launch_dependent(paged_weight_kernel, dim3((unsigned)pairs, (unsigned)parts), 256, st, c,
-                          (const float*)s.scores, (const float*)s.lse, a.n_heads, s.group);
+  return launch_overlapped(paged_weight_kernel, dim3((unsigned)pairs, (unsigned)parts), 256, 0, 0, st, c, s.scores,
+                           s.lse, a.n_heads, s.group);
 }
 
 }  // namespace qmoe

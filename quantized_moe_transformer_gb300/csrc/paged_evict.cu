@@ -9,6 +9,7 @@
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace qmoe {
 
@@ -113,6 +114,8 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
   __shared__ __align__(16) int sum[256];
   __shared__ int warp_cnt[3][EV_WARPS], cta_cnt[3], pick[3];
   __shared__ long long off[INLINE ? MV_MOVES : 1][2];
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -322,7 +325,8 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
 __global__ void __launch_bounds__(MV_THREADS, 5) evict_move_kernel(const PagedView c, const EvictArgs a,
                                                                    const EvictLists ls) {
   __shared__ long long off[MV_MOVES][2];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
   const long long pair = blockIdx.x;
   const int b = (int)(pair / c.n_kv), g = (int)(pair % c.n_kv);
   const int32_t* count = ls.count + pair;
@@ -384,35 +388,17 @@ cudaError_t launch_cache_evict(const PagedView& c, const EvictArgs& a, cudaStrea
   ls.mover = reinterpret_cast<int2*>(p + 2 * head + lists);
   const EvictPlan pl = evict_plan(c, a);
   if (pairs * pl.cluster > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(pairs * pl.cluster));
-  cfg.blockDim = dim3(EV_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = pl.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   auto* select = pl.long_slices ? (pl.inline_moves ? evict_select_kernel<true, true> : evict_select_kernel<true, false>)
                                 : (pl.inline_moves ? evict_select_kernel<false, true> : evict_select_kernel<false, false>);
-  cfg.dynamicSmemBytes = sizeof(uint32_t) * pl.keys;
-  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(select), cfg.dynamicSmemBytes);
+  const size_t smem = sizeof(uint32_t) * pl.keys;
+  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(select), smem);
   if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&cfg, select, c, a, ls);
+  e = launch_overlapped(select, dim3((unsigned)(pairs * pl.cluster)), EV_THREADS, smem, pl.cluster, st, c, a, ls);
   if (e != cudaSuccess || pl.inline_moves) return e;
   long long parts = (pl.moves + MV_MOVES - 1) / MV_MOVES;
   if (parts < 1) parts = 1;
   if (parts > 65535) parts = 65535;
-  cfg = cudaLaunchConfig_t{};
-  cfg.gridDim = dim3((unsigned)pairs, (unsigned)parts);
-  cfg.blockDim = dim3(MV_THREADS);
-  cfg.stream = st;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_move_kernel, c, a, ls);
+  return launch_overlapped(evict_move_kernel, dim3((unsigned)pairs, (unsigned)parts), MV_THREADS, 0, 0, st, c, a, ls);
 }
 
 }  // namespace qmoe
