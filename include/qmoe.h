@@ -257,11 +257,14 @@ int qmoe_moe_forward_noalloc(const qmoe_moe_desc *d, const float *X, const float
  *                          work item stored;
  *   QMOE_FAULT_ATTN_FINAL  block prefill attention (T > 16): the first CTA's
  *                          P V issuer never marks its output final, so its
- *                          softmax warps' last wait runs out.
+ *                          softmax warps' last wait runs out;
+ *   QMOE_FAULT_PAGED_COPY  paged attention: the first CTA's first warp never
+ *                          copies its first tile.
  * Returns QMOE_ERR_ARG for an unknown site or a negative wait. Not for use
  * outside tests; set QMOE_FAULT_NONE afterwards.
  */
-enum { QMOE_FAULT_NONE = 0, QMOE_FAULT_DECODE_COPY = 1, QMOE_FAULT_TC_ARRIVE = 2, QMOE_FAULT_ATTN_FINAL = 3 };
+enum { QMOE_FAULT_NONE = 0, QMOE_FAULT_DECODE_COPY = 1, QMOE_FAULT_TC_ARRIVE = 2, QMOE_FAULT_ATTN_FINAL = 3,
+       QMOE_FAULT_PAGED_COPY = 4 };
 int qmoe_test_inject(int site, int wait_us);
 
 /* Number of kernels this library has enqueued since it was loaded (a CUDA
@@ -435,6 +438,23 @@ size_t qmoe_cache_evict_workspace_bytes(const qmoe_paged_cache *c);
 int qmoe_cache_evict(const qmoe_paged_cache *c, const int32_t *next_pos, int budget, int recent,
                      int32_t *lens_out, float *weight_out, int32_t *pos_out, void *ws, size_t ws_bytes,
                      qmoe_stream_t stream);
+
+/*
+ * The block for one new token of each of c->n_seqs sequences at once:
+ *   h1 = X + O(attention over the cache), out = h1 + moe(RMSNorm(h1; g2)),
+ * rows X, out [n_seqs][H] fp32 (out may not alias X). Row b's key and value are
+ * appended as the next entry of sequence b (lens[b] grows by one) at position
+ * next_pos[b], then its query attends to all entries of the sequence, its own
+ * among them; with accumulate != 0 the entries' weights grow. A sequence
+ * without room is recorded as QMOE_ERR_DEVICE_ARG. c->n_kv and c->head_dim are the
+ * block's. Prompts come into the cache through qmoe_paged_append (from the
+ * contiguous caches that qmoe_block_forward filled, with rope_theta 0: their keys
+ * are rotated already); qmoe_cache_evict keeps it bounded between steps.
+ */
+size_t qmoe_block_decode_paged_workspace_bytes(const qmoe_block_desc *b, const qmoe_paged_cache *c, int accumulate);
+int qmoe_block_decode_paged(const qmoe_block_desc *b, const qmoe_paged_cache *c, const float *X, float *out,
+                            const int32_t *next_pos, int accumulate, void *ws, size_t ws_bytes,
+                            qmoe_stream_t stream);
 
 /* The CUDA runtime error code (cudaError_t) behind the last QMOE_ERR_LAUNCH
  * returned on this thread, 0 if none. */

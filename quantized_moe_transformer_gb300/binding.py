@@ -95,7 +95,8 @@ def exported_symbols() -> list[str]:
             "qmoe_last_cuda_error", "qmoe_rmsnorm", "qmoe_attn_workspace_bytes", "qmoe_attn_forward", "qmoe_block_workspace_bytes",
             "qmoe_block_forward", "qmoe_test_inject",
             "qmoe_paged_append", "qmoe_paged_attention_workspace_bytes", "qmoe_paged_attention",
-            "qmoe_cache_evict_workspace_bytes", "qmoe_cache_evict"]
+            "qmoe_cache_evict_workspace_bytes", "qmoe_cache_evict", "qmoe_block_decode_paged_workspace_bytes",
+            "qmoe_block_decode_paged"]
 
 
 def _check(status: int):
@@ -190,7 +191,7 @@ def moe_forward(layer: MoeLayer, X: torch.Tensor, R: torch.Tensor | None = None,
     return out
 
 
-FAULT_SITES = {"none": 0, "decode_copy": 1, "tc_arrive": 2, "attn_final": 3}
+FAULT_SITES = {"none": 0, "decode_copy": 1, "tc_arrive": 2, "attn_final": 3, "paged_copy": 4}
 
 
 def test_inject(site: str, wait_us: int = 0):
@@ -412,6 +413,9 @@ def _paged_lib():
         L.qmoe_cache_evict_workspace_bytes.restype = _c_size
         L.qmoe_cache_evict_workspace_bytes.argtypes = [P]
         L.qmoe_cache_evict.argtypes = [P, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_size, _vp]
+        L.qmoe_block_decode_paged_workspace_bytes.restype = _c_size
+        L.qmoe_block_decode_paged_workspace_bytes.argtypes = [ctypes.POINTER(BlockDesc), P, _c_int]
+        L.qmoe_block_decode_paged.argtypes = [ctypes.POINTER(BlockDesc), P, _vp, _vp, _vp, _c_int, _vp, _c_size, _vp]
         L._paged_declared = True
     return L
 
@@ -573,3 +577,26 @@ def cache_evict(cache: PagedCache, next_pos, budget: int, recent: int = 0, lens_
         None if pos_out is None else _need(pos_out, "pos_out", per_slot, torch.int32), _need(ws, "ws"), ws.numel(),
         _raw_stream(stream, cache.device)))
     return lens_out, weight_out, pos_out
+
+
+def block_decode_paged_workspace(block: Block, cache: PagedCache, accumulate: bool = False) -> torch.Tensor:
+    n = int(_paged_lib().qmoe_block_decode_paged_workspace_bytes(ctypes.byref(block.desc), cache._desc_ref,
+                                                                 int(accumulate)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def block_decode_paged(block: Block, cache: PagedCache, X, next_pos, out=None, accumulate: bool = False, ws=None,
+                       stream=None):
+    """The block for one new token X [sequences][H] fp32 of each sequence: its key
+    and value become the sequence's next entry (at position ``next_pos``), its
+    query attends to every entry; the lengths grow by one."""
+    shape = (cache.n_seqs, block.H)
+    if out is None:
+        out = torch.empty_like(X)
+    if ws is None:
+        ws = block_decode_paged_workspace(block, cache, accumulate)
+    _check(_paged_lib().qmoe_block_decode_paged(
+        ctypes.byref(block.desc), cache._desc_ref, _need(X, "X", shape, torch.float32),
+        _need(out, "out", shape, torch.float32), _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),
+        int(accumulate), _need(ws, "ws"), ws.numel(), _raw_stream(stream, cache.device)))
+    return out

@@ -342,33 +342,15 @@ cudaError_t dense_proj(const float* x, int T, int K, const void* W, int qt, int 
   return launch_down_gemv(g, qt, x, K, N, y, st);
 }
 
-int attn_impl(const qmoe_block_desc* b, const float* X, const float* R, float* out, int T, uint16_t* kc, uint16_t* vc,
-              int pos0, int ctx_cap, void* ws, size_t ws_bytes, cudaStream_t st) {
-  int r = check_block(b);
-  if (r != QMOE_OK) return r;
-  if (T < 0 || pos0 < 0) return QMOE_ERR_ARG;
-  if (T == 0) return QMOE_OK;
-  if ((long long)pos0 + T > ctx_cap) return QMOE_ERR_ARG;
-  if (!X || !out || !kc || !vc || !ws) return QMOE_ERR_NULL;
-  if (!aligned(X, 16) || !aligned(out, 16) || (R && !aligned(R, 16)) || !aligned(kc, 16) || !aligned(vc, 16) ||
-      !aligned(ws, 256))
-    return QMOE_ERR_ALIGN;
-  if (T > kChunkedAttnRows && b->head_dim != 128) return QMOE_ERR_ARG;
-  const AttnWs L = attn_ws_layout(b, T, pos0);
-  if (ws_bytes < L.total) return QMOE_ERR_WORKSPACE;
-  int* status = nullptr;
-  r = device_ready(&status);
-  if (r != QMOE_OK) return r;
-  char* base = static_cast<char*>(ws);
+// The attention branch ahead of the cache: RMSNorm(X; g1) and the Q, K, V
+// projections into the workspace. ``qkv_tc``: all three ran on the tensor cores.
+cudaError_t attn_project(const qmoe_block_desc* b, const float* X, int T, char* base, const AttnWs& L, int* status,
+                         bool* qkv_tc_out, cudaStream_t st) {
   float* rr = reinterpret_cast<float*>(base + L.r);
   float* q = reinterpret_cast<float*>(base + L.q);
   float* k = reinterpret_cast<float*>(base + L.k);
   float* v = reinterpret_cast<float*>(base + L.v);
-  float* o = reinterpret_cast<float*>(base + L.o);
-  float* part = reinterpret_cast<float*>(base + L.part);
   const int H = b->H, nh = b->n_heads, nkv = b->n_kv, hd = b->head_dim;
-  __nv_bfloat16* kcb = reinterpret_cast<__nv_bfloat16*>(kc);
-  __nv_bfloat16* vcb = reinterpret_cast<__nv_bfloat16*>(vc);
   cudaError_t e;
   // RMSNorm fused into the bf16 token operand when every one of the Q, K, V
   // projections runs on the tensor cores (a GEMV projection reads the fp32
@@ -390,23 +372,22 @@ int attn_impl(const qmoe_block_desc* b, const float* X, const float* R, float* o
     if (e == cudaSuccess) e = dense_proj(rr, T, H, b->Wk, QMOE_Q4K, nkv * hd, k, base, L, status, st);
     if (e == cudaSuccess) e = dense_proj(rr, T, H, b->Wv, QMOE_Q4K, nkv * hd, v, base, L, status, st);
   }
-  if (e == cudaSuccess) {
-    e = launch_rope_cache(q, k, v, kcb, vcb, T, pos0, nh, nkv, hd, (double)b->rope_theta, st);
-    g_launches.fetch_add(1);
-  }
-  // O projection on the tensor cores: the prefill attention writes its bf16
-  // token operand itself
-  // (with the route and chunk list of these rows from the Q, K, V projections)
+  *qkv_tc_out = qkv_tc;
+  return e;
+}
+
+// The attention branch behind the cache: out = R + O(o), o the workspace's
+// attention rows (``ob_written``: already there as the bf16 token operand).
+cudaError_t attn_output(const qmoe_block_desc* b, const float* R, float* out, int T, char* base, const AttnWs& L,
+                        bool qkv_tc, bool ob_written, int* status, cudaStream_t st) {
+  float* rr = reinterpret_cast<float*>(base + L.r);
+  float* o = reinterpret_cast<float*>(base + L.o);
+  const int H = b->H, nh = b->n_heads, hd = b->head_dim;
   const bool o_tc = dense_tc(T, H) && qkv_tc;
-  __nv_bfloat16* ob = (o_tc && !L.chunked) ? reinterpret_cast<__nv_bfloat16*>(base + L.xb) : nullptr;
-  if (e == cudaSuccess) {
-    e = launch_attention(q, kcb, vcb, part, o, ob, T, pos0, nh, nkv, hd, L.chunked, status, wait_limit_ns(),
-                         g_fault_site.load() == QMOE_FAULT_ATTN_FINAL ? 1 : 0, st);
-    g_launches.fetch_add(L.chunked ? 2 : 1);
-  }
+  cudaError_t e = cudaSuccess;
   if (o_tc) {
     // the dense route and chunk list are the Q, K, V projections' (the same rows)
-    if (e == cudaSuccess && ob == nullptr) {
+    if (!ob_written) {
       e = launch_to_bf16(o, reinterpret_cast<__nv_bfloat16*>(base + L.xb), T, nh * hd, nullptr, T, 1, nullptr, st);
       g_launches.fetch_add(1);
     }
@@ -421,6 +402,52 @@ int attn_impl(const qmoe_block_desc* b, const float* X, const float* R, float* o
     e = launch_add(R, proj_out, out, (size_t)T * H, st);
     g_launches.fetch_add(1);
   }
+  return e;
+}
+
+int attn_impl(const qmoe_block_desc* b, const float* X, const float* R, float* out, int T, uint16_t* kc, uint16_t* vc,
+              int pos0, int ctx_cap, void* ws, size_t ws_bytes, cudaStream_t st) {
+  int r = check_block(b);
+  if (r != QMOE_OK) return r;
+  if (T < 0 || pos0 < 0) return QMOE_ERR_ARG;
+  if (T == 0) return QMOE_OK;
+  if ((long long)pos0 + T > ctx_cap) return QMOE_ERR_ARG;
+  if (!X || !out || !kc || !vc || !ws) return QMOE_ERR_NULL;
+  if (!aligned(X, 16) || !aligned(out, 16) || (R && !aligned(R, 16)) || !aligned(kc, 16) || !aligned(vc, 16) ||
+      !aligned(ws, 256))
+    return QMOE_ERR_ALIGN;
+  if (T > kChunkedAttnRows && b->head_dim != 128) return QMOE_ERR_ARG;
+  const AttnWs L = attn_ws_layout(b, T, pos0);
+  if (ws_bytes < L.total) return QMOE_ERR_WORKSPACE;
+  int* status = nullptr;
+  r = device_ready(&status);
+  if (r != QMOE_OK) return r;
+  char* base = static_cast<char*>(ws);
+  float* q = reinterpret_cast<float*>(base + L.q);
+  float* k = reinterpret_cast<float*>(base + L.k);
+  float* v = reinterpret_cast<float*>(base + L.v);
+  float* o = reinterpret_cast<float*>(base + L.o);
+  float* part = reinterpret_cast<float*>(base + L.part);
+  const int H = b->H, nh = b->n_heads, nkv = b->n_kv, hd = b->head_dim;
+  __nv_bfloat16* kcb = reinterpret_cast<__nv_bfloat16*>(kc);
+  __nv_bfloat16* vcb = reinterpret_cast<__nv_bfloat16*>(vc);
+  bool qkv_tc = false;
+  cudaError_t e = attn_project(b, X, T, base, L, status, &qkv_tc, st);
+  if (e == cudaSuccess) {
+    e = launch_rope_cache(q, k, v, kcb, vcb, T, pos0, nh, nkv, hd, (double)b->rope_theta, st);
+    g_launches.fetch_add(1);
+  }
+  // O projection on the tensor cores: the prefill attention writes its bf16
+  // token operand itself
+  // (with the route and chunk list of these rows from the Q, K, V projections)
+  const bool o_tc = dense_tc(T, H) && qkv_tc;
+  __nv_bfloat16* ob = (o_tc && !L.chunked) ? reinterpret_cast<__nv_bfloat16*>(base + L.xb) : nullptr;
+  if (e == cudaSuccess) {
+    e = launch_attention(q, kcb, vcb, part, o, ob, T, pos0, nh, nkv, hd, L.chunked, status, wait_limit_ns(),
+                         g_fault_site.load() == QMOE_FAULT_ATTN_FINAL ? 1 : 0, st);
+    g_launches.fetch_add(L.chunked ? 2 : 1);
+  }
+  if (e == cudaSuccess) e = attn_output(b, R, out, T, base, L, qkv_tc, ob != nullptr, status, st);
   return launch_status(e);
 }
 
@@ -458,6 +485,15 @@ int paged_view(const qmoe_paged_cache* c, PagedView* out) {
   v.max_pages = c->max_pages;
   *out = v;
   return QMOE_OK;
+}
+
+// A block and the cache of its keys and values.
+int paged_block(const qmoe_block_desc* b, const qmoe_paged_cache* c, PagedView* view) {
+  int r = check_block(b);
+  if (r != QMOE_OK) return r;
+  r = paged_view(c, view);
+  if (r != QMOE_OK) return r;
+  return b->n_kv == c->n_kv && b->head_dim == c->head_dim && !(b->rope_theta > 1e30f) ? QMOE_OK : QMOE_ERR_ARG;
 }
 
 bool dtype_ok(int dtype) { return dtype == QMOE_F32 || dtype == QMOE_BF16; }
@@ -585,6 +621,8 @@ int qmoe_paged_attention(const qmoe_paged_cache* c, const void* q, void* out, in
   a.f32 = dtype == QMOE_F32;
   a.accumulate = accumulate != 0;
   a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)c->head_dim);
+  a.wait_ns = wait_limit_ns();
+  a.fault = g_fault_site.load() == QMOE_FAULT_PAGED_COPY;
   a.ws = ws;
   g_launches.fetch_add(paged_attention_launches(view, n_heads, a.accumulate));
   return launch_status(launch_paged_attention(view, a, reinterpret_cast<cudaStream_t>(stream)));
@@ -620,6 +658,60 @@ int qmoe_cache_evict(const qmoe_paged_cache* c, const int32_t* next_pos, int bud
   a.ws = ws;
   g_launches.fetch_add(cache_evict_launches(view, a));
   return launch_status(launch_cache_evict(view, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+
+size_t qmoe_block_decode_paged_workspace_bytes(const qmoe_block_desc* b, const qmoe_paged_cache* c, int accumulate) {
+  PagedView view;
+  if (paged_block(b, c, &view) != QMOE_OK) return 0;
+  const size_t attn = qmoe_paged_attention_workspace_bytes(c, b->n_heads, accumulate);
+  const size_t block = qmoe_block_workspace_bytes(b, c->n_seqs, 0);
+  return attn && block ? up256(attn) + block : 0;
+}
+
+int qmoe_block_decode_paged(const qmoe_block_desc* b, const qmoe_paged_cache* c, const float* X, float* out,
+                            const int32_t* next_pos, int accumulate, void* ws, size_t ws_bytes, qmoe_stream_t stream) {
+  PagedView view;
+  int r = paged_block(b, c, &view);
+  if (r != QMOE_OK) return r;
+  r = check_desc(&b->moe);
+  if (r != QMOE_OK) return r;
+  if (b->moe.H != b->H) return QMOE_ERR_ARG;
+  if (!X || !out || !next_pos || !ws || (accumulate && !c->weight)) return QMOE_ERR_NULL;
+  if (X == out) return QMOE_ERR_ARG;
+  if (!aligned(X, 16) || !aligned(out, 16) || !aligned(next_pos, 4) || !aligned(ws, 256)) return QMOE_ERR_ALIGN;
+  const size_t need = qmoe_block_decode_paged_workspace_bytes(b, c, accumulate);
+  if (need == 0) return QMOE_ERR_ARG;
+  if (ws_bytes < need) return QMOE_ERR_WORKSPACE;
+  int* status = nullptr;
+  r = device_ready(&status);
+  if (r != QMOE_OK) return r;
+  const int T = c->n_seqs;
+  const AttnWs L = attn_ws_layout(b, T, 0);
+  const size_t row_bytes = up256(sizeof(float) * (size_t)T * b->H);
+  const size_t p_bytes = up256(qmoe_paged_attention_workspace_bytes(c, b->n_heads, accumulate));
+  char* paged_ws = static_cast<char*>(ws);
+  char* base = paged_ws + p_bytes;
+  float* h1 = reinterpret_cast<float*>(base + L.total);
+  float* r2 = reinterpret_cast<float*>(base + L.total + row_bytes);
+  char* moe_ws = base + L.total + 2 * row_bytes;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  bool qkv_tc = false;
+  r = launch_status(attn_project(b, X, T, base, L, status, &qkv_tc, st));
+  if (r != QMOE_OK) return r;
+  float* q = reinterpret_cast<float*>(base + L.q);
+  float* o = reinterpret_cast<float*>(base + L.o);
+  r = qmoe_paged_append(c, q, q, base + L.k, base + L.v, QMOE_F32, nullptr, nullptr, next_pos, T, b->n_heads,
+                        b->rope_theta, stream);
+  if (r != QMOE_OK) return r;
+  r = qmoe_paged_attention(c, q, o, QMOE_F32, b->n_heads, 0.f, accumulate, paged_ws, p_bytes, stream);
+  if (r != QMOE_OK) return r;
+  r = launch_status(attn_output(b, X, h1, T, base, L, qkv_tc, false, status, st));
+  if (r != QMOE_OK) return r;
+  g_launches.fetch_add(1);
+  r = launch_status(launch_rmsnorm(h1, b->g2, b->eps, r2, T, b->H, st));
+  if (r != QMOE_OK) return r;
+  return qmoe_moe_forward(&b->moe, r2, h1, nullptr, nullptr, out, T, moe_ws, ws_bytes - (moe_ws - paged_ws), stream);
 }
 
 
@@ -1113,7 +1205,7 @@ int qmoe_moe_forward_host(const qmoe_moe_desc* d, const float* X_host, const flo
 long long qmoe_launch_count(void) { return g_launches.load(); }
 
 int qmoe_test_inject(int site, int wait_us) {
-  if (site < 0 || site > QMOE_FAULT_ATTN_FINAL || wait_us < 0) return QMOE_ERR_ARG;
+  if (site < 0 || site > QMOE_FAULT_PAGED_COPY || wait_us < 0) return QMOE_ERR_ARG;
   g_fault_wait_us.store(wait_us);
   g_fault_site.store(site);
   return QMOE_OK;

@@ -77,6 +77,8 @@ struct PagedAttnArgs {
   bool f32, accumulate;
   float scale;
   int* status;
+  unsigned long long wait_ns;  // bound on a device wait
+  bool fault;                  // test-only: the first CTA's first warp never copies its first tile
   void* ws;
 };
 size_t paged_attention_ws_bytes(const PagedView& c, int n_heads, bool accumulate);

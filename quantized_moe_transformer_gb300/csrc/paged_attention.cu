@@ -75,6 +75,8 @@ struct PaSplit {
   float* lse;        // [sequences][heads] log2 of the softmax's denominator, with accumulate
   float* scores;     // [sequences][KV heads][slots][group], with accumulate
   int* status;
+  unsigned long long wait_ns;
+  bool fault;
 };
 
 // ``part``: the 64 head dims from 64 part on, or with a box of all parts the first of them.
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     load_q(seg);
 #pragma unroll
     for (int s = 0; s < ST; ++s)
-      if (s < count) issue(s, at[s], pages[s]);
+      if (s < count && !(p.fault && s == 0 && blockIdx.x == 0 && warp == 0)) issue(s, at[s], pages[s]);
   }
   if (warp < W && lane == 0) s_walk[warp] = make_int4(ahead.b, ahead.vh, ahead.t, left);
   __syncthreads();
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
       }
       if (__any_sync(0xffffffffu, ready)) {
         since = tc::global_ns();
-      } else if ((spin & 255) == 0 && (*(volatile int*)&s_abort || tc::global_ns() - since > tc::kWaitLimitNs)) {
+      } else if ((spin & 255) == 0 && (*(volatile int*)&s_abort || tc::global_ns() - since > p.wait_ns)) {
         if (lane == 0) record_status(p.status, QMOE_ERR_TIMEOUT);
         break;
       }
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     float* row_scores = p.scores + ((long long)seg.b * c.n_kv + g) * paged_slots(c) * p.group + (h0 - g * p.group);
 #pragma unroll 1
     for (int turn = 0; turn < n_tiles; ++turn) {
-      if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &s_abort))) {
+      if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &s_abort, p.wait_ns))) {
         ok = false;
         if (lane == 0) record_status(p.status, QMOE_ERR_TIMEOUT);
       }
@@ -934,6 +936,8 @@ cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, c
   s.lse = a.accumulate ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
   s.scores = a.accumulate ? reinterpret_cast<float*>(ws + pl.scores) : nullptr;
   s.status = a.status;
+  s.wait_ns = a.wait_ns;
+  s.fault = a.fault;
   PaPlan run = pl;
   run.ctas = ctas;
   cudaError_t e = a.f32 ? pick_split<true>(s, run, st) : pick_split<false>(s, run, st);

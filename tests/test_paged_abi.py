@@ -109,3 +109,30 @@ def test_binding_refuses_tensors_of_another_kind():
         qb.PagedCache(k, k[:2], table, lens)
     with pytest.raises(qb.QmoeError, match="strides"):
         qb.PagedCache(k.transpose(2, 3), k.transpose(2, 3), table, lens)
+
+
+def block_desc(**kw):
+    moe = qb.MoeDesc(2048, 256, 8, 512, 0, 1, FAKE, FAKE, FAKE, FAKE, None, None, None)
+    d = qb.BlockDesc(2048, 16, 2, 128, 1e7, 1e-6, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, moe)
+    for name, value in kw.items():
+        setattr(d, name, value)
+    return d
+
+
+@pytest.mark.parametrize("block_kw,cache_kw,call_kw,status", [
+    ({"n_kv": 4}, {}, {}, ARG), ({"head_dim": 64, "n_heads": 32}, {}, {}, ARG), ({"H": 300}, {}, {}, ARG),
+    ({}, {"page": 48}, {}, ARG), ({}, {"k": None}, {}, NULL), ({}, {"weight": None}, {}, NULL), ({}, {}, {"X": None}, NULL),
+    ({}, {}, {"nxt": None}, NULL), ({}, {}, {"ws": None}, NULL), ({}, {}, {"out": FAKE}, ARG), ({}, {}, {"X": FAKE + 4}, ALIGN),
+    ({}, {}, {"ws_bytes": 1000}, WORKSPACE)])
+def test_block_decode_arguments(lib, block_kw, cache_kw, call_kw, status):
+    a = {"X": FAKE, "out": 2 * FAKE, "nxt": FAKE, "ws": FAKE, "ws_bytes": 1 << 40, **call_kw}
+    r = lib.qmoe_block_decode_paged(ctypes.byref(block_desc(**block_kw)), ctypes.byref(desc(**cache_kw)), a["X"], a["out"],
+                                    a["nxt"], 1, a["ws"], a["ws_bytes"], None)
+    assert r == status
+
+
+def test_block_decode_workspace(lib):
+    b, c = block_desc(), desc()
+    n = lib.qmoe_block_decode_paged_workspace_bytes(ctypes.byref(b), ctypes.byref(c), 0)
+    assert n > lib.qmoe_paged_attention_workspace_bytes(ctypes.byref(c), 16, 0) > 0
+    assert lib.qmoe_block_decode_paged_workspace_bytes(ctypes.byref(b), ctypes.byref(desc(n_kv=1)), 0) == 0
