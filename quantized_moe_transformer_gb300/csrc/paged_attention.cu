@@ -42,11 +42,12 @@ namespace {
 // the instruction; the output is O^T = V^T P^T with the head dims as rows. The
 // instructions are mma.sync: at 8 flops a byte the whole cache needs a tenth of
 // their rate, and a fragment's scores are in registers at once.
-// fp32 queries are split into three bf16 parts (exact), probabilities into two
-// (2^-17 of each), so fp32 rows come out at fp32 accuracy; sums are fp32.
+// fp32 queries are split into three bf16 parts (exact) and their probabilities
+// into three, so fp32 rows come out at fp32 accuracy; bf16 rows take two parts of
+// the probabilities (2^-17 of each). Sums are fp32.
 template <int HDP_, int NT_, bool F32_>
 struct PaCfg {
-  static constexpr int HDP = HDP_, NT = NT_, QP = F32_ ? 3 : 1;
+  static constexpr int HDP = HDP_, NT = NT_, QP = F32_ ? 3 : 1, PP = F32_ ? 3 : 2;
   static constexpr bool F32 = F32_;
   static constexpr int CHAINS = NT == 1 ? 4 : 2;
   static constexpr int KT = HDP == 64 ? 32 : 16;           // slots of a tile: 4 or 8 KB of keys
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
           }
       }
       // running maximum; the output is rescaled where one grew
-      uint32_t pf[KB][NT][2][2];  // P^T as B fragments: two bf16 parts, slots 0-7 and 8-15
+      uint32_t pf[KB][NT][C::PP][2];  // P^T as B fragments: bf16 parts, slots 0-7 and 8-15
       bool grew = false;
       float mn[NT][2];
 #pragma unroll
@@ -557,11 +558,17 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
           const float p2 = exp2f(s[kb][n][2] - r0), p3 = exp2f(s[kb][n][3] - r1);
           l[n][0] += p0 + p2;
           l[n][1] += p1 + p3;
-          const uint32_t ua = tc::pack_bf16x2(p0, p1), ub = tc::pack_bf16x2(p2, p3);
-          pf[kb][n][0][0] = pa_transpose(ua);
-          pf[kb][n][0][1] = pa_transpose(ub);
-          pf[kb][n][1][0] = pa_transpose(tc::pack_bf16x2(p0 - bf_lo(ua), p1 - bf_hi(ua)));
-          pf[kb][n][1][1] = pa_transpose(tc::pack_bf16x2(p2 - bf_lo(ub), p3 - bf_hi(ub)));
+          float r[4] = {p0, p1, p2, p3};
+#pragma unroll
+          for (int part = 0; part < C::PP; ++part) {
+            const uint32_t ua = tc::pack_bf16x2(r[0], r[1]), ub = tc::pack_bf16x2(r[2], r[3]);
+            pf[kb][n][part][0] = pa_transpose(ua);
+            pf[kb][n][part][1] = pa_transpose(ub);
+            r[0] -= bf_lo(ua);
+            r[1] -= bf_hi(ua);
+            r[2] -= bf_lo(ub);
+            r[3] -= bf_hi(ub);
+          }
         }
       }
       // O^T += V^T P^T: head dims x heads
@@ -574,9 +581,21 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
           const int ch = 2 * (i & 3) + ((lane >> 3) & 1);
           pa_ldsm_t(a, vt + (i >> 2) * C::HALF + tc::sw128_offset(r, ch));
 #pragma unroll
-          for (int part = 1; part >= 0; --part)
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (C::F32) {
+              // a tile's products apart, added by a rounded sum: the instruction's own sums are cut off, which over
+              // a long row is more than fp32 rows may be off
+              float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) pa_mma(o[i][n], a, pf[kb][n][part][0], pf[kb][n][part][1]);
+              for (int part = C::PP - 1; part >= 0; --part) pa_mma(x, a, pf[kb][n][part][0], pf[kb][n][part][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i][n][e] += x[e];
+            } else {
+#pragma unroll
+              for (int part = C::PP - 1; part >= 0; --part)
+                pa_mma(o[i][n], a, pf[kb][n][part][0], pf[kb][n][part][1]);
+            }
+          }
         }
       }
       __syncwarp();  // every lane has read the stage
