@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
   const long long total = __shfl_sync(0xffffffffu, ahead_of, 31) * rows;
   ahead_of = (ahead_of - own_tiles) * rows;
   // CTAs: one for each W tiles (a tile for each warp) as far as there are; those of a single sequence then begin at its rows
-  const long long fit = c.n_seqs == 1 ? (total / rows + W - 1) / W * rows : (total + W - 1) / W;
+  const long long fit = c.n_seqs != 1 ? (total + W - 1) / W : p.whole_rows ? rows : (total / rows + W - 1) / W * rows;
   const int n_ctas = (int)(fit < gridDim.x ? fit : gridDim.x);
   if (blockIdx.x >= n_ctas) {
     if (tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     w.t = (int)(x - (long long)w.vh * w.nt);
   };
   long long C0 = pa_share(total, blockIdx.x, n_ctas), C1 = pa_share(total, blockIdx.x + 1, n_ctas);
-  if (p.whole_rows) {
+  if (p.whole_rows && c.n_seqs > 1) {  // (those of one sequence begin at rows already)
     PaWalk w;
     locate(C0, w);
     C0 -= w.t;
@@ -763,9 +763,17 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PaJoin p) 
   const int grp = tid / lanes, col = 4 * (tid % lanes);
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < d.z; i0 += PJ_THREADS) {
-    const int n = min(PJ_THREADS, d.z - i0);
+  constexpr int U = 8;
+  for (int i0 = 0; i0 < d.z; i0 += U * groups) {
+    // the partials are on their way while their maxima are compared
+    const int n = min(U * groups, d.z - i0);
     const float2 ml = tid < n ? p.part_ml[at(i0 + tid)] : make_float2(-INFINITY, 0.f);
+    float4 x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = grp + k * groups;
+      x[k] = i < n ? *reinterpret_cast<const float4*>(&p.part_o[at(i0 + i) * p.hdp + col]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float mx = ml.x;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -792,14 +800,13 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PaJoin p) 
     acc.y *= old;
     acc.z *= old;
     acc.w *= old;
-#pragma unroll 8
-    for (int i = grp; i < n; i += groups) {
-      const float4 x = *reinterpret_cast<const float4*>(&p.part_o[at(i0 + i) * p.hdp + col]);
-      const float fi = fs[i];
-      acc.x = fmaf(x.x, fi, acc.x);
-      acc.y = fmaf(x.y, fi, acc.y);
-      acc.z = fmaf(x.z, fi, acc.z);
-      acc.w = fmaf(x.w, fi, acc.w);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const float fi = fs[min(grp + k * groups, PJ_THREADS - 1)];  // (0 behind the last partial)
+      acc.x = fmaf(x[k].x, fi, acc.x);
+      acc.y = fmaf(x[k].y, fi, acc.y);
+      acc.z = fmaf(x[k].z, fi, acc.z);
+      acc.w = fmaf(x[k].w, fi, acc.w);
     }
   }
   __syncthreads();
@@ -827,17 +834,35 @@ __global__ void __launch_bounds__(256) paged_weight_kernel(const PagedView c, co
   const int n = paged_len(c, b);
   const long long base = (long long)pair * paged_slots(c);
   const float* ls = lse + (long long)b * n_heads + (long long)g * group;
-  for (int j = blockIdx.y * 256 + threadIdx.x; j < n; j += gridDim.y * 256) {
-    const float* s = scores + (base + j) * group;
-    float w = 0.f;
+  constexpr int U = 4;  // slots of a thread at a time: all loads ahead of the stores
+  for (int j0 = blockIdx.y * 256 * U + threadIdx.x; j0 < n; j0 += gridDim.y * 256 * U) {
+    float w[U], old[U];
     if (group == 8) {
-      const float4 x = *reinterpret_cast<const float4*>(s), y = *reinterpret_cast<const float4*>(s + 4);
-      w = ((exp2f(x.x - ls[0]) + exp2f(x.y - ls[1])) + (exp2f(x.z - ls[2]) + exp2f(x.w - ls[3]))) +
-          ((exp2f(y.x - ls[4]) + exp2f(y.y - ls[5])) + (exp2f(y.z - ls[6]) + exp2f(y.w - ls[7])));
+      float4 x[U], y[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int j = min(j0 + 256 * k, n - 1);
+        const float4* s = reinterpret_cast<const float4*>(scores + (base + j) * 8);
+        x[k] = s[0];
+        y[k] = s[1];
+        old[k] = c.weight[base + j];
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        w[k] = ((exp2f(x[k].x - ls[0]) + exp2f(x[k].y - ls[1])) + (exp2f(x[k].z - ls[2]) + exp2f(x[k].w - ls[3]))) +
+               ((exp2f(y[k].x - ls[4]) + exp2f(y[k].y - ls[5])) + (exp2f(y[k].z - ls[6]) + exp2f(y[k].w - ls[7])));
     } else {
-      for (int h = 0; h < group; ++h) w += exp2f(s[h] - ls[h]);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int j = min(j0 + 256 * k, n - 1);
+        old[k] = c.weight[base + j];
+        w[k] = 0.f;
+        for (int h = 0; h < group; ++h) w[k] += exp2f(scores[(base + j) * group + h] - ls[h]);
+      }
     }
-    c.weight[base + j] += w;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (j0 + 256 * k < n) c.weight[base + j0 + 256 * k] = old[k] + w[k];
   }
 }
 
@@ -980,7 +1005,7 @@ cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, c
   if (e != cudaSuccess || !a.accumulate) return e;
   // about 8 CTAs an SM over all (sequence, KV head) pairs
   const long long pairs = (long long)c.n_seqs * c.n_kv;
-  long long parts = (paged_slots(c) + 255) / 256, most = (8ll * ctas + pairs - 1) / pairs;
+  long long parts = (paged_slots(c) + 1023) / 1024, most = (8ll * ctas + pairs - 1) / pairs;
   if (parts > most) parts = most;
   return launch_overlapped(paged_weight_kernel, dim3((unsigned)pairs, (unsigned)parts), 256, 0, 0, st, c, s.scores,
                            s.lse, a.n_heads, s.group);
