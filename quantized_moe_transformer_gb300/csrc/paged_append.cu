@@ -14,7 +14,7 @@ namespace qmoe {
 
 namespace {
 
-constexpr int AP_THREADS = 256, AP_ROWS = 16;
+constexpr int AP_THREADS = 256, AP_ROWS = 32, AP_CTAS_PER_SM = 5;
 
 // theta^(-2i/hd) / (2 pi), the turns of one position, as a fraction of 2^64.
 // Whole turns drop out of the product with a position modulo 2^64, so the
@@ -48,10 +48,10 @@ struct Four<__nv_bfloat16> {
 // A CTA takes ``rows`` rows. A unit is four elements of a head and the four
 // half a head further on, which turn together: one thread reads a unit, turns it
 // (queries and keys) and writes it to q_out or into the page; every byte is
-// read and written once, and four units of a thread are in flight at a time.
+// read and written once, 64 bytes of a thread at a time.
 // Small calls are bound by the launch, large ones by HBM.
 template <typename T, bool ROT>
-__global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const PagedView c, const AppendArgs a, int rows,
+__global__ void __launch_bounds__(AP_THREADS, AP_CTAS_PER_SM) append_kernel(const PagedView c, const AppendArgs a, int rows,
                                                             const __grid_constant__ AppendFreq fr) {
   __shared__ float2 turn[ROT ? AP_ROWS * 128 : 1];
   __shared__ long long off[AP_ROWS];
@@ -91,59 +91,62 @@ __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const PagedView c
     if (seq >= 0 && (int)(threadIdx.x & 31) == __ffs(peers) - 1) atomicMax(c.lens + seq, top + 1);
   }
   using F = Four<T>;
+  using B = Four<__nv_bfloat16>;
   using raw = typename F::raw;
-  const int per_head = hd / 8, units = (a.n_heads + 2 * c.n_kv) * per_head, total = n * units;
-  const T *qs = static_cast<const T*>(a.q), *ks = static_cast<const T*>(a.k), *vs = static_cast<const T*>(a.v);
-  constexpr int U = 16 / (int)sizeof(raw) * 2;  // 64 bytes of a thread in flight
+  const int per_head = hd / 8, units = (a.n_heads + 2 * c.n_kv) * per_head;
+  // a thread keeps its unit and walks rows; where a row has fewer units than the CTA threads, groups of threads take
+  // rows side by side
+  const int groups = units < AP_THREADS ? AP_THREADS / units : 1, group = units < AP_THREADS ? tid / units : 0;
+  constexpr int U = 64 / (int)sizeof(raw) / 2;  // 64 bytes of a thread in flight
   bool looked_up = false;
-  for (int i0 = tid; i0 - tid < total; i0 += U * AP_THREADS) {
-    raw x[U], y[U];
-    int r[U], h[U], d[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = i0 + k * AP_THREADS;
-      h[k] = -1;
-      if (i < total) {
-        r[k] = i / units;
-        const int u = i - r[k] * units;
-        h[k] = u / per_head;
-        d[k] = 4 * (u - h[k] * per_head);
-        const int g = h[k] - a.n_heads;
-        const T* src = (g < 0 ? qs + ((long long)(n0 + r[k]) * a.n_heads + h[k]) * hd
-                              : (g < c.n_kv ? ks + ((long long)(n0 + r[k]) * c.n_kv + g) * hd
-                                            : vs + ((long long)(n0 + r[k]) * c.n_kv + g - c.n_kv) * hd)) + d[k];
-        x[k] = *reinterpret_cast<const raw*>(src);
-        y[k] = *reinterpret_cast<const raw*>(src + half);
-      }
+  for (int u0 = 0; u0 < units; u0 += AP_THREADS) {
+    const int u = u0 + tid - group * units;
+    const bool mine = u < units && group < groups;
+    const int h = u / per_head, d = 4 * (u - h * per_head), g = h - a.n_heads;
+    const T* src = nullptr;
+    long long step = 0;  // elements between a tensor's rows
+    if (mine) {
+      step = (long long)(g < 0 ? a.n_heads : c.n_kv) * hd;
+      src = static_cast<const T*>(g < 0 ? a.q : g < c.n_kv ? a.k : a.v) + n0 * step +
+            (g < 0 ? h : g < c.n_kv ? g : g - c.n_kv) * hd + d;
     }
-    if (!looked_up) __syncthreads();  // the first reads go on while the pages are looked up
-    looked_up = true;
+    T* q_to = g < 0 ? static_cast<T*>(a.q_out) + n0 * step + h * hd + d : nullptr;
+    __nv_bfloat16* kv_to = g < 0 ? nullptr : (g < c.n_kv ? c.k + g * c.head_stride : c.v + (g - c.n_kv) * c.head_stride) + d;
+    for (int r0 = group; r0 - group < n; r0 += U * groups) {
+      raw x[U], y[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (h[k] < 0) continue;
-      const int g = h[k] - a.n_heads;
-      const long long o = off[r[k]];
-      if (g >= 0 && o < 0) continue;
-      float4 p = F::wide(x[k]), q = F::wide(y[k]);
-      if (ROT && g < c.n_kv) {
-        const float2* t = turn + r[k] * half + d[k];
-        const float2 t0 = t[0], t1 = t[1], t2 = t[2], t3 = t[3];
-        const float4 v = p, w = q;
-        p = make_float4(v.x * t0.x - w.x * t0.y, v.y * t1.x - w.y * t1.y, v.z * t2.x - w.z * t2.y,
-                        v.w * t3.x - w.w * t3.y);
-        q = make_float4(w.x * t0.x + v.x * t0.y, w.y * t1.x + v.y * t1.y, w.z * t2.x + v.z * t2.y,
-                        w.w * t3.x + v.w * t3.y);
+      for (int k = 0; k < U; ++k) {
+        const int r = r0 + k * groups;
+        if (mine && r < n) {
+          x[k] = *reinterpret_cast<const raw*>(src + r * step);
+          y[k] = *reinterpret_cast<const raw*>(src + r * step + half);
+        }
       }
-      if (g < 0) {
-        T* dst = static_cast<T*>(a.q_out) + ((long long)(n0 + r[k]) * a.n_heads + h[k]) * hd + d[k];
-        *reinterpret_cast<raw*>(dst) = F::narrow(p);
-        *reinterpret_cast<raw*>(dst + half) = F::narrow(q);
-      } else {
-        using B = Four<__nv_bfloat16>;
-        __nv_bfloat16* dst = (g < c.n_kv ? c.k + o + (long long)g * c.head_stride
-                                         : c.v + o + (long long)(g - c.n_kv) * c.head_stride) + d[k];
-        *reinterpret_cast<B::raw*>(dst) = B::narrow(p);
-        *reinterpret_cast<B::raw*>(dst + half) = B::narrow(q);
+      if (!looked_up) __syncthreads();  // the first reads go on while the pages are looked up
+      looked_up = true;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int r = r0 + k * groups;
+        if (!mine || r >= n) continue;
+        const long long o = off[r];
+        if (g >= 0 && o < 0) continue;
+        float4 p = F::wide(x[k]), q = F::wide(y[k]);
+        if (ROT && g < c.n_kv) {
+          const float2* t = turn + r * half + d;
+          const float2 t0 = t[0], t1 = t[1], t2 = t[2], t3 = t[3];
+          const float4 v = p, w = q;
+          p = make_float4(v.x * t0.x - w.x * t0.y, v.y * t1.x - w.y * t1.y, v.z * t2.x - w.z * t2.y,
+                          v.w * t3.x - w.w * t3.y);
+          q = make_float4(w.x * t0.x + v.x * t0.y, w.y * t1.x + v.y * t1.y, w.z * t2.x + v.z * t2.y,
+                          w.w * t3.x + v.w * t3.y);
+        }
+        if (g < 0) {
+          *reinterpret_cast<raw*>(q_to + r * step) = F::narrow(p);
+          *reinterpret_cast<raw*>(q_to + r * step + half) = F::narrow(q);
+        } else {
+          *reinterpret_cast<B::raw*>(kv_to + o) = B::narrow(p);
+          *reinterpret_cast<B::raw*>(kv_to + o + half) = B::narrow(q);
+        }
       }
     }
   }
@@ -158,9 +161,10 @@ __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const PagedView c
 
 template <typename T>
 cudaError_t append_rows(const PagedView& c, const AppendArgs& a, const AppendFreq& fr, cudaStream_t st) {
-  // one row a CTA until every SM has four, then up to 16 rows
-  int rows = a.n_rows / (4 * device_sm_count());
-  rows = rows < 1 ? 1 : rows > AP_ROWS ? AP_ROWS : rows;
+  // all CTAs at once on the SMs, as few rows in each as that allows
+  const int fit = AP_CTAS_PER_SM * device_sm_count();
+  int rows = (a.n_rows + fit - 1) / fit;
+  if (rows > AP_ROWS) rows = AP_ROWS;
   const int ctas = (a.n_rows + rows - 1) / rows;
   if (a.rotate)
     return launch_overlapped(append_kernel<T, true>, dim3(ctas), AP_THREADS, 0, 0, st, c, a, rows, fr);
