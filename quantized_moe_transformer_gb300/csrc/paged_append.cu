@@ -14,7 +14,7 @@ namespace qmoe {
 
 namespace {
 
-constexpr int AP_THREADS = 256, AP_ROWS = 32, AP_CTAS_PER_SM = 5;
+constexpr int AP_THREADS = 256, AP_MAX_THREADS = 512, AP_ROWS = 32, AP_CTAS_PER_SM = 4;
 
 // theta^(-2i/hd) / (2 pi), the turns of one position, as a fraction of 2^64.
 // Whole turns drop out of the product with a position modulo 2^64, so the
@@ -51,16 +51,16 @@ struct Four<__nv_bfloat16> {
 // read and written once, 64 bytes of a thread at a time.
 // Small calls are bound by the launch, large ones by HBM.
 template <typename T, bool ROT>
-__global__ void __launch_bounds__(AP_THREADS, AP_CTAS_PER_SM) append_kernel(const PagedView c, const AppendArgs a, int rows,
+__global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedView c, const AppendArgs a, int rows,
                                                             const __grid_constant__ AppendFreq fr) {
   __shared__ float2 turn[ROT ? AP_ROWS * 128 : 1];
   __shared__ long long off[AP_ROWS];
   __shared__ int2 at[AP_ROWS];  // (sequence, slot), slot -1: the row is not cached
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, hd = c.head_dim, half = hd / 2;
+  const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, threads = blockDim.x, hd = c.head_dim, half = hd / 2;
   if (ROT) {
-    for (int i = tid; i < n * half; i += AP_THREADS) {
+    for (int i = tid; i < n * half; i += threads) {
       const int r = i / half, d = i - r * half;
       const uint64_t frac = (uint64_t)(long long)a.pos[n0 + r] * fr.turns[d];
       // the upper 32 bits as a signed part of a turn: |error| <= 2^-33 turns, then one rounding to fp32
@@ -96,10 +96,10 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS_PER_SM) append_kernel(cons
   const int per_head = hd / 8, units = (a.n_heads + 2 * c.n_kv) * per_head;
   // a thread keeps its unit and walks rows; where a row has fewer units than the CTA threads, groups of threads take
   // rows side by side
-  const int groups = units < AP_THREADS ? AP_THREADS / units : 1, group = units < AP_THREADS ? tid / units : 0;
+  const int groups = units < threads ? threads / units : 1, group = units < threads ? tid / units : 0;
   constexpr int U = 64 / (int)sizeof(raw) / 2;  // 64 bytes of a thread in flight
   bool looked_up = false;
-  for (int u0 = 0; u0 < units; u0 += AP_THREADS) {
+  for (int u0 = 0; u0 < units; u0 += threads) {
     const int u = u0 + tid - group * units;
     const bool mine = u < units && group < groups;
     const int h = u / per_head, d = 4 * (u - h * per_head), g = h - a.n_heads;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS_PER_SM) append_kernel(cons
       }
     }
   }
-  for (int i = tid; i < n * c.n_kv; i += AP_THREADS) {
+  for (int i = tid; i < n * c.n_kv; i += threads) {
     const int r = i % n, g = i / n;
     if (at[r].y < 0) continue;
     const long long e = ((long long)at[r].x * c.n_kv + g) * paged_slots(c) + at[r].y;
@@ -165,10 +165,14 @@ cudaError_t append_rows(const PagedView& c, const AppendArgs& a, const AppendFre
   const int fit = AP_CTAS_PER_SM * device_sm_count();
   int rows = (a.n_rows + fit - 1) / fit;
   if (rows > AP_ROWS) rows = AP_ROWS;
+  // one row of many heads: a thread for each of its units
+  const int units = (a.n_heads + 2 * c.n_kv) * (c.head_dim / 8);
+  int threads = AP_THREADS;
+  while (rows == 1 && threads < AP_MAX_THREADS && threads < units) threads += 32;
   const int ctas = (a.n_rows + rows - 1) / rows;
   if (a.rotate)
-    return launch_overlapped(append_kernel<T, true>, dim3(ctas), AP_THREADS, 0, 0, st, c, a, rows, fr);
-  return launch_overlapped(append_kernel<T, false>, dim3(ctas), AP_THREADS, 0, 0, st, c, a, rows, fr);
+    return launch_overlapped(append_kernel<T, true>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
+  return launch_overlapped(append_kernel<T, false>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
 }
 
 }  // namespace
