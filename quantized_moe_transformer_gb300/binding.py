@@ -401,9 +401,13 @@ class PagedCacheDesc(ctypes.Structure):
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
+_paged = None
+
+
 def _paged_lib():
-    L = lib()
-    if not getattr(L, "_paged_declared", False):
+    global _paged
+    if _paged is None:
+        L = lib()
         P = ctypes.POINTER(PagedCacheDesc)
         L.qmoe_paged_append.argtypes = [P, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int, ctypes.c_float,
                                         _vp]
@@ -416,21 +420,29 @@ def _paged_lib():
         L.qmoe_block_decode_paged_workspace_bytes.restype = _c_size
         L.qmoe_block_decode_paged_workspace_bytes.argtypes = [ctypes.POINTER(BlockDesc), P, _c_int]
         L.qmoe_block_decode_paged.argtypes = [ctypes.POINTER(BlockDesc), P, _vp, _vp, _vp, _c_int, _vp, _c_size, _vp]
-        L._paged_declared = True
-    return L
+        _paged = L
+    return _paged
 
 
-def _need(t, what, shape=None, dtype=None):
-    """Checks one tensor argument: on a CUDA device, contiguous, shape and type."""
+def _need(t, what, shape, dtype):
+    """The address of one tensor argument, checked: on a CUDA device, contiguous,
+    of this shape and type (one line where all is well: it runs for each
+    argument of each call)."""
+    if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise QmoeError(f"{what} must be on a CUDA device")
-    if not t.is_contiguous():
-        raise QmoeError(f"{what} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise QmoeError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise QmoeError(f"{what} has type {t.dtype}, not {dtype}")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise QmoeError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise QmoeError(f"{what} must be contiguous")
+
+
+def _need_ws(ws):
+    if not ws.is_cuda or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise QmoeError("the workspace must be a contiguous uint8 tensor on a CUDA device")
+    return ws.data_ptr()
 
 
 class PagedCache:
@@ -459,7 +471,7 @@ class PagedCache:
         self.k, self.v, self.table, self.lens, self.weight, self.pos = k, v, table, lens, weight, pos
         self._desc = PagedCacheDesc(
             self.n_seqs, self.n_kv, self.head_dim, self.page, self.n_pages, self.max_pages, k.stride(0), k.stride(1),
-            k.stride(2), k.data_ptr(), v.data_ptr(), _need(table, "table", dtype=torch.int32),
+            k.stride(2), k.data_ptr(), v.data_ptr(), _need(table, "table", table.shape, torch.int32),
             _need(lens, "lens", (self.n_seqs,), torch.int32),
             None if weight is None else _need(weight, "weight", per_slot, torch.float32),
             None if pos is None else _need(pos, "pos", per_slot, torch.int32))
@@ -519,7 +531,7 @@ def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slo
     else:
         qp = qo = None
     _check(_paged_lib().qmoe_paged_append(
-        cache._desc_ref, qp, qo, _need(k, "k", kv_shape), _need(v, "v", kv_shape, dtype), _DTYPE[dtype],
+        cache._desc_ref, qp, qo, _need(k, "k", kv_shape, dtype), _need(v, "v", kv_shape, dtype), _DTYPE[dtype],
         None if seq is None else _need(seq, "seq", (rows,), torch.int32),
         None if slot is None else _need(slot, "slot", (rows,), torch.int32), _need(pos, "pos", (rows,), torch.int32),
         rows, heads, rope_theta, _raw_stream(stream, cache.device)))
@@ -546,8 +558,8 @@ def paged_attention(cache: PagedCache, q, out=None, scale: float = 0.0, accumula
     if ws is None:
         ws = paged_attention_workspace(cache, heads, accumulate)
     _check(_paged_lib().qmoe_paged_attention(
-        cache._desc_ref, _need(q, "q", shape), _need(out, "out", shape, dtype), _DTYPE[dtype], heads, scale,
-        int(accumulate), _need(ws, "ws"), ws.numel(), _raw_stream(stream, cache.device)))
+        cache._desc_ref, _need(q, "q", shape, dtype), _need(out, "out", shape, dtype), _DTYPE[dtype], heads, scale,
+        int(accumulate), _need_ws(ws), ws.numel(), _raw_stream(stream, cache.device)))
     return out
 
 
@@ -574,7 +586,7 @@ def cache_evict(cache: PagedCache, next_pos, budget: int, recent: int = 0, lens_
         cache._desc_ref, None if next_pos is None else _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),
         budget, recent, _need(lens_out, "lens_out", (cache.n_seqs,), torch.int32),
         _need(weight_out, "weight_out", per_slot, torch.float32),
-        None if pos_out is None else _need(pos_out, "pos_out", per_slot, torch.int32), _need(ws, "ws"), ws.numel(),
+        None if pos_out is None else _need(pos_out, "pos_out", per_slot, torch.int32), _need_ws(ws), ws.numel(),
         _raw_stream(stream, cache.device)))
     return lens_out, weight_out, pos_out
 
@@ -598,5 +610,5 @@ def block_decode_paged(block: Block, cache: PagedCache, X, next_pos, out=None, a
     _check(_paged_lib().qmoe_block_decode_paged(
         ctypes.byref(block.desc), cache._desc_ref, _need(X, "X", shape, torch.float32),
         _need(out, "out", shape, torch.float32), _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),
-        int(accumulate), _need(ws, "ws"), ws.numel(), _raw_stream(stream, cache.device)))
+        int(accumulate), _need_ws(ws), ws.numel(), _raw_stream(stream, cache.device)))
     return out
