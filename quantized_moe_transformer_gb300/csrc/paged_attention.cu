@@ -57,9 +57,10 @@ struct PaCfg {
   static constexpr int KBYTES = HALF * (HDP / 64);
   static constexpr int RING = WARPS * STAGES * 2 * KBYTES;
   static constexpr int HT = 8 * NT;                        // heads of a row
-  static constexpr int MERGE = WARPS * HT * HDP * 4;
+  static constexpr int MROW = HDP + 4;                     // a head's output in shared memory: rows apart by 4 banks
+  static constexpr int MERGE = WARPS * HT * MROW * 4;
   static constexpr int SMEM = 1024 + RING + MERGE + 2 * WARPS * HT * 8 + WARPS * STAGES * 20;
-  static_assert(HT * HDP * 4 <= STAGES * 2 * KBYTES, "a warp's output fits its ring");
+  static_assert(HT * MROW * 4 <= STAGES * 2 * KBYTES, "a warp's output fits its ring");
 };
 
 struct PaSplit {
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
   __shared__ int s_abort;
   const uint32_t s0 = tc::smem_u32(pa_smem_raw);
   uint8_t* smem = pa_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
-  float* merge_o = reinterpret_cast<float*>(smem + C::RING);                    // [W][HT][HDP]
+  float* merge_o = reinterpret_cast<float*>(smem + C::RING);                    // [W][HT][MROW]
   float2* merge_ml = reinterpret_cast<float2*>(smem + C::RING + C::MERGE);      // [2: head, tail][W][HT]
   uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + 2 * W * HT);          // [W][ST]
   uint64_t* empties = bars + W * ST;                                            // [W][ST]
@@ -194,13 +195,21 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
   long long ahead_of = 0;
   for (int b = lane * q; b < min(c.n_seqs, (lane + 1) * q); ++b) ahead_of += pa_tiles(c, b, KT);
   const long long own_tiles = ahead_of;
+  long long total;
+  if (c.n_seqs == 1) {
+    total = __shfl_sync(0xffffffffu, (int)own_tiles, 0);  // (a sequence's tiles are few enough)
+    ahead_of = lane > 0 ? total : 0;
+  } else {
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, ahead_of, off);
-    if (lane >= off) ahead_of += x;
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, ahead_of, off);
+      if (lane >= off) ahead_of += x;
+    }
+    total = __shfl_sync(0xffffffffu, ahead_of, 31);
+    ahead_of -= own_tiles;
   }
-  const long long total = __shfl_sync(0xffffffffu, ahead_of, 31) * rows;
-  ahead_of = (ahead_of - own_tiles) * rows;
+  total *= rows;
+  ahead_of *= rows;
   // CTAs: one for each W tiles (a tile for each warp) as far as there are; those of a single sequence then begin at its rows
   const long long fit = c.n_seqs != 1 ? (total + W - 1) / W : p.whole_rows ? rows : (total / rows + W - 1) / W * rows;
   const int n_ctas = (int)(fit < gridDim.x ? fit : gridDim.x);
@@ -247,38 +256,6 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
   const int boxes = p.at_once ? 1 : HDP / 64, pieces = KT / p.box_rows, page_mask = (1 << c.page_log2) - 1;
   int left = count;  // tiles still to look up
   PaWalk ahead = seg;
-  // page of this lane's piece of the tile at ``ahead``; -1: holds nothing
-  auto look_up = [&](int& page) {
-    page = -1;
-    const int slot = ahead.t * KT + lane * p.box_rows;
-    if (left > 0 && lane < pieces && slot < ahead.len)
-      page = __ldg(c.table + (long long)ahead.b * c.max_pages + (slot >> c.page_log2));
-  };
-  auto issue = [&](int st, const PaWalk& w, int page) {
-    const int slot = w.t * KT + lane * p.box_rows;
-    const bool want = lane < pieces && slot < w.len;
-    const bool there = want && (unsigned)page < (unsigned)c.n_pages;
-    if (want && !there) record_status(p.status, QMOE_ERR_DEVICE_ARG);
-    const unsigned ok = __ballot_sync(0xffffffffu, there);
-    // slots of the tile that hold entries: their piece has a page and they lie below the length
-    const int key = w.t * KT + lane;
-    const bool held = lane < KT && key < w.len && ((ok >> (lane / p.box_rows)) & 1u);
-    const unsigned m = __ballot_sync(0xffffffffu, held);
-    if (lane == 0) {
-      mask_of[st] = m;
-      tc::mbar_expect_tx(&full[st], (uint32_t)__popc(ok) * (uint32_t)p.box_rows * 2u * HDP * 2u);
-    }
-    __syncwarp();
-    if (there) {
-      const uint32_t dst = tc::smem_u32(ring + st * 2 * C::KBYTES) + (uint32_t)(lane * p.box_rows) * 128u;
-      const int g = w.vh / p.head_tiles;
-#pragma unroll 1
-      for (int h = 0; h < boxes; ++h) {
-        pa_tma(dst + h * C::HALF, &kmap, slot & page_mask, h, g, page, p.at_once, &full[st]);
-        pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, slot & page_mask, h, g, page, p.at_once, &full[st]);
-      }
-    }
-  };
   // a row's queries as B fragments hold them: head lane / 4, dims 2 (lane % 4) + {0, 1, 8, 9} of each 16
   float2 qx[C::F32 ? KS : 1][NT][2];
   uint32_t qf[KS][NT][C::QP][2];
@@ -304,19 +281,51 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
         }
     }
   };
-  if (count > 0) {
-    int pages[ST];
-    PaWalk at[ST];
+  // The copies of piece i of the tile at ``w`` into stage st of a warp's ring.
+  constexpr int PIECES = KT / 8;
+  auto copy = [&](const PaWalk& w, int to_warp, int st, int i, int page) {
+    const uint32_t dst = tc::smem_u32(smem + (to_warp * ST + st) * 2 * C::KBYTES) + (uint32_t)(i * p.box_rows) * 128u;
+    const int row = (w.t * KT + i * p.box_rows) & page_mask, g = w.vh / p.head_tiles;
+    uint64_t* bar = &bars[to_warp * ST + st];
+#pragma unroll 1
+    for (int h = 0; h < boxes; ++h) {
+      pa_tma(dst + h * C::HALF, &kmap, row, h, g, page, p.at_once, bar);
+      pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, row, h, g, page, p.at_once, bar);
+    }
+  };
+  // which of a tile's slots hold entries: their piece has a page (bits of ``ok``) and they lie below the length
+  auto held_of = [&](unsigned ok, int n_in) {
+    uint32_t held = 0;
 #pragma unroll
-    for (int s = 0; s < ST; ++s) {
-      look_up(pages[s]);
-      at[s] = ahead;
+    for (int i = 0; i < PIECES; ++i)
+      if ((ok >> i) & 1u) held |= (p.box_rows == 32 ? 0xffffffffu : (1u << p.box_rows) - 1u) << (i * p.box_rows);
+    return n_in >= 32 ? held : held & (n_in > 0 ? (1u << n_in) - 1u : 0u);
+  };
+  if (count > 0) {
+    // this warp's first ST tiles: lane 8 s + i copies piece i of the s-th
+    const int s = lane >> 3, piece = lane & 7;
+    PaWalk w{};
+#pragma unroll 1
+    for (int k = 0; k < ST; ++k) {
+      if (k == s) w = ahead;
       if (--left > 0) pa_step<KT>(c, rows, 1, ahead);
     }
+    const bool some = s < ST && s < count;
+    const int n_in = min(KT, w.len - w.t * KT), slot = w.t * KT + piece * p.box_rows;
+    const bool want = some && piece < pieces && piece * p.box_rows < n_in;
+    int page = -1;
+    if (want) page = __ldg(c.table + (long long)w.b * c.max_pages + (slot >> c.page_log2));
     load_q(seg);
-#pragma unroll
-    for (int s = 0; s < ST; ++s)
-      if (s < count && !(p.fault && s == 0 && blockIdx.x == 0 && warp == 0)) issue(s, at[s], pages[s]);
+    const bool there = want && (unsigned)page < (unsigned)c.n_pages;
+    if (want && !there) record_status(p.status, QMOE_ERR_DEVICE_ARG);
+    const unsigned ok = (__ballot_sync(0xffffffffu, there) >> (8 * s)) & 255u;
+    const bool dropped = p.fault && blockIdx.x == 0 && warp == 0 && s == 0;  // (the test-only fault)
+    if (some && piece == 0 && !dropped) {
+      masks[warp * ST + s] = held_of(ok, n_in);
+      tc::mbar_expect_tx(&bars[warp * ST + s], (uint32_t)__popc(ok) * (uint32_t)p.box_rows * 4u * HDP);
+    }
+    __syncwarp();
+    if (there && !dropped) copy(w, warp, s, piece, page);
   }
   if (warp < W && lane == 0) s_walk[warp] = make_int4(ahead.b, ahead.vh, ahead.t, left);
   __syncthreads();
@@ -330,7 +339,6 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     w.vh = from.y;
     w.t = from.z;
     left = from.w;
-    constexpr int PIECES = KT / 8;
     int pages[PIECES];
     auto pages_of = [&]() {
 #pragma unroll
@@ -341,8 +349,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
       }
     };
     pages_of();
-    uint8_t* to = smem + (lane < W ? lane : 0) * ST * 2 * C::KBYTES;
-    const int bar0 = (lane < W ? lane : 0) * ST;
+    const int to = lane < W ? lane : 0, bar0 = to * ST;
     int st = 0;
     uint32_t ph = 0;
     uint64_t since = tc::global_ns();
@@ -350,33 +357,20 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
       const bool ready = left > 0 && tc::mbar_test_wait(&empties[bar0 + st], ph);
       if (ready) {
         const int n_in = min(KT, w.len - w.t * KT);
-        uint32_t held = 0, bytes = 0;
+        unsigned there = 0;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
           const bool want = i < pieces && i * p.box_rows < n_in;
-          const bool there = want && (unsigned)pages[i] < (unsigned)c.n_pages;
-          if (want && !there) record_status(p.status, QMOE_ERR_DEVICE_ARG);
-          if (there) {
-            held |= (p.box_rows == 32 ? 0xffffffffu : (1u << p.box_rows) - 1u) << (i * p.box_rows);
-            bytes += (uint32_t)p.box_rows * 4u * HDP;
-          }
+          if (want && (unsigned)pages[i] < (unsigned)c.n_pages)
+            there |= 1u << i;
+          else if (want)
+            record_status(p.status, QMOE_ERR_DEVICE_ARG);
         }
-        if (n_in < 32) held &= n_in > 0 ? (1u << n_in) - 1u : 0u;
-        masks[bar0 + st] = held;
-        uint64_t* bar = &bars[bar0 + st];
-        tc::mbar_expect_tx(bar, bytes);
-        const int g = w.vh / p.head_tiles;
+        masks[bar0 + st] = held_of(there, n_in);
+        tc::mbar_expect_tx(&bars[bar0 + st], (uint32_t)__popc(there) * (uint32_t)p.box_rows * 4u * HDP);
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-          if (i >= pieces || i * p.box_rows >= n_in || (unsigned)pages[i] >= (unsigned)c.n_pages) continue;
-          const uint32_t dst = tc::smem_u32(to + st * 2 * C::KBYTES) + (uint32_t)(i * p.box_rows) * 128u;
-          const int row = (w.t * KT + i * p.box_rows) & page_mask;
-#pragma unroll 1
-          for (int h = 0; h < boxes; ++h) {
-            pa_tma(dst + h * C::HALF, &kmap, row, h, g, pages[i], p.at_once, bar);
-            pa_tma(dst + C::KBYTES + h * C::HALF, &vmap, row, h, g, pages[i], p.at_once, bar);
-          }
-        }
+        for (int i = 0; i < PIECES; ++i)
+          if ((there >> i) & 1u) copy(w, to, st, i, pages[i]);
         if (--left > 0) pa_step<KT>(c, rows, 1, w);
         pages_of();
         if (++st == ST) {
@@ -614,7 +608,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     // ---- the row's result, or what this warp leaves of it
     const bool begins = row.t == 0, goes_on = row.t + n_tiles < row.nt;
     const bool whole = begins && !goes_on;
-    float* left_o = begins ? reinterpret_cast<float*>(ring) : merge_o + warp * HT * HDP;
+    float* left_o = begins ? reinterpret_cast<float*>(ring) : merge_o + warp * HT * C::MROW;
     float2* left_ml = merge_ml + (begins ? W + warp : warp) * HT;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -629,8 +623,8 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
           if (lane < 4) left_ml[hh] = make_float2(m[n][e], x);
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
-            left_o[hh * HDP + 16 * i + (lane >> 2)] = o[i][n][e];
-            left_o[hh * HDP + 16 * i + 8 + (lane >> 2)] = o[i][n][e + 2];
+            left_o[hh * C::MROW + 16 * i + (lane >> 2)] = o[i][n][e];
+            left_o[hh * C::MROW + 16 * i + 8 + (lane >> 2)] = o[i][n][e + 2];
           }
           continue;
         }
@@ -682,7 +676,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
         x[w] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (w < W ? (mine >> w) & 1u : began) {
           ml[w] = merge_ml[(w < W ? w : W + first) * HT + hh];
-          x[w] = *reinterpret_cast<const float4*>((w < W ? merge_o + w * HT * HDP : tail_o) + hh * HDP + d);
+          x[w] = *reinterpret_cast<const float4*>((w < W ? merge_o + w * HT * C::MROW : tail_o) + hh * C::MROW + d);
         }
       }
       float M = -INFINITY, L = 0.f;
