@@ -879,8 +879,8 @@ PaPlan pa_plan(const PagedView& c, int n_heads, bool f32, bool accumulate, int c
   p.ctas = ctas;
   size_t o = 0;
   p.desc = o;   o += up256(sizeof(int4) * ctas);
-  p.ml = o;     o += up256(sizeof(float2) * ctas * 2 * 16);
-  p.o = o;      o += up256(sizeof(float) * ctas * 2 * 16 * (size_t)p.hdp);
+  p.ml = o;     o += up256(sizeof(float2) * ctas * 2 * p.head_tile);
+  p.o = o;      o += up256(sizeof(float) * ctas * 2 * p.head_tile * (size_t)p.hdp);
   p.lse = o;    o += accumulate ? up256(sizeof(float) * (size_t)c.n_seqs * n_heads) : 0;
   p.scores = o; o += accumulate ? up256(sizeof(float) * (size_t)c.n_seqs * n_heads * (size_t)paged_slots(c)) : 0;
   p.total = o;

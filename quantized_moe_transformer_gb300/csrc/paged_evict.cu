@@ -97,9 +97,10 @@ __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& 
 // One cluster of C CTAs per (sequence, KV head). CTA r takes the r-th slice of
 // the slots, warp w the w-th part of the slice, 32 slots at a time; the keys
 // stay in shared memory (slices beyond EV_MAX_KEYS are read again for each step). The m-th largest key is
-// found 8 bits at a time from the top: the keys that share the digits so far
-// are counted by their next digit in shared memory, over the cluster through
-// distributed shared memory, until all that share the digits stay. The staying
+// found 11 bits at a time from the top: the keys that share the digits so far
+// are counted by their next digit in shared memory, summed over the cluster
+// through distributed shared memory, until all that share the digits stay (two or three
+// digits; of 8 bits it took one more, which is 1 to 2 us). The staying
 // entries' ranks (counts over warps and CTAs) give each its place in the list
 // of holes or movers. Weights and positions are read once; what bounds it is a
 // chain of short steps: barriers (0.1 us in a CTA, 0.8 us in a cluster, so a
@@ -110,8 +111,8 @@ template <bool LONG, bool INLINE>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedView c, const EvictArgs a,
                                                                   const EvictLists ls) {
   extern __shared__ uint32_t ev_keys[];
-  __shared__ __align__(16) int hist[3][256];
-  __shared__ __align__(16) int sum[256];
+  __shared__ __align__(16) int2 hist[3][EV_THREADS];  // counts of 2048 digits, two of a thread, for each digit
+  __shared__ __align__(16) int2 mine[EV_THREADS];     // a cluster's CTA: its own counts
   __shared__ int warp_cnt[3][EV_WARPS], cta_cnt[3], pick[3];
   __shared__ long long off[INLINE ? MV_MOVES : 1][2];
   tc::grid_dep_launch();
@@ -152,7 +153,8 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     if (!LONG || i < EV_MAX_KEYS) return ev_keys[i];
     return evict_key(weights[i], a.recent > 0 && positions[i] >= young_from);
   };
-  if (tid < 256) hist[0][tid] = hist[1][tid] = hist[2][tid] = 0;
+  hist[0][tid] = hist[1][tid] = hist[2][tid] = mine[tid] = make_int2(0, 0);
+  if (C > 1) cluster.barrier_arrive();
   // read once; what stays in place goes to the outputs now (what moves into the holes is written over it later)
   // (four loads ahead of their stores, which the compiler could not tell from the inputs)
 #pragma unroll 1
@@ -180,54 +182,50 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
   uint32_t t = 0, known = 0;  // its digits so far, and which bits those are
   int need = m, equal = 0;    // of the ``equal`` keys with these digits, ``need`` stay
 #pragma unroll 1
-  for (int shift = 24, pass = 0; shift >= 0; shift -= 8, ++pass) {
-    int* h = hist[pass % 3];
-    if (pass > 0 && tid < 256) hist[(pass + 1) % 3][tid] = 0;  // (last read two barriers ago)
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;  // digits of 11, 11 and 10 bits
+    const uint32_t digits = pass == 2 ? 1023u : 2047u;
+    int2* h = C > 1 ? mine : hist[pass];
 #pragma unroll 2
     for (int i = w0 + lane; i < w1; i += 32) {
       const uint32_t k = key(i);
-      if ((k & known) == t) atomicAdd(&h[(k >> shift) & 255u], 1);
+      if ((k & known) == t) atomicAdd(reinterpret_cast<int*>(h) + ((k >> shift) & digits), 1);
+    }
+    if (C > 1) {
+      // every CTA adds its counts (of few digits but the first) to those of all
+      __syncthreads();
+      const int2 v = mine[tid];
+      mine[tid] = make_int2(0, 0);
+      if (pass == 0) cluster.barrier_wait();  // (the others' counts start at zero)
+      if (v.x | v.y)
+        for (int r = 0; r < C; ++r) {
+          int2* to = cluster.map_shared_rank(hist[pass], r) + tid;
+          if (v.x) atomicAdd(&to->x, v.x);
+          if (v.y) atomicAdd(&to->y, v.y);
+        }
     }
     all_sync();
-    if (C > 1) {
-      if (tid < 256) {
-        int v[EV_CLUSTER], s = 0;
+    // this thread's digits 2 tid and 2 tid + 1, and the keys with higher ones
+    const int2 d = hist[pass][tid];
+    const int own = d.x + d.y;
+    int above = own;
 #pragma unroll
-        for (int r = 0; r < EV_CLUSTER; ++r) v[r] = cluster.map_shared_rank(h, r < C ? r : rank)[tid];  // all at once
-#pragma unroll
-        for (int r = 0; r < EV_CLUSTER; ++r) s += r < C ? v[r] : 0;
-        sum[tid] = s;
-      }
-      __syncthreads();
-      h = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_down_sync(0xffffffffu, above, o);
+      if (lane + o < 32) above += x;
     }
-    if (warp == 0) {
-      // lane l holds the 8 digits from 8 l on; counts from the largest digit down
-      int d[8], own = 0;
-      *reinterpret_cast<int4*>(d) = reinterpret_cast<const int4*>(h)[2 * lane];
-      *reinterpret_cast<int4*>(d + 4) = reinterpret_cast<const int4*>(h)[2 * lane + 1];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) own += d[i];
-      int above = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_down_sync(0xffffffffu, above, o);
-        if (lane + o < 32) above += x;
-      }
-      above -= own;  // keys with digits of higher lanes
-#pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        if (above < need && above + d[i] >= need) {
-          pick[0] = 8 * lane + i;
-          pick[1] = need - above;
-          pick[2] = d[i];
-        }
-        above += d[i];
-      }
+    if (lane == 0) warp_cnt[0][warp] = above;
+    __syncthreads();
+    above += __reduce_add_sync(0xffffffffu, lane > warp ? warp_cnt[0][lane] : 0) - own;
+    if (above < need && above + own >= need) {
+      const bool upper = above + d.y >= need;
+      pick[0] = 2 * tid + upper;
+      pick[1] = upper ? need - above : need - above - d.y;
+      pick[2] = upper ? d.y : d.x;
     }
     __syncthreads();
     t |= (uint32_t)pick[0] << shift;
-    known |= 255u << shift;
+    known |= digits << shift;
     need = pick[1];
     equal = pick[2];
     if (need == equal) break;
