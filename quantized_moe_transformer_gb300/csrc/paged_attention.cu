@@ -49,7 +49,7 @@ template <int HDP_, int NT_, bool F32_>
 struct PaCfg {
   static constexpr int HDP = HDP_, NT = NT_, QP = F32_ ? 3 : 1, PP = F32_ ? 3 : 2;
   static constexpr bool F32 = F32_;
-  static constexpr int CHAINS = NT == 1 ? 4 : 2;
+  static constexpr int CHAINS = 2;                         // sums of a score side by side (4: the same time)
   static constexpr int KT = HDP == 64 ? 32 : 16;           // slots of a tile: 4 or 8 KB of keys
   static constexpr int WARPS = HDP == 256 ? 4 : 7;         // and one that feeds them (8 warps: 255 registers a thread)
   static constexpr int STAGES = NT == 1 ? 3 : 2;           // at most 192 KB in flight an SM
@@ -871,9 +871,13 @@ PaPlan pa_plan(const PagedView& c, int n_heads, bool f32, bool accumulate, int c
   PaPlan p{};
   const int group = n_heads / c.n_kv;
   p.hdp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
-  // rows of 16 heads where a group has more than 8 (each byte serves them all at once); three parts of
-  // 256-wide queries for 16 heads do not fit the registers
-  p.nt = group > 8 && !(p.hdp == 256 && f32) ? 2 : 1;
+  // A group of more than 8 heads is cut into rows of 8, or of 16 for bf16 queries over 32 MB and more: rows of 8
+  // read the cache once each, the second time out of L2 where it is not too large, and take less code, fewer
+  // registers and a stage more. bf16, G = 16: 1 x 4096 8.5 us with 8 against 10.8 with 16, 8 x 3000 12.5 against
+  // 13.9, 32 x 4096 of one KV head of 64 (32 MB) 17.9 against 16.7, 64 x 4096 78 against 59. fp32, whose queries are
+  // three parts, 64 x 4096: 79.5 against 77.5 with spills, 1 x 4096 8.8 against 13.7, so fp32 has rows of 8 only.
+  const double bytes = 4.0 * c.n_seqs * c.n_kv * (double)paged_slots(c) * c.head_dim;
+  p.nt = !f32 && group > 8 && bytes >= 32.0 * (1 << 20) ? 2 : 1;
   p.head_tile = 8 * p.nt;
   p.head_tiles = (group + p.head_tile - 1) / p.head_tile;
   p.ctas = ctas;
@@ -925,19 +929,11 @@ cudaError_t launch_split(PaSplit& s, int ctas, cudaStream_t st) {
   return launch_overlapped(paged_split_kernel<C>, dim3(ctas), 32 * (C::WARPS + 1), C::SMEM, 0, st, s, km, vm);
 }
 
-template <bool F32>
+template <bool F32, int NT>
 cudaError_t pick_split(PaSplit& s, const PaPlan& pl, cudaStream_t st) {
-  if (pl.hdp == 64) {
-    if (pl.nt == 1) return launch_split<PaCfg<64, 1, F32>>(s, pl.ctas, st);
-    return launch_split<PaCfg<64, 2, F32>>(s, pl.ctas, st);
-  }
-  if (pl.hdp == 128) {
-    if (pl.nt == 1) return launch_split<PaCfg<128, 1, F32>>(s, pl.ctas, st);
-    return launch_split<PaCfg<128, 2, F32>>(s, pl.ctas, st);
-  }
-  if (pl.nt == 1) return launch_split<PaCfg<256, 1, F32>>(s, pl.ctas, st);
-  if constexpr (!F32) return launch_split<PaCfg<256, 2, false>>(s, pl.ctas, st);
-  return cudaErrorInvalidValue;
+  if (pl.hdp == 64) return launch_split<PaCfg<64, NT, F32>>(s, pl.ctas, st);
+  if (pl.hdp == 128) return launch_split<PaCfg<128, NT, F32>>(s, pl.ctas, st);
+  return launch_split<PaCfg<256, NT, F32>>(s, pl.ctas, st);
 }
 
 }  // namespace
@@ -946,9 +942,11 @@ size_t paged_attention_ws_bytes(const PagedView& c, int n_heads, bool accumulate
   return pa_plan(c, n_heads, false, accumulate, PA_MAX_CTAS).total;
 }
 
-// Rows of at most 256 slots are not cut between CTAs: a row more or less for a
-// CTA costs less than the second launch that joins.
-static bool pa_whole_rows(const PagedView& c) { return paged_slots(c) <= 256; }
+// Rows of at most 512 slots are not cut between CTAs: a row more or less for a
+// CTA costs no more than the second launch that joins (64 sequences of 300 to 500
+// entries: 11.8 us whole, 15.9 cut; 256: 27.6 and 31.9; 8: 9.4 and 9.3; at 1024
+// slots 8 sequences take 13.8 and 9.6).
+static bool pa_whole_rows(const PagedView& c) { return paged_slots(c) <= 512; }
 
 int paged_attention_launches(const PagedView& c, int, bool accumulate) {
   return 1 + (pa_whole_rows(c) ? 0 : 1) + (accumulate ? 1 : 0);
@@ -978,7 +976,8 @@ cudaError_t launch_paged_attention(const PagedView& c, const PagedAttnArgs& a, c
   s.fault = a.fault;
   PaPlan run = pl;
   run.ctas = ctas;
-  cudaError_t e = a.f32 ? pick_split<true>(s, run, st) : pick_split<false>(s, run, st);
+  cudaError_t e = a.f32 ? pick_split<true, 1>(s, run, st)
+                        : run.nt == 1 ? pick_split<false, 1>(s, run, st) : pick_split<false, 2>(s, run, st);
   if (e != cudaSuccess) return e;
   PaJoin j{};
   j.desc = s.desc;

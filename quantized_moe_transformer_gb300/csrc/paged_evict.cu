@@ -353,20 +353,27 @@ struct EvictPlan {
   long long moves;    // of one pair, at most
 };
 
-// Clusters are taken beyond 8192 slots a CTA. The moves are made by the select
-// kernel where a CTA has at most 64 of them and no cluster that starts later
-// reads a length that another has replaced (a launch costs more than those
-// moves), else by a grid of their own.
+// One CTA for up to 8192 slots (1 x 4112: 9.4 us, with a cluster of 2 11.1; 16 x
+// 8100: 12.1 and with 4 11.8); beyond, clusters of 8 where they fit the SMs at once
+// (1 x 16000: 12.3 us, of 2 15.3; 1 x 32000: 13.6, of 4 15.7), else as small as
+// keeps a slice to 8192 slots. The moves are made by the select kernel where a
+// CTA has at most 128 of them and no cluster that starts later reads a length that
+// another has replaced (1 x 4112 to 4048: 9.6 us, 10.9 with a launch of their own; at
+// 256 moves 14.7 and 11.3), else by a grid of their own.
 EvictPlan evict_plan(const PagedView& c, const EvictArgs& a) {
   EvictPlan p{};
   const long long slots = paged_slots(c);
   p.cluster = 1;
-  while (p.cluster < EV_CLUSTER && slots > 8ll * EV_THREADS * p.cluster) p.cluster *= 2;
+  const long long pairs = (long long)c.n_seqs * c.n_kv;
+  if (slots > 8 * EV_THREADS && pairs * EV_CLUSTER <= device_sm_count())
+    p.cluster = EV_CLUSTER;
+  else
+    while (p.cluster < EV_CLUSTER && slots > 8ll * EV_THREADS * p.cluster) p.cluster *= 2;
   const long long per = ((slots + p.cluster - 1) / p.cluster + EV_THREADS - 1) / EV_THREADS * EV_THREADS;
   p.keys = per < EV_MAX_KEYS ? (int)per : EV_MAX_KEYS;
   p.long_slices = per > EV_MAX_KEYS;
   p.moves = a.budget < slots - a.budget ? a.budget : slots - a.budget;
-  p.inline_moves = p.moves <= MV_MOVES * p.cluster && (c.n_kv == 1 || a.lens_out != c.lens);
+  p.inline_moves = p.moves <= 2 * MV_MOVES * p.cluster && (c.n_kv == 1 || a.lens_out != c.lens);
   return p;
 }
 

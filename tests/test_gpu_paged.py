@@ -85,6 +85,19 @@ def test_attention_head_layouts(heads, kv, hd, dtype):
     assert bool((out[2] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heads,kv,hd", [(16, 1, 256), (20, 2, 128), (33, 1, 40), (32, 2, 64), (48, 2, 128), (8, 4, 96)])
+def test_attention_of_a_wide_table(heads, kv, hd, dtype):
+    """A table for tens of thousands of slots a sequence (bf16 groups of more than
+    8 heads take 16 at once there) with few entries, and with many."""
+    lens = [130, 1, 0, 2077, 600]
+    width = (1 << 25) // (4 * len(lens) * kv * hd * 16) + 1
+    c, g = ref.cache(2, lens, kv, hd, 16, width=max(width, 200))
+    q = torch.randn(5, heads, hd, generator=g, device="cuda").to(dtype)
+    out = check_attention(c, q, 16, accumulate=True)
+    assert bool((out[2] == 0).all())
+
+
 @pytest.mark.parametrize("page", [8, 16, 32, 64, 128, 512])
 @pytest.mark.parametrize("around", [1, 8, 16, 32, 64, 128, 256, 512])
 def test_attention_lengths_around_borders(page, around):
