@@ -16,7 +16,11 @@ namespace qmoe {
 namespace {
 
 // What bounds it: each cached byte is read once and serves the G query heads of
-// its KV head, 8 flops a byte at G = 8, so HBM bounds it.
+// its KV head, 8 flops a byte at G = 8, so HBM bounds it. 256 sequences of about
+// 4054 entries, 16 heads over 2 KV heads of 128, fp32 rows: 165 us, 6.45 TB/s (0.95
+// of the measured copy rate); one of 131075: 29.8 us, 4.5 TB/s, of which 20 are the
+// copy's, 4 the way to the first copies and 5 the merges and the join; 1 x 4096
+// 8.8 us, a chain of latencies.
 //
 // Work. A row is (sequence, KV head, tile of at most 8 NT query heads); its
 // slots are cut into tiles of KT. The tiles of all rows in order are dealt out
@@ -730,6 +734,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
 
 // Joins the partials of a row over several CTAs: one CTA per (CTA in which a
 // row may begin, head of the row). out = sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M).
+// A latency of about 3 us behind the split kernel (it starts while that ends).
 struct PaJoin {
   const int4* desc;
   const float2* part_ml;
@@ -819,7 +824,9 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PaJoin p) 
   }
 }
 
-// weight[b][g][j] += sum over the group's heads of 2^(score - lse).
+// weight[b][g][j] += sum over the group's heads of 2^(score - lse). The scores
+// (4 bytes a head and slot, 1/16 of the cache at 8 heads of 128) come back out of
+// L2: 64 sequences of up to 8191 entries, 25 MB in 8 us, with its start.
 __global__ void __launch_bounds__(256) paged_weight_kernel(const PagedView c, const float* __restrict__ scores,
                                                            const float* __restrict__ lse, int n_heads, int group) {
   tc::grid_dep_launch();
