@@ -103,10 +103,10 @@ __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& 
 // digits; of 8 bits it took one more, which is 1 to 2 us). The staying
 // entries' ranks (counts over warps and CTAs) give each its place in the list
 // of holes or movers. Weights and positions are read once; what bounds it is a
-// chain of short steps: barriers (0.1 us in a CTA, 0.8 us in a cluster, so a
-// cluster is only taken where a CTA would have more than 8 keys a thread) and code
-// that runs once, whose fetch shows (loops unrolled to 8 keys a thread in
-// registers ran longer than these).
+// chain of short steps: barriers (0.1 us in a CTA, 0.8 us in a cluster) and code
+// that runs once, whose fetch shows (keys in registers with every loop unrolled
+// over 8 of them ran longer, 16.5 against 12.0 us for 1 x 4112). 1 x 4112 takes 9.4 us
+// with its 16 moves, 64 sequences of 1500 to 8190 11 us, 3 x 65537 (8 CTAs each) 18 us.
 template <bool LONG, bool INLINE>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedView c, const EvictArgs a,
                                                                   const EvictLists ls) {
@@ -319,7 +319,8 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     evict_move<2>(c, a, ls, b, g, i0, &all, EV_THREADS, off);
 }
 
-// 64 moves a CTA.
+// 64 moves a CTA. 110 thousand moves of 512 bytes (64 sequences) take 20 us, 5.6 TB/s
+// of reads and writes in pieces of 256 bytes.
 __global__ void __launch_bounds__(MV_THREADS, 5) evict_move_kernel(const PagedView c, const EvictArgs a,
                                                                    const EvictLists ls) {
   __shared__ long long off[MV_MOVES][2];
