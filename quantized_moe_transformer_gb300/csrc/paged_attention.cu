@@ -55,8 +55,12 @@ struct PaCfg {
   static constexpr bool F32 = F32_;
   static constexpr int CHAINS = 2;                         // sums of a score side by side (4: the same time)
   static constexpr int KT = HDP == 64 ? 32 : 16;           // slots of a tile: 4 or 8 KB of keys
-  static constexpr int WARPS = HDP == 256 ? 4 : 7;         // and one that feeds them (8 warps: 255 registers a thread)
-  static constexpr int STAGES = NT == 1 ? 3 : 2;           // at most 192 KB in flight an SM
+  // Warps that compute, and one more that feeds them (8 in all have 255 registers a thread), with a ring of at most
+  // 192 KB an SM. fp32 rows of 256 are bound by their products: 5 warps with 2 stages 64 x 4096 in 101 us, 4 with 3
+  // in 110.
+  static constexpr bool WIDE = HDP == 256, WIDE_F32 = WIDE && F32_;
+  static constexpr int WARPS = WIDE_F32 ? 5 : WIDE ? 4 : 7;
+  static constexpr int STAGES = NT == 1 && !WIDE_F32 ? 3 : 2;
   static constexpr int HALF = KT * 128;                    // 64 head dims of a tile
   static constexpr int KBYTES = HALF * (HDP / 64);
   static constexpr int RING = WARPS * STAGES * 2 * KBYTES;
