@@ -432,6 +432,8 @@ int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, in
  *   written, the others are not touched. Each _out may be the cache's own array
  *   (nothing else of it); pos_out is NULL where the cache has no pos.
  *   0 <= recent <= budget; next_pos [n_seqs] int32 is read where recent > 0.
+ *   Entries are overwritten in place, so a page that holds slots below the budget
+ *   must belong to one sequence alone.
  *   ws: qmoe_cache_evict_workspace_bytes(c) bytes, 256-byte aligned.
  */
 size_t qmoe_cache_evict_workspace_bytes(const qmoe_paged_cache *c);

@@ -659,6 +659,15 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     }
   }
   __syncthreads();
+  if (*(volatile int*)&s_abort) {
+    // a wait ran out: nothing is issued any more; the copies still in flight land before the CTA leaves
+    if (warp < W && lane == 0) {
+      volatile int never = 0;
+      for (int s = stage; s < stage + ST; ++s)
+        tc::mbar_wait(&full[s % ST], s < ST ? phase : phase ^ 1u, &never, 1000000ull);
+    }
+    return;
+  }
 
   // ---- rows over several warps: the beginning that a warp left, then the ends that the next ones did
   const unsigned heads = __ballot_sync(0xffffffffu, lane < W && s_head[lane < W ? lane : 0].z);
