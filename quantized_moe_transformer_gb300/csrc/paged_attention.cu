@@ -53,7 +53,7 @@ template <int HDP_, int NT_, bool F32_>
 struct PaCfg {
   static constexpr int HDP = HDP_, NT = NT_, QP = F32_ ? 3 : 1, PP = F32_ ? 3 : 2;
   static constexpr bool F32 = F32_;
-  static constexpr int CHAINS = 2;                         // sums of a score side by side (4: the same time)
+  static constexpr int CHAINS = NT == 1 ? 4 : 2;           // sums of a score side by side (2: the same time, 1.5 times the error)
   static constexpr int KT = HDP == 64 ? 32 : 16;           // slots of a tile: 4 or 8 KB of keys
   // Warps that compute, and one more that feeds them (8 in all have 255 registers a thread), with a ring of at most
   // 192 KB an SM. fp32 rows of 256 are bound by their products: 5 warps with 2 stages 64 x 4096 in 101 us, 4 with 3

@@ -105,7 +105,7 @@ __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& 
 // of holes or movers. Weights and positions are read once; what bounds it is a
 // chain of short steps: barriers (0.1 us in a CTA, 0.8 us in a cluster) and code
 // that runs once, whose fetch shows (keys in registers with every loop unrolled
-// over 8 of them ran longer, 16.5 against 12.0 us for 1 x 4112). 1 x 4112 takes 9.4 us
+// over 8 of them ran longer, 16.5 against 12.0 us for 1 x 4112). 1 x 4112 takes 9.3 us
 // with its 16 moves, 64 sequences of 1500 to 8190 11 us, 3 x 65537 (8 CTAs each) 18 us.
 template <bool LONG, bool INLINE>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedView c, const EvictArgs a,
@@ -156,19 +156,19 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
   hist[0][tid] = hist[1][tid] = hist[2][tid] = mine[tid] = make_int2(0, 0);
   if (C > 1) cluster.barrier_arrive();
   // read once; what stays in place goes to the outputs now (what moves into the holes is written over it later)
-  // (four loads ahead of their stores, which the compiler could not tell from the inputs)
+  // (eight loads ahead of their stores, which the compiler could not tell from the inputs)
 #pragma unroll 1
-  for (int i0 = w0 + lane; i0 < w1; i0 += 128) {
-    float w[4];
-    int p[4];
+  for (int i0 = w0 + lane; i0 < w1; i0 += 256) {
+    float w[8];
+    int p[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const int i = i0 + 32 * k;
       w[k] = i < w1 ? weights[i] : 0.f;
       p[k] = i < w1 && c.pos != nullptr ? positions[i] : 0;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const int i = i0 + 32 * k;
       if (i >= w1) continue;
       if (!LONG || i < EV_MAX_KEYS) ev_keys[i] = evict_key(w[k], a.recent > 0 && p[k] >= young_from);
