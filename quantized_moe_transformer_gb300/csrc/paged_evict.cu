@@ -105,15 +105,16 @@ __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& 
 // of holes or movers. Weights and positions are read once; what bounds it is a
 // chain of short steps: barriers (0.1 us in a CTA, 0.8 us in a cluster) and code
 // that runs once, whose fetch shows (keys in registers with every loop unrolled
-// over 8 of them ran longer, 16.5 against 12.0 us for 1 x 4112). 1 x 4112 takes 9.3 us
-// with its 16 moves, 64 sequences of 1500 to 8190 11 us, 3 x 65537 (8 CTAs each) 18 us.
+// over 8 of them ran longer, 16.5 against 12.0 us for 1 x 4112). 1 x 4112 takes 8.8 us
+// with its 16 moves, 64 sequences of 1500 to 8190 11 us, 3 x 65537 (8 CTAs each) 17 us.
 template <bool LONG, bool INLINE>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedView c, const EvictArgs a,
                                                                   const EvictLists ls) {
   extern __shared__ uint32_t ev_keys[];
   __shared__ __align__(16) int2 hist[3][EV_THREADS];  // counts of 2048 digits, two of a thread, for each digit
   __shared__ __align__(16) int2 mine[EV_THREADS];     // a cluster's CTA: its own counts
-  __shared__ int warp_cnt[3][EV_WARPS], cta_cnt[3], pick[3];
+  __shared__ int4 warp_cnt[EV_WARPS], cta_cnt;
+  __shared__ int above_warp[EV_WARPS], pick[3];
   __shared__ long long off[INLINE ? MV_MOVES : 1][2];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
@@ -214,9 +215,9 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
       const int x = __shfl_down_sync(0xffffffffu, above, o);
       if (lane + o < 32) above += x;
     }
-    if (lane == 0) warp_cnt[0][warp] = above;
+    if (lane == 0) above_warp[warp] = above;
     __syncthreads();
-    above += __reduce_add_sync(0xffffffffu, lane > warp ? warp_cnt[0][lane] : 0) - own;
+    above += __reduce_add_sync(0xffffffffu, lane > warp ? above_warp[lane] : 0) - own;
     if (above < need && above + own >= need) {
       const bool upper = above + d.y >= need;
       pick[0] = 2 * tid + upper;
@@ -230,29 +231,66 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     equal = pick[2];
     if (need == equal) break;
   }
-  // ---- ranks
-  int eq_before = 0;
-  const bool rank_equal = need < equal;  // of the equal keys the lowest slots stay
-  if (rank_equal) {
-    int cnt = 0;
-#pragma unroll 2
-    for (int i = w0 + lane; i < w1; i += 32) cnt += key(i) == t;
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
-    if (lane == 0) warp_cnt[0][warp] = cnt;
-    __syncthreads();
-    const int v = warp_cnt[0][lane];
-    eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
-    if (C > 1) {
-      if (warp == 0) {
-        const int all = __reduce_add_sync(0xffffffffu, v);
-        if (lane == 0) cta_cnt[0] = all;
-      }
-      cluster.sync();
-      const int x = lane < rank ? *cluster.map_shared_rank(&cta_cnt[0], lane < rank ? lane : rank) : 0;
-      eq_before += __reduce_add_sync(0xffffffffu, x);
+  // ---- ranks. Entries above t stay, those below go, of the equal ones the first ``need`` stay (in the slots'
+  // order, so those in slots below m first). With the counts x, y of entries below t in slots below m and above t in
+  // slots from m on, z, w of equal ones in slots below m and from m on, a stretch of slots with ``before`` equal
+  // entries ahead of it has
+  auto ranked = [&](int4 c4, int before) {  // (holes, movers)
+    const int kept = max(0, min(need - before, c4.z + c4.w)), low = min(kept, c4.z);
+    return make_int2(c4.x + c4.z - low, c4.y + kept - low);
+  };
+  auto scan_equal = [&](int4 c4) {  // equal entries of the lanes below
+    int x = c4.z + c4.w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    return x - c4.z - c4.w;
+  };
+  auto sum4 = [&](int4 c4) {
+    return make_int4(__reduce_add_sync(0xffffffffu, c4.x), __reduce_add_sync(0xffffffffu, c4.y),
+                     __reduce_add_sync(0xffffffffu, c4.z), __reduce_add_sync(0xffffffffu, c4.w));
+  };
+  int4 cnt = make_int4(0, 0, 0, 0);
+#pragma unroll 2
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = key(i);
+    const bool low = lo + i < m;
+    cnt.x += k < t && low;
+    cnt.y += k > t && !low;
+    cnt.z += k == t && low;
+    cnt.w += k == t && !low;
+  }
+  cnt = sum4(cnt);
+  if (lane == 0) warp_cnt[warp] = cnt;
+  __syncthreads();
+  const int4 of_warp = warp_cnt[lane];
+  int eq_before = 0, holes = 0, movers = 0, all;
+  {
+    const int4 mine4 = sum4(of_warp);
+    if (C > 1) {
+      if (tid == 0) cta_cnt = mine4;
+      cluster.sync();
+      const int4 of_cta = *cluster.map_shared_rank(&cta_cnt, lane < C ? lane : rank);
+      const int4 c4 = lane < C ? of_cta : make_int4(0, 0, 0, 0);
+      const int before = scan_equal(c4);
+      const int2 r = ranked(c4, before);
+      eq_before = __shfl_sync(0xffffffffu, before, rank);
+      holes = __reduce_add_sync(0xffffffffu, lane < rank ? r.x : 0);
+      movers = __reduce_add_sync(0xffffffffu, lane < rank ? r.y : 0);
+      all = __reduce_add_sync(0xffffffffu, r.y);
+    } else {
+      all = ranked(mine4, 0).y;
+    }
+    const int before = eq_before + scan_equal(of_warp);
+    const int2 r = ranked(of_warp, before);
+    eq_before = __shfl_sync(0xffffffffu, before, warp);
+    holes += __reduce_add_sync(0xffffffffu, lane < warp ? r.x : 0);
+    movers += __reduce_add_sync(0xffffffffu, lane < warp ? r.y : 0);
   }
   // whether the entry stays (the whole warp asks for 32 in a row); ``eq`` runs over the equal ones before
+  const bool rank_equal = need < equal;
   const unsigned lower = (1u << lane) - 1u;
   auto stays = [&](int i, int& eq) {
     const uint32_t k = i < w1 ? key(i) : 0u;
@@ -265,38 +303,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     }
     return s;
   };
-  int holes = 0, movers = 0, eq = eq_before;
-#pragma unroll 2
-  for (int i = w0 + lane; i - lane < w1; i += 32) {
-    const bool s = stays(i, eq);
-    holes += i < w1 && !s && lo + i < m;
-    movers += s && lo + i >= m;
-  }
-  holes = __reduce_add_sync(0xffffffffu, holes);
-  movers = __reduce_add_sync(0xffffffffu, movers);
-  if (lane == 0) {
-    warp_cnt[1][warp] = holes;
-    warp_cnt[2][warp] = movers;
-  }
-  __syncthreads();
-  const int vh = warp_cnt[1][lane], vm = warp_cnt[2][lane];
-  int all = __reduce_add_sync(0xffffffffu, vm);
-  holes = __reduce_add_sync(0xffffffffu, lane < warp ? vh : 0);
-  movers = __reduce_add_sync(0xffffffffu, lane < warp ? vm : 0);
-  if (C > 1) {
-    const int all_h = __reduce_add_sync(0xffffffffu, vh);
-    if (tid == 0) {
-      cta_cnt[1] = all_h;
-      cta_cnt[2] = all;
-    }
-    cluster.sync();
-    const int* x = cluster.map_shared_rank(&cta_cnt[0], lane < C ? lane : rank);
-    const int xh = x[1], xm = x[2];
-    holes += __reduce_add_sync(0xffffffffu, lane < rank ? xh : 0);
-    movers += __reduce_add_sync(0xffffffffu, lane < rank ? xm : 0);
-    all = __reduce_add_sync(0xffffffffu, lane < C ? xm : 0);
-  }
-  eq = eq_before;
+  int eq = eq_before;
   const int32_t* table = c.table + (long long)b * c.max_pages;
 #pragma unroll 2
   for (int i = w0 + lane; i - lane < w1; i += 32) {
@@ -355,7 +362,7 @@ struct EvictPlan {
 };
 
 // One CTA for up to 8192 slots (1 x 4112: 9.4 us, with a cluster of 2 11.1; 16 x
-// 8100: 12.1 and with 4 11.8); beyond, clusters of 8 where they fit the SMs at once
+// 8100: 12.1 and with 4 11.8; all figures of this rule from one build); beyond, clusters of 8 where they fit the SMs at once
 // (1 x 16000: 12.3 us, of 2 15.3; 1 x 32000: 13.6, of 4 15.7), else as small as
 // keeps a slice to 8192 slots. The moves are made by the select kernel where a
 // CTA has at most 128 of them and no cluster that starts later reads a length that
