@@ -393,9 +393,16 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
       }
       if (__any_sync(0xffffffffu, ready)) {
         since = tc::global_ns();
-      } else if ((spin & 255) == 0 && (*(volatile int*)&s_abort || tc::global_ns() - since > p.wait_ns)) {
-        if (lane == 0) record_status(p.status, QMOE_ERR_TIMEOUT);
-        break;
+      } else if ((spin & 255) == 0) {
+        // (the lanes read their clocks apart and leave together: one that went on would wait for the others' votes)
+        const bool over = *(volatile int*)&s_abort || tc::global_ns() - since > p.wait_ns;
+        if (__any_sync(0xffffffffu, over)) {
+          if (lane == 0) {
+            record_status(p.status, QMOE_ERR_TIMEOUT);
+            *(volatile int*)&s_abort = 1;
+          }
+          break;
+        }
       }
     }
   }
