@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     w.t = (int)(x - (long long)w.vh * w.nt);
   };
   long long C0 = pa_share(total, blockIdx.x, n_ctas), C1 = pa_share(total, blockIdx.x + 1, n_ctas);
-  if (p.whole_rows && c.n_seqs > 1) {  // (those of one sequence begin at rows already)
+  if (p.whole_rows && (c.n_seqs > 1 || n_ctas < rows)) {  // (one sequence's rows, where each has a CTA, begin there already)
     PaWalk w;
     locate(C0, w);
     C0 -= w.t;

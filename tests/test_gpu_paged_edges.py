@@ -3,12 +3,14 @@ calls. Attention is compared with the plain 64-bit implementation at the toleran
 derived in test_gpu_paged.py.
 """
 
+import math
+
 import pytest
 import torch
 
 from quantized_moe_transformer_gb300 import binding as qb
 from tests import paged_ref as ref
-from tests.test_gpu_paged import handle
+from tests.test_gpu_paged import close_out, handle, score_tol, v_max
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +20,31 @@ def built():
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
     from quantized_moe_transformer_gb300 import build
     build.build()
+
+
+#: one sequence with a table of at most 512 slots: (heads, KV heads, head dim, entries)
+MANY_ROWS = [(160, 160, 64, 100), (153, 153, 128, 100), (153, 153, 128, 3), (152, 152, 64, 40), (1280, 20, 64, 512),
+             (400, 400, 256, 130), (305, 305, 8, 0)]
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heads,kv,hd,n", MANY_ROWS)
+def test_one_short_sequence_with_more_rows_than_sms(heads, kv, hd, n, dtype, accumulate):
+    c, g = ref.cache(50, [n], kv, hd, 64, width=max(2, -(-n // 64)))
+    q = torch.randn(1, heads, hd, generator=g, device="cuda").to(dtype)
+    before = c["weight"].clone()
+    out = torch.full_like(q, math.nan)
+    qb.paged_attention(handle(c), q, out=out, accumulate=accumulate)
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0
+    want, received, bound = ref.attention(q, c["k"], c["v"], c["table"], c["lens"], 64)
+    close_out(out, want, bound, hd, max(v_max(c), 1e-30))
+    if not accumulate:
+        assert torch.equal(c["weight"], before)
+        return
+    tol = received * (2 * score_tol(hd, bound) + (heads // kv + 8) * 2.0 ** -24) + (before.double() + received) * 2.0 ** -24
+    assert bool(((c["weight"].double() - before.double() - received).abs() <= tol + 1e-30).all())
 
 
 @pytest.mark.parametrize("n", [1000, 40000])
