@@ -7,6 +7,7 @@ missing or the device is not a GB300, the calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -120,6 +121,13 @@ def _ptr(t: torch.Tensor | None):
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _allocating(stream):
+    """Where a call allocates its own tensors: under the stream that it runs on. A
+    workspace is released at the call's return, and its bytes then go to that
+    stream's next work, not to work beside it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 class MoeLayer:
@@ -523,7 +531,8 @@ def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slo
     if q is not None:
         heads = q.shape[1]
         if q_out is None:
-            q_out = torch.empty_like(q)
+            with _allocating(stream):
+                q_out = torch.empty_like(q)
         q_shape = (rows, heads, cache.head_dim)
         qp, qo = _need(q, "q", q_shape, dtype), _need(q_out, "q_out", q_shape, dtype)
     elif q_out is not None:
@@ -553,10 +562,10 @@ def paged_attention(cache: PagedCache, q, out=None, scale: float = 0.0, accumula
         raise QmoeError(f"q has type {dtype}, not fp32 or bf16")
     heads = q.shape[1]
     shape = (cache.n_seqs, heads, cache.head_dim)
-    if out is None:
-        out = torch.empty_like(q)
-    if ws is None:
-        ws = paged_attention_workspace(cache, heads, accumulate)
+    if out is None or ws is None:
+        with _allocating(stream):
+            out = torch.empty_like(q) if out is None else out
+            ws = paged_attention_workspace(cache, heads, accumulate) if ws is None else ws
     _check(_paged_lib().qmoe_paged_attention(
         cache._desc_ref, _need(q, "q", shape, dtype), _need(out, "out", shape, dtype), _DTYPE[dtype], heads, scale,
         int(accumulate), _need_ws(ws), ws.numel(), _raw_stream(stream, cache.device)))
@@ -581,7 +590,8 @@ def cache_evict(cache: PagedCache, next_pos, budget: int, recent: int = 0, lens_
         raise QmoeError("the cache has no weights to evict by")
     per_slot = (cache.n_seqs, cache.n_kv, cache.slots)
     if ws is None:
-        ws = cache_evict_workspace(cache)
+        with _allocating(stream):
+            ws = cache_evict_workspace(cache)
     _check(_paged_lib().qmoe_cache_evict(
         cache._desc_ref, None if next_pos is None else _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),
         budget, recent, _need(lens_out, "lens_out", (cache.n_seqs,), torch.int32),
@@ -603,10 +613,10 @@ def block_decode_paged(block: Block, cache: PagedCache, X, next_pos, out=None, a
     and value become the sequence's next entry (at position ``next_pos``), its
     query attends to every entry; the lengths grow by one."""
     shape = (cache.n_seqs, block.H)
-    if out is None:
-        out = torch.empty_like(X)
-    if ws is None:
-        ws = block_decode_paged_workspace(block, cache, accumulate)
+    if out is None or ws is None:
+        with _allocating(stream):
+            out = torch.empty_like(X) if out is None else out
+            ws = block_decode_paged_workspace(block, cache, accumulate) if ws is None else ws
     _check(_paged_lib().qmoe_block_decode_paged(
         ctypes.byref(block.desc), cache._desc_ref, _need(X, "X", shape, torch.float32),
         _need(out, "out", shape, torch.float32), _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from quantized_moe_transformer_gb300 import binding as qb
+from quantized_moe_transformer_gb300 import inputs
 from tests import paged_ref as ref
 from tests.test_gpu_paged import close_out, handle, score_tol, v_max
 
@@ -45,6 +46,46 @@ def test_one_short_sequence_with_more_rows_than_sms(heads, kv, hd, n, dtype, acc
         return
     tol = received * (2 * score_tol(hd, bound) + (heads // kv + 8) * 2.0 ** -24) + (before.double() + received) * 2.0 ** -24
     assert bool(((c["weight"].double() - before.double() - received).abs() <= tol + 1e-30).all())
+
+
+@pytest.fixture
+def allocations(monkeypatch):
+    """The stream that is current at each allocation."""
+    seen = []
+    for name in ("empty", "empty_like"):
+        plain = getattr(torch, name)
+
+        def noted(*a, plain=plain, **kw):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return plain(*a, **kw)
+
+        monkeypatch.setattr(torch, name, noted)
+    return seen
+
+
+def test_temporaries_of_a_call_on_another_stream(allocations):
+    """Outputs and workspaces that a call allocates belong to the stream it runs
+    on: released at its return, their bytes go to that stream's next calls, not to
+    work that runs beside it."""
+    c, g = ref.cache(52, [300, 20], 2, 128, 64)
+    h = handle(c)
+    q = torch.randn(2, 16, 128, generator=g, device="cuda")
+    rows = torch.randn(2, 2, 128, generator=g, device="cuda")
+    pos = torch.tensor([300, 20], dtype=torch.int32, device="cuda")
+    arr = inputs.block(5, ctx=64)
+    blk = qb.Block.from_arrays(arr, 8)
+    X = torch.from_numpy(inputs.hidden(7, 2, 2048)).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    allocations.clear()
+    qb.paged_append(h, rows, rows, pos, q=q, rope_theta=1e4, stream=side)
+    qb.paged_attention(h, q, accumulate=True, stream=side)
+    qb.block_decode_paged(blk, h, X, pos + 1, accumulate=True, stream=side)
+    qb.cache_evict(h, pos + 2, 200, 10, stream=side)
+    side.synchronize()
+    assert qb.query_status() == 0
+    assert len(allocations) >= 6
+    assert set(allocations) == {side.cuda_stream}
 
 
 @pytest.mark.parametrize("n", [1000, 40000])
