@@ -174,11 +174,12 @@ def moe_route(X: torch.Tensor, Wr: torch.Tensor, k: int, ws: torch.Tensor | None
     """ids [T,k] int32 and w [T,k] fp32 of rows X [T,H] under router Wr [H,E]."""
     T, H = X.shape
     E = Wr.shape[1]
-    ids = torch.empty((T, k), dtype=torch.int32, device=X.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=X.device)
     need = int(lib().qmoe_moe_route_workspace_bytes(T, H, E, k))
-    if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=X.device)
+    with _allocating(stream):
+        ids = torch.empty((T, k), dtype=torch.int32, device=X.device)
+        w = torch.empty((T, k), dtype=torch.float32, device=X.device)
+        if ws is None:
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=X.device)
     _check(lib().qmoe_moe_route(_ptr(X), _ptr(Wr), T, H, E, k, _ptr(ids), _ptr(w), _ptr(ws),
                                 ws.numel(), _stream(stream)))
     return ids, w
@@ -190,10 +191,10 @@ def moe_forward(layer: MoeLayer, X: torch.Tensor, R: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """out = R + shared(X) + sum_s w_s expert_{ids_s}(X), enqueued on ``stream``."""
     T = X.shape[0]
-    if out is None:
-        out = torch.empty_like(X)
-    if ws is None:
-        ws = layer.workspace(T)
+    if out is None or ws is None:
+        with _allocating(stream):
+            out = torch.empty_like(X) if out is None else out
+            ws = layer.workspace(T) if ws is None else ws
     _check(lib().qmoe_moe_forward(ctypes.byref(layer.desc), _ptr(X), _ptr(R), _ptr(ids), _ptr(w),
                                   _ptr(out), T, _ptr(ws), ws.numel(), _stream(stream)))
     return out
@@ -245,7 +246,8 @@ def moe_forward_host(layer: MoeLayer, X: torch.Tensor, R: torch.Tensor | None = 
         out = torch.empty_like(X)
     if ws is None:
         n = int(lib().qmoe_moe_forward_host_workspace_bytes(ctypes.byref(layer.desc), T))
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=layer.Wr.device)
+        with _allocating(stream):
+            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=layer.Wr.device)
     for t in (X, R, out):
         if t is not None and (t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous()):
             raise QmoeError("moe_forward_host takes contiguous fp32 host tensors")
@@ -294,7 +296,8 @@ def moe_forward_noalloc(layer: MoeLayer, X: torch.Tensor, R: torch.Tensor | None
     workspace (for callers that cannot allocate); raises for T beyond it."""
     T = X.shape[0]
     if out is None:
-        out = torch.empty_like(X)
+        with _allocating(stream):
+            out = torch.empty_like(X)
     _check(lib().qmoe_moe_forward_noalloc(ctypes.byref(layer.desc), _ptr(X), _ptr(R), _ptr(out), T,
                                           _stream(stream)))
     return out
@@ -365,7 +368,8 @@ def cache_from_bits(bits: np.ndarray, device="cuda") -> torch.Tensor:
 def rmsnorm(X: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, out=None, stream=None):
     T, H = X.shape
     if out is None:
-        out = torch.empty_like(X)
+        with _allocating(stream):
+            out = torch.empty_like(X)
     _check(_block_lib().qmoe_rmsnorm(_ptr(X), _ptr(gamma), eps, _ptr(out), T, H, _stream(stream)))
     return out
 
@@ -374,10 +378,10 @@ def attn_forward(block: Block, X: torch.Tensor, R: torch.Tensor | None, k_cache:
                  v_cache: torch.Tensor, pos0: int, out=None, ws=None, stream=None):
     """out = R + O(attention(...)) for rows at positions pos0..pos0+T-1 (R may be None)."""
     T = X.shape[0]
-    if out is None:
-        out = torch.empty_like(X)
-    if ws is None:
-        ws = block.attn_workspace(T, pos0)
+    if out is None or ws is None:
+        with _allocating(stream):
+            out = torch.empty_like(X) if out is None else out
+            ws = block.attn_workspace(T, pos0) if ws is None else ws
     _check(_block_lib().qmoe_attn_forward(ctypes.byref(block.desc), _ptr(X), _ptr(R), _ptr(out), T,
                                           _ptr(k_cache), _ptr(v_cache), pos0, k_cache.shape[0], _ptr(ws),
                                           ws.numel(), _stream(stream)))
@@ -387,10 +391,10 @@ def attn_forward(block: Block, X: torch.Tensor, R: torch.Tensor | None, k_cache:
 def block_forward(block: Block, X: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pos0: int,
                   out=None, ws=None, stream=None):
     T = X.shape[0]
-    if out is None:
-        out = torch.empty_like(X)
-    if ws is None:
-        ws = block.workspace(T, pos0)
+    if out is None or ws is None:
+        with _allocating(stream):
+            out = torch.empty_like(X) if out is None else out
+            ws = block.workspace(T, pos0) if ws is None else ws
     _check(_block_lib().qmoe_block_forward(ctypes.byref(block.desc), _ptr(X), _ptr(out), T, _ptr(k_cache),
                                            _ptr(v_cache), pos0, k_cache.shape[0], _ptr(ws), ws.numel(),
                                            _stream(stream)))
