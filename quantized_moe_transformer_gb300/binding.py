@@ -436,14 +436,13 @@ def _paged_lib():
     return _paged
 
 
-def _need(t, what, shape, dtype):
-    """The address of one tensor argument, checked: on a CUDA device, contiguous,
-    of this shape and type (one line where all is well: it runs for each
-    argument of each call)."""
-    if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+def _need(t, what, shape, dtype, device):
+    """The address of one tensor argument, checked: on this CUDA device,
+    contiguous, of this shape and type (one line where all is well: it runs for
+    each argument of each call)."""
+    if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
-    if not t.is_cuda:
-        raise QmoeError(f"{what} must be on a CUDA device")
+    _need_device(t, what, device)
     if t.dtype is not dtype:
         raise QmoeError(f"{what} has type {t.dtype}, not {dtype}")
     if t.shape != shape:
@@ -451,9 +450,17 @@ def _need(t, what, shape, dtype):
     raise QmoeError(f"{what} must be contiguous")
 
 
-def _need_ws(ws):
+def _need_device(t, what, device):
+    if not t.is_cuda:
+        raise QmoeError(f"{what} must be on a CUDA device")
+    if t.get_device() != device:
+        raise QmoeError(f"{what} is on cuda:{t.get_device()}, the cache on cuda:{device}")
+
+
+def _need_ws(ws, device):
     if not ws.is_cuda or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise QmoeError("the workspace must be a contiguous uint8 tensor on a CUDA device")
+    _need_device(ws, "the workspace", device)
     return ws.data_ptr()
 
 
@@ -474,6 +481,9 @@ class PagedCache:
                 raise QmoeError(f"{what} must be on a CUDA device")
             if t.dtype != torch.bfloat16:
                 raise QmoeError(f"{what} has type {t.dtype}, not {torch.bfloat16}")
+        self.device = dev = k.get_device()  # the calls run on this device
+        self.one_of_many = torch.cuda.device_count() > 1
+        _need_device(v, "v", dev)
         self.n_pages, self.page, self.n_kv, self.head_dim = k.shape
         if table.dim() != 2:
             raise QmoeError("the table must be [sequences][pages of a sequence]")
@@ -483,12 +493,11 @@ class PagedCache:
         self.k, self.v, self.table, self.lens, self.weight, self.pos = k, v, table, lens, weight, pos
         self._desc = PagedCacheDesc(
             self.n_seqs, self.n_kv, self.head_dim, self.page, self.n_pages, self.max_pages, k.stride(0), k.stride(1),
-            k.stride(2), k.data_ptr(), v.data_ptr(), _need(table, "table", table.shape, torch.int32),
-            _need(lens, "lens", (self.n_seqs,), torch.int32),
-            None if weight is None else _need(weight, "weight", per_slot, torch.float32),
-            None if pos is None else _need(pos, "pos", per_slot, torch.int32))
+            k.stride(2), k.data_ptr(), v.data_ptr(), _need(table, "table", table.shape, torch.int32, dev),
+            _need(lens, "lens", (self.n_seqs,), torch.int32, dev),
+            None if weight is None else _need(weight, "weight", per_slot, torch.float32, dev),
+            None if pos is None else _need(pos, "pos", per_slot, torch.int32, dev))
         self._desc_ref = ctypes.byref(self._desc)
-        self.device = k.device.index  # the calls' default stream is this device's current one
 
     @classmethod
     def empty(cls, n_seqs, max_len, n_kv, head_dim, page=64, n_pages=None, device="cuda"):
@@ -511,11 +520,18 @@ class PagedCache:
         return self._desc
 
 
-def _raw_stream(stream, device):
+def _raw_stream(stream, cache):
     """The stream's handle; without one, that of the device's current stream (by
     PyTorch's accessor of the bare handle: 0.1 us against 2.9 us through a
-    torch.cuda.Stream object on the GB300's host)."""
+    torch.cuda.Stream object on the GB300's host). The library launches on the
+    current device, which has to be the cache's (asked where there is another:
+    0.4 us)."""
+    device = cache.device
+    if cache.one_of_many and torch._C._cuda_getDevice() != device:
+        raise QmoeError(f"the cache is on cuda:{device}, the current device is cuda:{torch._C._cuda_getDevice()}")
     if stream is not None:
+        if stream.device_index != device:
+            raise QmoeError(f"the stream is of cuda:{stream.device_index}, the cache on cuda:{device}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device)
 
@@ -527,7 +543,7 @@ def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slo
     of sequence n; a slot below 0: not cached), at position ``pos[n]``, keys (and
     the queries q [rows][heads][hd], returned) rotated when ``rope_theta`` > 0."""
     rows = k.shape[0]
-    dtype = k.dtype
+    dtype, dev = k.dtype, cache.device
     if dtype not in _DTYPE:
         raise QmoeError(f"k has type {dtype}, not fp32 or bf16")
     kv_shape = (rows, cache.n_kv, cache.head_dim)
@@ -538,16 +554,16 @@ def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slo
             with _allocating(stream):
                 q_out = torch.empty_like(q)
         q_shape = (rows, heads, cache.head_dim)
-        qp, qo = _need(q, "q", q_shape, dtype), _need(q_out, "q_out", q_shape, dtype)
+        qp, qo = _need(q, "q", q_shape, dtype, dev), _need(q_out, "q_out", q_shape, dtype, dev)
     elif q_out is not None:
         raise QmoeError("q_out without q")
     else:
         qp = qo = None
     _check(_paged_lib().qmoe_paged_append(
-        cache._desc_ref, qp, qo, _need(k, "k", kv_shape, dtype), _need(v, "v", kv_shape, dtype), _DTYPE[dtype],
-        None if seq is None else _need(seq, "seq", (rows,), torch.int32),
-        None if slot is None else _need(slot, "slot", (rows,), torch.int32), _need(pos, "pos", (rows,), torch.int32),
-        rows, heads, rope_theta, _raw_stream(stream, cache.device)))
+        cache._desc_ref, qp, qo, _need(k, "k", kv_shape, dtype, dev), _need(v, "v", kv_shape, dtype, dev), _DTYPE[dtype],
+        None if seq is None else _need(seq, "seq", (rows,), torch.int32, dev),
+        None if slot is None else _need(slot, "slot", (rows,), torch.int32, dev),
+        _need(pos, "pos", (rows,), torch.int32, dev), rows, heads, rope_theta, _raw_stream(stream, cache)))
     return q_out
 
 
@@ -570,9 +586,10 @@ def paged_attention(cache: PagedCache, q, out=None, scale: float = 0.0, accumula
         with _allocating(stream):
             out = torch.empty_like(q) if out is None else out
             ws = paged_attention_workspace(cache, heads, accumulate) if ws is None else ws
+    dev = cache.device
     _check(_paged_lib().qmoe_paged_attention(
-        cache._desc_ref, _need(q, "q", shape, dtype), _need(out, "out", shape, dtype), _DTYPE[dtype], heads, scale,
-        int(accumulate), _need_ws(ws), ws.numel(), _raw_stream(stream, cache.device)))
+        cache._desc_ref, _need(q, "q", shape, dtype, dev), _need(out, "out", shape, dtype, dev), _DTYPE[dtype], heads,
+        scale, int(accumulate), _need_ws(ws, dev), ws.numel(), _raw_stream(stream, cache)))
     return out
 
 
@@ -592,16 +609,16 @@ def cache_evict(cache: PagedCache, next_pos, budget: int, recent: int = 0, lens_
     pos_out = cache.pos if pos_out is None else pos_out
     if weight_out is None:
         raise QmoeError("the cache has no weights to evict by")
-    per_slot = (cache.n_seqs, cache.n_kv, cache.slots)
+    per_slot, dev = (cache.n_seqs, cache.n_kv, cache.slots), cache.device
     if ws is None:
         with _allocating(stream):
             ws = cache_evict_workspace(cache)
     _check(_paged_lib().qmoe_cache_evict(
-        cache._desc_ref, None if next_pos is None else _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),
-        budget, recent, _need(lens_out, "lens_out", (cache.n_seqs,), torch.int32),
-        _need(weight_out, "weight_out", per_slot, torch.float32),
-        None if pos_out is None else _need(pos_out, "pos_out", per_slot, torch.int32), _need_ws(ws), ws.numel(),
-        _raw_stream(stream, cache.device)))
+        cache._desc_ref, None if next_pos is None else _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32, dev),
+        budget, recent, _need(lens_out, "lens_out", (cache.n_seqs,), torch.int32, dev),
+        _need(weight_out, "weight_out", per_slot, torch.float32, dev),
+        None if pos_out is None else _need(pos_out, "pos_out", per_slot, torch.int32, dev), _need_ws(ws, dev),
+        ws.numel(), _raw_stream(stream, cache)))
     return lens_out, weight_out, pos_out
 
 
@@ -621,8 +638,10 @@ def block_decode_paged(block: Block, cache: PagedCache, X, next_pos, out=None, a
         with _allocating(stream):
             out = torch.empty_like(X) if out is None else out
             ws = block_decode_paged_workspace(block, cache, accumulate) if ws is None else ws
+    dev = cache.device
+    _need_device(block.Wq, "the block", dev)
     _check(_paged_lib().qmoe_block_decode_paged(
-        ctypes.byref(block.desc), cache._desc_ref, _need(X, "X", shape, torch.float32),
-        _need(out, "out", shape, torch.float32), _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32),
-        int(accumulate), _need_ws(ws), ws.numel(), _raw_stream(stream, cache.device)))
+        ctypes.byref(block.desc), cache._desc_ref, _need(X, "X", shape, torch.float32, dev),
+        _need(out, "out", shape, torch.float32, dev), _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32, dev),
+        int(accumulate), _need_ws(ws, dev), ws.numel(), _raw_stream(stream, cache)))
     return out
