@@ -109,3 +109,32 @@ def test_withheld_copy_of_a_short_and_a_long_row(n):
     torch.cuda.synchronize()
     assert qb.query_status() == 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n", [1000, 40000])
+def test_weights_survive_a_wait_that_runs_out(n):
+    """A call that gives up reports it and leaves the accumulated weights alone (an
+    infinite weight would hold its entry through every later eviction); the next
+    call is right."""
+    c, g = ref.cache(53, [n], 2, 128, 64)
+    q = torch.randn(1, 16, 128, generator=g, device="cuda")
+    h = handle(c)
+    ws = qb.paged_attention_workspace(h, 16, True)
+    before = c["weight"].clone()
+    want = qb.paged_attention(h, q, accumulate=True, ws=ws)
+    want_w = c["weight"].clone()
+    c["weight"].copy_(before)
+    ws.fill_(0x7F)  # whatever an earlier call left there
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0
+    qb.test_inject("paged_copy", 2000)
+    try:
+        qb.paged_attention(h, q, accumulate=True, ws=ws)
+        assert qb.query_status() == -7
+    finally:
+        qb.test_inject("none")
+    assert torch.equal(c["weight"], before)
+    got = qb.paged_attention(h, q, accumulate=True, ws=ws)
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0
+    assert torch.equal(got, want) and torch.equal(c["weight"], want_w)
