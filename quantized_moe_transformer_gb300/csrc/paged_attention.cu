@@ -849,18 +849,21 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const PaJoin p) 
 // L2: 64 sequences of up to 8191 entries, 25 MB in 8 us, with its start. Where one
 // of the ``ctas`` CTAs gave up, scores and denominators are missing and no weight
 // is touched (asking costs 0.4 us; behind the loads instead of ahead of them 0.5).
-__global__ void __launch_bounds__(256) paged_weight_kernel(const PagedView c, const float* __restrict__ scores,
-                                                           const float* __restrict__ lse, int n_heads, int group,
-                                                           const int4* desc, int ctas) {
+// (Plain pointers: the kernel that writes scores and lse still runs when this one starts.)
+__global__ void __launch_bounds__(256) paged_weight_kernel(const PagedView c, const float* scores, const float* lse,
+                                                           int n_heads, int group, const int4* desc, int ctas) {
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int pair = blockIdx.x, b = pair / c.n_kv, g = pair % c.n_kv;
   const int n = paged_len(c, b);
+  const long long base = (long long)pair * paged_slots(c);
+  const float* ls = lse + (long long)b * n_heads + (long long)g * group;
+  float ls8[8];  // (the compiler cannot keep them: a store might change them)
+#pragma unroll
+  for (int h = 0; h < 8; ++h) ls8[h] = group == 8 ? ls[h] : 0.f;
   int gave_up = 0;
   for (int i = threadIdx.x; i < ctas; i += 256) gave_up |= desc[i].w;
   if (__syncthreads_or(gave_up)) return;
-  const long long base = (long long)pair * paged_slots(c);
-  const float* ls = lse + (long long)b * n_heads + (long long)g * group;
   constexpr int U = 4;  // slots of a thread at a time: all loads ahead of the stores
   for (int j0 = blockIdx.y * 256 * U + threadIdx.x; j0 < n; j0 += gridDim.y * 256 * U) {
     float w[U], old[U];
@@ -876,8 +879,8 @@ __global__ void __launch_bounds__(256) paged_weight_kernel(const PagedView c, co
       }
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        w[k] = ((exp2f(x[k].x - ls[0]) + exp2f(x[k].y - ls[1])) + (exp2f(x[k].z - ls[2]) + exp2f(x[k].w - ls[3]))) +
-               ((exp2f(y[k].x - ls[4]) + exp2f(y[k].y - ls[5])) + (exp2f(y[k].z - ls[6]) + exp2f(y[k].w - ls[7])));
+        w[k] = ((exp2f(x[k].x - ls8[0]) + exp2f(x[k].y - ls8[1])) + (exp2f(x[k].z - ls8[2]) + exp2f(x[k].w - ls8[3]))) +
+               ((exp2f(y[k].x - ls8[4]) + exp2f(y[k].y - ls8[5])) + (exp2f(y[k].z - ls8[6]) + exp2f(y[k].w - ls8[7])));
     } else {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
