@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
       const int row = n0 + tid;
       seq = a.seq ? a.seq[row] : row;
       const bool known = seq >= 0 && seq < c.n_seqs;
-      slot = a.slot ? a.slot[row] : known ? c.lens[seq] : 0;
+      slot = a.slot ? a.slot[row] : known ? paged_len(c, seq) : 0;
       const bool padding = a.slot && slot < 0;
       if (known && slot >= 0 && slot < paged_slots(c)) o = paged_offset(c, seq, slot);
       if (o < 0 && !padding) record_status(a.status, QMOE_ERR_DEVICE_ARG);

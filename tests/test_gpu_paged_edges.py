@@ -48,6 +48,23 @@ def test_one_short_sequence_with_more_rows_than_sms(heads, kv, hd, n, dtype, acc
     assert bool(((c["weight"].double() - before.double() - received).abs() <= tol + 1e-30).all())
 
 
+def test_append_to_a_length_below_zero():
+    """A length below zero is taken as zero: the next entry is slot 0."""
+    c, g = ref.cache(51, [32, 32, 32], 2, 128, 16)
+    c["lens"].copy_(torch.tensor([-5, 3, -(1 << 31)]))
+    row = torch.randn(3, 2, 128, generator=g, device="cuda")
+    pos = torch.tensor([7, 8, 9], dtype=torch.int32, device="cuda")
+    qb.paged_append(handle(c), row, row, pos)
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0
+    assert c["lens"].tolist() == [1, 4, 1]
+    for b, slot in ((0, 0), (1, 3), (2, 0)):
+        page = int(c["table"][b, 0])
+        assert torch.equal(c["k"][page, slot], row[b].to(torch.bfloat16))
+        assert torch.equal(c["v"][page, slot], row[b].to(torch.bfloat16))
+        assert c["pos"][b, :, slot].tolist() == [7 + b] * 2 and c["weight"][b, :, slot].tolist() == [0.0] * 2
+
+
 @pytest.fixture
 def allocations(monkeypatch):
     """The stream that is current at each allocation."""
