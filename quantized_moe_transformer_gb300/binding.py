@@ -464,6 +464,14 @@ def _need_ws(ws, device):
     return ws.data_ptr()
 
 
+def _size(t, dim, what):
+    """One size of an argument whose other sizes are checked with its type."""
+    try:
+        return t.shape[dim]
+    except IndexError:
+        raise QmoeError(f"{what} has shape {tuple(t.shape)}, not three dimensions") from None
+
+
 class PagedCache:
     """Keys and values of many sequences in pages, and what eviction goes by.
 
@@ -542,14 +550,14 @@ def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slo
     slot ``slot[n]`` of sequence ``seq[n]`` (both None: row n is the next entry
     of sequence n; a slot below 0: not cached), at position ``pos[n]``, keys (and
     the queries q [rows][heads][hd], returned) rotated when ``rope_theta`` > 0."""
-    rows = k.shape[0]
+    rows = _size(k, 0, "k")
     dtype, dev = k.dtype, cache.device
     if dtype not in _DTYPE:
         raise QmoeError(f"k has type {dtype}, not fp32 or bf16")
     kv_shape = (rows, cache.n_kv, cache.head_dim)
     heads = 0
     if q is not None:
-        heads = q.shape[1]
+        heads = _size(q, 1, "q")
         if q_out is None:
             with _allocating(stream):
                 q_out = torch.empty_like(q)
@@ -580,7 +588,7 @@ def paged_attention(cache: PagedCache, q, out=None, scale: float = 0.0, accumula
     dtype = q.dtype
     if dtype not in _DTYPE:
         raise QmoeError(f"q has type {dtype}, not fp32 or bf16")
-    heads = q.shape[1]
+    heads = _size(q, 1, "q")
     shape = (cache.n_seqs, heads, cache.head_dim)
     if out is None or ws is None:
         with _allocating(stream):

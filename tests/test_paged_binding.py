@@ -119,3 +119,13 @@ def test_a_stream_of_another_device(fake, call):
     with pytest.raises(qb.QmoeError, match="stream is of cuda:0"):
         run(call, {name: On(t) for name, t in arguments(call).items()}, SimpleNamespace(device_index=0, cuda_stream=5))
     assert not fake.calls
+
+
+@pytest.mark.parametrize("call,name", [("append", "k"), ("append", "q"), ("attend", "q")])
+@pytest.mark.parametrize("shape", [(), (3,), (3, 8), (3, 8, 64, 1)])
+def test_rows_of_another_rank(fake, call, name, shape):
+    a = {n: On(t) for n, t in arguments(call).items()}
+    a[name] = On(torch.zeros(shape))
+    with pytest.raises(qb.QmoeError, match="has shape"):
+        run(call, a)
+    assert not fake.calls
