@@ -5,13 +5,16 @@ derived in test_gpu_paged.py.
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
 from quantized_moe_transformer_gb300 import binding as qb
 from quantized_moe_transformer_gb300 import inputs
 from tests import paged_ref as ref
+from tests.parity import TOL_TC, assert_close
 from tests.test_gpu_paged import close_out, handle, score_tol, v_max
+from tests.test_gpu_paged_block import MANY, filled
 
 pytestmark = pytest.mark.gpu
 
@@ -155,3 +158,67 @@ def test_weights_survive_a_wait_that_runs_out(n):
     torch.cuda.synchronize()
     assert qb.query_status() == 0
     assert torch.equal(got, want) and torch.equal(c["weight"], want_w)
+
+
+# ---------------------------------------------------------------- the block
+
+@pytest.fixture(scope="module")
+def quiet():
+    """A block whose scores are a few units (gains of 1/32 ahead of the
+    projections, where the seeded weights' scores reach thousands), once with its
+    experts and once with experts that give zero, whose output is the attention
+    branch and the residual alone."""
+    arr = inputs.block(5, ctx=1024)
+    arr["g1"] = arr["g1"] / np.float32(32)
+    whole = qb.Block.from_arrays(arr, 8)
+    moe = dict(arr["moe"])
+    for name in ("Wd", "Sd"):
+        moe[name] = moe[name].copy()
+        moe[name][..., :4] = 0  # the super-blocks' scale and minimum
+    return arr, whole, qb.Block.from_arrays({**arr, "moe": moe}, 8)
+
+
+@pytest.mark.parametrize("threshold", [None, 1 << 20])
+def test_attention_branch_of_every_row(oracle, quiet, threshold):
+    """20 sequences at once, on the tensor-core projections (the default threshold)
+    and on the fp32 ones: every row's attention branch equals the oracle's for that
+    sequence alone to the tensor-core tolerance of its own largest value."""
+    arr, _, attn_only = quiet
+    B = len(MANY)
+    old = qb.get_gemm_threshold()
+    assert B > old
+    if threshold is not None:
+        qb.set_gemm_threshold(threshold)
+    try:
+        cache, _ = filled(arr, MANY)
+        X = inputs.hidden(60, B, 2048)
+        pos = torch.tensor(MANY, dtype=torch.int32, device="cuda")
+        out = qb.block_decode_paged(attn_only, cache, torch.from_numpy(X).cuda(), pos).cpu().numpy()
+    finally:
+        qb.set_gemm_threshold(old)
+    assert qb.query_status() == 0
+    for b, n in enumerate(MANY):
+        kc, vc = (oracle.bf16_bits_to_f64(np.roll(arr[name], b, axis=0)) for name in ("k_cache", "v_cache"))
+        want = X[b:b + 1] + oracle.attn_sublayer(X[b:b + 1], arr, n, kc, vc)
+        assert_close(out[b:b + 1], want, TOL_TC)
+
+
+@pytest.mark.parametrize("threshold", [None, 1 << 20])
+def test_experts_follow_the_attention_branch(quiet, threshold):
+    """The whole block equals norm and experts, by their own calls, on the attention
+    branch's rows: the same kernels, so the same bits."""
+    arr, whole, attn_only = quiet
+    X = torch.from_numpy(inputs.hidden(61, len(MANY), 2048)).cuda()
+    pos = torch.tensor(MANY, dtype=torch.int32, device="cuda")
+    old = qb.get_gemm_threshold()
+    if threshold is not None:
+        qb.set_gemm_threshold(threshold)
+    try:
+        h1 = qb.block_decode_paged(attn_only, filled(arr, MANY)[0], X, pos)
+        out = qb.block_decode_paged(whole, filled(arr, MANY)[0], X, pos)
+        r2 = qb.rmsnorm(h1, whole.g2)
+        want = qb.moe_forward(whole.moe, r2, R=h1)
+    finally:
+        qb.set_gemm_threshold(old)
+    assert qb.query_status() == 0
+    assert torch.equal(out, want)
