@@ -369,6 +369,8 @@ int qmoe_block_forward(const qmoe_block_desc *b, const float *X, float *out, int
  *              heads evict apart, so a slot's entries differ between them.
  * An entry's slot is not its position once something was evicted; keys carry
  * their rotation with them, and attention does not depend on the slots' order.
+ * The calls size grids and workspaces by the table's width, not by the lengths:
+ * a table much wider than its longest sequence costs time.
  */
 typedef enum { QMOE_F32 = 0, QMOE_BF16 = 1 } qmoe_dtype;
 
@@ -391,10 +393,11 @@ typedef struct {
  *   q, q_out [n_rows][n_heads][hd] (q_out may be q), or both NULL; k, v
  *   [n_rows][n_kv][hd]; all four of type dtype (qmoe_dtype).
  *   rope_theta > 0: rot turns pairs (i, i + hd/2) by pos * theta^(-2i/hd) (the
- *   angle in double); 0: rot leaves the values as they are.
+ *   angle in double, its sine and cosine in fp32, to 2^-20); 0: rot leaves the
+ *   values as they are.
  *   seq, slot, pos [n_rows] int32. seq and slot NULL: n_rows == n_seqs, row n is
- *   the next entry of sequence n (slot lens[n]). slot < 0: a padding row, which
- *   is not cached (its q is still turned). Two rows of one call must not have the
+ *   the next entry of sequence n (slot lens[n], 0 below 0). slot < 0: a padding
+ *   row, which is not cached (its q is still turned). Two rows of one call must not have the
  *   same (seq, slot). A seq or slot out of range is recorded as
  *   QMOE_ERR_DEVICE_ARG and its row is not cached.
  */
@@ -408,13 +411,17 @@ int qmoe_paged_append(const qmoe_paged_cache *c, const void *q, void *q_out, con
  *   s_j = scale * q . k_j,  p = softmax(s),  out = sum_j p_j v_j,
  * with accumulate != 0 also weight[b][g][j] += sum over the heads h of g of p_j.
  *   q, out [n_seqs][n_heads][hd] of type dtype (fp32 rows are taken with all
- *   their bits, bf16 rows are exact as they are); out may be q. A sequence
- *   without entries gives zeros. What the cache holds outside the entries is
- *   never used (it may be NaN).
+ *   their bits, bf16 rows are exact as they are); out may be q. Probabilities and
+ *   sums are fp32 for both types; bf16 rows are rounded once. A sequence without
+ *   entries gives zeros. What the cache holds outside the entries is never used
+ *   (it may be NaN); queries and entries are finite (an infinity may come out as
+ *   NaN).
  *   scale: finite; 0 takes 1 / sqrt(head_dim).
  *   ws: qmoe_paged_attention_workspace_bytes(c, n_heads, accumulate) bytes,
- *   256-byte aligned. The sums are taken in a fixed order: the same call gives
- *   the same bits.
+ *   256-byte aligned; with accumulate it holds a score for each head and slot of
+ *   the table (4 n_seqs n_heads max_pages page bytes). The sums are taken in a
+ *   fixed order: the same call gives the same bits. A call whose wait runs out
+ *   (QMOE_ERR_TIMEOUT) leaves out undefined and the weights as they were.
  */
 size_t qmoe_paged_attention_workspace_bytes(const qmoe_paged_cache *c, int n_heads, int accumulate);
 int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, int dtype, int n_heads,
@@ -423,8 +430,9 @@ int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, in
 /*
  * Brings every (sequence, KV head) to at most ``budget`` entries. Those that
  * stay are the first m = min(lens[b], budget) in the order
- *   pos >= next_pos[b] - recent first (the newest; recent 0: none),
- *   then larger weight (NaN as -infinity), then lower slot.
+ *   pos >= next_pos[b] - recent first (the newest, among themselves by lower
+ *   slot; recent 0: none), then larger weight (NaN as -infinity), then lower
+ *   slot.
  * An entry that stays in a slot below m stays where it is; the i-th staying
  * entry of the slots from m on moves to the i-th slot below m whose entry
  * goes, with its key, value, weight and position. lens_out[b] = m.

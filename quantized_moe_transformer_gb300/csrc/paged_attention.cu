@@ -17,10 +17,10 @@ namespace {
 
 // What bounds it: each cached byte is read once and serves the G query heads of
 // its KV head, 8 flops a byte at G = 8, so HBM bounds it. 256 sequences of about
-// 4054 entries, 16 heads over 2 KV heads of 128, fp32 rows: 165 us, 6.45 TB/s (0.95
-// of the measured copy rate); one of 131075: 29.8 us, 4.5 TB/s, of which 20 are the
+// 4054 entries, 16 heads over 2 KV heads of 128, fp32 rows: 167 us, 6.40 TB/s (0.96
+// of the measured copy rate); one of 131075: 30.5 us, 4.4 TB/s, of which 20 are the
 // copy's, 4 the way to the first copies and 5 the merges and the join; 1 x 4096
-// 8.8 us, a chain of latencies.
+// 9.1 us, a chain of latencies.
 //
 // Work. A row is (sequence, KV head, tile of at most 8 NT query heads); its
 // slots are cut into tiles of KT. The tiles of all rows in order are dealt out
@@ -909,9 +909,11 @@ PaPlan pa_plan(const PagedView& c, int n_heads, bool f32, bool accumulate, int c
   p.hdp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   // A group of more than 8 heads is cut into rows of 8, or of 16 for bf16 queries over 32 MB and more: rows of 8
   // read the cache once each, the second time out of L2 where it is not too large, and take less code, fewer
-  // registers and a stage more. bf16, G = 16: 1 x 4096 8.5 us with 8 against 10.8 with 16, 8 x 3000 12.5 against
-  // 13.9, 32 x 4096 of one KV head of 64 (32 MB) 17.9 against 16.7, 64 x 4096 78 against 59. fp32, whose queries are
-  // three parts, 64 x 4096: 79.5 against 77.5 with spills, 1 x 4096 8.8 against 13.7, so fp32 has rows of 8 only.
+  // registers and a stage more. bf16, G = 16: 1 x 4096 8.9 us with 8 against 11.2 with 16, 8 x 3000 11.6 against
+  // 12.9, 32 x 4096 of one KV head of 64 (32 MB) 19.2 against 17.5, 64 x 4096 of two KV heads of 128 78.7 against
+  // 62.4 and of 256 171 against 122 (16 x 2000 of one of 256, at the border, 20.0 against 22.6); G = 10, 64 x 4096
+  // 77.0 against 59.0. fp32, whose queries are three parts, 64 x 4096: 79.5 against 77.5 with spills, 1 x 4096 8.8
+  // against 13.7, so fp32 has rows of 8 only.
   const double bytes = 4.0 * c.n_seqs * c.n_kv * (double)paged_slots(c) * c.head_dim;
   p.nt = !f32 && group > 8 && bytes >= 32.0 * (1 << 20) ? 2 : 1;
   p.head_tile = 8 * p.nt;
@@ -979,9 +981,9 @@ size_t paged_attention_ws_bytes(const PagedView& c, int n_heads, bool accumulate
 }
 
 // Rows of at most 512 slots are not cut between CTAs: a row more or less for a
-// CTA costs no more than the second launch that joins (64 sequences of 300 to 500
-// entries: 11.8 us whole, 15.9 cut; 256: 27.6 and 31.9; 8: 9.4 and 9.3; at 1024
-// slots 8 sequences take 13.8 and 9.6).
+// CTA costs no more than the second launch that joins (bf16, 64 sequences of 300 to
+// 500 entries: 12.0 us whole, 15.6 cut; 256: 27.1 and 31.4; 8: 9.3 and 9.4; at 1024
+// slots 8 sequences take 14.0 and 9.8).
 static bool pa_whole_rows(const PagedView& c) { return paged_slots(c) <= 512; }
 
 int paged_attention_launches(const PagedView& c, int, bool accumulate) {

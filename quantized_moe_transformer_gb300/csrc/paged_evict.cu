@@ -1,7 +1,7 @@
 // Eviction from a paged key-value cache by accumulated attention weight.
 //
 // For each (sequence, KV head) the m entries that stay are the first m in the
-// order (newest positions first, then larger weight, then lower slot). What
+// order (newest positions first, by lower slot; then larger weight, then lower slot). What
 // stays in a slot below m is not touched; the i-th staying entry of the slots
 // from m on moves into the i-th slot below m whose entry goes. Attention does
 // not depend on the order of a cache's entries, so this is the least that has
@@ -105,7 +105,7 @@ __device__ __forceinline__ void evict_move(const PagedView& c, const EvictArgs& 
 // of holes or movers. Weights and positions are read once; what bounds it is a
 // chain of short steps: barriers (0.1 us in a CTA, 0.8 us in a cluster) and code
 // that runs once, whose fetch shows (keys in registers with every loop unrolled
-// over 8 of them ran longer, 16.5 against 12.0 us for 1 x 4112). 1 x 4112 takes 8.8 us
+// over 8 of them ran longer, 16.5 against 12.0 us for 1 x 4112). 1 x 4112 takes 8.9 us
 // with its 16 moves, 64 sequences of 1500 to 8190 11 us, 3 x 65537 (8 CTAs each) 17 us.
 template <bool LONG, bool INLINE>
 __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedView c, const EvictArgs a,
@@ -367,7 +367,11 @@ struct EvictPlan {
 // keeps a slice to 8192 slots. The moves are made by the select kernel where a
 // CTA has at most 128 of them and no cluster that starts later reads a length that
 // another has replaced (1 x 4112 to 4048: 9.6 us, 10.9 with a launch of their own; at
-// 256 moves 14.7 and 11.3), else by a grid of their own.
+// 256 moves 14.7 and 11.3), else by a grid of their own. All of it goes by the
+// table's width: one entry over a budget of 4096 takes 7.8 us for one sequence
+// with a table of 8192 slots and outputs of its own, 8.6 in place; 64 sequences
+// 15.4 us, but 74 in place with tables of 131072 slots, whose slices and grids
+// are sized for them.
 EvictPlan evict_plan(const PagedView& c, const EvictArgs& a) {
   EvictPlan p{};
   const long long slots = paged_slots(c);
