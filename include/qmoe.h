@@ -259,12 +259,14 @@ int qmoe_moe_forward_noalloc(const qmoe_moe_desc *d, const float *X, const float
  *                          P V issuer never marks its output final, so its
  *                          softmax warps' last wait runs out;
  *   QMOE_FAULT_PAGED_COPY  paged attention: the first CTA's first warp never
- *                          copies its first tile.
+ *                          copies its first tile;
+ *   QMOE_FAULT_PREFILL_COPY attention of packed rows on the tensor cores: the first
+ *                          CTA never copies its first keys.
  * Returns QMOE_ERR_ARG for an unknown site or a negative wait. Not for use
  * outside tests; set QMOE_FAULT_NONE afterwards.
  */
 enum { QMOE_FAULT_NONE = 0, QMOE_FAULT_DECODE_COPY = 1, QMOE_FAULT_TC_ARRIVE = 2, QMOE_FAULT_ATTN_FINAL = 3,
-       QMOE_FAULT_PAGED_COPY = 4 };
+       QMOE_FAULT_PAGED_COPY = 4, QMOE_FAULT_PREFILL_COPY = 5 };
 int qmoe_test_inject(int site, int wait_us);
 
 /* Number of kernels this library has enqueued since it was loaded (a CUDA
@@ -406,6 +408,94 @@ int qmoe_paged_append(const qmoe_paged_cache *c, const void *q, void *q_out, con
                       int n_heads, float rope_theta, qmoe_stream_t stream);
 
 /*
+ * Rotary positions. A qmoe_rope_desc says how a head turns: its first ``dims``
+ * elements (a multiple of 8, 8..head_dim) are dims / 2 pairs, (i, i + dims/2) in the
+ * half layout and (2i, 2i + 1) in the interleaved one; pair i at position pos turns by
+ * pos * f_i and is multiplied by ``scale``; the elements from dims on stay as they are.
+ *   turns[i] = f_i / (2 pi) as a fraction of 2^64 (whole turns left out). A caller with
+ *   frequencies of its own fills it in itself; qmoe_rope_init fills it from
+ *   f_i = theta^(-2i/dims)
+ *     QMOE_ROPE_PLAIN    as they are;
+ *     QMOE_ROPE_LINEAR   f_i / factor;
+ *     QMOE_ROPE_PARTS    f_i (g + (1 - g) / factor), g = (r_i - low) / (high - low)
+ *                        cut to 0..1, r_i = context f_i / (2 pi): pairs that turn high times and
+ *                        more within the first ``context`` positions keep their frequency, those
+ *                        that turn low times and less are stretched.
+ *   1 <= theta <= 1e30, 1 <= factor <= 1e6, 0 < context <= 2^30, 0 <= low < high <= 2^30 (what the
+ *   scaling does not read is not looked at), scale finite.
+ * qmoe_rope turns rows of queries and, with k not NULL, of keys:
+ *   x, y [n_rows][heads][head_dim] of type dtype, element (n, h, d) at
+ *   n * row_stride + h * head_stride + d of its array (strides of at least 0, multiples of 8; the
+ *   elements of an array must not overlap, which is not checked). y may be x with the same strides.
+ *   pos [n_rows] int32. transpose != 0: by the negative angles (times scale): the
+ *   transpose of the map, which takes the gradient of y to that of x.
+ *   A position times turns[i] is reduced to less than a turn exactly, in integers; sines and
+ *   cosines are off by 2^-22 at most; products and sums are fp32.
+ * The structures are host memory: a call takes what they hold when it is made.
+ */
+typedef enum { QMOE_ROPE_HALF = 0, QMOE_ROPE_INTERLEAVED = 1 } qmoe_rope_layout;
+typedef enum { QMOE_ROPE_PLAIN = 0, QMOE_ROPE_LINEAR = 1, QMOE_ROPE_PARTS = 2 } qmoe_rope_scaling;
+
+typedef struct {
+  int layout, dims;
+  float scale;
+  uint64_t turns[128];
+} qmoe_rope_desc;
+
+typedef struct {
+  const void *x;
+  void *y;
+  int n_heads;
+  long long x_row_stride, x_head_stride, y_row_stride, y_head_stride;
+} qmoe_rope_rows;
+
+int qmoe_rope_init(qmoe_rope_desc *r, int layout, int dims, double theta, int scaling, double factor, double context,
+                   double low, double high, float scale);
+int qmoe_rope(const qmoe_rope_desc *r, const qmoe_rope_rows *q, const qmoe_rope_rows *k, int dtype, const int32_t *pos,
+              int n_rows, int head_dim, int transpose, qmoe_stream_t stream);
+
+/*
+ * qmoe_paged_append whose queries and keys turn by a descriptor. (Its sines and
+ * cosines are those of qmoe_rope, 2^-22 instead of 2^-20.)
+ */
+int qmoe_paged_append_rope(const qmoe_paged_cache *c, const void *q, void *q_out, const void *k, const void *v,
+                           int dtype, const int32_t *seq, const int32_t *slot, const int32_t *pos, int n_rows,
+                           int n_heads, const qmoe_rope_desc *rope, qmoe_stream_t stream);
+
+/*
+ * A step's plan: which pages and slots the new rows of all sequences take. The pool
+ * is a stack: free_pages [n_pages] int32, of which the first *n_free are the numbers of
+ * free pages, the last of them the next to go. A sequence's pages are its table
+ * entries up to the first that is no page number (-1, say). In this order:
+ *   1. keep not NULL, keep[b] >= 0: sequence b is cut to its first keep[b] entries,
+ *      lens[b] = min(lens[b], keep[b]), and its pages from the first that holds none of
+ *      them on go back: their table entries become -1, and they are pushed onto the stack in
+ *      the order of the sequences and of their pages. keep[b] = 0 gives a sequence
+ *      up, lens[b] returns the pages that eviction or a refused draft left empty.
+ *   2. count[b] new rows (0 below 0) for each sequence get the rows first[b] ..
+ *      first[b] + count[b] - 1 of the step, first[b] the sum of the counts before b.
+ *   3. The pages that slots lens[b] .. lens[b] + count[b] - 1 miss come off the stack,
+ *      sequence by sequence, lower slots first, and into the table. granted[b] =
+ *      count[b] where the rows end at n_rows and the slots at the table's width at
+ *      most and the pages are there, else 0: then the sequence takes no page, and those behind it
+ *      that need pages too get none if the pool was what failed.
+ *   4. Row n of a sequence b: seq[n] = b, slot[n] its slot, -1 where the rows are not
+ *      granted, pos[n] = next_pos[b] + its place among the sequence's rows
+ *      (next_pos NULL: lens[b]). Rows behind the last: seq -1, slot -1, pos 0.
+ * lens does not grow: qmoe_paged_append does that, with these maps (a slot of -1 is its padding).
+ *   count, first, granted [n_seqs]; keep, next_pos [n_seqs] or NULL; seq, slot, pos
+ *   [n_rows], may be NULL where n_rows is 0; all int32, no two of them the same array. The call
+ *   writes the cache's table. A page belongs to one sequence alone. A count of free pages out
+ *   of range, a free page's number out of range (its entry becomes -1) and pages that come back
+ *   more than once are recorded as QMOE_ERR_DEVICE_ARG.
+ *   ws: qmoe_paged_plan_workspace_bytes(c) bytes, 256-byte aligned.
+ */
+size_t qmoe_paged_plan_workspace_bytes(const qmoe_paged_cache *c);
+int qmoe_paged_plan(const qmoe_paged_cache *c, int32_t *free_pages, int32_t *n_free, const int32_t *count,
+                    const int32_t *keep, const int32_t *next_pos, int n_rows, int32_t *first, int32_t *granted,
+                    int32_t *seq, int32_t *slot, int32_t *pos, void *ws, size_t ws_bytes, qmoe_stream_t stream);
+
+/*
  * Attention of one new token for each sequence: for query head h of sequence b,
  * g = h / (n_heads / n_kv), over the slots j < lens[b]
  *   s_j = scale * q . k_j,  p = softmax(s),  out = sum_j p_j v_j,
@@ -426,6 +516,30 @@ int qmoe_paged_append(const qmoe_paged_cache *c, const void *q, void *q_out, con
 size_t qmoe_paged_attention_workspace_bytes(const qmoe_paged_cache *c, int n_heads, int accumulate);
 int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, int dtype, int n_heads,
                          float scale, int accumulate, void *ws, size_t ws_bytes, qmoe_stream_t stream);
+
+/*
+ * Causal attention of packed rows: whole prompts, parts of prompts behind what is
+ * cached, single new tokens, of many sequences in one call. Sequence b has the rows
+ * first[b] .. first[b] + count[b] - 1 (none for a count of 0 or less), whose entries are the last
+ * count[b] of its cache, appended before. Row first[b] + i sees the entries of the slots
+ *   j < lens[b] - count[b] + i + 1
+ * (none where that is 0 or less: its output is zeros), with the scores, scale, heads and
+ * types of qmoe_paged_attention. Rows of no sequence are not written.
+ *   q, out [n_rows][n_heads][hd] of type dtype; out may be q. fp32 rows are taken with all
+ *   their bits and fp32 accuracy is kept; for bf16 rows, which are exact as they are,
+ *   probabilities are rounded to bf16 (2^-9) before they weigh the values, sums are fp32,
+ *   and the result is rounded once.
+ *   first, count [n_seqs] int32; the sequences' rows must not overlap. Rows out of range
+ *   are recorded as QMOE_ERR_DEVICE_ARG and the sequence has none.
+ *   What the cache holds outside the entries is never used; queries and entries are finite.
+ *   ws: qmoe_paged_prefill_attention_workspace_bytes(c, n_rows, n_heads) bytes, 256-byte
+ *   aligned. The sums are taken in a fixed order: the same call gives the same bits. A call whose wait runs
+ *   out (QMOE_ERR_TIMEOUT) leaves out undefined.
+ */
+size_t qmoe_paged_prefill_attention_workspace_bytes(const qmoe_paged_cache *c, int n_rows, int n_heads);
+int qmoe_paged_prefill_attention(const qmoe_paged_cache *c, const void *q, void *out, int dtype,
+                                 const int32_t *first, const int32_t *count, int n_rows, int n_heads, float scale,
+                                 void *ws, size_t ws_bytes, qmoe_stream_t stream);
 
 /*
  * Brings every (sequence, KV head) to at most ``budget`` entries. Those that

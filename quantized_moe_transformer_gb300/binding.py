@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -97,7 +98,9 @@ def exported_symbols() -> list[str]:
             "qmoe_block_forward", "qmoe_test_inject",
             "qmoe_paged_append", "qmoe_paged_attention_workspace_bytes", "qmoe_paged_attention",
             "qmoe_cache_evict_workspace_bytes", "qmoe_cache_evict", "qmoe_block_decode_paged_workspace_bytes",
-            "qmoe_block_decode_paged"]
+            "qmoe_block_decode_paged", "qmoe_rope_init", "qmoe_rope", "qmoe_paged_append_rope",
+            "qmoe_paged_plan_workspace_bytes", "qmoe_paged_plan", "qmoe_paged_prefill_attention_workspace_bytes",
+            "qmoe_paged_prefill_attention"]
 
 
 def _check(status: int):
@@ -200,7 +203,7 @@ def moe_forward(layer: MoeLayer, X: torch.Tensor, R: torch.Tensor | None = None,
     return out
 
 
-FAULT_SITES = {"none": 0, "decode_copy": 1, "tc_arrive": 2, "attn_final": 3, "paged_copy": 4}
+FAULT_SITES = {"none": 0, "decode_copy": 1, "tc_arrive": 2, "attn_final": 3, "paged_copy": 4, "prefill_copy": 5}
 
 
 def test_inject(site: str, wait_us: int = 0):
@@ -410,6 +413,16 @@ class PagedCacheDesc(ctypes.Structure):
                 ("weight", _vp), ("pos", _vp)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("layout", _c_int), ("dims", _c_int), ("scale", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
+
+
+class RopeRows(ctypes.Structure):
+    _fields_ = [("x", _vp), ("y", _vp), ("n_heads", _c_int), ("x_row_stride", ctypes.c_longlong),
+                ("x_head_stride", ctypes.c_longlong), ("y_row_stride", ctypes.c_longlong),
+                ("y_head_stride", ctypes.c_longlong)]
+
+
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -432,6 +445,18 @@ def _paged_lib():
         L.qmoe_block_decode_paged_workspace_bytes.restype = _c_size
         L.qmoe_block_decode_paged_workspace_bytes.argtypes = [ctypes.POINTER(BlockDesc), P, _c_int]
         L.qmoe_block_decode_paged.argtypes = [ctypes.POINTER(BlockDesc), P, _vp, _vp, _vp, _c_int, _vp, _c_size, _vp]
+        R = ctypes.POINTER(RopeDesc)
+        L.qmoe_rope_init.argtypes = [R, _c_int, _c_int, ctypes.c_double, _c_int] + [ctypes.c_double] * 4 + [ctypes.c_float]
+        L.qmoe_rope.argtypes = [R, ctypes.POINTER(RopeRows), ctypes.POINTER(RopeRows), _c_int, _vp, _c_int, _c_int, _c_int,
+                                _vp]
+        L.qmoe_paged_append_rope.argtypes = [P, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int, R, _vp]
+        L.qmoe_paged_plan_workspace_bytes.restype = _c_size
+        L.qmoe_paged_plan_workspace_bytes.argtypes = [P]
+        L.qmoe_paged_plan.argtypes = [P] + [_vp] * 5 + [_c_int] + [_vp] * 6 + [_c_size, _vp]
+        L.qmoe_paged_prefill_attention_workspace_bytes.restype = _c_size
+        L.qmoe_paged_prefill_attention_workspace_bytes.argtypes = [P, _c_int, _c_int]
+        L.qmoe_paged_prefill_attention.argtypes = [P, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, ctypes.c_float, _vp,
+                                                   _c_size, _vp]
         _paged = L
     return _paged
 
@@ -534,22 +559,100 @@ def _raw_stream(stream, cache):
     torch.cuda.Stream object on the GB300's host). The library launches on the
     current device, which has to be the cache's (asked where there is another:
     0.4 us)."""
-    device = cache.device
-    if cache.one_of_many and torch._C._cuda_getDevice() != device:
-        raise QmoeError(f"the cache is on cuda:{device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return _stream_on(stream, cache.device, "the cache", cache.one_of_many)
+
+
+def _stream_on(stream, device, what, one_of_many):
+    if one_of_many and torch._C._cuda_getDevice() != device:
+        raise QmoeError(f"{what} is on cuda:{device}, the current device is cuda:{torch._C._cuda_getDevice()}")
     if stream is not None:
         if stream.device_index != device:
-            raise QmoeError(f"the stream is of cuda:{stream.device_index}, the cache on cuda:{device}")
+            raise QmoeError(f"the stream is of cuda:{stream.device_index}, {what} on cuda:{device}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {None: 0, "linear": 1, "parts": 2}
+
+
+class Rope:
+    """How heads turn by their positions: the first ``dims`` elements, in pairs half
+    of them apart ("half") or of neighbours ("interleaved"), by theta^(-2i/dims) a
+    position, scaled for long contexts ("linear": divided by ``factor``; "parts":
+    only where a pair turns less than ``high`` times within ``context`` positions,
+    in full below ``low``), the result times ``scale``. ``frequencies`` (an angle
+    of one position for each pair) take the place of theta and the scaling."""
+
+    def __init__(self, dims, theta=1e7, layout="half", scaling=None, factor=1.0, context=0.0, low=0.0, high=0.0,
+                 scale=1.0, frequencies=None):
+        if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+            raise QmoeError(f"no rotary layout {layout!r} with scaling {scaling!r}")
+        self.dims, self.desc = dims, RopeDesc()
+        self.one_of_many = torch.cuda.device_count() > 1
+        kind = ROPE_SCALINGS[scaling if frequencies is None else None]
+        _check(_paged_lib().qmoe_rope_init(ctypes.byref(self.desc), ROPE_LAYOUTS[layout], dims, theta, kind, factor, context,
+                                           low, high, scale))
+        if frequencies is not None:
+            if len(frequencies) != dims // 2:
+                raise QmoeError(f"{len(frequencies)} frequencies for {dims // 2} pairs")
+            for i, f in enumerate(frequencies):
+                turn = float(f) / (2 * math.pi)
+                if not math.isfinite(turn):
+                    raise QmoeError("frequencies must be finite")
+                self.desc.turns[i] = int((turn - math.floor(turn)) * 2.0 ** 64) & (2 ** 64 - 1)
+        self._ref = ctypes.byref(self.desc)
+
+
+def _rope_rows(x, y, what, rows, hd, dtype, dev):
+    """One array of rows of ``rope`` and where it goes: on this device, of this
+    type, [rows][heads][hd] with elements one after the other."""
+    shape = (rows, _size(x, 1, what), hd)
+    for t, name in ((x, what), (y, f"{what}_out")):
+        if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or t.stride(2) != 1:
+            if not t.is_cuda or t.get_device() != dev:
+                raise QmoeError(f"{name} must be on cuda:{dev}, as pos is")
+            if t.dtype is not dtype:
+                raise QmoeError(f"{name} has type {t.dtype}, not {dtype}")
+            if t.shape != shape:
+                raise QmoeError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+            raise QmoeError(f"the elements of a head of {name} must be one after the other")
+    xs, ys = x.stride(), y.stride()
+    return RopeRows(x.data_ptr(), y.data_ptr(), shape[1], xs[0], xs[1], ys[0], ys[1])
+
+
+def rope(rope: Rope, pos, q, k=None, q_out=None, k_out=None, transpose: bool = False, stream=None):
+    """Rows q [rows][heads][hd] and k [rows][kv heads][hd] (fp32 or bf16; any row and
+    head strides that are multiples of 8, such as parts of a joint projection) turned
+    by their positions ``pos`` [rows] int32; ``transpose``: turned back (times the
+    scale), which takes gradients of the results to those of the rows. Returns q_out
+    and k_out, new tensors by default; they may be q and k."""
+    dtype, dev, rows, hd = q.dtype, pos.get_device(), _size(q, 0, "q"), _size(q, 2, "q")
+    if dtype not in _DTYPE:
+        raise QmoeError(f"q has type {dtype}, not fp32 or bf16")
+    at = _need(pos, "pos", (rows,), torch.int32, dev)
+    if not pos.is_cuda:
+        raise QmoeError("pos must be on a CUDA device")
+    if k is None and k_out is not None:
+        raise QmoeError("k_out without k")
+    if q_out is None or (k is not None and k_out is None):
+        with _allocating(stream):
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
+            k_out = torch.empty(k.shape, dtype=dtype, device=k.device) if k is not None and k_out is None else k_out
+    rq = _rope_rows(q, q_out, "q", rows, hd, dtype, dev)
+    rk = None if k is None else ctypes.byref(_rope_rows(k, k_out, "k", rows, hd, dtype, dev))
+    _check(_paged_lib().qmoe_rope(rope._ref, ctypes.byref(rq), rk, _DTYPE[dtype], at, rows, hd, int(transpose),
+                                  _stream_on(stream, dev, "pos", rope.one_of_many)))
+    return q_out if k is None else (q_out, k_out)
+
+
 def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slot=None, rope_theta: float = 0.0,
-                 stream=None):
+                 stream=None, rope: Rope | None = None):
     """Rows k, v [rows][kv heads][hd] (fp32 or bf16) into the cache: row n to
     slot ``slot[n]`` of sequence ``seq[n]`` (both None: row n is the next entry
     of sequence n; a slot below 0: not cached), at position ``pos[n]``, keys (and
-    the queries q [rows][heads][hd], returned) rotated when ``rope_theta`` > 0."""
+    the queries q [rows][heads][hd], returned) rotated when ``rope_theta`` > 0,
+    or as ``rope`` says."""
     rows = _size(k, 0, "k")
     dtype, dev = k.dtype, cache.device
     if dtype not in _DTYPE:
@@ -567,11 +670,16 @@ def paged_append(cache: PagedCache, k, v, pos, q=None, q_out=None, seq=None, slo
         raise QmoeError("q_out without q")
     else:
         qp = qo = None
-    _check(_paged_lib().qmoe_paged_append(
-        cache._desc_ref, qp, qo, _need(k, "k", kv_shape, dtype, dev), _need(v, "v", kv_shape, dtype, dev), _DTYPE[dtype],
-        None if seq is None else _need(seq, "seq", (rows,), torch.int32, dev),
-        None if slot is None else _need(slot, "slot", (rows,), torch.int32, dev),
-        _need(pos, "pos", (rows,), torch.int32, dev), rows, heads, rope_theta, _raw_stream(stream, cache)))
+    args = (cache._desc_ref, qp, qo, _need(k, "k", kv_shape, dtype, dev), _need(v, "v", kv_shape, dtype, dev), _DTYPE[dtype],
+            None if seq is None else _need(seq, "seq", (rows,), torch.int32, dev),
+            None if slot is None else _need(slot, "slot", (rows,), torch.int32, dev),
+            _need(pos, "pos", (rows,), torch.int32, dev), rows, heads)
+    if rope is None:
+        _check(_paged_lib().qmoe_paged_append(*args, rope_theta, _raw_stream(stream, cache)))
+    elif rope_theta:
+        raise QmoeError("rope_theta and rope are two ways to say how rows turn: give one")
+    else:
+        _check(_paged_lib().qmoe_paged_append_rope(*args, rope._ref, _raw_stream(stream, cache)))
     return q_out
 
 
@@ -599,6 +707,86 @@ def paged_attention(cache: PagedCache, q, out=None, scale: float = 0.0, accumula
         cache._desc_ref, _need(q, "q", shape, dtype, dev), _need(out, "out", shape, dtype, dev), _DTYPE[dtype], heads,
         scale, int(accumulate), _need_ws(ws, dev), ws.numel(), _raw_stream(stream, cache)))
     return out
+
+
+def paged_prefill_attention_workspace(cache: PagedCache, n_rows: int, n_heads: int) -> torch.Tensor:
+    n = int(_paged_lib().qmoe_paged_prefill_attention_workspace_bytes(cache._desc_ref, n_rows, n_heads))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def paged_prefill_attention(cache: PagedCache, q, first, count, out=None, scale: float = 0.0, ws=None, stream=None):
+    """Causal attention of packed rows q [rows][heads][hd] (fp32 or bf16): rows
+    first[b] .. first[b] + count[b] - 1 are the last count[b] entries of sequence b,
+    appended before, and each sees the entries up to its own. Rows of no sequence
+    are not written (a new ``out`` holds zeros there). scale 0: 1/sqrt(hd)."""
+    dtype = q.dtype
+    if dtype not in _DTYPE:
+        raise QmoeError(f"q has type {dtype}, not fp32 or bf16")
+    rows, heads = _size(q, 0, "q"), _size(q, 1, "q")
+    shape = (rows, heads, cache.head_dim)
+    if out is None or ws is None:
+        with _allocating(stream):
+            out = torch.zeros_like(q) if out is None else out
+            ws = paged_prefill_attention_workspace(cache, rows, heads) if ws is None else ws
+    dev = cache.device
+    _check(_paged_lib().qmoe_paged_prefill_attention(
+        cache._desc_ref, _need(q, "q", shape, dtype, dev), _need(out, "out", shape, dtype, dev), _DTYPE[dtype],
+        _need(first, "first", (cache.n_seqs,), torch.int32, dev), _need(count, "count", (cache.n_seqs,), torch.int32, dev),
+        rows, heads, scale, _need_ws(ws, dev), ws.numel(), _raw_stream(stream, cache)))
+    return out
+
+
+class PagePool:
+    """The free pages of a cache's pools, a stack: ``free`` [pages] int32, of which the
+    first ``n_free`` [1] int32 are free, the last of them the next to go."""
+
+    def __init__(self, free, n_free):
+        self.free, self.n_free = free, n_free
+
+    @classmethod
+    def full(cls, cache: PagedCache):
+        """All pages of a cache free, page 0 the first to go. The cache's table must name none."""
+        n = cache.n_pages
+        return cls(torch.arange(n - 1, -1, -1, dtype=torch.int32, device=cache.k.device),
+                   torch.full((1,), n, dtype=torch.int32, device=cache.k.device))
+
+
+def paged_plan_workspace(cache: PagedCache) -> torch.Tensor:
+    n = int(_paged_lib().qmoe_paged_plan_workspace_bytes(cache._desc_ref))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def paged_plan(cache: PagedCache, pool: PagePool, count, keep=None, next_pos=None, n_rows: int | None = None, first=None,
+               granted=None, seq=None, slot=None, pos=None, ws=None, stream=None):
+    """The pages and slots of a step's new rows, count[b] for each sequence, after
+    sequence b was cut to its first keep[b] entries (below 0, or without ``keep``: left as it
+    is) and the pages behind them went back to ``pool``. Returns (first, granted, seq, slot,
+    pos): each sequence's first row of ``n_rows`` and how many rows it was granted (all
+    or none), each row's sequence, slot (-1: not granted) and position (next_pos[b] and on). The
+    length of ``seq`` is n_rows where it is given."""
+    dev, seqs = cache.device, (cache.n_seqs,)
+    if n_rows is None:
+        if seq is None:
+            raise QmoeError("a plan needs n_rows or an array of that length for seq")
+        n_rows = _size(seq, 0, "seq")
+    rows = (n_rows,)
+    if any(t is None for t in (first, granted, seq, slot, pos, ws)):
+        if n_rows < 0:
+            raise QmoeError("n_rows is below 0")
+        with _allocating(stream):
+            new = lambda t, n: torch.empty(n, dtype=torch.int32, device=cache.k.device) if t is None else t
+            first, granted = new(first, seqs), new(granted, seqs)
+            seq, slot, pos = new(seq, rows), new(slot, rows), new(pos, rows)
+            ws = paged_plan_workspace(cache) if ws is None else ws
+    i32 = torch.int32
+    _check(_paged_lib().qmoe_paged_plan(
+        cache._desc_ref, _need(pool.free, "the pool's pages", (cache.n_pages,), i32, dev),
+        _need(pool.n_free, "the pool's count", (1,), i32, dev), _need(count, "count", seqs, i32, dev),
+        None if keep is None else _need(keep, "keep", seqs, i32, dev),
+        None if next_pos is None else _need(next_pos, "next_pos", seqs, i32, dev), n_rows, _need(first, "first", seqs, i32, dev),
+        _need(granted, "granted", seqs, i32, dev), _need(seq, "seq", rows, i32, dev), _need(slot, "slot", rows, i32, dev),
+        _need(pos, "pos", rows, i32, dev), _need_ws(ws, dev), ws.numel(), _raw_stream(stream, cache)))
+    return first, granted, seq, slot, pos
 
 
 def cache_evict_workspace(cache: PagedCache) -> torch.Tensor:

@@ -4,11 +4,13 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <cstdio>
 
 #include "kernels.cuh"
 #include "paged.cuh"
+#include "rope.cuh"
 
 using namespace qmoe;
 
@@ -498,6 +500,60 @@ int paged_block(const qmoe_block_desc* b, const qmoe_paged_cache* c, PagedView* 
 
 bool dtype_ok(int dtype) { return dtype == QMOE_F32 || dtype == QMOE_BF16; }
 
+// A descriptor of rotary positions for heads of ``head_dim``.
+bool rope_ok(const qmoe_rope_desc& r, int head_dim) {
+  return (r.layout == QMOE_ROPE_HALF || r.layout == QMOE_ROPE_INTERLEAVED) && r.dims >= 8 && r.dims % 8 == 0 &&
+         r.dims <= head_dim && std::isfinite(r.scale);
+}
+
+// One array of rows of qmoe_rope.
+int rope_rows(const qmoe_rope_rows& t, RopeRows* out) {
+  if (t.n_heads < 1 || t.n_heads > 65535) return QMOE_ERR_ARG;
+  for (const long long s : {t.x_row_stride, t.x_head_stride, t.y_row_stride, t.y_head_stride})
+    if (s < 0 || s % 8 != 0) return QMOE_ERR_ARG;
+  if (!t.x || !t.y) return QMOE_ERR_NULL;
+  if (!aligned(t.x, 16) || !aligned(t.y, 16)) return QMOE_ERR_ALIGN;
+  *out = RopeRows{t.x, t.y, t.n_heads, t.x_row_stride, t.x_head_stride, t.y_row_stride, t.y_head_stride};
+  return QMOE_OK;
+}
+
+// ``rope`` NULL: by rope_theta.
+int append_impl(const qmoe_paged_cache* c, const void* q, void* q_out, const void* k, const void* v, int dtype,
+                const int32_t* seq, const int32_t* slot, const int32_t* pos, int n_rows, int n_heads, float rope_theta,
+                const qmoe_rope_desc* rope, qmoe_stream_t stream) {
+  PagedView view;
+  int r = paged_view(c, &view);
+  if (r != QMOE_OK) return r;
+  if (!dtype_ok(dtype) || n_rows < 0 || !(rope_theta >= 0.f) || rope_theta > 1e30f) return QMOE_ERR_ARG;
+  if (rope && !rope_ok(*rope, c->head_dim)) return QMOE_ERR_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (seq == nullptr) != (slot == nullptr)) return QMOE_ERR_NULL;
+  if (q && (n_heads < 1 || n_heads > 65535)) return QMOE_ERR_ARG;
+  if (n_rows == 0) return QMOE_OK;
+  if (!seq && n_rows != c->n_seqs) return QMOE_ERR_ARG;
+  if (!k || !v || !pos) return QMOE_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(seq, 4) ||
+      !aligned(slot, 4) || !aligned(pos, 4))
+    return QMOE_ERR_ALIGN;
+  AppendArgs a{};
+  r = device_ready(&a.status);
+  if (r != QMOE_OK) return r;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.seq = seq;
+  a.slot = slot;
+  a.pos = pos;
+  a.n_rows = n_rows;
+  a.n_heads = q ? n_heads : 0;
+  a.f32 = dtype == QMOE_F32;
+  a.rotate = rope_theta > 0.f;
+  a.theta = (double)rope_theta;
+  a.rope = rope;
+  g_launches.fetch_add(1);
+  return launch_status(launch_paged_append(view, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -565,35 +621,105 @@ int qmoe_block_forward(const qmoe_block_desc* b, const float* X, float* out, int
 int qmoe_paged_append(const qmoe_paged_cache* c, const void* q, void* q_out, const void* k, const void* v, int dtype,
                       const int32_t* seq, const int32_t* slot, const int32_t* pos, int n_rows, int n_heads,
                       float rope_theta, qmoe_stream_t stream) {
+  return append_impl(c, q, q_out, k, v, dtype, seq, slot, pos, n_rows, n_heads, rope_theta, nullptr, stream);
+}
+
+int qmoe_paged_append_rope(const qmoe_paged_cache* c, const void* q, void* q_out, const void* k, const void* v,
+                           int dtype, const int32_t* seq, const int32_t* slot, const int32_t* pos, int n_rows,
+                           int n_heads, const qmoe_rope_desc* rope, qmoe_stream_t stream) {
+  if (!rope) return QMOE_ERR_NULL;
+  return append_impl(c, q, q_out, k, v, dtype, seq, slot, pos, n_rows, n_heads, 0.f, rope, stream);
+}
+
+int qmoe_rope_init(qmoe_rope_desc* r, int layout, int dims, double theta, int scaling, double factor, double context,
+                   double low, double high, float scale) {
+  if (!r) return QMOE_ERR_NULL;
+  if (scaling != QMOE_ROPE_PLAIN && scaling != QMOE_ROPE_LINEAR && scaling != QMOE_ROPE_PARTS) return QMOE_ERR_ARG;
+  if (!(theta >= 1.0 && theta <= 1e30)) return QMOE_ERR_ARG;
+  if (scaling != QMOE_ROPE_PLAIN && !(factor >= 1.0 && factor <= 1e6)) return QMOE_ERR_ARG;
+  if (scaling == QMOE_ROPE_PARTS &&
+      !(context > 0.0 && context <= 1073741824.0 && low >= 0.0 && high > low && high <= 1073741824.0))
+    return QMOE_ERR_ARG;
+  qmoe_rope_desc d{};
+  d.layout = layout;
+  d.dims = dims;
+  d.scale = scale;
+  if (!rope_ok(d, 256)) return QMOE_ERR_ARG;
+  for (int i = 0; i < dims / 2; ++i) {
+    double t = std::pow(theta, -2.0 * i / (double)dims) * 0.15915494309189535;  // turns of one position
+    if (scaling == QMOE_ROPE_LINEAR) t /= factor;
+    if (scaling == QMOE_ROPE_PARTS) {
+      double g = (context * t - low) / (high - low);
+      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      t *= g + (1.0 - g) / factor;
+    }
+    d.turns[i] = (uint64_t)((t - std::floor(t)) * 18446744073709551616.0);
+  }
+  *r = d;
+  return QMOE_OK;
+}
+
+int qmoe_rope(const qmoe_rope_desc* r, const qmoe_rope_rows* q, const qmoe_rope_rows* k, int dtype, const int32_t* pos,
+              int n_rows, int head_dim, int transpose, qmoe_stream_t stream) {
+  if (!r || !q) return QMOE_ERR_NULL;
+  if (!dtype_ok(dtype) || n_rows < 0 || head_dim < 8 || head_dim > 256 || head_dim % 8 != 0 || !rope_ok(*r, head_dim))
+    return QMOE_ERR_ARG;
+  if (n_rows == 0) return QMOE_OK;
+  RopeArgs a{};
+  int e = rope_rows(*q, &a.q);
+  if (e == QMOE_OK && k) e = rope_rows(*k, &a.k);
+  if (e != QMOE_OK) return e;
+  if (!pos) return QMOE_ERR_NULL;
+  if (!aligned(pos, 4)) return QMOE_ERR_ALIGN;
+  int* status = nullptr;
+  e = device_ready(&status);
+  if (e != QMOE_OK) return e;
+  a.pos = pos;
+  a.n_rows = n_rows;
+  a.head_dim = head_dim;
+  a.f32 = dtype == QMOE_F32;
+  a.sign = transpose ? -1.f : 1.f;
+  g_launches.fetch_add(1);
+  return launch_status(launch_rope(*r, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qmoe_paged_plan_workspace_bytes(const qmoe_paged_cache* c) {
+  PagedView view;
+  if (paged_view(c, &view) != QMOE_OK) return 0;
+  return paged_plan_ws_bytes(view);
+}
+
+int qmoe_paged_plan(const qmoe_paged_cache* c, int32_t* free_pages, int32_t* n_free, const int32_t* count,
+                    const int32_t* keep, const int32_t* next_pos, int n_rows, int32_t* first, int32_t* granted,
+                    int32_t* seq, int32_t* slot, int32_t* pos, void* ws, size_t ws_bytes, qmoe_stream_t stream) {
   PagedView view;
   int r = paged_view(c, &view);
   if (r != QMOE_OK) return r;
-  if (!dtype_ok(dtype) || n_rows < 0 || !(rope_theta >= 0.f) || rope_theta > 1e30f) return QMOE_ERR_ARG;
-  if ((q == nullptr) != (q_out == nullptr) || (seq == nullptr) != (slot == nullptr)) return QMOE_ERR_NULL;
-  if (q && (n_heads < 1 || n_heads > 65535)) return QMOE_ERR_ARG;
-  if (n_rows == 0) return QMOE_OK;
-  if (!seq && n_rows != c->n_seqs) return QMOE_ERR_ARG;
-  if (!k || !v || !pos) return QMOE_ERR_NULL;
-  if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(seq, 4) ||
-      !aligned(slot, 4) || !aligned(pos, 4))
-    return QMOE_ERR_ALIGN;
-  AppendArgs a{};
+  if (n_rows < 0) return QMOE_ERR_ARG;
+  if (!free_pages || !n_free || !count || !first || !granted || !ws) return QMOE_ERR_NULL;
+  if (n_rows > 0 && (!seq || !slot || !pos)) return QMOE_ERR_NULL;
+  for (const void* p : std::initializer_list<const void*>{free_pages, n_free, count, keep, next_pos, first, granted,
+                                                          seq, slot, pos})
+    if (!aligned(p, 4)) return QMOE_ERR_ALIGN;
+  if (!aligned(ws, 256)) return QMOE_ERR_ALIGN;
+  if (ws_bytes < paged_plan_ws_bytes(view)) return QMOE_ERR_WORKSPACE;
+  PlanArgs a{};
   r = device_ready(&a.status);
   if (r != QMOE_OK) return r;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_out = q_out;
+  a.free_pages = free_pages;
+  a.n_free = n_free;
+  a.keep = keep;
+  a.count = count;
+  a.next_pos = next_pos;
+  a.n_rows = n_rows;
+  a.first = first;
+  a.granted = granted;
   a.seq = seq;
   a.slot = slot;
   a.pos = pos;
-  a.n_rows = n_rows;
-  a.n_heads = q ? n_heads : 0;
-  a.f32 = dtype == QMOE_F32;
-  a.rotate = rope_theta > 0.f;
-  a.theta = (double)rope_theta;
-  g_launches.fetch_add(1);
-  return launch_status(launch_paged_append(view, a, reinterpret_cast<cudaStream_t>(stream)));
+  a.ws = ws;
+  g_launches.fetch_add(paged_plan_launches(view, a));
+  return launch_status(launch_paged_plan(view, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t qmoe_paged_attention_workspace_bytes(const qmoe_paged_cache* c, int n_heads, int accumulate) {
@@ -626,6 +752,44 @@ int qmoe_paged_attention(const qmoe_paged_cache* c, const void* q, void* out, in
   a.ws = ws;
   g_launches.fetch_add(paged_attention_launches(view, n_heads, a.accumulate));
   return launch_status(launch_paged_attention(view, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qmoe_paged_prefill_attention_workspace_bytes(const qmoe_paged_cache* c, int n_rows, int n_heads) {
+  PagedView view;
+  if (paged_view(c, &view) != QMOE_OK || n_rows < 0 || n_heads < 1 || n_heads > 65535 || n_heads % c->n_kv != 0) return 0;
+  return paged_prefill_ws_bytes(view, n_rows, n_heads);
+}
+
+int qmoe_paged_prefill_attention(const qmoe_paged_cache* c, const void* q, void* out, int dtype, const int32_t* first,
+                                 const int32_t* count, int n_rows, int n_heads, float scale, void* ws, size_t ws_bytes,
+                                 qmoe_stream_t stream) {
+  PagedView view;
+  int r = paged_view(c, &view);
+  if (r != QMOE_OK) return r;
+  if (!dtype_ok(dtype) || n_rows < 0 || n_heads < 1 || n_heads > 65535 || n_heads % c->n_kv != 0 ||
+      !std::isfinite(scale))
+    return QMOE_ERR_ARG;
+  if (n_rows == 0) return QMOE_OK;
+  if (!q || !out || !first || !count || !ws) return QMOE_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(first, 4) || !aligned(count, 4) || !aligned(ws, 256))
+    return QMOE_ERR_ALIGN;
+  if (ws_bytes < paged_prefill_ws_bytes(view, n_rows, n_heads)) return QMOE_ERR_WORKSPACE;
+  PrefillArgs a{};
+  r = device_ready(&a.status);
+  if (r != QMOE_OK) return r;
+  a.q = q;
+  a.out = out;
+  a.first = first;
+  a.count = count;
+  a.n_rows = n_rows;
+  a.n_heads = n_heads;
+  a.f32 = dtype == QMOE_F32;
+  a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)c->head_dim);
+  a.wait_ns = wait_limit_ns();
+  a.fault = g_fault_site.load() == QMOE_FAULT_PREFILL_COPY;
+  a.ws = ws;
+  g_launches.fetch_add(paged_prefill_launches(view, a));
+  return launch_status(launch_paged_prefill(view, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t qmoe_cache_evict_workspace_bytes(const qmoe_paged_cache* c) {
@@ -1205,7 +1369,7 @@ int qmoe_moe_forward_host(const qmoe_moe_desc* d, const float* X_host, const flo
 long long qmoe_launch_count(void) { return g_launches.load(); }
 
 int qmoe_test_inject(int site, int wait_us) {
-  if (site < 0 || site > QMOE_FAULT_PAGED_COPY || wait_us < 0) return QMOE_ERR_ARG;
+  if (site < 0 || site > QMOE_FAULT_PREFILL_COPY || wait_us < 0) return QMOE_ERR_ARG;
   g_fault_wait_us.store(wait_us);
   g_fault_site.store(site);
   return QMOE_OK;

@@ -1,5 +1,5 @@
 // Kernels of the paged key-value cache (host-side launchers): paged_append.cu,
-// paged_attention.cu, paged_evict.cu. The operations and the cache's layout
+// paged_attention.cu, paged_evict.cu, paged_plan.cu, paged_prefill.cu. The operations and the cache's layout
 // are defined in include/qmoe.h.
 #pragma once
 
@@ -66,6 +66,7 @@ struct AppendArgs {
   int n_rows, n_heads;
   bool f32, rotate;
   double theta;
+  const qmoe_rope_desc* rope;  // not null: turns instead of theta
   int* status;
 };
 cudaError_t launch_paged_append(const PagedView& c, const AppendArgs& a, cudaStream_t st);
@@ -97,5 +98,33 @@ struct EvictArgs {
 size_t cache_evict_ws_bytes(const PagedView& c);
 int cache_evict_launches(const PagedView& c, const EvictArgs& a);
 cudaError_t launch_cache_evict(const PagedView& c, const EvictArgs& a, cudaStream_t st);
+
+struct PlanArgs {
+  int32_t *free_pages, *n_free;
+  const int32_t *keep, *count, *next_pos;
+  int n_rows;
+  int32_t *first, *granted, *seq, *slot, *pos;
+  int* status;
+  void* ws;
+};
+size_t paged_plan_ws_bytes(const PagedView& c);
+int paged_plan_launches(const PagedView& c, const PlanArgs& a);
+cudaError_t launch_paged_plan(const PagedView& c, const PlanArgs& a, cudaStream_t st);
+
+struct PrefillArgs {
+  const void* q;
+  void* out;
+  const int32_t *first, *count;
+  int n_rows, n_heads;
+  bool f32;
+  float scale;
+  int* status;
+  unsigned long long wait_ns;  // bound on a device wait
+  bool fault;                  // test-only: the first CTA never copies its first keys
+  void* ws;
+};
+size_t paged_prefill_ws_bytes(const PagedView& c, int n_rows, int n_heads);
+int paged_prefill_launches(const PagedView& c, const PrefillArgs& a);
+cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaStream_t st);
 
 }  // namespace qmoe

@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "paged.cuh"
+#include "rope.cuh"
 #include "tc.cuh"
 
 namespace qmoe {
@@ -16,34 +17,9 @@ namespace {
 
 constexpr int AP_THREADS = 256, AP_MAX_THREADS = 512, AP_ROWS = 32, AP_CTAS_PER_SM = 4;
 
-// theta^(-2i/hd) / (2 pi), the turns of one position, as a fraction of 2^64.
-// Whole turns drop out of the product with a position modulo 2^64, so the
-// angle of any position is reduced exactly in integers.
-struct AppendFreq {
-  uint64_t turns[128];
-};
-
-// Four elements in memory, as fp32, and back.
-template <typename T>
-struct Four;
-template <>
-struct Four<float> {
-  using raw = float4;
-  static __device__ __forceinline__ float4 wide(raw v) { return v; }
-  static __device__ __forceinline__ raw narrow(float4 v) { return v; }
-};
-template <>
-struct Four<__nv_bfloat16> {
-  using raw = uint2;
-  static __device__ __forceinline__ float4 wide(raw u) {
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xFFFF0000u));
-  }
-  static __device__ __forceinline__ raw narrow(float4 v) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  }
-};
+// How the rows turn: not at all; by theta, the whole head, pairs half a head apart
+// (single precision sines); by a qmoe_rope_desc (rope.cuh).
+enum AppendTurn { AP_AS_IS = 0, AP_THETA = 1, AP_ROPE = 2 };
 
 // A CTA takes ``rows`` rows. A unit is four elements of a head and the four
 // half a head further on, which turn together: one thread reads a unit, turns it
@@ -52,16 +28,24 @@ struct Four<__nv_bfloat16> {
 // One row takes 3.1 us (the launch, the page look-up, one read and one write); 16372
 // bf16 rows of two KV heads of 128 6.5 us, 4.9 TB/s of reads and writes. Angles are
 // exact to 2^-33 turns; a sine or cosine is single precision, off by 2^-21 at most.
-template <typename T, bool ROT>
+template <typename T, int ROT>
 __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedView c, const AppendArgs a, int rows,
-                                                            const __grid_constant__ AppendFreq fr) {
+                                                            const __grid_constant__ qmoe_rope_desc fr) {
+  // fr: the turns of one position as fractions of 2^64; whole turns drop out of the product with a position modulo
+  // 2^64, so the angle of any position is reduced exactly in integers
   __shared__ float2 turn[ROT ? AP_ROWS * 128 : 1];
   __shared__ long long off[AP_ROWS];
   __shared__ int2 at[AP_ROWS];  // (sequence, slot), slot -1: the row is not cached
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, threads = blockDim.x, hd = c.head_dim, half = hd / 2;
-  if (ROT) {
+  const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, threads = blockDim.x, hd = c.head_dim, half = (ROT == AP_ROPE ? fr.dims : hd) / 2;
+  if (ROT == AP_ROPE) {
+    for (int i = tid; i < n * half; i += threads) {
+      const int r = i / half;
+      turn[i] = rope_turn(a.pos[n0 + r], fr.turns[i - r * half], fr.scale);
+    }
+  }
+  if (ROT == AP_THETA) {
     for (int i = tid; i < n * half; i += threads) {
       const int r = i / half, d = i - r * half;
       const uint64_t frac = (uint64_t)(long long)a.pos[n0 + r] * fr.turns[d];
@@ -95,6 +79,7 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
   using F = Four<T>;
   using B = Four<__nv_bfloat16>;
   using raw = typename F::raw;
+  const bool inter = ROT == AP_ROPE && fr.layout == QMOE_ROPE_INTERLEAVED;
   const int per_head = hd / 8, units = (a.n_heads + 2 * c.n_kv) * per_head;
   // a thread keeps its unit and walks rows; where a row has fewer units than the CTA threads, groups of threads take
   // rows side by side
@@ -104,7 +89,11 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
   for (int u0 = 0; u0 < units; u0 += threads) {
     const int u = u0 + tid - group * units;
     const bool mine = u < units && group < groups;
-    const int h = u / per_head, d = 4 * (u - h * per_head), g = h - a.n_heads;
+    const int h = u / per_head, g = h - a.n_heads;
+    // the unit's two places and its first angle (values never turn: any two places do)
+    const RopeUnit at_ = ROT == AP_ROPE ? rope_unit(u - h * per_head, fr.dims, inter)
+                                        : RopeUnit{4 * (u - h * per_head), 4 * (u - h * per_head) + hd / 2, true};
+    const int d = at_.a, apart = at_.b - at_.a, angle = 4 * (u - h * per_head);
     const T* src = nullptr;
     long long step = 0;  // elements between a tensor's rows
     if (mine) {
@@ -121,7 +110,7 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
         const int r = r0 + k * groups;
         if (mine && r < n) {
           x[k] = *reinterpret_cast<const raw*>(src + r * step);
-          y[k] = *reinterpret_cast<const raw*>(src + r * step + half);
+          y[k] = *reinterpret_cast<const raw*>(src + r * step + apart);
         }
       }
       if (!looked_up) __syncthreads();  // the first reads go on while the pages are looked up
@@ -133,7 +122,8 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
         const long long o = off[r];
         if (g >= 0 && o < 0) continue;
         float4 p = F::wide(x[k]), q = F::wide(y[k]);
-        if (ROT && g < c.n_kv) {
+        if (ROT == AP_ROPE && g < c.n_kv && at_.turned) rope_apply(p, q, turn + r * half + angle, inter);
+        if (ROT == AP_THETA && g < c.n_kv) {
           const float2* t = turn + r * half + d;
           const float2 t0 = t[0], t1 = t[1], t2 = t[2], t3 = t[3];
           const float4 v = p, w = q;
@@ -144,10 +134,10 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
         }
         if (g < 0) {
           *reinterpret_cast<raw*>(q_to + r * step) = F::narrow(p);
-          *reinterpret_cast<raw*>(q_to + r * step + half) = F::narrow(q);
+          *reinterpret_cast<raw*>(q_to + r * step + apart) = F::narrow(q);
         } else {
           *reinterpret_cast<B::raw*>(kv_to + o) = B::narrow(p);
-          *reinterpret_cast<B::raw*>(kv_to + o + half) = B::narrow(q);
+          *reinterpret_cast<B::raw*>(kv_to + o + apart) = B::narrow(q);
         }
       }
     }
@@ -162,7 +152,7 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
 }
 
 template <typename T>
-cudaError_t append_rows(const PagedView& c, const AppendArgs& a, const AppendFreq& fr, cudaStream_t st) {
+cudaError_t append_rows(const PagedView& c, const AppendArgs& a, const qmoe_rope_desc& fr, cudaStream_t st) {
   // all CTAs at once on the SMs, as few rows in each as that allows
   const int fit = AP_CTAS_PER_SM * device_sm_count();
   int rows = (a.n_rows + fit - 1) / fit;
@@ -172,16 +162,17 @@ cudaError_t append_rows(const PagedView& c, const AppendArgs& a, const AppendFre
   int threads = AP_THREADS;
   while (rows == 1 && threads < AP_MAX_THREADS && threads < units) threads += 32;
   const int ctas = (a.n_rows + rows - 1) / rows;
-  if (a.rotate)
-    return launch_overlapped(append_kernel<T, true>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
-  return launch_overlapped(append_kernel<T, false>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
+  if (a.rope) return launch_overlapped(append_kernel<T, AP_ROPE>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
+  if (a.rotate) return launch_overlapped(append_kernel<T, AP_THETA>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
+  return launch_overlapped(append_kernel<T, AP_AS_IS>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedView& c, const AppendArgs& a, cudaStream_t st) {
-  AppendFreq fr;
-  if (a.rotate) {
+  qmoe_rope_desc fr{};
+  if (a.rope) fr = *a.rope;
+  if (a.rotate && !a.rope) {
     // powers of the ratio by squares and one product (an error of i half steps of a double at the i-th)
     double inv[128];
     const double ratio = std::pow(a.theta, -2.0 / (double)c.head_dim);
