@@ -4,6 +4,10 @@
 // "CKE Zip: From Splitting Tokens To Splitting Qwen3.5 Weights", "What PR #382
 // Now Splits": 16 query heads over 2 KV heads, causal. Pages and packed rows have
 // no counterpart there.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cfloat>
 #include <cmath>
 
 #include "paged.cuh"
@@ -13,20 +17,17 @@ namespace qmoe {
 
 namespace {
 
-constexpr int PP_THREADS = 128, PP_WARPS = 4;
-
 struct PrefillView {
   PagedView c;
   PrefillArgs a;
-  float scale_log2;
-  int group;
+  float scale_log2;  // scores in units of log2(e)
+  int group;         // query heads of a KV head
 };
 
-// The rows of sequence b: (first row, rows, entries that its first row sees), no
+// The rows of sequence b: (first row, rows, entries, entries before the first row), no
 // rows where they do not lie in the call's.
 struct PrefillRows {
-  int first, count, len;
-  long long before;
+  int first, count, len, before;
 };
 __device__ __forceinline__ PrefillRows prefill_rows(const PrefillView& p, int b) {
   PrefillRows r{p.a.first[b], p.a.count[b], paged_len(p.c, b), 0};
@@ -35,9 +36,787 @@ __device__ __forceinline__ PrefillRows prefill_rows(const PrefillView& p, int b)
     record_status(p.a.status, QMOE_ERR_DEVICE_ARG);
     r.count = 0;
   }
-  r.before = (long long)r.len - r.count;
+  r.before = r.len - r.count;
   return r;
 }
+
+// ---------------------------------------------------------------- work of a CTA
+// A tile is ``span`` positions of a sequence for the query heads of one "head
+// row" (a KV head's heads, or 128 of them at most). All tiles in order, head row by
+// head row, sequence by sequence, are dealt out evenly over the CTAs by their cost,
+// the entries that they see and PF_TILE_COST more; a cut inside a tile falls between
+// key blocks, at least PF_MIN_BLOCKS from its ends. So a CTA has whole tiles, and at
+// most one part of a tile that began in an earlier CTA (slot 0) and one of a tile that
+// goes on in a later one (slot 1); the join kernel puts those together.
+constexpr int PF_KEYS = 128, PF_MIN_BLOCKS = 2, PF_TILE_COST = 256, PF_ITEMS = 4;
+
+struct PfTiling {
+  int span, head_rows, row_heads;  // positions of a tile; head rows in all, of a KV head's heads row_heads each
+  int ctas;
+  int4* desc;  // [CTAs][2] a part of a tile: (sequence or -1, tile, head row, 1 if it is the tile's last)
+};
+
+struct PfItem {
+  int b, t, row, kb0, kb1, first, count, len, before, slot;  // b -1: no more; slot -1: a whole tile
+};
+
+__device__ __forceinline__ long long pf_cost(long long tiles, long long before, int span) {
+  return tiles * (PF_TILE_COST + before) + span * (tiles * (tiles + 1) / 2);
+}
+__device__ __forceinline__ int pf_blocks(const PrefillRows& r, int t, int span) {
+  const int end = r.before + min((t + 1) * span, r.count);
+  return end > 0 ? (end + PF_KEYS - 1) / PF_KEYS : 0;
+}
+
+struct PfCut {
+  int row, b, t, kb;
+};
+
+// The place ``x`` (in units of cost, inside sequence b) cuts the sequence's tiles at.
+__device__ __forceinline__ PfCut pf_cut(const PrefillRows& r, int row, int b, long long x, int span) {
+  const long long before = max(r.before, 0);
+  const double half = PF_TILE_COST + before + 0.5 * span;
+  long long t = (long long)((sqrt(half * half + 2.0 * span * (double)x) - half) / span);
+  const int tiles = (r.count + span - 1) / span;
+  t = max(0ll, min(t, (long long)tiles - 1));
+  while (t > 0 && pf_cost(t, before, span) > x) --t;
+  while (t + 1 < tiles && pf_cost(t + 1, before, span) <= x) ++t;
+  const int blocks = pf_blocks(r, (int)t, span);
+  const long long off = x - pf_cost(t, before, span) - PF_TILE_COST + PF_KEYS / 2;
+  int kb = off > 0 ? (int)(off / PF_KEYS) : 0;
+  if (kb < PF_MIN_BLOCKS) kb = 0;
+  if (blocks - kb < PF_MIN_BLOCKS && kb > 0) return PfCut{row, b, (int)t + 1, 0};
+  return PfCut{row, b, (int)t, kb};
+}
+
+// Where this CTA's work begins and ends, by all threads of the CTA.
+template <int THREADS>
+__device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w, PfCut* cuts, long long* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int WARPS = THREADS / 32;
+  const int each = (p.c.n_seqs + THREADS - 1) / THREADS, b0 = min(tid * each, p.c.n_seqs), b1 = min(b0 + each, p.c.n_seqs);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const PrefillRows r = prefill_rows(p, b);
+    if (r.count > 0) mine += pf_cost((r.count + w.span - 1) / w.span, max(r.before, 0), w.span);
+  }
+  long long v = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  if (lane == 31) sums[warp] = v;
+  if (tid < 2) cuts[tid] = PfCut{w.head_rows, 0, 0, 0};
+  __syncthreads();
+  long long before = v - mine, total = 0;
+  for (int i = 0; i < WARPS; ++i) {
+    if (i < warp) before += sums[i];
+    total += sums[i];
+  }
+  if (total == 0) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = blockIdx.x + k;
+    if (i >= w.ctas) continue;
+    const long long x = total * w.head_rows / w.ctas * i + total * w.head_rows % w.ctas * i / w.ctas;
+    const int row = (int)(x / total);
+    long long at = x - row * total - before;
+    if (row >= w.head_rows || at < 0 || at >= mine) continue;
+    for (int b = b0; b < b1; ++b) {
+      const PrefillRows r = prefill_rows(p, b);
+      const long long cost = r.count > 0 ? pf_cost((r.count + w.span - 1) / w.span, max(r.before, 0), w.span) : 0;
+      if (at < cost) {
+        cuts[k] = pf_cut(r, row, b, at, w.span);
+        break;
+      }
+      at -= cost;
+    }
+  }
+}
+
+// Walks a CTA's share; one warp, whose lanes hold the rows of 32 sequences.
+struct PfWalk {
+  PfCut at, end;
+  PrefillRows mine;
+  int window;
+  bool whole;  // the tile is taken from its first block on
+
+  __device__ __forceinline__ void look(const PrefillView& p, int b) {
+    window = b & ~31;
+    const int s = window + (int)(threadIdx.x & 31);
+    mine = s < p.c.n_seqs ? prefill_rows(p, s) : PrefillRows{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ PrefillRows rows(int b) const {
+    PrefillRows r;
+    r.first = __shfl_sync(0xffffffffu, mine.first, b & 31);
+    r.count = __shfl_sync(0xffffffffu, mine.count, b & 31);
+    r.len = __shfl_sync(0xffffffffu, mine.len, b & 31);
+    r.before = r.len - r.count;
+    return r;
+  }
+  // On to the first tile of the next sequence with rows.
+  __device__ __forceinline__ void next_sequence(const PrefillView& p) {
+    at.t = at.kb = 0;
+    unsigned left = __ballot_sync(0xffffffffu, mine.count > 0) & ~(0xffffffffu >> (31 - (at.b & 31)));
+    while (left == 0) {
+      if (at.row > end.row || (at.row == end.row && window >= end.b)) {  // behind the end already
+        at.row = end.row + 1;
+        return;
+      }
+      int to = window + 32;
+      if (to >= p.c.n_seqs) {
+        to = 0;
+        ++at.row;
+      }
+      look(p, to);
+      left = __ballot_sync(0xffffffffu, mine.count > 0);
+      if (at.row > end.row) return;
+    }
+    at.b = window + __ffs(left) - 1;
+  }
+  __device__ __forceinline__ void begin(const PrefillView& p, const PfCut* cuts) {
+    at = cuts[0];
+    end = cuts[1];
+    look(p, at.b);
+  }
+  // The next item; false: no more.
+  __device__ __forceinline__ bool next(const PrefillView& p, const PfTiling& w, PfItem* item) {
+    for (;;) {
+      if (at.row >= w.head_rows || at.row > end.row) return false;
+      const PrefillRows r = rows(at.b);
+      if ((long long)at.t * w.span >= r.count) {
+        next_sequence(p);
+        continue;
+      }
+      if (at.row == end.row && (at.b > end.b || (at.b == end.b && at.t > end.t))) return false;
+      const bool last = at.row == end.row && at.b == end.b && at.t == end.t;
+      if (last && end.kb == 0) return false;
+      const int blocks = pf_blocks(r, at.t, w.span), to = last ? end.kb : blocks;
+      *item = PfItem{at.b, at.t, at.row, at.kb, to, r.first, r.count, r.len, r.before, -1};
+      if (at.kb > 0)
+        item->slot = 0;
+      else if (to < blocks)
+        item->slot = 1;
+      const bool some = to > at.kb || blocks == 0;
+      if (last)
+        at.row = end.row + 1;
+      else
+        ++at.t;
+      at.kb = 0;
+      if (some) return true;
+    }
+  }
+};
+
+// ---------------------------------------------------------------- tensor cores, bf16 rows
+// A tile is two blocks of 128 query rows (positions x heads of one KV head, so
+// that short parts of prompts fill it too) that share the copies of K and V.
+//   S_j = Q K_j^T   128 rows x 128 keys, Q and K_j in shared memory (128-byte swizzled,
+//                   K-major), fp32 S in tensor memory. One S buffer for both blocks in
+//                   turn: the softmax takes a whole row into its registers (a thread has a row,
+//                   so nothing is exchanged) and frees the buffer before it computes.
+//   P_j             exp2(s - m) rounded to bf16, in tensor memory (64 columns a block), the A operand of
+//   O += P_j V_j    V_j as an MN-major operand, fp32 O in tensor memory.
+// While one block's softmax runs, the tensor core works on the other's products: S of
+// block 0, P V of block 1, S of block 1, P V of block 0, in whatever order their operands
+// come. m is a reference: O and l are rescaled only where a row's maximum exceeds it by more than
+// 2^8. The products are issued from two threads (one thread issues an MMA in about 80 cycles, one
+// of 128 x 128 x 16 takes 64).
+// Warps: 0-3 and 4-7 softmax of block 0 and 1; 8 walks the CTA's work and copies K, 10 copies
+// V, 9 issues S, 11 P V. Every wait is bounded.
+template <int HDP_>
+struct PfCfg {
+  static constexpr int HDP = HDP_, NH = HDP / 64;
+  static constexpr int HALF = 128 * 128;  // 64 head dims of 128 rows
+  static constexpr int TILE = NH * HALF;  // a block of queries, keys or values
+  static constexpr int KST = HDP == 128 ? 2 : 4, VST = HDP == 128 ? 3 : 4;
+  static constexpr int SMEM = 1024 + (2 + KST + VST) * TILE;
+};
+constexpr int PF_THREADS = 384, PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10;
+constexpr uint32_t PF_S_COL = 0, PF_P_COL = 128, PF_O_COL = 256;  // P at + 64 block, O at + HDP block
+constexpr float PF_RESCALE_LOG2 = 8.f;
+
+struct PfArgs {
+  PrefillView p;
+  PfTiling w;
+  float scale;       // of scores, in units of log2(e), at least FLT_MIN
+  uint32_t flip;     // sign bits of q where the scale is negative
+  int box_rows;      // slots of a copy
+  int block_pos;     // positions of a block of 128 query rows
+  float2* part_ml;   // [CTAs][2 slots][256 rows]
+  float* part_o;     // [CTAs][2][256][HDP]
+};
+
+__device__ __forceinline__ void pf_tma(uint32_t dst, const CUtensorMap* map, int dim, int row, int head, int page,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(dim), "r"(row), "r"(head), "r"(page), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// 32 lanes x 32 consecutive 32-bit columns of tensor memory, without the wait.
+__device__ __forceinline__ void pf_ld32(uint32_t ta, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(ta)
+      : "memory");
+}
+// Waits for this thread's loads from tensor memory; the registers pass through, so
+// that no use of them moves ahead of the wait.
+__device__ __forceinline__ void pf_wait_ld(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+// Descriptor of an MN-major operand with 128-byte swizzle: rows of 128 bytes (64
+// values along N) for consecutive K, 8-row atoms of 1024 bytes; the leading byte
+// offset steps to the next 64 values along N, the stride byte offset to the next 8
+// rows along K.
+__device__ __forceinline__ uint64_t pf_mn_desc(uint32_t smem_addr, uint32_t lbo_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// One key block of K or V into a stage: the lanes' pages (PfPages), a copy for each page (or
+// each 128 slots of one) and 64 head dims.
+struct PfPages {
+  int page, row;   // this lane's copy; ``page`` n_pages: out of range, reads zeros
+  uint32_t there;  // bit i: keys 8 i .. 8 i + 7 of the block lie in a page that exists
+};
+__device__ __forceinline__ PfPages pf_pages(const PfArgs& a, const PfItem& it, int kb) {
+  const int lane = threadIdx.x & 31, boxes = PF_KEYS / a.box_rows, slot = kb * PF_KEYS + lane * a.box_rows;
+  const PagedView& c = a.p.c;
+  PfPages r{c.n_pages, 0, 0xFFFFu};
+  bool ok = true;
+  if (lane < boxes && slot < it.len) {
+    const int page = __ldg(c.table + (long long)it.b * c.max_pages + (slot >> c.page_log2));
+    ok = (unsigned)page < (unsigned)c.n_pages;
+    if (ok)
+      r.page = page;
+    else
+      record_status(a.p.a.status, QMOE_ERR_DEVICE_ARG);
+    r.row = slot & ((1 << c.page_log2) - 1);
+  }
+  const unsigned gone = __ballot_sync(0xffffffffu, !ok);
+  if (gone) {
+    const int per = a.box_rows / 8;
+    for (int i = 0; i < boxes; ++i)
+      if ((gone >> i) & 1u) r.there &= ~(((per == 16 ? 0x10000u : 1u << per) - 1u) << (i * per));
+  }
+  return r;
+}
+
+template <class C>
+__device__ __forceinline__ void pf_copy(const PfArgs& a, const PfItem& it, const PfPages& pg, const CUtensorMap* map,
+                                        uint8_t* stage, uint64_t* bar) {
+  const int lane = threadIdx.x & 31, boxes = PF_KEYS / a.box_rows;
+  if (lane == 0) tc::mbar_expect_tx(bar, C::TILE);
+  __syncwarp();
+  if (lane < boxes) {
+    const uint32_t dst = tc::smem_u32(stage) + lane * a.box_rows * 128;
+    const int g = it.row / (a.w.head_rows / a.p.c.n_kv);
+#pragma unroll
+    for (int h = 0; h < C::NH; ++h) pf_tma(dst + h * C::HALF, map, 64 * h, pg.row, g, pg.page, bar);
+  }
+  __syncwarp();
+}
+
+template <class C>
+__global__ void __launch_bounds__(PF_THREADS, 1)
+    prefill_tc_kernel(const PfArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ uint8_t pf_smem_raw[];
+  __shared__ PfCut cuts[2];
+  __shared__ long long sums[PF_THREADS / 32];
+  __shared__ PfItem items[PF_ITEMS];
+  __shared__ uint32_t there[2 * C::KST];
+  __shared__ __align__(8) uint64_t k_full[C::KST], k_empty[C::KST], v_full[C::VST], v_empty[C::VST];
+  __shared__ __align__(8) uint64_t it_full[PF_ITEMS], it_empty[PF_ITEMS];
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], p_free[2], s_free, drain[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  const uint32_t s0 = tc::smem_u32(pf_smem_raw);
+  uint8_t* smem = pf_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
+  uint8_t* sQ = smem;                       // [2 blocks]
+  uint8_t* sK = sQ + 2 * C::TILE;           // [KST]
+  uint8_t* sV = sK + C::KST * C::TILE;      // [VST]
+  volatile int* abort_flag = &abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t lim = a.p.a.wait_ns;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::KST; ++i) {
+      tc::mbar_init(&k_full[i], 1);
+      tc::mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::VST; ++i) {
+      tc::mbar_init(&v_full[i], 1);
+      tc::mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < PF_ITEMS; ++i) {
+      tc::mbar_init(&it_full[i], 1);
+      tc::mbar_init(&it_empty[i], 11);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&q_full[i], 4);
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_full[i], 4);
+      tc::mbar_init(&p_free[i], 1);
+      tc::mbar_init(&drain[i], 1);
+    }
+    tc::mbar_init(&s_free, 4);
+    abort_word = 0;
+    tc::fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
+  if (warp == PF_SWARP) tc::tmem_alloc(&tmem_slot, 512);
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  pf_share<PF_THREADS>(a.p, a.w, cuts, sums);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int hd = a.p.c.head_dim;
+
+  // The next item for a consumer warp (n: items taken so far); false: none, or given up.
+  PfItem it;
+  auto take = [&](int n) -> bool {
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(&it_full[n % PF_ITEMS], (n / PF_ITEMS) & 1, abort_flag, lim))) return false;
+    it = items[n % PF_ITEMS];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&it_empty[n % PF_ITEMS]);
+    return it.b >= 0;
+  };
+
+  // a softmax thread holds a row of 128 scores: 2 x 128 x 208 + 128 x 80 registers of the CTA's 384 x 168
+  if (warp < 8)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int blk = warp >> 2, r = threadIdx.x & 127;
+    const int place = r / a.w.row_heads, hr = r - place * a.w.row_heads;  // position in the block, head in the head row
+    const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t tS = tq + PF_S_COL, tP = tq + PF_P_COL + 64u * blk, tO = tq + PF_O_COL + (uint32_t)(C::HDP * blk);
+    const int group = a.p.group, rows_of_kv = a.w.head_rows / a.p.c.n_kv;
+    uint8_t* q_dst = sQ + blk * C::TILE;
+    const float c = a.scale;
+    int n_blocks = 0;  // key blocks of this block of rows so far
+    int k0 = 0;        // key blocks of the CTA's items before this one
+    bool ok = true;
+    for (int n = 0; ok && take(n); k0 += it.kb1 - it.kb0, ++n) {
+      const int pos = it.t * a.w.span + blk * a.block_pos + place, left = it.count - it.t * a.w.span;
+      if (blk * a.block_pos >= left) continue;  // no rows in this block
+      const int g = it.row / rows_of_kv, h = (it.row - g * rows_of_kv) * a.w.row_heads + hr;
+      const bool valid = place < a.block_pos && pos < it.count && h < group;
+      const long long row_at = ((long long)(it.first + pos) * a.p.a.n_heads + g * group + h) * hd;
+      const int vis = valid ? max(it.before + pos + 1, 0) : 0;
+      float m = -INFINITY, l = 0.f;
+      if (it.kb1 > it.kb0) {
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.p.a.q) + row_at;
+#pragma unroll
+        for (int ch = 0; ch < C::HDP / 8; ++ch) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (valid && 8 * ch < hd) x = *reinterpret_cast<const uint4*>(q + 8 * ch);
+          x.x ^= a.flip; x.y ^= a.flip; x.z ^= a.flip; x.w ^= a.flip;
+          *reinterpret_cast<uint4*>(q_dst + (ch >> 3) * C::HALF + tc::sw128_offset(r, ch & 7)) = x;
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&q_full[blk]);
+      }
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++n_blocks) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&s_full[blk], n_blocks & 1, abort_flag, lim))) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf_ld32(tS + 32 * i, v + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf_wait_ld(v + 32 * i);
+        const int lim_keys = vis - kb * PF_KEYS;  // keys of the block that the row sees
+        const uint32_t exist = there[(k0 + kb - it.kb0) % (2 * C::KST)];
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s_free);
+        if (__any_sync(0xffffffffu, lim_keys < PF_KEYS)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= lim_keys) v[i] = 0xFF800000u;
+        }
+        if (exist != 0xFFFFu) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (!((exist >> (i / 8)) & 1u)) v[i] = 0xFF800000u;
+        }
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 2)
+          mx4[(i >> 1) & 3] = fmaxf(fmaxf(mx4[(i >> 1) & 3], __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+        float alpha = 1.f;
+        const bool need = mx > m + PF_RESCALE_LOG2;
+        if (need) {
+          alpha = exp2f(m - mx);
+          m = mx;
+          l *= alpha;
+        }
+        const bool rescale = kb > it.kb0 && __any_sync(0xffffffffu, need);
+        const float mref = m == -INFINITY ? 0.f : m;
+        const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c));
+        const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
+          const float p0 = exp2f(d.x), p1 = exp2f(d.y);
+          l4[i & 3] += p0 + p1;
+          v[i] = tc::pack_bf16x2(p0, p1);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        // P (and O) are this warp's again once P V of the block before is done
+        if (n_blocks > 0 &&
+            !__all_sync(0xffffffffu, tc::mbar_wait_poll(&p_free[blk], (n_blocks - 1) & 1, abort_flag, lim))) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        if (rescale) {
+#pragma unroll 1
+          for (int i = 0; i < C::HDP / 32; ++i) {
+            uint32_t o[32];
+            pf_ld32(tO + 32 * i, o);
+            pf_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st16(tO + 32 * i, o);
+            tc::tmem_st16(tO + 32 * i + 16, o + 16);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc::tmem_st16(tP + 16 * i, v + 16 * i);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[blk]);
+      }
+      if (!ok) break;
+      // out = O / l, or the part's O, m and l
+      if (it.kb1 > it.kb0) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&p_free[blk], (n_blocks - 1) & 1, abort_flag, lim))) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+      }
+      const float il = l > 0.f ? 1.f / l : 0.f;
+      const long long part = ((long long)blockIdx.x * 2 + it.slot) * 256 + blk * 128 + r;
+      if (it.slot >= 0 && valid) a.part_ml[part] = make_float2(m, l);
+#pragma unroll 1
+      for (int i = 0; i < C::HDP / 32; ++i) {
+        uint32_t o[32];
+        if (it.kb1 > it.kb0) {
+          pf_ld32(tO + 32 * i, o);
+          pf_wait_ld(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (valid && it.slot >= 0) {
+          float* to = a.part_o + part * C::HDP + 32 * i;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(to + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else if (valid) {
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.a.out) + row_at + 32 * i;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = tc::pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * il, __uint_as_float(o[8 * e + 2 * k + 1]) * il);
+            if (32 * i + 8 * e < hd) *reinterpret_cast<uint4*>(out + 8 * e) = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        __syncwarp();
+      }
+      tc::tc_fence_before();
+    }
+  } else if (warp == PF_KWARP) {
+    // ------------------------------------------------------------ the CTA's work, copies of K
+    int4* desc = a.w.desc + 2 * blockIdx.x;
+    if (lane < 2) desc[lane] = make_int4(-1, 0, 0, 0);
+    __syncwarp();
+    PfWalk walk;
+    walk.begin(a.p, cuts);
+    int n = 0, k = 0;
+    bool ok = true, more = true;
+    const bool withhold = a.p.a.fault && blockIdx.x == 0;
+    while (ok && more) {
+      more = walk.next(a.p, a.w, &it);
+      if (!more) it.b = -1;
+      if (n >= PF_ITEMS &&
+          !__all_sync(0xffffffffu, tc::mbar_wait(&it_empty[n % PF_ITEMS], (n / PF_ITEMS - 1) & 1, abort_flag, lim)))
+        break;
+      if (lane == 0) {
+        items[n % PF_ITEMS] = it;
+        if (more && it.slot >= 0) {
+          const PrefillRows rr{it.first, it.count, it.len, it.before};
+          desc[it.slot] = make_int4(it.b, it.t, it.row, it.kb1 == pf_blocks(rr, it.t, a.w.span) ? 1 : 0);
+        }
+        tc::mbar_arrive(&it_full[n % PF_ITEMS]);
+      }
+      __syncwarp();
+      ++n;
+      if (!more) break;
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
+        const PfPages pg = pf_pages(a, it, kb);
+        const int st = k % C::KST;
+        if (k >= C::KST &&
+            !__all_sync(0xffffffffu, tc::mbar_wait(&k_empty[st], (k / C::KST - 1) & 1, abort_flag, lim))) {
+          ok = false;
+          break;
+        }
+        if (withhold && k == 0) {
+          // test-only: never copied
+          volatile int late = 0;
+          tc::mbar_wait(&k_full[0], 0, &late, lim);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        if (lane == 0) there[k % (2 * C::KST)] = pg.there;
+        pf_copy<C>(a, it, pg, &kmap, sK + st * C::TILE, &k_full[st]);
+      }
+    }
+    // copies in flight land before the CTA leaves
+    volatile int never = 0;
+    for (int i = max(0, k - C::KST); i < k; ++i) tc::mbar_wait(&k_full[i % C::KST], (i / C::KST) & 1, &never, lim);
+    __syncwarp();
+  } else if (warp == PF_VWARP) {
+    // ------------------------------------------------------------ copies of V
+    int k = 0;
+    bool ok = true;
+    for (int n = 0; ok && take(n); ++n) {
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
+        const PfPages pg = pf_pages(a, it, kb);
+        const int st = k % C::VST;
+        if (k >= C::VST &&
+            !__all_sync(0xffffffffu, tc::mbar_wait(&v_empty[st], (k / C::VST - 1) & 1, abort_flag, lim))) {
+          ok = false;
+          break;
+        }
+        pf_copy<C>(a, it, pg, &vmap, sV + st * C::TILE, &v_full[st]);
+      }
+    }
+    volatile int never = 0;
+    for (int i = max(0, k - C::VST); i < k; ++i) tc::mbar_wait(&v_full[i % C::VST], (i / C::VST) & 1, &never, lim);
+    __syncwarp();
+  } else if (warp == PF_SWARP) {
+    // ------------------------------------------------------------ S = Q K^T
+    const uint32_t idesc = tc::idesc_bf16_f32(128, PF_KEYS);
+    const int steps = (hd + 15) / 16;
+    int k = 0, u = 0, q_n[2] = {0, 0};
+    bool ok = true;
+    for (int n = 0; ok && take(n); ++n) {
+      const int left = it.count - it.t * a.w.span, blocks = left > a.block_pos ? 2 : 1;
+      for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
+        const int st = k % C::KST;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&k_full[st], (k / C::KST) & 1, abort_flag, lim));
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          if (!ok || blk >= blocks) break;
+          if (kb == it.kb0) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[blk], q_n[blk] & 1, abort_flag, lim));
+            ++q_n[blk];
+          }
+          ok = ok && (u == 0 || __all_sync(0xffffffffu, tc::mbar_wait_poll(&s_free, (u - 1) & 1, abort_flag, lim)));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (lane == 0) {
+            const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + blk * C::TILE));
+            const uint64_t kd = tc::sw128_desc(tc::smem_u32(sK + st * C::TILE));
+            for (int kk = 0; kk < steps; ++kk) {
+              const uint64_t off = (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3));
+              tc::mma_bf16(tmem + PF_S_COL, qd + off, kd + off, idesc, kk != 0);
+            }
+            tc::mma_commit(&s_full[blk]);
+            if (blk == blocks - 1) tc::mma_commit(&k_empty[st]);
+          }
+          __syncwarp();
+          ++u;
+        }
+      }
+    }
+    if (lane == 0) {
+      tc::mma_commit(&drain[0]);
+      volatile int never = 0;
+      tc::mbar_wait(&drain[0], 0, &never, lim);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ O += P V
+    const uint32_t idesc = tc::idesc_bf16_f32(128, (hd + 15) / 16 * 16) | (1u << 16);  // B (V) MN-major
+    int k = 0, p_n[2] = {0, 0};
+    bool ok = true;
+    for (int n = 0; ok && take(n); ++n) {
+      const int left = it.count - it.t * a.w.span, blocks = left > a.block_pos ? 2 : 1;
+      for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
+        const int st = k % C::VST;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&v_full[st], (k / C::VST) & 1, abort_flag, lim));
+        if (!ok) break;
+        uint8_t* vs = sV + st * C::TILE;
+        // rows behind the sequence's last entry may hold anything, NaN too: zero weights need zero values
+        if (it.len - kb * PF_KEYS < PF_KEYS) {
+          const int r0 = it.len - kb * PF_KEYS;
+          for (int i = 8 * r0 + lane; i < 8 * 128; i += 32) {
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h)
+              *reinterpret_cast<uint4*>(vs + h * C::HALF + 16 * i) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          if (!ok || blk >= blocks) break;
+          ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&p_full[blk], p_n[blk] & 1, abort_flag, lim));
+          if (!ok) break;
+          ++p_n[blk];
+          tc::tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < PF_KEYS / 16; ++kk)
+              tc::mma_bf16_ts(tmem + PF_O_COL + (uint32_t)(C::HDP * blk), tmem + PF_P_COL + 64u * blk + 8u * kk,
+                              pf_mn_desc(tc::smem_u32(vs) + 2048u * kk, C::HALF), idesc, kb > it.kb0 || kk != 0);
+            tc::mma_commit(&p_free[blk]);
+            if (blk == blocks - 1) tc::mma_commit(&v_empty[st]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) {
+      tc::mma_commit(&drain[1]);
+      volatile int never = 0;
+      tc::mbar_wait(&drain[1], 0, &never, lim);
+    }
+    __syncwarp();
+  }
+
+  if (*abort_flag && threadIdx.x == 0) record_status(a.p.a.status, QMOE_ERR_TIMEOUT);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == PF_SWARP) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- parts of tiles
+// A tile that begins in CTA x and goes on: its parts, in order of the CTAs, joined by
+// their maxima. A warp has a row; the lanes take 32 parts' weights at a time.
+constexpr int PJ_THREADS = 256, PJ_SPLIT = 4;
+constexpr int PF_MAX_CTAS = 256;  // the workspace does not depend on the device
+
+struct PfJoin {
+  PrefillView p;
+  PfTiling w;
+  int block_pos, blocks, hdp;  // positions of a block of 128 rows, blocks of a tile
+  const float2* part_ml;
+  const float* part_o;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j) {
+  __shared__ int parts[PF_MAX_CTAS], n_parts;
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  const int4 d = j.w.desc[2 * blockIdx.x + 1];
+  if (d.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hd = j.p.c.head_dim;
+  if (warp == 0) {
+    int n = 1;
+    if (lane == 0) parts[0] = 2 * blockIdx.x + 1;
+    bool open = true;
+    for (int x = blockIdx.x + 1; open && x < j.w.ctas; x += 32) {
+      const int4 e = x + lane < j.w.ctas ? j.w.desc[2 * (x + lane)] : make_int4(-1, 0, 0, 0);
+      const bool mine = e.x == d.x && e.y == d.y && e.z == d.z;
+      unsigned have = __ballot_sync(0xffffffffu, mine);
+      const unsigned last = __ballot_sync(0xffffffffu, mine && e.w);
+      if (last) {
+        have &= 0xffffffffu >> (32 - __ffs(last));
+        open = false;
+      }
+      if ((have >> lane) & 1u) parts[n + __popc(have & ((1u << lane) - 1u))] = 2 * (x + lane);
+      n += __popc(have);
+    }
+    if (lane == 0) n_parts = n;
+  }
+  __syncthreads();
+  const int n = n_parts, rows_of_kv = j.w.head_rows / j.p.c.n_kv, g = d.z / rows_of_kv;
+  const PrefillRows r = prefill_rows(j.p, d.x);
+  for (int row = blockIdx.y * (PJ_THREADS / 32) + warp; row < 128 * j.blocks; row += PJ_SPLIT * (PJ_THREADS / 32)) {
+    const int in = row & 127, place = in / j.w.row_heads;
+    const int pos = d.y * j.w.span + (row >> 7) * j.block_pos + place;
+    const int h = (d.z - g * rows_of_kv) * j.w.row_heads + in - place * j.w.row_heads;
+    if (place >= j.block_pos || pos >= r.count || h >= j.p.group) continue;
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, j.part_ml[(long long)parts[i] * 256 + row].x);
+#pragma unroll
+    for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float wgt = 0.f;
+      if (i0 + lane < n) {
+        const float2 ml = j.part_ml[(long long)parts[i0 + lane] * 256 + row];
+        wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+        l += wgt * ml.y;
+      }
+      const int many = min(32, n - i0);
+#pragma unroll 4
+      for (int i = 0; i < many; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wgt, i);
+        if (wi == 0.f) continue;
+        const float* o = j.part_o + ((long long)parts[i0 + i] * 256 + row) * j.hdp;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (lane + 32 * e < hd) acc[e] = fmaf(wi, o[lane + 32 * e], acc[e]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float il = l > 0.f ? 1.f / l : 0.f;
+    T* out = static_cast<T*>(j.p.a.out) + ((long long)(r.first + pos) * j.p.a.n_heads + g * j.p.group + h) * hd;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (lane + 32 * e < hd) out[lane + 32 * e] = (T)(acc[e] * il);
+  }
+}
+
+// ---------------------------------------------------------------- any head size
+constexpr int PP_THREADS = 128, PP_WARPS = 4;
 
 // A warp has one row and head: a lane scores one key of 32 at a time, then all
 // lanes add the 32 values, a part of the head dims each.
@@ -49,8 +828,6 @@ __global__ void __launch_bounds__(PP_THREADS) prefill_rows_kernel(const PrefillV
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hd = p.c.head_dim;
   const PrefillRows r = prefill_rows(p, blockIdx.y);
   const int32_t* table = p.c.table + (long long)blockIdx.y * p.c.max_pages;
-  const int items = p.a.n_heads * gridDim.x * PP_WARPS;
-  (void)items;
   for (long long it = (long long)blockIdx.x * PP_WARPS + warp; it < (long long)r.count * p.a.n_heads;
        it += (long long)gridDim.x * PP_WARPS) {
     const int i = (int)(it / p.a.n_heads), h = (int)(it - (long long)i * p.a.n_heads), g = h / p.group;
@@ -59,8 +836,7 @@ __global__ void __launch_bounds__(PP_THREADS) prefill_rows_kernel(const PrefillV
     __syncwarp();
     for (int d = lane; d < hd; d += 32) sq[warp][d] = (float)q[d];
     __syncwarp();
-    const long long sees = r.before + i + 1;
-    const int n = sees < 0 ? 0 : (int)sees;
+    const int n = max(r.before + i + 1, 0);
     float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int j0 = 0; j0 < n; j0 += 32) {
       const int j = j0 + lane;
@@ -114,19 +890,107 @@ __global__ void __launch_bounds__(PP_THREADS) prefill_rows_kernel(const PrefillV
   }
 }
 
+// ---------------------------------------------------------------- host
+struct PfPlan {
+  bool tc;          // on the tensor cores
+  int hdp, row_heads, row_tiles, block_pos, blocks, span, ctas;
+  bool cuts;        // tiles may be cut between CTAs
+  size_t desc, ml, o, total;
+};
+
+size_t pf_up(size_t v) { return (v + 255) & ~size_t(255); }
+
+PfPlan pf_plan(const PagedView& c, int n_rows, int n_heads, bool f32) {
+  PfPlan p{};
+  const int group = n_heads / c.n_kv;
+  p.tc = c.head_dim <= 128 && !f32;
+  p.hdp = c.head_dim <= 64 ? 64 : 128;
+  p.blocks = 2;
+  p.row_tiles = (group + 127) / 128;
+  p.row_heads = (group + p.row_tiles - 1) / p.row_tiles;
+  p.block_pos = 128 / p.row_heads;
+  p.span = p.blocks * p.block_pos;
+  const long long seqs = c.n_seqs < n_rows ? c.n_seqs : n_rows;
+  const long long tiles = ((long long)n_rows / p.span + seqs) * c.n_kv * p.row_tiles;
+  const long long keys = (paged_slots(c) + PF_KEYS - 1) / PF_KEYS;
+  p.cuts = keys >= 2 * PF_MIN_BLOCKS;
+  const long long pieces = tiles * (p.cuts ? keys / PF_MIN_BLOCKS : 1);
+  p.ctas = pieces < 1 ? 1 : pieces < PF_MAX_CTAS ? (int)pieces : PF_MAX_CTAS;
+  size_t o = 0;
+  p.desc = o; o += pf_up(sizeof(int4) * 2 * (size_t)p.ctas);
+  p.ml = o;   o += p.cuts ? pf_up(sizeof(float2) * 512 * (size_t)p.ctas) : 0;
+  p.o = o;    o += p.cuts ? pf_up(sizeof(float) * 512 * (size_t)p.hdp * p.ctas) : 0;
+  p.total = p.tc ? o : 256;
+  return p;
+}
+
+// A pool as a tensor map [head dim][slot of a page][KV head][page], boxes of 64 head
+// dims (those from head_dim on read as zero) by ``box_rows`` slots, 128-byte swizzled.
+bool pf_encode(CUtensorMap* m, const void* base, const PagedView& c, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t ss = (cuuint64_t)c.slot_stride * 2;
+  // (a dimension of one element never steps: its stride may be anything that is valid)
+  const cuuint64_t strides[3] = {ss, c.n_kv > 1 ? (cuuint64_t)c.head_stride * 2 : ss,
+                                 c.n_pages > 1 ? (cuuint64_t)c.page_stride * 2 : ss};
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)1 << c.page_log2, (cuuint64_t)c.n_kv,
+                              (cuuint64_t)c.n_pages};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t launch_tc(PfArgs& x, cudaStream_t st) {
+  const PagedView& c = x.p.c;
+  x.box_rows = 1 << c.page_log2 < PF_KEYS ? 1 << c.page_log2 : PF_KEYS;
+  CUtensorMap km, vm;
+  if (!pf_encode(&km, c.k, c, x.box_rows) || !pf_encode(&vm, c.v, c, x.box_rows)) return cudaErrorInvalidValue;
+  cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(prefill_tc_kernel<C>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(prefill_tc_kernel<C>, dim3(x.w.ctas), PF_THREADS, C::SMEM, 0, st, x, km, vm);
+}
+
 }  // namespace
 
-size_t paged_prefill_ws_bytes(const PagedView&, int, int) { return 256; }
+size_t paged_prefill_ws_bytes(const PagedView& c, int n_rows, int n_heads) {
+  const size_t a = pf_plan(c, n_rows, n_heads, false).total, b = pf_plan(c, n_rows, n_heads, true).total;
+  return a > b ? a : b;
+}
 
-int paged_prefill_launches(const PagedView&, const PrefillArgs&) { return 1; }
+int paged_prefill_launches(const PagedView& c, const PrefillArgs& a) {
+  const PfPlan pl = pf_plan(c, a.n_rows, a.n_heads, a.f32);
+  return pl.tc && pl.cuts ? 2 : 1;
+}
 
 cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaStream_t st) {
+  const PfPlan pl = pf_plan(c, a.n_rows, a.n_heads, a.f32);
   PrefillView p{c, a, a.scale * 1.4426950408889634f, a.n_heads / c.n_kv};
-  long long ctas = ((long long)a.n_rows * a.n_heads + PP_WARPS - 1) / PP_WARPS;
-  if (ctas > 16384) ctas = 16384;
-  const dim3 grid((unsigned)ctas, (unsigned)c.n_seqs);
-  return a.f32 ? launch_overlapped(prefill_rows_kernel<float>, grid, PP_THREADS, 0, 0, st, p)
-               : launch_overlapped(prefill_rows_kernel<__nv_bfloat16>, grid, PP_THREADS, 0, 0, st, p);
+  if (!pl.tc) {
+    long long ctas = ((long long)a.n_rows * a.n_heads + PP_WARPS - 1) / PP_WARPS;
+    if (ctas > 16384) ctas = 16384;
+    const dim3 grid((unsigned)ctas, (unsigned)c.n_seqs);
+    return a.f32 ? launch_overlapped(prefill_rows_kernel<float>, grid, PP_THREADS, 0, 0, st, p)
+                 : launch_overlapped(prefill_rows_kernel<__nv_bfloat16>, grid, PP_THREADS, 0, 0, st, p);
+  }
+  char* ws = static_cast<char*>(a.ws);
+  PfArgs x{};
+  x.p = p;
+  x.w.span = pl.span;
+  x.w.head_rows = c.n_kv * pl.row_tiles;
+  x.w.row_heads = pl.row_heads;
+  x.w.ctas = device_sm_count() < pl.ctas ? device_sm_count() : pl.ctas;
+  x.w.desc = reinterpret_cast<int4*>(ws + pl.desc);
+  x.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
+  x.part_o = reinterpret_cast<float*>(ws + pl.o);
+  x.block_pos = pl.block_pos;
+  x.scale = fminf(fmaxf(fabsf(p.scale_log2), FLT_MIN), FLT_MAX);
+  x.flip = a.scale < 0.f ? 0x80008000u : 0u;
+  cudaError_t e = pl.hdp == 64 ? launch_tc<PfCfg<64>>(x, st) : launch_tc<PfCfg<128>>(x, st);
+  if (e != cudaSuccess || !pl.cuts) return e;
+  PfJoin j{p, x.w, pl.block_pos, pl.blocks, pl.hdp, x.part_ml, x.part_o};
+  return launch_overlapped(prefill_join_kernel<__nv_bfloat16>, dim3(x.w.ctas, PJ_SPLIT), PJ_THREADS, 0, 0, st, j);
 }
 
 }  // namespace qmoe
