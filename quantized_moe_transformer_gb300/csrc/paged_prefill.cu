@@ -225,16 +225,24 @@ struct PfWalk {
 // of 128 x 128 x 16 takes 64).
 // Warps: 0-3 and 4-7 softmax of block 0 and 1; 8 walks the CTA's work and copies K, 10 copies
 // V, 9 issues S, 11 P V. Every wait is bounded.
-template <int HDP_>
+// fp32 rows: a tile is one block of 128 rows, q and each probability are three bf16 parts
+// (24 bits), so S and P V take three products each, small parts first. P V of a key block goes into
+// a fresh accumulator; warps 4-7 add it, rounded, to the output in their registers (a thread has
+// a row), so nothing is cut off over a long axis.
+template <int HDP_, bool F32_>
 struct PfCfg {
+  static constexpr bool F32 = F32_;
   static constexpr int HDP = HDP_, NH = HDP / 64;
+  static constexpr int BLOCKS = F32 ? 1 : 2, PARTS = F32 ? 3 : 1;
+  static constexpr int QT = F32 ? 3 : 2;  // blocks or parts of queries
   static constexpr int HALF = 128 * 128;  // 64 head dims of 128 rows
   static constexpr int TILE = NH * HALF;  // a block of queries, keys or values
-  static constexpr int KST = HDP == 128 ? 2 : 4, VST = HDP == 128 ? 3 : 4;
-  static constexpr int SMEM = 1024 + (2 + KST + VST) * TILE;
+  static constexpr int KST = HDP == 128 ? 2 : 4, VST = HDP == 128 ? (F32 ? 2 : 3) : 4;
+  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE;
+  static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;  // P at + 64 block or part, O at + HDP block
 };
 constexpr int PF_THREADS = 384, PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10;
-constexpr uint32_t PF_S_COL = 0, PF_P_COL = 128, PF_O_COL = 256;  // P at + 64 block, O at + HDP block
+constexpr uint32_t PF_S_COL = 0;
 constexpr float PF_RESCALE_LOG2 = 8.f;
 
 struct PfArgs {
@@ -340,6 +348,210 @@ __device__ __forceinline__ void pf_copy(const PfArgs& a, const PfItem& it, const
   __syncwarp();
 }
 
+// Row ``r`` of a block of 128: its position, query head and where it lies.
+struct PfRow {
+  int pos, vis;  // vis: entries that it sees (0 where the row is none)
+  bool valid;
+  long long at;  // element of q and out
+};
+__device__ __forceinline__ PfRow pf_row(const PfArgs& a, const PfItem& it, int blk, int r) {
+  const int place = r / a.w.row_heads, rows_of_kv = a.w.head_rows / a.p.c.n_kv, g = it.row / rows_of_kv;
+  const int h = (it.row - g * rows_of_kv) * a.w.row_heads + r - place * a.w.row_heads;
+  PfRow x;
+  x.pos = it.t * a.w.span + blk * a.block_pos + place;
+  x.valid = place < a.block_pos && x.pos < it.count && h < a.p.group;
+  x.vis = x.valid ? max(it.before + x.pos + 1, 0) : 0;
+  x.at = ((long long)(it.first + x.pos) * a.p.a.n_heads + g * a.p.group + h) * a.p.c.head_dim;
+  return x;
+}
+
+// Scores that a row does not see: those from ``seen`` on, and those of missing pages.
+__device__ __forceinline__ void pf_mask(uint32_t* v, int seen, uint32_t exist) {
+  if (__any_sync(0xffffffffu, seen < PF_KEYS)) {
+#pragma unroll
+    for (int i = 0; i < PF_KEYS; ++i)
+      if (i >= seen) v[i] = 0xFF800000u;
+  }
+  if (exist != 0xFFFFu) {
+#pragma unroll
+    for (int i = 0; i < PF_KEYS; ++i)
+      if (!((exist >> (i / 8)) & 1u)) v[i] = 0xFF800000u;
+  }
+}
+
+__device__ __forceinline__ float pf_max(const uint32_t* v) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < PF_KEYS; i += 2)
+    m[(i >> 1) & 3] = fmaxf(fmaxf(m[(i >> 1) & 3], __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Warps 0-7 of a tile of fp32 rows.
+template <class C, class Take>
+__device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, const PfItem& it, uint32_t tmem, uint8_t* sQ,
+                                                 const uint32_t* there, uint64_t* q_full, uint64_t* s_full,
+                                                 uint64_t* s_free, uint64_t* p_full, uint64_t* p_free, uint64_t* o_read,
+                                                 uint64_t* l_full, float (*factor)[C::F32 ? 128 : 1], volatile int* abort_flag) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127, hd = a.p.c.head_dim;
+  const uint64_t lim = a.p.a.wait_ns;
+  const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::O_COL;
+  const float c = a.scale;
+  int j = 0;   // key blocks so far
+  int nl = 0;  // items with key blocks so far
+  bool ok = true;
+  if (warp < 4) {
+    for (int n = 0; ok && take(n); ++n) {
+      const PfRow row = pf_row(a, it, 0, r);
+      if (it.kb1 <= it.kb0) continue;
+      // q as three bf16 parts, which hold all its bits
+      const float* q = static_cast<const float*>(a.p.a.q) + row.at;
+#pragma unroll 4
+      for (int ch = 0; ch < C::HDP / 8; ++ch) {
+        uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (row.valid && 8 * ch < hd) {
+          const uint4 lo = *reinterpret_cast<const uint4*>(q + 8 * ch), hi = *reinterpret_cast<const uint4*>(q + 8 * ch + 4);
+          x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+          x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+        }
+        const uint32_t at = (ch >> 3) * C::HALF + tc::sw128_offset(r, ch & 7);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(x[e] ^ (a.flip & 0x80000000u));
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = tc::pack_bf16x2(f[2 * e], f[2 * e + 1]);
+            f[2 * e] -= __uint_as_float(w[e] << 16);
+            f[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
+          }
+          *reinterpret_cast<uint4*>(sQ + part * C::TILE + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_full);
+      float m = -INFINITY, l = 0.f;
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(s_full, j & 1, abort_flag, lim))) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        uint32_t v[PF_KEYS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf_ld32(tq + PF_S_COL + 32 * i, v + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf_wait_ld(v + 32 * i);
+        const uint32_t exist = there[j % (2 * C::KST)];
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(s_free);
+        pf_mask(v, row.vis - kb * PF_KEYS, exist);
+        const float mx = pf_max(v) * c;
+        float alpha = 1.f;
+        if (mx > m + PF_RESCALE_LOG2) {
+          alpha = exp2f(m - mx);
+          m = mx;
+          l *= alpha;
+        }
+        const float mref = m == -INFINITY ? 0.f : m;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < PF_KEYS; ++i) {
+          const float x = exp2f(fmaf(__uint_as_float(v[i]), c, -mref));
+          l4[i & 3] += x;
+          v[i] = __float_as_uint(x);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        // P is this warp's again once P V of the block before is done
+        if (j > 0 && !__all_sync(0xffffffffu, tc::mbar_wait_poll(p_free, (j - 1) & 1, abort_flag, lim))) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        if (kb > it.kb0) factor[j & 1][r] = alpha;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x0 = __uint_as_float(v[32 * i + 2 * e]), x1 = __uint_as_float(v[32 * i + 2 * e + 1]);
+              w[e] = tc::pack_bf16x2(x0, x1);
+              if (part < 2) {
+                v[32 * i + 2 * e] = __float_as_uint(x0 - __uint_as_float(w[e] << 16));
+                v[32 * i + 2 * e + 1] = __float_as_uint(x1 - __uint_as_float(w[e] & 0xFFFF0000u));
+              }
+            }
+            tc::tmem_st16(tq + C::P_COL + 64 * part + 16 * i, w);
+          }
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      // the slot of the block before the last is read once P V of the last is done: the sums take 1 / l from there
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(p_free, (j - 1) & 1, abort_flag, lim))) break;
+      factor[j & 1][r] = l > 0.f ? 1.f / l : 0.f;
+      if (it.slot >= 0 && row.valid) a.part_ml[((long long)blockIdx.x * 2 + it.slot) * 256 + r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(l_full);
+    }
+    return;
+  }
+  for (int n = 0; ok && take(n); ++n) {
+    const PfRow row = pf_row(a, it, 0, r);
+    float acc[C::HDP];
+#pragma unroll
+    for (int i = 0; i < C::HDP; ++i) acc[i] = 0.f;
+    for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(p_free, j & 1, abort_flag, lim))) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const float alpha = kb > it.kb0 ? factor[j & 1][r] : 0.f;
+#pragma unroll
+      for (int i = 0; i < C::HDP / 32; ++i) {
+        uint32_t o[32];
+        pf_ld32(tO + 32 * i, o);
+        pf_wait_ld(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[32 * i + e] = fmaf(acc[32 * i + e], alpha, __uint_as_float(o[e]));
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(o_read);
+    }
+    if (!ok) break;
+    float il = 0.f;
+    if (it.kb1 > it.kb0) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(l_full, nl & 1, abort_flag, lim))) break;
+      ++nl;
+      il = factor[j & 1][r];
+    }
+    if (!row.valid) continue;
+    if (it.slot >= 0) {
+      float* to = a.part_o + (((long long)blockIdx.x * 2 + it.slot) * 256 + r) * C::HDP;
+#pragma unroll
+      for (int i = 0; i < C::HDP; i += 4)
+        *reinterpret_cast<float4*>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    } else {
+      float* out = static_cast<float*>(a.p.a.out) + row.at;
+#pragma unroll
+      for (int i = 0; i < C::HDP; i += 4)
+        if (i < hd)
+          *reinterpret_cast<float4*>(out + i) = make_float4(acc[i] * il, acc[i + 1] * il, acc[i + 2] * il, acc[i + 3] * il);
+    }
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(PF_THREADS, 1)
     prefill_tc_kernel(const PfArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -351,12 +563,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   __shared__ __align__(8) uint64_t k_full[C::KST], k_empty[C::KST], v_full[C::VST], v_empty[C::VST];
   __shared__ __align__(8) uint64_t it_full[PF_ITEMS], it_empty[PF_ITEMS];
   __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], p_free[2], s_free, drain[2];
+  __shared__ float factor[C::F32 ? 2 : 1][C::F32 ? 128 : 1];  // fp32 rows: O's factor at a key block; at the end 1 / l
+  __shared__ __align__(8) uint64_t o_read, l_full;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t s0 = tc::smem_u32(pf_smem_raw);
   uint8_t* smem = pf_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
-  uint8_t* sQ = smem;                       // [2 blocks]
-  uint8_t* sK = sQ + 2 * C::TILE;           // [KST]
+  uint8_t* sQ = smem;                       // [2 blocks] or [3 parts]
+  uint8_t* sK = sQ + C::QT * C::TILE;       // [KST]
   uint8_t* sV = sK + C::KST * C::TILE;      // [VST]
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -383,6 +597,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       tc::mbar_init(&drain[i], 1);
     }
     tc::mbar_init(&s_free, 4);
+    tc::mbar_init(&o_read, 4);
+    tc::mbar_init(&l_full, 4);
     abort_word = 0;
     tc::fence_barrier_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
@@ -413,28 +629,27 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   else
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp < 8) {
+  if (C::F32 && warp < 8) {
+    // ------------------------------------------------------------ fp32 rows: softmax (warps 0-3), sums (4-7)
+    prefill_f32_rows<C>(a, take, it, tmem, sQ, there, &q_full[0], &s_full[0], &s_free, &p_full[0], &p_free[0], &o_read,
+                        &l_full, factor, abort_flag);
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
     const int blk = warp >> 2, r = threadIdx.x & 127;
-    const int place = r / a.w.row_heads, hr = r - place * a.w.row_heads;  // position in the block, head in the head row
     const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t tS = tq + PF_S_COL, tP = tq + PF_P_COL + 64u * blk, tO = tq + PF_O_COL + (uint32_t)(C::HDP * blk);
-    const int group = a.p.group, rows_of_kv = a.w.head_rows / a.p.c.n_kv;
+    const uint32_t tS = tq + PF_S_COL, tP = tq + C::P_COL + 64u * blk, tO = tq + C::O_COL + (uint32_t)(C::HDP * blk);
     uint8_t* q_dst = sQ + blk * C::TILE;
     const float c = a.scale;
     int n_blocks = 0;  // key blocks of this block of rows so far
     int k0 = 0;        // key blocks of the CTA's items before this one
     bool ok = true;
     for (int n = 0; ok && take(n); k0 += it.kb1 - it.kb0, ++n) {
-      const int pos = it.t * a.w.span + blk * a.block_pos + place, left = it.count - it.t * a.w.span;
-      if (blk * a.block_pos >= left) continue;  // no rows in this block
-      const int g = it.row / rows_of_kv, h = (it.row - g * rows_of_kv) * a.w.row_heads + hr;
-      const bool valid = place < a.block_pos && pos < it.count && h < group;
-      const long long row_at = ((long long)(it.first + pos) * a.p.a.n_heads + g * group + h) * hd;
-      const int vis = valid ? max(it.before + pos + 1, 0) : 0;
+      if (blk * a.block_pos >= it.count - it.t * a.w.span) continue;  // no rows in this block
+      const PfRow row = pf_row(a, it, blk, r);
+      const bool valid = row.valid;
       float m = -INFINITY, l = 0.f;
       if (it.kb1 > it.kb0) {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.p.a.q) + row_at;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.p.a.q) + row.at;
 #pragma unroll
         for (int ch = 0; ch < C::HDP / 8; ++ch) {
           uint4 x = make_uint4(0, 0, 0, 0);
@@ -457,26 +672,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int i = 0; i < 4; ++i) pf_ld32(tS + 32 * i, v + 32 * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) pf_wait_ld(v + 32 * i);
-        const int lim_keys = vis - kb * PF_KEYS;  // keys of the block that the row sees
         const uint32_t exist = there[(k0 + kb - it.kb0) % (2 * C::KST)];
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&s_free);
-        if (__any_sync(0xffffffffu, lim_keys < PF_KEYS)) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= lim_keys) v[i] = 0xFF800000u;
-        }
-        if (exist != 0xFFFFu) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (!((exist >> (i / 8)) & 1u)) v[i] = 0xFF800000u;
-        }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 128; i += 2)
-          mx4[(i >> 1) & 3] = fmaxf(fmaxf(mx4[(i >> 1) & 3], __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+        pf_mask(v, row.vis - kb * PF_KEYS, exist);
+        const float mx = pf_max(v) * c;
         float alpha = 1.f;
         const bool need = mx > m + PF_RESCALE_LOG2;
         if (need) {
@@ -551,7 +752,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint4*>(to + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         } else if (valid) {
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.a.out) + row_at + 32 * i;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.a.out) + row.at + 32 * i;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t x[4];
@@ -642,12 +843,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     int k = 0, u = 0, q_n[2] = {0, 0};
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int left = it.count - it.t * a.w.span, blocks = left > a.block_pos ? 2 : 1;
+      const int left = it.count - it.t * a.w.span, blocks = C::BLOCKS == 2 && left > a.block_pos ? 2 : 1;
       for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
         const int st = k % C::KST;
         ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&k_full[st], (k / C::KST) & 1, abort_flag, lim));
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
+        for (int blk = 0; blk < C::BLOCKS; ++blk) {
           if (!ok || blk >= blocks) break;
           if (kb == it.kb0) {
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[blk], q_n[blk] & 1, abort_flag, lim));
@@ -657,11 +858,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (!ok) break;
           tc::tc_fence_after();
           if (lane == 0) {
-            const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + blk * C::TILE));
             const uint64_t kd = tc::sw128_desc(tc::smem_u32(sK + st * C::TILE));
-            for (int kk = 0; kk < steps; ++kk) {
-              const uint64_t off = (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3));
-              tc::mma_bf16(tmem + PF_S_COL, qd + off, kd + off, idesc, kk != 0);
+#pragma unroll
+            for (int part = C::PARTS - 1; part >= 0; --part) {
+              const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + (blk + part) * C::TILE));
+              for (int kk = 0; kk < steps; ++kk) {
+                const uint64_t off = (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3));
+                tc::mma_bf16(tmem + PF_S_COL, qd + off, kd + off, idesc, part != C::PARTS - 1 || kk != 0);
+              }
             }
             tc::mma_commit(&s_full[blk]);
             if (blk == blocks - 1) tc::mma_commit(&k_empty[st]);
@@ -683,7 +887,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     int k = 0, p_n[2] = {0, 0};
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int left = it.count - it.t * a.w.span, blocks = left > a.block_pos ? 2 : 1;
+      const int left = it.count - it.t * a.w.span, blocks = C::BLOCKS == 2 && left > a.block_pos ? 2 : 1;
       for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
         const int st = k % C::VST;
         ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&v_full[st], (k / C::VST) & 1, abort_flag, lim));
@@ -701,17 +905,24 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           __syncwarp();
         }
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
+        for (int blk = 0; blk < C::BLOCKS; ++blk) {
           if (!ok || blk >= blocks) break;
           ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&p_full[blk], p_n[blk] & 1, abort_flag, lim));
+          if (C::F32 && ok && p_n[0] > 0)
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&o_read, (p_n[0] - 1) & 1, abort_flag, lim));
           if (!ok) break;
           ++p_n[blk];
           tc::tc_fence_after();
           if (lane == 0) {
 #pragma unroll
-            for (int kk = 0; kk < PF_KEYS / 16; ++kk)
-              tc::mma_bf16_ts(tmem + PF_O_COL + (uint32_t)(C::HDP * blk), tmem + PF_P_COL + 64u * blk + 8u * kk,
-                              pf_mn_desc(tc::smem_u32(vs) + 2048u * kk, C::HALF), idesc, kb > it.kb0 || kk != 0);
+            for (int part = C::PARTS - 1; part >= 0; --part) {
+#pragma unroll
+              for (int kk = 0; kk < PF_KEYS / 16; ++kk)
+                tc::mma_bf16_ts(tmem + C::O_COL + (uint32_t)(C::HDP * blk),
+                                tmem + C::P_COL + 64u * (blk + part) + 8u * kk,
+                                pf_mn_desc(tc::smem_u32(vs) + 2048u * kk, C::HALF), idesc,
+                                part != C::PARTS - 1 || kk != 0 || (!C::F32 && kb > it.kb0));
+            }
             tc::mma_commit(&p_free[blk]);
             if (blk == blocks - 1) tc::mma_commit(&v_empty[st]);
           }
@@ -903,9 +1114,9 @@ size_t pf_up(size_t v) { return (v + 255) & ~size_t(255); }
 PfPlan pf_plan(const PagedView& c, int n_rows, int n_heads, bool f32) {
   PfPlan p{};
   const int group = n_heads / c.n_kv;
-  p.tc = c.head_dim <= 128 && !f32;
+  p.tc = c.head_dim <= 128;
   p.hdp = c.head_dim <= 64 ? 64 : 128;
-  p.blocks = 2;
+  p.blocks = f32 ? 1 : 2;
   p.row_tiles = (group + 127) / 128;
   p.row_heads = (group + p.row_tiles - 1) / p.row_tiles;
   p.block_pos = 128 / p.row_heads;
@@ -987,10 +1198,13 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.block_pos = pl.block_pos;
   x.scale = fminf(fmaxf(fabsf(p.scale_log2), FLT_MIN), FLT_MAX);
   x.flip = a.scale < 0.f ? 0x80008000u : 0u;
-  cudaError_t e = pl.hdp == 64 ? launch_tc<PfCfg<64>>(x, st) : launch_tc<PfCfg<128>>(x, st);
+  cudaError_t e = a.f32 ? (pl.hdp == 64 ? launch_tc<PfCfg<64, true>>(x, st) : launch_tc<PfCfg<128, true>>(x, st))
+                        : (pl.hdp == 64 ? launch_tc<PfCfg<64, false>>(x, st) : launch_tc<PfCfg<128, false>>(x, st));
   if (e != cudaSuccess || !pl.cuts) return e;
   PfJoin j{p, x.w, pl.block_pos, pl.blocks, pl.hdp, x.part_ml, x.part_o};
-  return launch_overlapped(prefill_join_kernel<__nv_bfloat16>, dim3(x.w.ctas, PJ_SPLIT), PJ_THREADS, 0, 0, st, j);
+  const dim3 grid(x.w.ctas, PJ_SPLIT);
+  return a.f32 ? launch_overlapped(prefill_join_kernel<float>, grid, PJ_THREADS, 0, 0, st, j)
+               : launch_overlapped(prefill_join_kernel<__nv_bfloat16>, grid, PJ_THREADS, 0, 0, st, j);
 }
 
 }  // namespace qmoe
