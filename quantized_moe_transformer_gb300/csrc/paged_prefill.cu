@@ -48,7 +48,7 @@ __device__ __forceinline__ PrefillRows prefill_rows(const PrefillView& p, int b)
 // key blocks, at least PF_MIN_BLOCKS from its ends. So a CTA has whole tiles, and at
 // most one part of a tile that began in an earlier CTA (slot 0) and one of a tile that
 // goes on in a later one (slot 1); the join kernel puts those together.
-constexpr int PF_KEYS = 128, PF_MIN_BLOCKS = 2, PF_TILE_COST = 256, PF_ITEMS = 4;
+constexpr int PF_KEYS = 64, PF_MIN_BLOCKS = 4, PF_TILE_COST = 256, PF_ITEMS = 4;
 
 struct PfTiling {
   int span, head_rows, row_heads;  // positions of a tile; head rows in all, of a KV head's heads row_heads each
@@ -75,8 +75,9 @@ struct PfCut {
 // The place ``x`` (in units of cost, inside sequence b) cuts the sequence's tiles at.
 __device__ __forceinline__ PfCut pf_cut(const PrefillRows& r, int row, int b, long long x, int span) {
   const long long before = max(r.before, 0);
-  const double half = PF_TILE_COST + before + 0.5 * span;
-  long long t = (long long)((sqrt(half * half + 2.0 * span * (double)x) - half) / span);
+  // the tile whose sum of costs reaches x: near the root of the quadratic, then exactly
+  const float half = (float)PF_TILE_COST + (float)before + 0.5f * span, xf = (float)x;
+  long long t = (long long)(2.f * xf / (half + sqrtf(half * half + 2.f * span * xf)));
   const int tiles = (r.count + span - 1) / span;
   t = max(0ll, min(t, (long long)tiles - 1));
   while (t > 0 && pf_cost(t, before, span) > x) --t;
@@ -96,6 +97,7 @@ __device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w
   constexpr int WARPS = THREADS / 32;
   const int each = (p.c.n_seqs + THREADS - 1) / THREADS, b0 = min(tid * each, p.c.n_seqs), b1 = min(b0 + each, p.c.n_seqs);
   long long mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const PrefillRows r = prefill_rows(p, b);
     if (r.count > 0) mine += pf_cost((r.count + w.span - 1) / w.span, max(r.before, 0), w.span);
@@ -115,14 +117,17 @@ __device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w
     total += sums[i];
   }
   if (total == 0) return;
-#pragma unroll
+  const long long all = total * w.head_rows, per = all / w.ctas, more = all - per * w.ctas;
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     const int i = blockIdx.x + k;
-    if (i >= w.ctas) continue;
-    const long long x = total * w.head_rows / w.ctas * i + total * w.head_rows % w.ctas * i / w.ctas;
-    const int row = (int)(x / total);
+    if (i >= w.ctas) break;
+    const long long x = per * i + min((long long)i, more);
+    int row = (int)((float)x / (float)total);
+    while (row > 0 && row * total > x) --row;
+    while ((row + 1) * total <= x) ++row;
     long long at = x - row * total - before;
-    if (row >= w.head_rows || at < 0 || at >= mine) continue;
+    if (at < 0 || at >= mine) continue;
     for (int b = b0; b < b1; ++b) {
       const PrefillRows r = prefill_rows(p, b);
       const long long cost = r.count > 0 ? pf_cost((r.count + w.span - 1) / w.span, max(r.before, 0), w.span) : 0;
@@ -209,51 +214,62 @@ struct PfWalk {
   }
 };
 
-// ---------------------------------------------------------------- tensor cores, bf16 rows
-// A tile is two blocks of 128 query rows (positions x heads of one KV head, so
-// that short parts of prompts fill it too) that share the copies of K and V.
-//   S_j = Q K_j^T   128 rows x 128 keys, Q and K_j in shared memory (128-byte swizzled,
-//                   K-major), fp32 S in tensor memory. One S buffer for both blocks in
-//                   turn: the softmax takes a whole row into its registers (a thread has a row,
-//                   so nothing is exchanged) and frees the buffer before it computes.
-//   P_j             exp2(s - m) rounded to bf16, in tensor memory (64 columns a block), the A operand of
+// ---------------------------------------------------------------- tensor cores
+// A block is 128 query rows: positions x the heads of one KV head, so that short parts of
+// prompts fill it too.
+//   S_j = Q K_j^T   128 rows x 64 keys, Q and K_j in shared memory (128-byte swizzled,
+//                   K-major), fp32 S in tensor memory, two buffers a block of rows in turn.
+//   P_j             exp2(s - m), a thread a row, back to tensor memory: the A operand of
 //   O += P_j V_j    V_j as an MN-major operand, fp32 O in tensor memory.
-// While one block's softmax runs, the tensor core works on the other's products: S of
-// block 0, P V of block 1, S of block 1, P V of block 0, in whatever order their operands
-// come. m is a reference: O and l are rescaled only where a row's maximum exceeds it by more than
-// 2^8. The products are issued from two threads (one thread issues an MMA in about 80 cycles, one
-// of 128 x 128 x 16 takes 64).
-// Warps: 0-3 and 4-7 softmax of block 0 and 1; 8 walks the CTA's work and copies K, 10 copies
-// V, 9 issues S, 11 P V. Every wait is bounded.
-// fp32 rows: a tile is one block of 128 rows, q and each probability are three bf16 parts
-// (24 bits), so S and P V take three products each, small parts first. P V of a key block goes into
-// a fresh accumulator; warps 4-7 add it, rounded, to the output in their registers (a thread has
-// a row), so nothing is cut off over a long axis.
+// m is a reference: O and l are rescaled only where a row's maximum exceeds it by more than 2^8.
+// bf16 rows: a tile is two blocks of rows that share the copies of K and V. P_j, rounded to bf16, lies in
+// S_j's own columns; S_{j+2} takes them again when P_j V_j is done. While one block's softmax runs, the
+// tensor core has the other's products and the same block's next S.
+// fp32 rows: a tile is one block; q and each probability are three bf16 parts (24 bits), so S and P V
+// take three products each, small parts first. P V of a key block goes into a fresh accumulator; warps 4-7 add
+// it, rounded, to the output in their registers (a thread a row), so nothing is cut off over a long axis.
+// Warps: bf16 0-3 and 4-7 softmax of block 0 and 1, fp32 0-3 softmax, 4-7 sums; 8 walks the CTA's work and
+// copies K (and bf16 Q), 10 copies V, 9 issues S, 11 P V. Every wait is bounded.
 template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;
   static constexpr int HDP = HDP_, NH = HDP / 64;
   static constexpr int BLOCKS = F32 ? 1 : 2, PARTS = F32 ? 3 : 1;
-  static constexpr int QT = F32 ? 3 : 2;  // blocks or parts of queries
-  static constexpr int HALF = 128 * 128;  // 64 head dims of 128 rows
-  static constexpr int TILE = NH * HALF;  // a block of queries, keys or values
-  static constexpr int KST = HDP == 128 ? 2 : 4, VST = HDP == 128 ? (F32 ? 2 : 3) : 4;
-  static constexpr int SMEM = 1024 + (QT + KST + VST) * TILE;
-  static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;  // P at + 64 block or part, O at + HDP block
+  static constexpr int QT = F32 ? 3 : 2;           // blocks or parts of queries
+  static constexpr int QHALF = 128 * 128;          // 64 head dims of 128 query rows
+  static constexpr int QTILE = NH * QHALF;
+  static constexpr int HALF = PF_KEYS * 128;       // 64 head dims of a key block
+  static constexpr int TILE = NH * HALF;
+  static constexpr int KST = HDP == 128 ? 4 : 6, VST = HDP == 128 && F32 ? 3 : 6;
+  static constexpr int SMEM = 1024 + QT * QTILE + (KST + VST) * TILE;
+  static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;
+  // tensor memory: S of (block, buffer), P of (block or part, buffer), O of a block
+  static __device__ __forceinline__ uint32_t s_col(int blk, int buf) { return 64u * (2 * blk + buf); }
+  static __device__ __forceinline__ uint32_t p_col(int blk, int part, int buf) {
+    return F32 ? P_COL + 96u * buf + 32u * part : s_col(blk, buf);
+  }
+  static __device__ __forceinline__ uint32_t o_col(int blk) { return O_COL + (uint32_t)HDP * blk; }
 };
 constexpr int PF_THREADS = 384, PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10;
-constexpr uint32_t PF_S_COL = 0;
 constexpr float PF_RESCALE_LOG2 = 8.f;
 
 struct PfArgs {
   PrefillView p;
   PfTiling w;
   float scale;       // of scores, in units of log2(e), at least FLT_MIN
-  uint32_t flip;     // sign bits of q where the scale is negative
+  uint32_t flip;     // the sign bit where the scale is negative
   int box_rows;      // slots of a copy
   int block_pos;     // positions of a block of 128 query rows
   float2* part_ml;   // [CTAs][2 slots][256 rows]
   float* part_o;     // [CTAs][2][256][HDP]
+};
+
+struct PfBars {
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t it_full[PF_ITEMS], it_empty[PF_ITEMS];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [block][buffer]
+  uint64_t o_read, l_full, drain[2];
 };
 
 __device__ __forceinline__ void pf_tma(uint32_t dst, const CUtensorMap* map, int dim, int row, int head, int page,
@@ -304,16 +320,23 @@ __device__ __forceinline__ uint64_t pf_mn_desc(uint32_t smem_addr, uint32_t lbo_
   return d;
 }
 
-// One key block of K or V into a stage: the lanes' pages (PfPages), a copy for each page (or
-// each 128 slots of one) and 64 head dims.
+__device__ __forceinline__ void pf_tma_q(uint32_t dst, const CUtensorMap* map, int dim, int head, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(dim), "r"(head), "r"(row), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// A key block of K or V: this lane's copy (a page, or as many slots of one as a block has).
 struct PfPages {
-  int page, row;   // this lane's copy; ``page`` n_pages: out of range, reads zeros
+  int page, row;   // ``page`` n_pages: out of range, reads zeros
   uint32_t there;  // bit i: keys 8 i .. 8 i + 7 of the block lie in a page that exists
 };
 __device__ __forceinline__ PfPages pf_pages(const PfArgs& a, const PfItem& it, int kb) {
   const int lane = threadIdx.x & 31, boxes = PF_KEYS / a.box_rows, slot = kb * PF_KEYS + lane * a.box_rows;
   const PagedView& c = a.p.c;
-  PfPages r{c.n_pages, 0, 0xFFFFu};
+  PfPages r{c.n_pages, 0, 0xFFu};
   bool ok = true;
   if (lane < boxes && slot < it.len) {
     const int page = __ldg(c.table + (long long)it.b * c.max_pages + (slot >> c.page_log2));
@@ -328,40 +351,47 @@ __device__ __forceinline__ PfPages pf_pages(const PfArgs& a, const PfItem& it, i
   if (gone) {
     const int per = a.box_rows / 8;
     for (int i = 0; i < boxes; ++i)
-      if ((gone >> i) & 1u) r.there &= ~(((per == 16 ? 0x10000u : 1u << per) - 1u) << (i * per));
+      if ((gone >> i) & 1u) r.there &= ~(((1u << per) - 1u) << (i * per));
   }
   return r;
 }
 
 template <class C>
-__device__ __forceinline__ void pf_copy(const PfArgs& a, const PfItem& it, const PfPages& pg, const CUtensorMap* map,
-                                        uint8_t* stage, uint64_t* bar) {
+__device__ __forceinline__ void pf_copy(const PfArgs& a, int g, const PfPages& pg, const CUtensorMap* map, uint8_t* stage,
+                                        uint64_t* bar) {
   const int lane = threadIdx.x & 31, boxes = PF_KEYS / a.box_rows;
   if (lane == 0) tc::mbar_expect_tx(bar, C::TILE);
   __syncwarp();
   if (lane < boxes) {
     const uint32_t dst = tc::smem_u32(stage) + lane * a.box_rows * 128;
-    const int g = it.row / (a.w.head_rows / a.p.c.n_kv);
 #pragma unroll
     for (int h = 0; h < C::NH; ++h) pf_tma(dst + h * C::HALF, map, 64 * h, pg.row, g, pg.page, bar);
   }
   __syncwarp();
 }
 
-// Row ``r`` of a block of 128: its position, query head and where it lies.
+// The KV head and the first query head of a head row.
+struct PfHeads {
+  int g, h0, n;  // n: heads of the row that exist
+};
+__device__ __forceinline__ PfHeads pf_heads(const PfArgs& a, int row) {
+  if (a.w.head_rows == a.p.c.n_kv) return PfHeads{row, row * a.p.group, a.p.group};
+  const int rows = a.w.head_rows / a.p.c.n_kv, g = row / rows, at = (row - g * rows) * a.w.row_heads;
+  return PfHeads{g, g * a.p.group + at, min(a.w.row_heads, a.p.group - at)};
+}
+
+// Row r of a block of 128: position ``place``, head ``head`` of the block's.
 struct PfRow {
-  int pos, vis;  // vis: entries that it sees (0 where the row is none)
+  int vis;  // entries that it sees (0 where the row is none)
   bool valid;
   long long at;  // element of q and out
 };
-__device__ __forceinline__ PfRow pf_row(const PfArgs& a, const PfItem& it, int blk, int r) {
-  const int place = r / a.w.row_heads, rows_of_kv = a.w.head_rows / a.p.c.n_kv, g = it.row / rows_of_kv;
-  const int h = (it.row - g * rows_of_kv) * a.w.row_heads + r - place * a.w.row_heads;
+__device__ __forceinline__ PfRow pf_row(const PfArgs& a, const PfItem& it, const PfHeads& hs, int blk, int place, int head) {
+  const int pos = it.t * a.w.span + blk * a.block_pos + place;
   PfRow x;
-  x.pos = it.t * a.w.span + blk * a.block_pos + place;
-  x.valid = place < a.block_pos && x.pos < it.count && h < a.p.group;
-  x.vis = x.valid ? max(it.before + x.pos + 1, 0) : 0;
-  x.at = ((long long)(it.first + x.pos) * a.p.a.n_heads + g * a.p.group + h) * a.p.c.head_dim;
+  x.valid = place < a.block_pos && pos < it.count && head < hs.n;
+  x.vis = x.valid ? max(it.before + pos + 1, 0) : 0;
+  x.at = ((long long)(it.first + pos) * a.p.a.n_heads + hs.h0 + head) * a.p.c.head_dim;
   return x;
 }
 
@@ -372,7 +402,7 @@ __device__ __forceinline__ void pf_mask(uint32_t* v, int seen, uint32_t exist) {
     for (int i = 0; i < PF_KEYS; ++i)
       if (i >= seen) v[i] = 0xFF800000u;
   }
-  if (exist != 0xFFFFu) {
+  if (exist != 0xFFu) {
 #pragma unroll
     for (int i = 0; i < PF_KEYS; ++i)
       if (!((exist >> (i / 8)) & 1u)) v[i] = 0xFF800000u;
@@ -387,69 +417,230 @@ __device__ __forceinline__ float pf_max(const uint32_t* v) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Warps 0-7 of a tile of fp32 rows.
+// Four lanes with 64 bytes of a row each exchange 16-byte pieces: then lane q of them has
+// piece q of the four rows, which a store puts side by side (a store of a row's own 16 bytes a
+// lane would touch 32 lines).
+__device__ __forceinline__ void pf_quad(uint32_t* w) {
+  const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, b0 ? w[4 * k + i] : w[4 * k + 4 + i], 1);
+      if (b0)
+        w[4 * k + i] = y;
+      else
+        w[4 * k + 4 + i] = y;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t y = __shfl_xor_sync(0xffffffffu, b1 ? w[4 * k + i] : w[4 * k + 8 + i], 2);
+      if (b1)
+        w[4 * k + i] = y;
+      else
+        w[4 * k + 8 + i] = y;
+    }
+  }
+}
+
+// Where the rows of four lanes go: element, and whether they exist.
+struct PfQuad {
+  long long at[4];
+  bool valid[4];
+};
+__device__ __forceinline__ PfQuad pf_quad_rows(long long at, bool valid) {
+  PfQuad q;
+  const unsigned all = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int src = ((int)threadIdx.x & 28) + k;
+    q.at[k] = __shfl_sync(0xffffffffu, at, src);
+    q.valid[k] = (all >> src) & 1u;
+  }
+  return q;
+}
+
+// 16 fp32 columns of each row from ``col`` on, columns from ``n`` on left out.
+__device__ __forceinline__ void pf_store16(float* base, const PfQuad& q, uint32_t* w, int col, int n) {
+  pf_quad(w);
+  const int c = col + 4 * ((int)threadIdx.x & 3);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (q.valid[k] && c < n) *reinterpret_cast<uint4*>(base + q.at[k] + c) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+}
+
+// Warps 0-7 of tiles of bf16 rows.
+template <class C, class Take>
+__device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, const PfItem& it, uint32_t tmem,
+                                                  const uint32_t* there, PfBars& bar, volatile int* abort_flag) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hd = a.p.c.head_dim;
+  const uint64_t lim = a.p.a.wait_ns;
+  const int blk = warp >> 2, r = threadIdx.x & 127;
+  const int place = r / a.w.row_heads, head = r - place * a.w.row_heads;
+  const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::o_col(blk);
+  const float c = a.scale;
+  const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c)), one2 = pack2(0x3F800000u, 0x3F800000u);
+  int j = 0;   // key blocks of this block of rows so far
+  int k0 = 0;  // key blocks of the CTA's items before this one
+  for (int n = 0; take(n); k0 += it.kb1 - it.kb0, ++n) {
+    if (blk * a.block_pos >= it.count - it.t * a.w.span) continue;  // no rows in this block
+    const PfRow row = pf_row(a, it, pf_heads(a, it.row), blk, place, head);
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
+      const int buf = j & 1;
+      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.s_full[blk][buf], (j >> 1) & 1, abort_flag, lim))) return;
+      tc::tc_fence_after();
+      const uint32_t tS = tq + C::s_col(blk, buf);
+      uint32_t v[PF_KEYS];
+      pf_ld32(tS, v);
+      pf_ld32(tS + 32, v + 32);
+      pf_wait_ld(v);
+      pf_wait_ld(v + 32);
+      if (a.flip) {
+#pragma unroll
+        for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
+      }
+      pf_mask(v, row.vis - kb * PF_KEYS, there[(k0 + kb - it.kb0) % (2 * C::KST)]);
+      const float mx = pf_max(v) * c;
+      const bool need = mx > m + PF_RESCALE_LOG2;
+      if (__any_sync(0xffffffffu, need)) {
+        const float alpha = need ? exp2f(m - mx) : 1.f;
+        if (need) m = mx;
+        l *= alpha;
+        if (kb > it.kb0) {
+          // O holds P V of the block before once that is done
+          if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][buf ^ 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
+            return;
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < C::HDP / 32; ++i) {
+            uint32_t o[32];
+            pf_ld32(tO + 32 * i, o);
+            pf_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st16(tO + 32 * i, o);
+            tc::tmem_st16(tO + 32 * i + 16, o + 16);
+          }
+        }
+      }
+      const float mref = m == -INFINITY ? 0.f : m;
+      const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
+      uint64_t l2[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < PF_KEYS / 2; ++i) {
+        const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
+        const float p0 = exp2f(d.x), p1 = exp2f(d.y);
+        l2[i & 1] = ffma2(pack2(__float_as_uint(p0), __float_as_uint(p1)), one2, l2[i & 1]);
+        v[i] = tc::pack_bf16x2(p0, p1);
+      }
+      const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
+      l += (la.x + la.y) + (lb.x + lb.y);
+      tc::tmem_st16(tS, v);
+      tc::tmem_st16(tS + 16, v + 16);
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.p_full[blk][buf]);
+    }
+    // out = O / l, or the part's O, m and l
+    const bool some = it.kb1 > it.kb0;
+    if (some) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
+        return;
+      tc::tc_fence_after();
+    }
+    const float il = l > 0.f ? 1.f / l : 0.f;
+    const long long part = ((long long)blockIdx.x * 2 + it.slot) * 256 + blk * 128 + r;
+    if (it.slot >= 0 && row.valid) a.part_ml[part] = make_float2(m, l);
+    const PfQuad q = pf_quad_rows(it.slot >= 0 ? part * C::HDP : row.at, row.valid);
+#pragma unroll 1
+    for (int i = 0; i < C::HDP / 32; ++i) {
+      uint32_t o[32];
+      if (some) {
+        pf_ld32(tO + 32 * i, o);
+        pf_wait_ld(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      if (it.slot >= 0) {
+        pf_store16(a.part_o, q, o, 32 * i, C::HDP);
+        pf_store16(a.part_o, q, o + 16, 32 * i + 16, C::HDP);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          o[e] = tc::pack_bf16x2(__uint_as_float(o[2 * e]) * il, __uint_as_float(o[2 * e + 1]) * il);
+        pf_quad(o);
+        const int col = 32 * i + 8 * (lane & 3);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.a.out) + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (q.valid[k] && col < hd)
+            *reinterpret_cast<uint4*>(out + q.at[k]) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+    tc::tc_fence_before();
+  }
+}
+
+// Warps 0-7 of tiles of fp32 rows.
 template <class C, class Take>
 __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, const PfItem& it, uint32_t tmem, uint8_t* sQ,
-                                                 const uint32_t* there, uint64_t* q_full, uint64_t* s_full,
-                                                 uint64_t* s_free, uint64_t* p_full, uint64_t* p_free, uint64_t* o_read,
-                                                 uint64_t* l_full, float (*factor)[C::F32 ? 128 : 1], volatile int* abort_flag) {
+                                                 const uint32_t* there, PfBars& bar, float (*factor)[128],
+                                                 volatile int* abort_flag) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127, hd = a.p.c.head_dim;
   const uint64_t lim = a.p.a.wait_ns;
-  const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::O_COL;
+  const int place = r / a.w.row_heads, head = r - place * a.w.row_heads;
+  const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::o_col(0);
   const float c = a.scale;
   int j = 0;   // key blocks so far
-  int nl = 0;  // items with key blocks so far
-  bool ok = true;
   if (warp < 4) {
-    for (int n = 0; ok && take(n); ++n) {
-      const PfRow row = pf_row(a, it, 0, r);
+    for (int n = 0; take(n); ++n) {
       if (it.kb1 <= it.kb0) continue;
-      // q as three bf16 parts, which hold all its bits
-      const float* q = static_cast<const float*>(a.p.a.q) + row.at;
+      const PfRow row = pf_row(a, it, pf_heads(a, it.row), 0, place, head);
+      // q as three bf16 parts, which hold all its bits: a row's head dims over HDP / 4 lanes
+      constexpr int LANES = C::HDP / 4, ROWS = 32 / LANES;
+      const int sub = lane / LANES, d = 4 * (lane - sub * LANES);
+      // (the S products of the item before are done: this warp has taken their results)
 #pragma unroll 4
-      for (int ch = 0; ch < C::HDP / 8; ++ch) {
-        uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (row.valid && 8 * ch < hd) {
-          const uint4 lo = *reinterpret_cast<const uint4*>(q + 8 * ch), hi = *reinterpret_cast<const uint4*>(q + 8 * ch + 4);
-          x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-          x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
-        }
-        const uint32_t at = (ch >> 3) * C::HALF + tc::sw128_offset(r, ch & 7);
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(x[e] ^ (a.flip & 0x80000000u));
+      for (int i = 0; i < 32; i += ROWS) {
+        const long long at = __shfl_sync(0xffffffffu, row.at, i + sub);
+        const bool there_ = __shfl_sync(0xffffffffu, (int)row.valid, i + sub);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there_ && d < hd) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.p.a.q) + at + d);
+        const int rr = 32 * warp + i + sub, ch = d >> 3;
+        const uint32_t to = (ch >> 3) * C::QHALF + tc::sw128_offset(rr, ch & 7) + 2 * (d & 4);
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] = tc::pack_bf16x2(f[2 * e], f[2 * e + 1]);
-            f[2 * e] -= __uint_as_float(w[e] << 16);
-            f[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
-          }
-          *reinterpret_cast<uint4*>(sQ + part * C::TILE + at) = make_uint4(w[0], w[1], w[2], w[3]);
+          const uint32_t w0 = tc::pack_bf16x2(x.x, x.y), w1 = tc::pack_bf16x2(x.z, x.w);
+          x.x -= __uint_as_float(w0 << 16);
+          x.y -= __uint_as_float(w0 & 0xFFFF0000u);
+          x.z -= __uint_as_float(w1 << 16);
+          x.w -= __uint_as_float(w1 & 0xFFFF0000u);
+          *reinterpret_cast<uint2*>(sQ + part * C::QTILE + to) = make_uint2(w0, w1);
         }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(q_full);
+      if (lane == 0) tc::mbar_arrive(&bar.q_full[0]);
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(s_full, j & 1, abort_flag, lim))) {
-          ok = false;
-          break;
-        }
+        const int buf = j & 1;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.s_full[0][buf], (j >> 1) & 1, abort_flag, lim))) return;
         tc::tc_fence_after();
         uint32_t v[PF_KEYS];
+        pf_ld32(tq + C::s_col(0, buf), v);
+        pf_ld32(tq + C::s_col(0, buf) + 32, v + 32);
+        pf_wait_ld(v);
+        pf_wait_ld(v + 32);
+        if (a.flip) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pf_ld32(tq + PF_S_COL + 32 * i, v + 32 * i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pf_wait_ld(v + 32 * i);
-        const uint32_t exist = there[j % (2 * C::KST)];
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(s_free);
-        pf_mask(v, row.vis - kb * PF_KEYS, exist);
+          for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
+        }
+        pf_mask(v, row.vis - kb * PF_KEYS, there[j % (2 * C::KST)]);
         const float mx = pf_max(v) * c;
         float alpha = 1.f;
         if (mx > m + PF_RESCALE_LOG2) {
@@ -466,139 +657,123 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
           v[i] = __float_as_uint(x);
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        // P is this warp's again once P V of the block before is done
-        if (j > 0 && !__all_sync(0xffffffffu, tc::mbar_wait_poll(p_free, (j - 1) & 1, abort_flag, lim))) {
-          ok = false;
-          break;
-        }
+        // P's buffer, and the slot of the factor, are free once P V of two blocks before is done
+        if (j > 1 && !__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[0][buf], ((j >> 1) - 1) & 1, abort_flag, lim)))
+          return;
         tc::tc_fence_after();
-        if (kb > it.kb0) factor[j & 1][r] = alpha;
+        if (kb > it.kb0) factor[j & 3][r] = alpha;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < PF_KEYS / 32; ++i) {
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float x0 = __uint_as_float(v[32 * i + 2 * e]), x1 = __uint_as_float(v[32 * i + 2 * e + 1]);
+              const float x0 = __uint_as_float(v[32 * i + 2 * e]), x1 = __uint_as_float(v[32 * i + 2 * e + 1]);
               w[e] = tc::pack_bf16x2(x0, x1);
               if (part < 2) {
                 v[32 * i + 2 * e] = __float_as_uint(x0 - __uint_as_float(w[e] << 16));
                 v[32 * i + 2 * e + 1] = __float_as_uint(x1 - __uint_as_float(w[e] & 0xFFFF0000u));
               }
             }
-            tc::tmem_st16(tq + C::P_COL + 64 * part + 16 * i, w);
+            tc::tmem_st16(tq + C::p_col(0, part, buf) + 16 * i, w);
           }
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full);
+        if (lane == 0) tc::mbar_arrive(&bar.p_full[0][buf]);
       }
-      if (!ok) break;
-      // the slot of the block before the last is read once P V of the last is done: the sums take 1 / l from there
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(p_free, (j - 1) & 1, abort_flag, lim))) break;
-      factor[j & 1][r] = l > 0.f ? 1.f / l : 0.f;
+      // 1 / l goes by the slot behind the last block's (the sums have read it when P V of the block before the
+      // last is done and read)
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar.pv_done[0][(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, lim))) return;
+      factor[j & 3][r] = l > 0.f ? 1.f / l : 0.f;
       if (it.slot >= 0 && row.valid) a.part_ml[((long long)blockIdx.x * 2 + it.slot) * 256 + r] = make_float2(m, l);
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(l_full);
+      if (lane == 0) tc::mbar_arrive(&bar.l_full);
     }
     return;
   }
-  for (int n = 0; ok && take(n); ++n) {
-    const PfRow row = pf_row(a, it, 0, r);
-    float acc[C::HDP];
+  int nl = 0;  // items with key blocks so far
+  for (int n = 0; take(n); ++n) {
+    const PfRow row = pf_row(a, it, pf_heads(a, it.row), 0, place, head);
+    uint32_t acc[C::HDP];
 #pragma unroll
-    for (int i = 0; i < C::HDP; ++i) acc[i] = 0.f;
+    for (int i = 0; i < C::HDP; ++i) acc[i] = 0u;
+#pragma unroll 1
     for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(p_free, j & 1, abort_flag, lim))) {
-        ok = false;
-        break;
-      }
+      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[0][j & 1], (j >> 1) & 1, abort_flag, lim))) return;
       tc::tc_fence_after();
-      const float alpha = kb > it.kb0 ? factor[j & 1][r] : 0.f;
+      const float alpha = kb > it.kb0 ? factor[j & 3][r] : 0.f;
 #pragma unroll
       for (int i = 0; i < C::HDP / 32; ++i) {
         uint32_t o[32];
         pf_ld32(tO + 32 * i, o);
         pf_wait_ld(o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[32 * i + e] = fmaf(acc[32 * i + e], alpha, __uint_as_float(o[e]));
+        for (int e = 0; e < 32; ++e)
+          acc[32 * i + e] = __float_as_uint(fmaf(__uint_as_float(acc[32 * i + e]), alpha, __uint_as_float(o[e])));
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(o_read);
+      if (lane == 0) tc::mbar_arrive(&bar.o_read);
     }
-    if (!ok) break;
     float il = 0.f;
     if (it.kb1 > it.kb0) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(l_full, nl & 1, abort_flag, lim))) break;
+      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.l_full, nl & 1, abort_flag, lim))) return;
       ++nl;
-      il = factor[j & 1][r];
+      il = factor[j & 3][r];
     }
-    if (!row.valid) continue;
-    if (it.slot >= 0) {
-      float* to = a.part_o + (((long long)blockIdx.x * 2 + it.slot) * 256 + r) * C::HDP;
+    const long long part = ((long long)blockIdx.x * 2 + it.slot) * 256 + r;
+    const PfQuad q = pf_quad_rows(it.slot >= 0 ? part * C::HDP : row.at, row.valid);
+    if (it.slot < 0) {
 #pragma unroll
-      for (int i = 0; i < C::HDP; i += 4)
-        *reinterpret_cast<float4*>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-    } else {
-      float* out = static_cast<float*>(a.p.a.out) + row.at;
-#pragma unroll
-      for (int i = 0; i < C::HDP; i += 4)
-        if (i < hd)
-          *reinterpret_cast<float4*>(out + i) = make_float4(acc[i] * il, acc[i + 1] * il, acc[i + 2] * il, acc[i + 3] * il);
+      for (int i = 0; i < C::HDP; ++i) acc[i] = __float_as_uint(__uint_as_float(acc[i]) * il);
     }
+    float* to = it.slot >= 0 ? a.part_o : static_cast<float*>(a.p.a.out);
+    const int cols = it.slot >= 0 ? C::HDP : hd;
+#pragma unroll
+    for (int i = 0; i < C::HDP; i += 16) pf_store16(to, q, acc + i, i, cols);
   }
 }
 
 template <class C>
 __global__ void __launch_bounds__(PF_THREADS, 1)
-    prefill_tc_kernel(const PfArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    prefill_tc_kernel(const PfArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t pf_smem_raw[];
   __shared__ PfCut cuts[2];
   __shared__ long long sums[PF_THREADS / 32];
   __shared__ PfItem items[PF_ITEMS];
   __shared__ uint32_t there[2 * C::KST];
-  __shared__ __align__(8) uint64_t k_full[C::KST], k_empty[C::KST], v_full[C::VST], v_empty[C::VST];
-  __shared__ __align__(8) uint64_t it_full[PF_ITEMS], it_empty[PF_ITEMS];
-  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_full[2], p_free[2], s_free, drain[2];
-  __shared__ float factor[C::F32 ? 2 : 1][C::F32 ? 128 : 1];  // fp32 rows: O's factor at a key block; at the end 1 / l
-  __shared__ __align__(8) uint64_t o_read, l_full;
+  __shared__ __align__(8) PfBars bar;
+  __shared__ float factor[C::F32 ? 4 : 1][128];  // fp32 rows: O's factor at a key block; at the end 1 / l
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t s0 = tc::smem_u32(pf_smem_raw);
   uint8_t* smem = pf_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
   uint8_t* sQ = smem;                       // [2 blocks] or [3 parts]
-  uint8_t* sK = sQ + C::QT * C::TILE;       // [KST]
+  uint8_t* sK = sQ + C::QT * C::QTILE;      // [KST]
   uint8_t* sV = sK + C::KST * C::TILE;      // [VST]
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = a.p.a.wait_ns;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::KST; ++i) {
-      tc::mbar_init(&k_full[i], 1);
-      tc::mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < C::VST; ++i) {
-      tc::mbar_init(&v_full[i], 1);
-      tc::mbar_init(&v_empty[i], 1);
-    }
-    for (int i = 0; i < PF_ITEMS; ++i) {
-      tc::mbar_init(&it_full[i], 1);
-      tc::mbar_init(&it_empty[i], 11);
-    }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&q_full[i], 4);
-      tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&p_full[i], 4);
-      tc::mbar_init(&p_free[i], 1);
-      tc::mbar_init(&drain[i], 1);
-    }
-    tc::mbar_init(&s_free, 4);
-    tc::mbar_init(&o_read, 4);
-    tc::mbar_init(&l_full, 4);
+    const auto init = [](uint64_t* b, int n, uint32_t count) {
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) tc::mbar_init(b + i, count);
+    };
+    init(bar.k_full, 24, 1);  // and k_empty, v_full, v_empty
+    init(bar.it_full, PF_ITEMS, 1);
+    init(bar.it_empty, PF_ITEMS, 11);
+    init(bar.q_full, 2, C::F32 ? 4 : 1);
+    init(bar.q_empty, 2, 1);
+    init(&bar.s_full[0][0], 4, 1);
+    init(&bar.p_full[0][0], 4, 4);
+    init(&bar.pv_done[0][0], 4, 1);
+    init(&bar.o_read, 2, 4);  // and l_full
+    init(bar.drain, 2, 1);
     abort_word = 0;
     tc::fence_barrier_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
@@ -617,170 +792,34 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   // The next item for a consumer warp (n: items taken so far); false: none, or given up.
   PfItem it;
   auto take = [&](int n) -> bool {
-    if (!__all_sync(0xffffffffu, tc::mbar_wait(&it_full[n % PF_ITEMS], (n / PF_ITEMS) & 1, abort_flag, lim))) return false;
+    if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar.it_full[n % PF_ITEMS], (n / PF_ITEMS) & 1, abort_flag, lim))) return false;
     it = items[n % PF_ITEMS];
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&it_empty[n % PF_ITEMS]);
+    if (lane == 0) tc::mbar_arrive(&bar.it_empty[n % PF_ITEMS]);
     return it.b >= 0;
   };
+  auto blocks_of = [&]() { return C::BLOCKS == 2 && it.count - it.t * a.w.span > a.block_pos ? 2 : 1; };
 
-  // a softmax thread holds a row of 128 scores: 2 x 128 x 208 + 128 x 80 registers of the CTA's 384 x 168
-  if (warp < 8)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (C::F32 && warp < 8) {
-    // ------------------------------------------------------------ fp32 rows: softmax (warps 0-3), sums (4-7)
-    prefill_f32_rows<C>(a, take, it, tmem, sQ, there, &q_full[0], &s_full[0], &s_free, &p_full[0], &p_free[0], &o_read,
-                        &l_full, factor, abort_flag);
-  } else if (warp < 8) {
-    // ------------------------------------------------------------ softmax
-    const int blk = warp >> 2, r = threadIdx.x & 127;
-    const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t tS = tq + PF_S_COL, tP = tq + C::P_COL + 64u * blk, tO = tq + C::O_COL + (uint32_t)(C::HDP * blk);
-    uint8_t* q_dst = sQ + blk * C::TILE;
-    const float c = a.scale;
-    int n_blocks = 0;  // key blocks of this block of rows so far
-    int k0 = 0;        // key blocks of the CTA's items before this one
-    bool ok = true;
-    for (int n = 0; ok && take(n); k0 += it.kb1 - it.kb0, ++n) {
-      if (blk * a.block_pos >= it.count - it.t * a.w.span) continue;  // no rows in this block
-      const PfRow row = pf_row(a, it, blk, r);
-      const bool valid = row.valid;
-      float m = -INFINITY, l = 0.f;
-      if (it.kb1 > it.kb0) {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.p.a.q) + row.at;
-#pragma unroll
-        for (int ch = 0; ch < C::HDP / 8; ++ch) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (valid && 8 * ch < hd) x = *reinterpret_cast<const uint4*>(q + 8 * ch);
-          x.x ^= a.flip; x.y ^= a.flip; x.z ^= a.flip; x.w ^= a.flip;
-          *reinterpret_cast<uint4*>(q_dst + (ch >> 3) * C::HALF + tc::sw128_offset(r, ch & 7)) = x;
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&q_full[blk]);
-      }
-      for (int kb = it.kb0; kb < it.kb1; ++kb, ++n_blocks) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&s_full[blk], n_blocks & 1, abort_flag, lim))) {
-          ok = false;
-          break;
-        }
-        tc::tc_fence_after();
-        uint32_t v[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pf_ld32(tS + 32 * i, v + 32 * i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pf_wait_ld(v + 32 * i);
-        const uint32_t exist = there[(k0 + kb - it.kb0) % (2 * C::KST)];
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s_free);
-        pf_mask(v, row.vis - kb * PF_KEYS, exist);
-        const float mx = pf_max(v) * c;
-        float alpha = 1.f;
-        const bool need = mx > m + PF_RESCALE_LOG2;
-        if (need) {
-          alpha = exp2f(m - mx);
-          m = mx;
-          l *= alpha;
-        }
-        const bool rescale = kb > it.kb0 && __any_sync(0xffffffffu, need);
-        const float mref = m == -INFINITY ? 0.f : m;
-        const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c));
-        const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
-          const float p0 = exp2f(d.x), p1 = exp2f(d.y);
-          l4[i & 3] += p0 + p1;
-          v[i] = tc::pack_bf16x2(p0, p1);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        // P (and O) are this warp's again once P V of the block before is done
-        if (n_blocks > 0 &&
-            !__all_sync(0xffffffffu, tc::mbar_wait_poll(&p_free[blk], (n_blocks - 1) & 1, abort_flag, lim))) {
-          ok = false;
-          break;
-        }
-        tc::tc_fence_after();
-        if (rescale) {
-#pragma unroll 1
-          for (int i = 0; i < C::HDP / 32; ++i) {
-            uint32_t o[32];
-            pf_ld32(tO + 32 * i, o);
-            pf_wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st16(tO + 32 * i, o);
-            tc::tmem_st16(tO + 32 * i + 16, o + 16);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc::tmem_st16(tP + 16 * i, v + 16 * i);
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_full[blk]);
-      }
-      if (!ok) break;
-      // out = O / l, or the part's O, m and l
-      if (it.kb1 > it.kb0) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(&p_free[blk], (n_blocks - 1) & 1, abort_flag, lim))) {
-          ok = false;
-          break;
-        }
-        tc::tc_fence_after();
-      }
-      const float il = l > 0.f ? 1.f / l : 0.f;
-      const long long part = ((long long)blockIdx.x * 2 + it.slot) * 256 + blk * 128 + r;
-      if (it.slot >= 0 && valid) a.part_ml[part] = make_float2(m, l);
-#pragma unroll 1
-      for (int i = 0; i < C::HDP / 32; ++i) {
-        uint32_t o[32];
-        if (it.kb1 > it.kb0) {
-          pf_ld32(tO + 32 * i, o);
-          pf_wait_ld(o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (valid && it.slot >= 0) {
-          float* to = a.part_o + part * C::HDP + 32 * i;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(to + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else if (valid) {
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.a.out) + row.at + 32 * i;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              x[k] = tc::pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * il, __uint_as_float(o[8 * e + 2 * k + 1]) * il);
-            if (32 * i + 8 * e < hd) *reinterpret_cast<uint4*>(out + 8 * e) = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        }
-        __syncwarp();
-      }
-      tc::tc_fence_before();
-    }
+  if (warp < 8) {
+    if constexpr (C::F32)
+      prefill_f32_rows<C>(a, take, it, tmem, sQ, there, bar, factor, abort_flag);
+    else
+      prefill_bf16_rows<C>(a, take, it, tmem, there, bar, abort_flag);
   } else if (warp == PF_KWARP) {
-    // ------------------------------------------------------------ the CTA's work, copies of K
+    // ------------------------------------------------------------ the CTA's work, copies of K and bf16 Q
     int4* desc = a.w.desc + 2 * blockIdx.x;
     if (lane < 2) desc[lane] = make_int4(-1, 0, 0, 0);
     __syncwarp();
     PfWalk walk;
     walk.begin(a.p, cuts);
-    int n = 0, k = 0;
-    bool ok = true, more = true;
+    int k = 0, q_n[2] = {0, 0};
+    bool ok = true;
     const bool withhold = a.p.a.fault && blockIdx.x == 0;
-    while (ok && more) {
-      more = walk.next(a.p, a.w, &it);
+    for (int n = 0; ok; ++n) {
+      const bool more = walk.next(a.p, a.w, &it);
       if (!more) it.b = -1;
       if (n >= PF_ITEMS &&
-          !__all_sync(0xffffffffu, tc::mbar_wait(&it_empty[n % PF_ITEMS], (n / PF_ITEMS - 1) & 1, abort_flag, lim)))
+          !__all_sync(0xffffffffu, tc::mbar_wait(&bar.it_empty[n % PF_ITEMS], (n / PF_ITEMS - 1) & 1, abort_flag, lim)))
         break;
       if (lane == 0) {
         items[n % PF_ITEMS] = it;
@@ -788,97 +827,140 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const PrefillRows rr{it.first, it.count, it.len, it.before};
           desc[it.slot] = make_int4(it.b, it.t, it.row, it.kb1 == pf_blocks(rr, it.t, a.w.span) ? 1 : 0);
         }
-        tc::mbar_arrive(&it_full[n % PF_ITEMS]);
+        tc::mbar_arrive(&bar.it_full[n % PF_ITEMS]);
       }
       __syncwarp();
-      ++n;
       if (!more) break;
+      if (it.kb1 <= it.kb0) continue;
+      const PfHeads hs = pf_heads(a, it.row);
+      if (!C::F32) {
+        // a block's queries once S of the item before no longer reads its space; what lies behind the rows
+        // (other sequences' rows, zeros from n_rows on) is masked
+        const int blocks = blocks_of();
+#pragma unroll 1
+        for (int blk = 0; blk < blocks; ++blk) {
+          if (q_n[blk] > 0 &&
+              !__all_sync(0xffffffffu, tc::mbar_wait(&bar.q_empty[blk], (q_n[blk] - 1) & 1, abort_flag, lim))) {
+            ok = false;
+            break;
+          }
+          ++q_n[blk];
+          if (lane == 0) {
+            tc::mbar_expect_tx(&bar.q_full[blk], C::NH * 128 * a.w.row_heads * a.block_pos);
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h)
+              pf_tma_q(tc::smem_u32(sQ) + blk * C::QTILE + h * C::QHALF, &qmap, 64 * h, hs.h0,
+                       it.first + it.t * a.w.span + blk * a.block_pos, &bar.q_full[blk]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+#pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const PfPages pg = pf_pages(a, it, kb);
         const int st = k % C::KST;
         if (k >= C::KST &&
-            !__all_sync(0xffffffffu, tc::mbar_wait(&k_empty[st], (k / C::KST - 1) & 1, abort_flag, lim))) {
+            !__all_sync(0xffffffffu, tc::mbar_wait(&bar.k_empty[st], (k / C::KST - 1) & 1, abort_flag, lim))) {
           ok = false;
           break;
         }
         if (withhold && k == 0) {
           // test-only: never copied
           volatile int late = 0;
-          tc::mbar_wait(&k_full[0], 0, &late, lim);
+          tc::mbar_wait(&bar.k_full[0], 0, &late, lim);
           *abort_flag = 1;
           ok = false;
           break;
         }
         if (lane == 0) there[k % (2 * C::KST)] = pg.there;
-        pf_copy<C>(a, it, pg, &kmap, sK + st * C::TILE, &k_full[st]);
+        pf_copy<C>(a, hs.g, pg, &kmap, sK + st * C::TILE, &bar.k_full[st]);
       }
     }
     // copies in flight land before the CTA leaves
     volatile int never = 0;
-    for (int i = max(0, k - C::KST); i < k; ++i) tc::mbar_wait(&k_full[i % C::KST], (i / C::KST) & 1, &never, lim);
+#pragma unroll 1
+    for (int i = max(0, k - C::KST); i < k; ++i) tc::mbar_wait(&bar.k_full[i % C::KST], (i / C::KST) & 1, &never, lim);
+    if (!C::F32) {
+#pragma unroll 1
+      for (int blk = 0; blk < 2; ++blk)
+        if (q_n[blk] > 0) tc::mbar_wait(&bar.q_full[blk], (q_n[blk] - 1) & 1, &never, lim);
+    }
     __syncwarp();
   } else if (warp == PF_VWARP) {
     // ------------------------------------------------------------ copies of V
     int k = 0;
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
+      const int g = pf_heads(a, it.row).g;
+#pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const PfPages pg = pf_pages(a, it, kb);
         const int st = k % C::VST;
         if (k >= C::VST &&
-            !__all_sync(0xffffffffu, tc::mbar_wait(&v_empty[st], (k / C::VST - 1) & 1, abort_flag, lim))) {
+            !__all_sync(0xffffffffu, tc::mbar_wait(&bar.v_empty[st], (k / C::VST - 1) & 1, abort_flag, lim))) {
           ok = false;
           break;
         }
-        pf_copy<C>(a, it, pg, &vmap, sV + st * C::TILE, &v_full[st]);
+        pf_copy<C>(a, g, pg, &vmap, sV + st * C::TILE, &bar.v_full[st]);
       }
     }
     volatile int never = 0;
-    for (int i = max(0, k - C::VST); i < k; ++i) tc::mbar_wait(&v_full[i % C::VST], (i / C::VST) & 1, &never, lim);
+#pragma unroll 1
+    for (int i = max(0, k - C::VST); i < k; ++i) tc::mbar_wait(&bar.v_full[i % C::VST], (i / C::VST) & 1, &never, lim);
     __syncwarp();
   } else if (warp == PF_SWARP) {
     // ------------------------------------------------------------ S = Q K^T
     const uint32_t idesc = tc::idesc_bf16_f32(128, PF_KEYS);
     const int steps = (hd + 15) / 16;
-    int k = 0, u = 0, q_n[2] = {0, 0};
+    int k = 0, q_n[2] = {0, 0}, s_n[2] = {0, 0};
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int left = it.count - it.t * a.w.span, blocks = C::BLOCKS == 2 && left > a.block_pos ? 2 : 1;
+      const int blocks = blocks_of();
+#pragma unroll 1
       for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
         const int st = k % C::KST;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&k_full[st], (k / C::KST) & 1, abort_flag, lim));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.k_full[st], (k / C::KST) & 1, abort_flag, lim));
 #pragma unroll
         for (int blk = 0; blk < C::BLOCKS; ++blk) {
           if (!ok || blk >= blocks) break;
           if (kb == it.kb0) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[blk], q_n[blk] & 1, abort_flag, lim));
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.q_full[blk], q_n[blk] & 1, abort_flag, lim));
             ++q_n[blk];
           }
-          ok = ok && (u == 0 || __all_sync(0xffffffffu, tc::mbar_wait_poll(&s_free, (u - 1) & 1, abort_flag, lim)));
+          // the buffer is free again: bf16 once P V of two blocks before, which reads P there, is done; fp32 once
+          // the softmax has taken S of two blocks before
+          const int j = s_n[blk], buf = j & 1;
+          uint64_t* free_bar = C::F32 ? &bar.p_full[0][buf] : &bar.pv_done[blk][buf];
+          ok = ok && (j < 2 || __all_sync(0xffffffffu, tc::mbar_wait_poll(free_bar, ((j >> 1) - 1) & 1, abort_flag, lim)));
           if (!ok) break;
+          ++s_n[blk];
           tc::tc_fence_after();
           if (lane == 0) {
             const uint64_t kd = tc::sw128_desc(tc::smem_u32(sK + st * C::TILE));
+            const uint32_t d = tmem + C::s_col(blk, buf);
 #pragma unroll
             for (int part = C::PARTS - 1; part >= 0; --part) {
-              const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + (blk + part) * C::TILE));
-              for (int kk = 0; kk < steps; ++kk) {
-                const uint64_t off = (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3));
-                tc::mma_bf16(tmem + PF_S_COL, qd + off, kd + off, idesc, part != C::PARTS - 1 || kk != 0);
-              }
+              const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + (blk + part) * C::QTILE));
+#pragma unroll
+              for (int kk = 0; kk < C::HDP / 16; ++kk)
+                if (kk < steps)
+                  tc::mma_bf16(d, qd + (uint64_t)((kk >> 2) * (C::QHALF >> 4) + 2 * (kk & 3)),
+                               kd + (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3)), idesc,
+                               part != C::PARTS - 1 || kk != 0);
             }
-            tc::mma_commit(&s_full[blk]);
-            if (blk == blocks - 1) tc::mma_commit(&k_empty[st]);
+            tc::mma_commit(&bar.s_full[blk][buf]);
+            if (blk == blocks - 1) tc::mma_commit(&bar.k_empty[st]);
+            if (!C::F32 && kb == it.kb1 - 1) tc::mma_commit(&bar.q_empty[blk]);
           }
           __syncwarp();
-          ++u;
         }
       }
     }
     if (lane == 0) {
-      tc::mma_commit(&drain[0]);
+      tc::mma_commit(&bar.drain[0]);
       volatile int never = 0;
-      tc::mbar_wait(&drain[0], 0, &never, lim);
+      tc::mbar_wait(&bar.drain[0], 0, &never, lim);
     }
     __syncwarp();
   } else {
@@ -887,16 +969,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     int k = 0, p_n[2] = {0, 0};
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int left = it.count - it.t * a.w.span, blocks = C::BLOCKS == 2 && left > a.block_pos ? 2 : 1;
+      const int blocks = blocks_of();
+#pragma unroll 1
       for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
         const int st = k % C::VST;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&v_full[st], (k / C::VST) & 1, abort_flag, lim));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.v_full[st], (k / C::VST) & 1, abort_flag, lim));
         if (!ok) break;
         uint8_t* vs = sV + st * C::TILE;
         // rows behind the sequence's last entry may hold anything, NaN too: zero weights need zero values
         if (it.len - kb * PF_KEYS < PF_KEYS) {
           const int r0 = it.len - kb * PF_KEYS;
-          for (int i = 8 * r0 + lane; i < 8 * 128; i += 32) {
+#pragma unroll 1
+          for (int i = 8 * r0 + lane; i < 8 * PF_KEYS; i += 32) {
 #pragma unroll
             for (int h = 0; h < C::NH; ++h)
               *reinterpret_cast<uint4*>(vs + h * C::HALF + 16 * i) = make_uint4(0, 0, 0, 0);
@@ -907,37 +991,39 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
         for (int blk = 0; blk < C::BLOCKS; ++blk) {
           if (!ok || blk >= blocks) break;
-          ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&p_full[blk], p_n[blk] & 1, abort_flag, lim));
-          if (C::F32 && ok && p_n[0] > 0)
-            ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&o_read, (p_n[0] - 1) & 1, abort_flag, lim));
+          const int j = p_n[blk], buf = j & 1;
+          ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.p_full[blk][buf], (j >> 1) & 1, abort_flag, lim));
+          if (C::F32 && ok && j > 0)
+            ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.o_read, (j - 1) & 1, abort_flag, lim));
           if (!ok) break;
           ++p_n[blk];
           tc::tc_fence_after();
           if (lane == 0) {
+            const uint64_t vd = pf_mn_desc(tc::smem_u32(vs), C::HALF);
 #pragma unroll
             for (int part = C::PARTS - 1; part >= 0; --part) {
 #pragma unroll
               for (int kk = 0; kk < PF_KEYS / 16; ++kk)
-                tc::mma_bf16_ts(tmem + C::O_COL + (uint32_t)(C::HDP * blk),
-                                tmem + C::P_COL + 64u * (blk + part) + 8u * kk,
-                                pf_mn_desc(tc::smem_u32(vs) + 2048u * kk, C::HALF), idesc,
+                tc::mma_bf16_ts(tmem + C::o_col(blk), tmem + C::p_col(blk, part, buf) + 8u * kk,
+                                vd + (uint64_t)(2048 / 16 * kk), idesc,
                                 part != C::PARTS - 1 || kk != 0 || (!C::F32 && kb > it.kb0));
             }
-            tc::mma_commit(&p_free[blk]);
-            if (blk == blocks - 1) tc::mma_commit(&v_empty[st]);
+            tc::mma_commit(&bar.pv_done[blk][buf]);
+            if (blk == blocks - 1) tc::mma_commit(&bar.v_empty[st]);
           }
           __syncwarp();
         }
       }
     }
     if (lane == 0) {
-      tc::mma_commit(&drain[1]);
+      tc::mma_commit(&bar.drain[1]);
       volatile int never = 0;
-      tc::mbar_wait(&drain[1], 0, &never, lim);
+      tc::mbar_wait(&bar.drain[1], 0, &never, lim);
     }
     __syncwarp();
   }
 
+  __syncwarp();
   if (*abort_flag && threadIdx.x == 0) record_status(a.p.a.status, QMOE_ERR_TIMEOUT);
   tc::tc_fence_before();
   __syncthreads();
@@ -1152,15 +1238,28 @@ bool pf_encode(CUtensorMap* m, const void* base, const PagedView& c, int box_row
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 queries as a tensor map [head dim][head][row], boxes of a block's rows.
+bool pf_encode_q(CUtensorMap* m, const PfArgs& x) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t hd = (cuuint64_t)x.p.c.head_dim, heads = (cuuint64_t)x.p.a.n_heads;
+  const cuuint64_t dims[3] = {hd, heads, (cuuint64_t)x.p.a.n_rows}, strides[2] = {2 * hd, 2 * hd * heads};
+  const cuuint32_t box[3] = {64, (cuuint32_t)x.w.row_heads, (cuuint32_t)x.block_pos}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p.a.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class C>
 cudaError_t launch_tc(PfArgs& x, cudaStream_t st) {
   const PagedView& c = x.p.c;
   x.box_rows = 1 << c.page_log2 < PF_KEYS ? 1 << c.page_log2 : PF_KEYS;
-  CUtensorMap km, vm;
-  if (!pf_encode(&km, c.k, c, x.box_rows) || !pf_encode(&vm, c.v, c, x.box_rows)) return cudaErrorInvalidValue;
+  CUtensorMap km, vm, qm{};
+  if (!pf_encode(&km, c.k, c, x.box_rows) || !pf_encode(&vm, c.v, c, x.box_rows) || (!C::F32 && !pf_encode_q(&qm, x)))
+    return cudaErrorInvalidValue;
   cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(prefill_tc_kernel<C>), C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(prefill_tc_kernel<C>, dim3(x.w.ctas), PF_THREADS, C::SMEM, 0, st, x, km, vm);
+  return launch_overlapped(prefill_tc_kernel<C>, dim3(x.w.ctas), PF_THREADS, C::SMEM, 0, st, x, km, vm, qm);
 }
 
 }  // namespace
@@ -1197,7 +1296,7 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.part_o = reinterpret_cast<float*>(ws + pl.o);
   x.block_pos = pl.block_pos;
   x.scale = fminf(fmaxf(fabsf(p.scale_log2), FLT_MIN), FLT_MAX);
-  x.flip = a.scale < 0.f ? 0x80008000u : 0u;
+  x.flip = a.scale < 0.f ? 0x80000000u : 0u;
   cudaError_t e = a.f32 ? (pl.hdp == 64 ? launch_tc<PfCfg<64, true>>(x, st) : launch_tc<PfCfg<128, true>>(x, st))
                         : (pl.hdp == 64 ? launch_tc<PfCfg<64, false>>(x, st) : launch_tc<PfCfg<128, false>>(x, st));
   if (e != cudaSuccess || !pl.cuts) return e;
