@@ -328,6 +328,39 @@ __device__ __forceinline__ void pf_tma_q(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// MMAs and their commits by one lane of a whole warp: predicated instead of branched
+// around, so that descriptors stay in uniform registers (in a branch of one lane every operand is moved there
+// first, about 70 cycles an MMA).
+__device__ __forceinline__ uint32_t pf_leader() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one;
+}
+__device__ __forceinline__ void pf_mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void pf_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void pf_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ int pf_same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // A key block of K or V: this lane's copy (a page, or as many slots of one as a block has).
 struct PfPages {
   int page, row;   // ``page`` n_pages: out of range, reads zeros
@@ -756,7 +789,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   uint8_t* sK = sQ + C::QT * C::QTILE;      // [KST]
   uint8_t* sV = sK + C::KST * C::TILE;      // [VST]
   volatile int* abort_flag = &abort_word;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = pf_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint64_t lim = a.p.a.wait_ns;
 
   if (threadIdx.x == 0) {
@@ -788,6 +821,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int hd = a.p.c.head_dim;
+  const uint32_t leader = pf_leader();
 
   // The next item for a consumer warp (n: items taken so far); false: none, or given up.
   PfItem it;
@@ -936,32 +970,28 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (!ok) break;
           ++s_n[blk];
           tc::tc_fence_after();
-          if (lane == 0) {
-            const uint64_t kd = tc::sw128_desc(tc::smem_u32(sK + st * C::TILE));
-            const uint32_t d = tmem + C::s_col(blk, buf);
+          const uint64_t kd = tc::sw128_desc(tc::smem_u32(sK) + (uint32_t)(pf_same(st) * C::TILE));
+          const uint32_t d = pf_same(tmem) + C::s_col(blk, pf_same(buf));
 #pragma unroll
-            for (int part = C::PARTS - 1; part >= 0; --part) {
-              const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + (blk + part) * C::QTILE));
+          for (int part = C::PARTS - 1; part >= 0; --part) {
+            const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + (blk + part) * C::QTILE));
 #pragma unroll
-              for (int kk = 0; kk < C::HDP / 16; ++kk)
-                if (kk < steps)
-                  tc::mma_bf16(d, qd + (uint64_t)((kk >> 2) * (C::QHALF >> 4) + 2 * (kk & 3)),
-                               kd + (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3)), idesc,
-                               part != C::PARTS - 1 || kk != 0);
-            }
-            tc::mma_commit(&bar.s_full[blk][buf]);
-            if (blk == blocks - 1) tc::mma_commit(&bar.k_empty[st]);
-            if (!C::F32 && kb == it.kb1 - 1) tc::mma_commit(&bar.q_empty[blk]);
+            for (int kk = 0; kk < C::HDP / 16; ++kk)
+              if (kk < steps)
+                pf_mma(leader, d, qd + (uint64_t)((kk >> 2) * (C::QHALF >> 4) + 2 * (kk & 3)),
+                       kd + (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3)), idesc,
+                       part != C::PARTS - 1 || kk != 0);
           }
+          pf_commit(leader, &bar.s_full[blk][buf]);
+          if (blk == blocks - 1) pf_commit(leader, &bar.k_empty[st]);
+          if (!C::F32 && kb == it.kb1 - 1) pf_commit(leader, &bar.q_empty[blk]);
           __syncwarp();
         }
       }
     }
-    if (lane == 0) {
-      tc::mma_commit(&bar.drain[0]);
-      volatile int never = 0;
-      tc::mbar_wait(&bar.drain[0], 0, &never, lim);
-    }
+    pf_commit(leader, &bar.drain[0]);
+    volatile int never = 0;
+    tc::mbar_wait(&bar.drain[0], 0, &never, lim);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ O += P V
@@ -998,28 +1028,26 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (!ok) break;
           ++p_n[blk];
           tc::tc_fence_after();
-          if (lane == 0) {
-            const uint64_t vd = pf_mn_desc(tc::smem_u32(vs), C::HALF);
+          const uint64_t vd = pf_mn_desc(tc::smem_u32(sV) + (uint32_t)(pf_same(st) * C::TILE), C::HALF);
+          const uint32_t d = pf_same(tmem) + C::o_col(blk);
+          const bool first = !C::F32 && kb == it.kb0;
 #pragma unroll
-            for (int part = C::PARTS - 1; part >= 0; --part) {
+          for (int part = C::PARTS - 1; part >= 0; --part) {
+            const uint32_t pa = pf_same(tmem) + C::p_col(blk, part, pf_same(buf));
 #pragma unroll
-              for (int kk = 0; kk < PF_KEYS / 16; ++kk)
-                tc::mma_bf16_ts(tmem + C::o_col(blk), tmem + C::p_col(blk, part, buf) + 8u * kk,
-                                vd + (uint64_t)(2048 / 16 * kk), idesc,
-                                part != C::PARTS - 1 || kk != 0 || (!C::F32 && kb > it.kb0));
-            }
-            tc::mma_commit(&bar.pv_done[blk][buf]);
-            if (blk == blocks - 1) tc::mma_commit(&bar.v_empty[st]);
+            for (int kk = 0; kk < PF_KEYS / 16; ++kk)
+              pf_mma_ts(leader, d, pa + 8u * kk, vd + (uint64_t)(2048 / 16 * kk), idesc,
+                        part != C::PARTS - 1 || kk != 0 || (!C::F32 && !first));
           }
+          pf_commit(leader, &bar.pv_done[blk][buf]);
+          if (blk == blocks - 1) pf_commit(leader, &bar.v_empty[st]);
           __syncwarp();
         }
       }
     }
-    if (lane == 0) {
-      tc::mma_commit(&bar.drain[1]);
-      volatile int never = 0;
-      tc::mbar_wait(&bar.drain[1], 0, &never, lim);
-    }
+    pf_commit(leader, &bar.drain[1]);
+    volatile int never = 0;
+    tc::mbar_wait(&bar.drain[1], 0, &never, lim);
     __syncwarp();
   }
 
