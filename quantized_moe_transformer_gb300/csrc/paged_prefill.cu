@@ -229,18 +229,19 @@ struct PfWalk {
 // take three products each, small parts first. P V of a key block goes into a fresh accumulator; warps 4-7 add
 // it, rounded, to the output in their registers (a thread a row), so nothing is cut off over a long axis.
 // Warps: bf16 0-3 and 4-7 softmax of block 0 and 1, fp32 0-3 softmax, 4-7 sums; 8 walks the CTA's work and
-// copies K (and bf16 Q), 10 copies V, 9 issues S, 11 P V. Every wait is bounded.
+// copies K (and bf16 Q), 10 copies V; 9 and 11 issue block 0's S and P V, 12 and 13 block 1's. Every wait is bounded.
 template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;
   static constexpr int HDP = HDP_, NH = HDP / 64;
   static constexpr int BLOCKS = F32 ? 1 : 2, PARTS = F32 ? 3 : 1;
-  static constexpr int QT = F32 ? 3 : 2;           // blocks or parts of queries
+  static constexpr int THREADS = 32 * (10 + 2 * BLOCKS);
+  static constexpr int QT = 3;                     // bf16: a ring of blocks of queries; fp32: their parts
   static constexpr int QHALF = 128 * 128;          // 64 head dims of 128 query rows
   static constexpr int QTILE = NH * QHALF;
   static constexpr int HALF = PF_KEYS * 128;       // 64 head dims of a key block
   static constexpr int TILE = NH * HALF;
-  static constexpr int KST = HDP == 128 ? 4 : 6, VST = HDP == 128 && F32 ? 3 : 6;
+  static constexpr int KST = 4, VST = HDP == 128 ? (F32 ? 3 : 4) : 6;
   static constexpr int SMEM = 1024 + QT * QTILE + (KST + VST) * TILE;
   static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;
   // tensor memory: S of (block, buffer), P of (block or part, buffer), O of a block
@@ -250,7 +251,7 @@ struct PfCfg {
   }
   static __device__ __forceinline__ uint32_t o_col(int blk) { return O_COL + (uint32_t)HDP * blk; }
 };
-constexpr int PF_THREADS = 384, PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10;
+constexpr int PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10, PF_OWARP = 11;  // S and P V of block 1: 12 and 13
 constexpr float PF_RESCALE_LOG2 = 8.f;
 
 struct PfArgs {
@@ -265,11 +266,11 @@ struct PfArgs {
 };
 
 struct PfBars {
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t k_full[6], v_full[6], k_empty[6], v_empty[6];
   uint64_t it_full[PF_ITEMS], it_empty[PF_ITEMS];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[3], q_empty[3];                      // bf16: of the ring; fp32: q_full[0]
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [block][buffer]
-  uint64_t o_read, l_full, drain[2];
+  uint64_t o_read, l_full, drain[4];
 };
 
 __device__ __forceinline__ void pf_tma(uint32_t dst, const CUtensorMap* map, int dim, int row, int head, int page,
@@ -306,18 +307,12 @@ __device__ __forceinline__ void pf_wait_ld(uint32_t* v) {
                : "memory");
 }
 
-// Descriptor of an MN-major operand with 128-byte swizzle: rows of 128 bytes (64
-// values along N) for consecutive K, 8-row atoms of 1024 bytes; the leading byte
-// offset steps to the next 64 values along N, the stride byte offset to the next 8
-// rows along K.
-__device__ __forceinline__ uint64_t pf_mn_desc(uint32_t smem_addr, uint32_t lbo_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
+// Shared-memory matrix descriptors with 128-byte swizzle, low words: address and
+// leading byte offset. K-major operands (rows of 128 bytes, 64 values along K) do not
+// use the offset; MN-major ones (rows of 64 values along N for consecutive K) step by it to
+// the next 64 values along N. 8-row atoms of 1024 bytes lie one after the other.
+__device__ __forceinline__ uint32_t pf_desc(uint32_t smem_addr, uint32_t lbo_bytes) {
+  return ((smem_addr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);
 }
 
 __device__ __forceinline__ void pf_tma_q(uint32_t dst, const CUtensorMap* map, int dim, int head, int row, uint64_t* bar) {
@@ -336,20 +331,24 @@ __device__ __forceinline__ uint32_t pf_leader() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
   return one;
 }
-__device__ __forceinline__ void pf_mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// (descriptors by their low words; the high word, stride and swizzle, is the same for all)
+constexpr uint32_t PF_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void pf_mma(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
+      "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader), "n"(PF_DESC_HI)
       : "memory");
 }
-__device__ __forceinline__ void pf_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void pf_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader)
+      "mov.b64 y, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader), "n"(PF_DESC_HI)
       : "memory");
 }
 __device__ __forceinline__ void pf_commit(uint32_t leader, uint64_t* bar) {
@@ -518,6 +517,8 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
   for (int n = 0; take(n); k0 += it.kb1 - it.kb0, ++n) {
     if (blk * a.block_pos >= it.count - it.t * a.w.span) continue;  // no rows in this block
     const PfRow row = pf_row(a, it, pf_heads(a, it.row), blk, place, head);
+    // key blocks that all rows of the warp see whole (a negative scale takes the long way)
+    const int whole = a.flip ? 0 : __reduce_min_sync(0xffffffffu, row.valid ? row.vis : 0x7FFFFFFF) / PF_KEYS;
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
     for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
@@ -525,51 +526,74 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
       if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.s_full[blk][buf], (j >> 1) & 1, abort_flag, lim))) return;
       tc::tc_fence_after();
       const uint32_t tS = tq + C::s_col(blk, buf);
+      const uint32_t exist = there[(k0 + kb - it.kb0) % (2 * C::KST)];
       uint32_t v[PF_KEYS];
       pf_ld32(tS, v);
       pf_ld32(tS + 32, v + 32);
       pf_wait_ld(v);
       pf_wait_ld(v + 32);
-      if (a.flip) {
+      // p = exp2(c s - m) as bf16 over the scores, their sum in l
+      const auto weights = [&]() {
+        const float mref = m == -INFINITY ? 0.f : m;
+        const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
+        uint64_t l2[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
-      }
-      pf_mask(v, row.vis - kb * PF_KEYS, there[(k0 + kb - it.kb0) % (2 * C::KST)]);
-      const float mx = pf_max(v) * c;
-      const bool need = mx > m + PF_RESCALE_LOG2;
-      if (__any_sync(0xffffffffu, need)) {
-        const float alpha = need ? exp2f(m - mx) : 1.f;
-        if (need) m = mx;
-        l *= alpha;
-        if (kb > it.kb0) {
-          // O holds P V of the block before once that is done
-          if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][buf ^ 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
-            return;
-          tc::tc_fence_after();
-#pragma unroll 1
-          for (int i = 0; i < C::HDP / 32; ++i) {
-            uint32_t o[32];
-            pf_ld32(tO + 32 * i, o);
-            pf_wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st16(tO + 32 * i, o);
-            tc::tmem_st16(tO + 32 * i + 16, o + 16);
-          }
+        for (int i = 0; i < PF_KEYS / 2; ++i) {
+          const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
+          const float p0 = exp2f(d.x), p1 = exp2f(d.y);
+          l2[i & 1] = ffma2(pack2(__float_as_uint(p0), __float_as_uint(p1)), one2, l2[i & 1]);
+          v[i] = tc::pack_bf16x2(p0, p1);
+        }
+        const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
+        return (la.x + la.y) + (lb.x + lb.y);
+      };
+      // Most blocks are seen whole and do not move the reference: their weights are formed while their maximum is
+      // sought. Where it does move, the scores are taken again (they are overwritten only below).
+      bool done = false;
+      if (kb > it.kb0 && kb < whole && exist == 0xFFu) {
+        const float mx = pf_max(v) * c;
+        const float lb = weights();
+        done = !__any_sync(0xffffffffu, mx > m + PF_RESCALE_LOG2);
+        if (done) {
+          l += lb;
+        } else {
+          pf_ld32(tS, v);
+          pf_ld32(tS + 32, v + 32);
+          pf_wait_ld(v);
+          pf_wait_ld(v + 32);
         }
       }
-      const float mref = m == -INFINITY ? 0.f : m;
-      const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
-      uint64_t l2[2] = {0, 0};
+      if (!done) {
+        if (a.flip) {
 #pragma unroll
-      for (int i = 0; i < PF_KEYS / 2; ++i) {
-        const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
-        const float p0 = exp2f(d.x), p1 = exp2f(d.y);
-        l2[i & 1] = ffma2(pack2(__float_as_uint(p0), __float_as_uint(p1)), one2, l2[i & 1]);
-        v[i] = tc::pack_bf16x2(p0, p1);
+          for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
+        }
+        pf_mask(v, row.vis - kb * PF_KEYS, exist);
+        const float mx = pf_max(v) * c;
+        const bool need = mx > m + PF_RESCALE_LOG2;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? exp2f(m - mx) : 1.f;
+          if (need) m = mx;
+          l *= alpha;
+          if (kb > it.kb0) {
+            // O holds P V of the block before once that is done
+            if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][buf ^ 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
+              return;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < C::HDP / 32; ++i) {
+              uint32_t o[32];
+              pf_ld32(tO + 32 * i, o);
+              pf_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc::tmem_st16(tO + 32 * i, o);
+              tc::tmem_st16(tO + 32 * i + 16, o + 16);
+            }
+          }
+        }
+        l += weights();
       }
-      const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
-      l += (la.x + la.y) + (lb.x + lb.y);
       tc::tmem_st16(tS, v);
       tc::tmem_st16(tS + 16, v + 16);
       tc::tmem_wait_st();
@@ -771,12 +795,12 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
 }
 
 template <class C>
-__global__ void __launch_bounds__(PF_THREADS, 1)
+__global__ void __launch_bounds__(C::THREADS, 1)
     prefill_tc_kernel(const PfArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t pf_smem_raw[];
   __shared__ PfCut cuts[2];
-  __shared__ long long sums[PF_THREADS / 32];
+  __shared__ long long sums[C::THREADS / 32];
   __shared__ PfItem items[PF_ITEMS];
   __shared__ uint32_t there[2 * C::KST];
   __shared__ __align__(8) PfBars bar;
@@ -785,7 +809,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   __shared__ int abort_word;
   const uint32_t s0 = tc::smem_u32(pf_smem_raw);
   uint8_t* smem = pf_smem_raw + (((s0 + 1023u) & ~1023u) - s0);
-  uint8_t* sQ = smem;                       // [2 blocks] or [3 parts]
+  uint8_t* sQ = smem;                       // [QT]
   uint8_t* sK = sQ + C::QT * C::QTILE;      // [KST]
   uint8_t* sV = sK + C::KST * C::TILE;      // [VST]
   volatile int* abort_flag = &abort_word;
@@ -797,16 +821,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll 1
       for (int i = 0; i < n; ++i) tc::mbar_init(b + i, count);
     };
-    init(bar.k_full, 24, 1);  // and k_empty, v_full, v_empty
+    init(bar.k_full, 12, 1);               // and v_full
+    init(bar.k_empty, 12, C::BLOCKS);      // and v_empty
     init(bar.it_full, PF_ITEMS, 1);
-    init(bar.it_empty, PF_ITEMS, 11);
-    init(bar.q_full, 2, C::F32 ? 4 : 1);
-    init(bar.q_empty, 2, 1);
+    init(bar.it_empty, PF_ITEMS, 9 + 2 * C::BLOCKS);
+    init(bar.q_full, 3, C::F32 ? 4 : 1);
+    init(bar.q_empty, 3, 1);
     init(&bar.s_full[0][0], 4, 1);
     init(&bar.p_full[0][0], 4, 4);
     init(&bar.pv_done[0][0], 4, 1);
     init(&bar.o_read, 2, 4);  // and l_full
-    init(bar.drain, 2, 1);
+    init(bar.drain, 4, 1);
     abort_word = 0;
     tc::fence_barrier_init();
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
@@ -815,7 +840,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   if (warp == PF_SWARP) tc::tmem_alloc(&tmem_slot, 512);
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  pf_share<PF_THREADS>(a.p, a.w, cuts, sums);
+  pf_share<C::THREADS>(a.p, a.w, cuts, sums);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -846,7 +871,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     __syncwarp();
     PfWalk walk;
     walk.begin(a.p, cuts);
-    int k = 0, q_n[2] = {0, 0};
+    int k = 0, q_n = 0;
     bool ok = true;
     const bool withhold = a.p.a.fault && blockIdx.x == 0;
     for (int n = 0; ok; ++n) {
@@ -867,29 +892,28 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       if (!more) break;
       if (it.kb1 <= it.kb0) continue;
       const PfHeads hs = pf_heads(a, it.row);
-      if (!C::F32) {
-        // a block's queries once S of the item before no longer reads its space; what lies behind the rows
-        // (other sequences' rows, zeros from n_rows on) is masked
-        const int blocks = blocks_of();
-#pragma unroll 1
-        for (int blk = 0; blk < blocks; ++blk) {
-          if (q_n[blk] > 0 &&
-              !__all_sync(0xffffffffu, tc::mbar_wait(&bar.q_empty[blk], (q_n[blk] - 1) & 1, abort_flag, lim))) {
-            ok = false;
-            break;
-          }
-          ++q_n[blk];
-          if (lane == 0) {
-            tc::mbar_expect_tx(&bar.q_full[blk], C::NH * 128 * a.w.row_heads * a.block_pos);
+      const int blocks = blocks_of();
+      // A block's queries go into the space of the third block before, once S no longer reads that; what lies behind
+      // the rows (other sequences' rows, zeros from n_rows on) is masked. The second block's wait for the item
+      // before: it comes behind the first keys.
+      const auto queries = [&](int blk) -> bool {
+        const int qs = q_n % 3;
+        if (q_n >= 3 &&
+            !__all_sync(0xffffffffu, tc::mbar_wait(&bar.q_empty[qs], (q_n / 3 - 1) & 1, abort_flag, lim)))
+          return false;
+        ++q_n;
+        if (lane == 0) {
+          tc::mbar_expect_tx(&bar.q_full[qs], C::NH * 128 * a.w.row_heads * a.block_pos);
 #pragma unroll
-            for (int h = 0; h < C::NH; ++h)
-              pf_tma_q(tc::smem_u32(sQ) + blk * C::QTILE + h * C::QHALF, &qmap, 64 * h, hs.h0,
-                       it.first + it.t * a.w.span + blk * a.block_pos, &bar.q_full[blk]);
-          }
-          __syncwarp();
+          for (int h = 0; h < C::NH; ++h)
+            pf_tma_q(tc::smem_u32(sQ) + qs * C::QTILE + h * C::QHALF, &qmap, 64 * h, hs.h0,
+                     it.first + it.t * a.w.span + blk * a.block_pos, &bar.q_full[qs]);
         }
-        if (!ok) break;
-      }
+        __syncwarp();
+        return true;
+      };
+      if (!C::F32 && !queries(0)) break;
+      const int second = it.kb0 + min(C::KST - 1, it.kb1 - it.kb0 - 1);
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const PfPages pg = pf_pages(a, it, kb);
@@ -909,6 +933,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
         if (lane == 0) there[k % (2 * C::KST)] = pg.there;
         pf_copy<C>(a, hs.g, pg, &kmap, sK + st * C::TILE, &bar.k_full[st]);
+        if (!C::F32 && kb == second && blocks == 2 && !queries(1)) {
+          ++k;
+          ok = false;
+          break;
+        }
       }
     }
     // copies in flight land before the CTA leaves
@@ -917,8 +946,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     for (int i = max(0, k - C::KST); i < k; ++i) tc::mbar_wait(&bar.k_full[i % C::KST], (i / C::KST) & 1, &never, lim);
     if (!C::F32) {
 #pragma unroll 1
-      for (int blk = 0; blk < 2; ++blk)
-        if (q_n[blk] > 0) tc::mbar_wait(&bar.q_full[blk], (q_n[blk] - 1) & 1, &never, lim);
+      for (int i = max(0, q_n - 3); i < q_n; ++i) tc::mbar_wait(&bar.q_full[i % 3], (i / 3) & 1, &never, lim);
     }
     __syncwarp();
   } else if (warp == PF_VWARP) {
@@ -943,70 +971,76 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll 1
     for (int i = max(0, k - C::VST); i < k; ++i) tc::mbar_wait(&bar.v_full[i % C::VST], (i / C::VST) & 1, &never, lim);
     __syncwarp();
-  } else if (warp == PF_SWARP) {
+  } else if (warp == PF_SWARP || warp == 12) {
     // ------------------------------------------------------------ S = Q K^T
+    const int blk = C::BLOCKS == 2 && warp == 12 ? 1 : 0;
     const uint32_t idesc = tc::idesc_bf16_f32(128, PF_KEYS);
     const int steps = (hd + 15) / 16;
-    int k = 0, q_n[2] = {0, 0}, s_n[2] = {0, 0};
+    int k = 0, j = 0, q_n = 0;  // j: S products so far; q_n: bf16 blocks of queries (fp32: tiles) of the items before
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int blocks = blocks_of();
+      const int blocks = blocks_of(), q = q_n + blk, qs = C::F32 ? 0 : q % 3;
 #pragma unroll 1
-      for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
-        const int st = k % C::KST;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.k_full[st], (k / C::KST) & 1, abort_flag, lim));
-#pragma unroll
-        for (int blk = 0; blk < C::BLOCKS; ++blk) {
-          if (!ok || blk >= blocks) break;
-          if (kb == it.kb0) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.q_full[blk], q_n[blk] & 1, abort_flag, lim));
-            ++q_n[blk];
-          }
-          // the buffer is free again: bf16 once P V of two blocks before, which reads P there, is done; fp32 once
-          // the softmax has taken S of two blocks before
-          const int j = s_n[blk], buf = j & 1;
-          uint64_t* free_bar = C::F32 ? &bar.p_full[0][buf] : &bar.pv_done[blk][buf];
-          ok = ok && (j < 2 || __all_sync(0xffffffffu, tc::mbar_wait_poll(free_bar, ((j >> 1) - 1) & 1, abort_flag, lim)));
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
+        const int st = k % C::KST, buf = j & 1;
+        ok = tc::mbar_wait_poll(&bar.k_full[st], (k / C::KST) & 1, abort_flag, lim);
+        if (blk >= blocks) {  // no rows in this block: the stage is free as far as this warp goes
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          ++s_n[blk];
-          tc::tc_fence_after();
-          const uint64_t kd = tc::sw128_desc(tc::smem_u32(sK) + (uint32_t)(pf_same(st) * C::TILE));
-          const uint32_t d = pf_same(tmem) + C::s_col(blk, pf_same(buf));
-#pragma unroll
-          for (int part = C::PARTS - 1; part >= 0; --part) {
-            const uint64_t qd = tc::sw128_desc(tc::smem_u32(sQ + (blk + part) * C::QTILE));
-#pragma unroll
-            for (int kk = 0; kk < C::HDP / 16; ++kk)
-              if (kk < steps)
-                pf_mma(leader, d, qd + (uint64_t)((kk >> 2) * (C::QHALF >> 4) + 2 * (kk & 3)),
-                       kd + (uint64_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3)), idesc,
-                       part != C::PARTS - 1 || kk != 0);
-          }
-          pf_commit(leader, &bar.s_full[blk][buf]);
-          if (blk == blocks - 1) pf_commit(leader, &bar.k_empty[st]);
-          if (!C::F32 && kb == it.kb1 - 1) pf_commit(leader, &bar.q_empty[blk]);
-          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar.k_empty[st]);
+          continue;
         }
+        if (kb == it.kb0) ok = ok && tc::mbar_wait_poll(&bar.q_full[qs], (C::F32 ? q : q / 3) & 1, abort_flag, lim);
+        // the buffer is free again: bf16 once P V of two blocks before, which reads P there, is done; fp32 once
+        // the softmax has taken S of two blocks before
+        uint64_t* free_bar = C::F32 ? &bar.p_full[0][buf] : &bar.pv_done[blk][buf];
+        ok = ok && (j < 2 || tc::mbar_wait_poll(free_bar, ((j >> 1) - 1) & 1, abort_flag, lim));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++j;
+        tc::tc_fence_after();
+        const uint32_t kd = pf_same(pf_desc(tc::smem_u32(sK) + (uint32_t)(st * C::TILE), 16));
+        const uint32_t d = pf_same(tmem + C::s_col(blk, buf));
+#pragma unroll
+        for (int part = C::PARTS - 1; part >= 0; --part) {
+          const uint32_t qd = pf_same(pf_desc(tc::smem_u32(sQ) + (uint32_t)((qs + part) * C::QTILE), 16));
+#pragma unroll
+          for (int kk = 0; kk < C::HDP / 16; ++kk)
+            if (kk < steps)
+              pf_mma(leader, d, qd + (uint32_t)((kk >> 2) * (C::QHALF >> 4) + 2 * (kk & 3)),
+                     kd + (uint32_t)((kk >> 2) * (C::HALF >> 4) + 2 * (kk & 3)), idesc,
+                     part != C::PARTS - 1 || kk != 0);
+        }
+        pf_commit(leader, &bar.s_full[blk][buf]);
+        pf_commit(leader, &bar.k_empty[st]);
+        if (!C::F32 && kb == it.kb1 - 1) pf_commit(leader, &bar.q_empty[qs]);
       }
+      if (it.kb1 > it.kb0) q_n += blocks;
     }
-    pf_commit(leader, &bar.drain[0]);
+    pf_commit(leader, &bar.drain[blk]);
     volatile int never = 0;
-    tc::mbar_wait(&bar.drain[0], 0, &never, lim);
+    tc::mbar_wait(&bar.drain[blk], 0, &never, lim);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ O += P V
+    const int blk = C::BLOCKS == 2 && warp == 13 ? 1 : 0;
     const uint32_t idesc = tc::idesc_bf16_f32(128, (hd + 15) / 16 * 16) | (1u << 16);  // B (V) MN-major
-    int k = 0, p_n[2] = {0, 0};
+    int k = 0, j = 0;  // j: P V products so far
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
       const int blocks = blocks_of();
 #pragma unroll 1
-      for (int kb = it.kb0; ok && kb < it.kb1; ++kb, ++k) {
-        const int st = k % C::VST;
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
+        const int st = k % C::VST, buf = j & 1;
         ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.v_full[st], (k / C::VST) & 1, abort_flag, lim));
         if (!ok) break;
+        if (blk >= blocks) {
+          if (lane == 0) tc::mbar_arrive(&bar.v_empty[st]);
+          continue;
+        }
         uint8_t* vs = sV + st * C::TILE;
-        // rows behind the sequence's last entry may hold anything, NaN too: zero weights need zero values
+        // rows behind the sequence's last entry may hold anything, NaN too: zero weights need zero values (both
+        // blocks' warps write the zeros, each ahead of its own products)
         if (it.len - kb * PF_KEYS < PF_KEYS) {
           const int r0 = it.len - kb * PF_KEYS;
 #pragma unroll 1
@@ -1018,36 +1052,30 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
+        ok = tc::mbar_wait_poll(&bar.p_full[blk][buf], (j >> 1) & 1, abort_flag, lim);
+        if (C::F32) ok = ok && (j == 0 || tc::mbar_wait_poll(&bar.o_read, (j - 1) & 1, abort_flag, lim));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++j;
+        tc::tc_fence_after();
+        const uint32_t vd = pf_same(pf_desc(tc::smem_u32(sV) + (uint32_t)(st * C::TILE), C::HALF));
+        const uint32_t d = pf_same(tmem + C::o_col(blk));
+        const bool first = !C::F32 && kb == it.kb0;
 #pragma unroll
-        for (int blk = 0; blk < C::BLOCKS; ++blk) {
-          if (!ok || blk >= blocks) break;
-          const int j = p_n[blk], buf = j & 1;
-          ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.p_full[blk][buf], (j >> 1) & 1, abort_flag, lim));
-          if (C::F32 && ok && j > 0)
-            ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.o_read, (j - 1) & 1, abort_flag, lim));
-          if (!ok) break;
-          ++p_n[blk];
-          tc::tc_fence_after();
-          const uint64_t vd = pf_mn_desc(tc::smem_u32(sV) + (uint32_t)(pf_same(st) * C::TILE), C::HALF);
-          const uint32_t d = pf_same(tmem) + C::o_col(blk);
-          const bool first = !C::F32 && kb == it.kb0;
+        for (int part = C::PARTS - 1; part >= 0; --part) {
+          const uint32_t pa = pf_same(tmem + C::p_col(blk, part, buf));
 #pragma unroll
-          for (int part = C::PARTS - 1; part >= 0; --part) {
-            const uint32_t pa = pf_same(tmem) + C::p_col(blk, part, pf_same(buf));
-#pragma unroll
-            for (int kk = 0; kk < PF_KEYS / 16; ++kk)
-              pf_mma_ts(leader, d, pa + 8u * kk, vd + (uint64_t)(2048 / 16 * kk), idesc,
-                        part != C::PARTS - 1 || kk != 0 || (!C::F32 && !first));
-          }
-          pf_commit(leader, &bar.pv_done[blk][buf]);
-          if (blk == blocks - 1) pf_commit(leader, &bar.v_empty[st]);
-          __syncwarp();
+          for (int kk = 0; kk < PF_KEYS / 16; ++kk)
+            pf_mma_ts(leader, d, pa + 8u * kk, vd + (uint32_t)(2048 / 16 * kk), idesc,
+                      part != C::PARTS - 1 || kk != 0 || (!C::F32 && !first));
         }
+        pf_commit(leader, &bar.pv_done[blk][buf]);
+        pf_commit(leader, &bar.v_empty[st]);
       }
     }
-    pf_commit(leader, &bar.drain[1]);
+    pf_commit(leader, &bar.drain[2 + blk]);
     volatile int never = 0;
-    tc::mbar_wait(&bar.drain[1], 0, &never, lim);
+    tc::mbar_wait(&bar.drain[2 + blk], 0, &never, lim);
     __syncwarp();
   }
 
@@ -1287,7 +1315,7 @@ cudaError_t launch_tc(PfArgs& x, cudaStream_t st) {
     return cudaErrorInvalidValue;
   cudaError_t e = ensure_kernel_smem(reinterpret_cast<const void*>(prefill_tc_kernel<C>), C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(prefill_tc_kernel<C>, dim3(x.w.ctas), PF_THREADS, C::SMEM, 0, st, x, km, vm, qm);
+  return launch_overlapped(prefill_tc_kernel<C>, dim3(x.w.ctas), C::THREADS, C::SMEM, 0, st, x, km, vm, qm);
 }
 
 }  // namespace
