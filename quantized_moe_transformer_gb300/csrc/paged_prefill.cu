@@ -235,7 +235,7 @@ struct PfCfg {
   static constexpr bool F32 = F32_;
   static constexpr int HDP = HDP_, NH = HDP / 64;
   static constexpr int BLOCKS = F32 ? 1 : 2, PARTS = F32 ? 3 : 1;
-  static constexpr int THREADS = 32 * (10 + 2 * BLOCKS);
+  static constexpr int THREADS = F32 ? 384 : 512;  // (bf16: two warps more, so that warps give registers up by fours)
   static constexpr int QT = 3;                     // bf16: a ring of blocks of queries; fp32: their parts
   static constexpr int QHALF = 128 * 128;          // 64 head dims of 128 query rows
   static constexpr int QTILE = NH * QHALF;
@@ -251,7 +251,7 @@ struct PfCfg {
   }
   static __device__ __forceinline__ uint32_t o_col(int blk) { return O_COL + (uint32_t)HDP * blk; }
 };
-constexpr int PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10, PF_OWARP = 11;  // S and P V of block 1: 12 and 13
+constexpr int PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10;  // 11 P V; block 1's S and P V 12 and 13
 constexpr float PF_RESCALE_LOG2 = 8.f;
 
 struct PfArgs {
@@ -291,6 +291,33 @@ __device__ __forceinline__ void pf_ld32(uint32_t ta, uint32_t* v) {
         "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
         "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
         "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(ta)
+      : "memory");
+}
+// 32 lanes x 64 columns and the wait, in one statement: the registers come out of it as they
+// are (loads and wait apart, with the registers passing through the wait, cost a move each).
+__device__ __forceinline__ void pf_ld64(uint32_t ta, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]),
+        "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]),
+        "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]),
+        "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]),
+        "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+      : "r"(ta)
+      : "memory");
+}
+// 16 columns and the wait.
+__device__ __forceinline__ void pf_ld16(uint32_t ta, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(ta)
       : "memory");
 }
@@ -441,11 +468,15 @@ __device__ __forceinline__ void pf_mask(uint32_t* v, int seen, uint32_t exist) {
   }
 }
 
+__device__ __forceinline__ float pf_max3(float a, uint32_t b, uint32_t c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return m;
+}
 __device__ __forceinline__ float pf_max(const uint32_t* v) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < PF_KEYS; i += 2)
-    m[(i >> 1) & 3] = fmaxf(fmaxf(m[(i >> 1) & 3], __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
+  for (int i = 0; i < PF_KEYS; i += 2) m[(i >> 1) & 3] = pf_max3(m[(i >> 1) & 3], v[i], v[i + 1]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
@@ -513,11 +544,14 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
   const float c = a.scale;
   const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c)), one2 = pack2(0x3F800000u, 0x3F800000u);
   int j = 0;   // key blocks of this block of rows so far
-  int k0 = 0;  // key blocks of the CTA's items before this one
-  for (int n = 0; take(n); k0 += it.kb1 - it.kb0, ++n) {
-    if (blk * a.block_pos >= it.count - it.t * a.w.span) continue;  // no rows in this block
+  int ring = 0;  // the key block's place in the ring of ``there``
+  for (int n = 0; take(n); ++n) {
+    if (blk * a.block_pos >= it.count - it.t * a.w.span) {  // no rows in this block
+      ring = (ring + it.kb1 - it.kb0) % (2 * C::KST);
+      continue;
+    }
     const PfRow row = pf_row(a, it, pf_heads(a, it.row), blk, place, head);
-    // key blocks that all rows of the warp see whole (a negative scale takes the long way)
+    // key blocks that all rows of the warp see whole (with a negative scale all are gone through)
     const int whole = a.flip ? 0 : __reduce_min_sync(0xffffffffu, row.valid ? row.vis : 0x7FFFFFFF) / PF_KEYS;
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -526,76 +560,57 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
       if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.s_full[blk][buf], (j >> 1) & 1, abort_flag, lim))) return;
       tc::tc_fence_after();
       const uint32_t tS = tq + C::s_col(blk, buf);
-      const uint32_t exist = there[(k0 + kb - it.kb0) % (2 * C::KST)];
-      uint32_t v[PF_KEYS];
-      pf_ld32(tS, v);
-      pf_ld32(tS + 32, v + 32);
-      pf_wait_ld(v);
-      pf_wait_ld(v + 32);
-      // p = exp2(c s - m) as bf16 over the scores, their sum in l
-      const auto weights = [&]() {
+      uint32_t v[PF_KEYS], w[PF_KEYS / 2];
+      const uint32_t exist = there[ring];
+      ring = ring + 1 == 2 * C::KST ? 0 : ring + 1;
+      pf_ld64(tS, v);
+      if (kb >= whole || exist != 0xFFu) {
+        if (a.flip) {
+#pragma unroll
+          for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
+        }
+        pf_mask(v, row.vis - kb * PF_KEYS, exist);
+      }
+      // p = exp2(c s - m) as bf16, their sum in fp32. Most blocks do not move the reference: the weights are formed while
+      // the maximum is sought, and again where it does (as in a tile's first block).
+      float lb;
+      for (;;) {
         const float mref = m == -INFINITY ? 0.f : m;
         const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
+        const float mx = pf_max(v) * c;
         uint64_t l2[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < PF_KEYS / 2; ++i) {
           const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
           const float p0 = exp2f(d.x), p1 = exp2f(d.y);
           l2[i & 1] = ffma2(pack2(__float_as_uint(p0), __float_as_uint(p1)), one2, l2[i & 1]);
-          v[i] = tc::pack_bf16x2(p0, p1);
+          w[i] = tc::pack_bf16x2(p0, p1);
         }
-        const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
-        return (la.x + la.y) + (lb.x + lb.y);
-      };
-      // Most blocks are seen whole and do not move the reference: their weights are formed while their maximum is
-      // sought. Where it does move, the scores are taken again (they are overwritten only below).
-      bool done = false;
-      if (kb > it.kb0 && kb < whole && exist == 0xFFu) {
-        const float mx = pf_max(v) * c;
-        const float lb = weights();
-        done = !__any_sync(0xffffffffu, mx > m + PF_RESCALE_LOG2);
-        if (done) {
-          l += lb;
-        } else {
-          pf_ld32(tS, v);
-          pf_ld32(tS + 32, v + 32);
-          pf_wait_ld(v);
-          pf_wait_ld(v + 32);
-        }
-      }
-      if (!done) {
-        if (a.flip) {
-#pragma unroll
-          for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
-        }
-        pf_mask(v, row.vis - kb * PF_KEYS, exist);
-        const float mx = pf_max(v) * c;
+        const float2 la = unpack2(l2[0]), lc = unpack2(l2[1]);
+        lb = (la.x + la.y) + (lc.x + lc.y);
         const bool need = mx > m + PF_RESCALE_LOG2;
-        if (__any_sync(0xffffffffu, need)) {
-          const float alpha = need ? exp2f(m - mx) : 1.f;
-          if (need) m = mx;
-          l *= alpha;
-          if (kb > it.kb0) {
-            // O holds P V of the block before once that is done
-            if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][buf ^ 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
-              return;
-            tc::tc_fence_after();
+        if (!__any_sync(0xffffffffu, need)) break;
+        const float alpha = need ? exp2f(m - mx) : 1.f;
+        if (need) m = mx;
+        l *= alpha;
+        if (kb > it.kb0) {
+          // O holds P V of the block before once that is done
+          if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][buf ^ 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
+            return;
+          tc::tc_fence_after();
 #pragma unroll 1
-            for (int i = 0; i < C::HDP / 32; ++i) {
-              uint32_t o[32];
-              pf_ld32(tO + 32 * i, o);
-              pf_wait_ld(o);
+          for (int i = 0; i < C::HDP / 16; ++i) {
+            uint32_t o[16];
+            pf_ld16(tO + 16 * i, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc::tmem_st16(tO + 32 * i, o);
-              tc::tmem_st16(tO + 32 * i + 16, o + 16);
-            }
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st16(tO + 16 * i, o);
           }
         }
-        l += weights();
       }
-      tc::tmem_st16(tS, v);
-      tc::tmem_st16(tS + 16, v + 16);
+      l += lb;
+      tc::tmem_st16(tS, w);
+      tc::tmem_st16(tS + 16, w + 16);
       tc::tmem_wait_st();
       tc::tc_fence_before();
       __syncwarp();
@@ -689,10 +704,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
         if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.s_full[0][buf], (j >> 1) & 1, abort_flag, lim))) return;
         tc::tc_fence_after();
         uint32_t v[PF_KEYS];
-        pf_ld32(tq + C::s_col(0, buf), v);
-        pf_ld32(tq + C::s_col(0, buf) + 32, v + 32);
-        pf_wait_ld(v);
-        pf_wait_ld(v + 32);
+        pf_ld64(tq + C::s_col(0, buf), v);
         if (a.flip) {
 #pragma unroll
           for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
@@ -859,6 +871,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   };
   auto blocks_of = [&]() { return C::BLOCKS == 2 && it.count - it.t * a.w.span > a.block_pos ? 2 : 1; };
 
+  // registers of 512 threads go from the others to the softmax, which holds 64 scores and 32 weights: 256 x 168 + 256 x 80
+  if constexpr (!C::F32) {
+    if (warp < 8)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  }
   if (warp < 8) {
     if constexpr (C::F32)
       prefill_f32_rows<C>(a, take, it, tmem, sQ, there, bar, factor, abort_flag);
@@ -983,7 +1002,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const int st = k % C::KST, buf = j & 1;
-        ok = tc::mbar_wait_poll(&bar.k_full[st], (k / C::KST) & 1, abort_flag, lim);
+        ok = tc::mbar_wait(&bar.k_full[st], (k / C::KST) & 1, abort_flag, lim);
         if (blk >= blocks) {  // no rows in this block: the stage is free as far as this warp goes
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -994,7 +1013,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // the buffer is free again: bf16 once P V of two blocks before, which reads P there, is done; fp32 once
         // the softmax has taken S of two blocks before
         uint64_t* free_bar = C::F32 ? &bar.p_full[0][buf] : &bar.pv_done[blk][buf];
-        ok = ok && (j < 2 || tc::mbar_wait_poll(free_bar, ((j >> 1) - 1) & 1, abort_flag, lim));
+        ok = ok && (j < 2 || tc::mbar_wait(free_bar, ((j >> 1) - 1) & 1, abort_flag, lim));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++j;
@@ -1021,7 +1040,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     volatile int never = 0;
     tc::mbar_wait(&bar.drain[blk], 0, &never, lim);
     __syncwarp();
-  } else {
+  } else if (warp == 11 || warp == 13) {
     // ------------------------------------------------------------ O += P V
     const int blk = C::BLOCKS == 2 && warp == 13 ? 1 : 0;
     const uint32_t idesc = tc::idesc_bf16_f32(128, (hd + 15) / 16 * 16) | (1u << 16);  // B (V) MN-major
@@ -1032,7 +1051,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const int st = k % C::VST, buf = j & 1;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.v_full[st], (k / C::VST) & 1, abort_flag, lim));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bar.v_full[st], (k / C::VST) & 1, abort_flag, lim));
         if (!ok) break;
         if (blk >= blocks) {
           if (lane == 0) tc::mbar_arrive(&bar.v_empty[st]);
