@@ -260,8 +260,8 @@ int qmoe_moe_forward_noalloc(const qmoe_moe_desc *d, const float *X, const float
  *                          softmax warps' last wait runs out;
  *   QMOE_FAULT_PAGED_COPY  paged attention: the first CTA's first warp never
  *                          copies its first tile;
- *   QMOE_FAULT_PREFILL_COPY attention of packed rows on the tensor cores: the first
- *                          CTA never copies its first keys.
+ *   QMOE_FAULT_PREFILL_COPY attention of packed rows on the tensor cores: no CTA
+ *                          copies its first keys.
  * Returns QMOE_ERR_ARG for an unknown site or a negative wait. Not for use
  * outside tests; set QMOE_FAULT_NONE afterwards.
  */
@@ -579,6 +579,23 @@ size_t qmoe_block_decode_paged_workspace_bytes(const qmoe_block_desc *b, const q
 int qmoe_block_decode_paged(const qmoe_block_desc *b, const qmoe_paged_cache *c, const float *X, float *out,
                             const int32_t *next_pos, int accumulate, void *ws, size_t ws_bytes,
                             qmoe_stream_t stream);
+
+/*
+ * The block for packed rows of prompts, parts of prompts and single new tokens of
+ * c->n_seqs sequences at once: rows X, out [n_rows][H] fp32 (out may not alias X). The
+ * rows' keys and values are appended (seq, slot, pos as in qmoe_paged_append, a slot below 0
+ * padding), then row first[b] + i of sequence b attends as in
+ * qmoe_paged_prefill_attention, then O, residual, norm and MoE. qmoe_paged_plan
+ * gives all five (granted as count); rows of no sequence come out with no attention added.
+ *   rope: how queries and keys turn, or NULL: by the block's rope_theta.
+ *   c->n_kv and c->head_dim are the block's.
+ *   ws: qmoe_block_prefill_paged_workspace_bytes(b, c, n_rows) bytes, 256-byte aligned.
+ */
+size_t qmoe_block_prefill_paged_workspace_bytes(const qmoe_block_desc *b, const qmoe_paged_cache *c, int n_rows);
+int qmoe_block_prefill_paged(const qmoe_block_desc *b, const qmoe_paged_cache *c, const float *X, float *out,
+                             int n_rows, const int32_t *first, const int32_t *count, const int32_t *seq,
+                             const int32_t *slot, const int32_t *pos, const qmoe_rope_desc *rope, void *ws,
+                             size_t ws_bytes, qmoe_stream_t stream);
 
 /* The CUDA runtime error code (cudaError_t) behind the last QMOE_ERR_LAUNCH
  * returned on this thread, 0 if none. */

@@ -100,7 +100,7 @@ def exported_symbols() -> list[str]:
             "qmoe_cache_evict_workspace_bytes", "qmoe_cache_evict", "qmoe_block_decode_paged_workspace_bytes",
             "qmoe_block_decode_paged", "qmoe_rope_init", "qmoe_rope", "qmoe_paged_append_rope",
             "qmoe_paged_plan_workspace_bytes", "qmoe_paged_plan", "qmoe_paged_prefill_attention_workspace_bytes",
-            "qmoe_paged_prefill_attention"]
+            "qmoe_paged_prefill_attention", "qmoe_block_prefill_paged_workspace_bytes", "qmoe_block_prefill_paged"]
 
 
 def _check(status: int):
@@ -457,6 +457,10 @@ def _paged_lib():
         L.qmoe_paged_prefill_attention_workspace_bytes.argtypes = [P, _c_int, _c_int]
         L.qmoe_paged_prefill_attention.argtypes = [P, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, ctypes.c_float, _vp,
                                                    _c_size, _vp]
+        L.qmoe_block_prefill_paged_workspace_bytes.restype = _c_size
+        L.qmoe_block_prefill_paged_workspace_bytes.argtypes = [ctypes.POINTER(BlockDesc), P, _c_int]
+        L.qmoe_block_prefill_paged.argtypes = [ctypes.POINTER(BlockDesc), P, _vp, _vp, _c_int] + [_vp] * 5 + [R, _vp, _c_size,
+                                                                                                       _vp]
         _paged = L
     return _paged
 
@@ -840,4 +844,31 @@ def block_decode_paged(block: Block, cache: PagedCache, X, next_pos, out=None, a
         ctypes.byref(block.desc), cache._desc_ref, _need(X, "X", shape, torch.float32, dev),
         _need(out, "out", shape, torch.float32, dev), _need(next_pos, "next_pos", (cache.n_seqs,), torch.int32, dev),
         int(accumulate), _need_ws(ws, dev), ws.numel(), _raw_stream(stream, cache)))
+    return out
+
+
+def block_prefill_paged_workspace(block: Block, cache: PagedCache, n_rows: int) -> torch.Tensor:
+    n = int(_paged_lib().qmoe_block_prefill_paged_workspace_bytes(ctypes.byref(block.desc), cache._desc_ref, n_rows))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def block_prefill_paged(block: Block, cache: PagedCache, X, first, count, seq, slot, pos, rope: Rope | None = None,
+                        out=None, ws=None, stream=None):
+    """The block for packed rows X [rows][H] fp32 of many sequences' prompts, parts of
+    prompts and single tokens, placed as ``paged_plan`` says (``count``: the rows granted): their
+    keys and values are appended, and each row attends to its sequence's entries up to
+    its own. ``rope``: how queries and keys turn, by the block's theta without it."""
+    rows, dev = X.shape[0] if X.dim() else 0, cache.device
+    shape, seqs, per_row, i32 = (rows, block.H), (cache.n_seqs,), (rows,), torch.int32
+    if out is None or ws is None:
+        with _allocating(stream):
+            out = torch.empty_like(X) if out is None else out
+            ws = block_prefill_paged_workspace(block, cache, rows) if ws is None else ws
+    _need_device(block.Wq, "the block", dev)
+    _check(_paged_lib().qmoe_block_prefill_paged(
+        ctypes.byref(block.desc), cache._desc_ref, _need(X, "X", shape, torch.float32, dev),
+        _need(out, "out", shape, torch.float32, dev), rows, _need(first, "first", seqs, i32, dev),
+        _need(count, "count", seqs, i32, dev), _need(seq, "seq", per_row, i32, dev), _need(slot, "slot", per_row, i32, dev),
+        _need(pos, "pos", per_row, i32, dev), None if rope is None else rope._ref, _need_ws(ws, dev), ws.numel(),
+        _raw_stream(stream, cache)))
     return out

@@ -879,6 +879,68 @@ int qmoe_block_decode_paged(const qmoe_block_desc* b, const qmoe_paged_cache* c,
 }
 
 
+size_t qmoe_block_prefill_paged_workspace_bytes(const qmoe_block_desc* b, const qmoe_paged_cache* c, int n_rows) {
+  PagedView view;
+  if (paged_block(b, c, &view) != QMOE_OK || n_rows < 1) return 0;
+  const size_t attn = qmoe_paged_prefill_attention_workspace_bytes(c, n_rows, b->n_heads);
+  const size_t block = qmoe_block_workspace_bytes(b, n_rows, 0);
+  return attn && block ? up256(attn) + block : 0;
+}
+
+int qmoe_block_prefill_paged(const qmoe_block_desc* b, const qmoe_paged_cache* c, const float* X, float* out, int n_rows,
+                             const int32_t* first, const int32_t* count, const int32_t* seq, const int32_t* slot,
+                             const int32_t* pos, const qmoe_rope_desc* rope, void* ws, size_t ws_bytes,
+                             qmoe_stream_t stream) {
+  PagedView view;
+  int r = paged_block(b, c, &view);
+  if (r != QMOE_OK) return r;
+  r = check_desc(&b->moe);
+  if (r != QMOE_OK) return r;
+  if (b->moe.H != b->H || n_rows < 0 || (rope && !rope_ok(*rope, b->head_dim))) return QMOE_ERR_ARG;
+  if (n_rows == 0) return QMOE_OK;
+  if (!X || !out || !first || !count || !seq || !slot || !pos || !ws) return QMOE_ERR_NULL;
+  if (X == out) return QMOE_ERR_ARG;
+  if (!aligned(X, 16) || !aligned(out, 16) || !aligned(first, 4) || !aligned(count, 4) || !aligned(seq, 4) ||
+      !aligned(slot, 4) || !aligned(pos, 4) || !aligned(ws, 256))
+    return QMOE_ERR_ALIGN;
+  const size_t need = qmoe_block_prefill_paged_workspace_bytes(b, c, n_rows);
+  if (need == 0) return QMOE_ERR_ARG;
+  if (ws_bytes < need) return QMOE_ERR_WORKSPACE;
+  int* status = nullptr;
+  r = device_ready(&status);
+  if (r != QMOE_OK) return r;
+  const int T = n_rows;
+  const AttnWs L = attn_ws_layout(b, T, 0);
+  const size_t row_bytes = up256(sizeof(float) * (size_t)T * b->H);
+  const size_t p_bytes = up256(qmoe_paged_prefill_attention_workspace_bytes(c, T, b->n_heads));
+  char* paged_ws = static_cast<char*>(ws);
+  char* base = paged_ws + p_bytes;
+  float* h1 = reinterpret_cast<float*>(base + L.total);
+  float* r2 = reinterpret_cast<float*>(base + L.total + row_bytes);
+  char* moe_ws = base + L.total + 2 * row_bytes;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  bool qkv_tc = false;
+  r = launch_status(attn_project(b, X, T, base, L, status, &qkv_tc, st));
+  if (r != QMOE_OK) return r;
+  float* q = reinterpret_cast<float*>(base + L.q);
+  float* o = reinterpret_cast<float*>(base + L.o);
+  r = append_impl(c, q, q, base + L.k, base + L.v, QMOE_F32, seq, slot, pos, T, b->n_heads, rope ? 0.f : b->rope_theta,
+                  rope, stream);
+  if (r != QMOE_OK) return r;
+  // rows of no sequence: no attention
+  r = launch_status(cudaMemsetAsync(o, 0, sizeof(float) * (size_t)T * b->n_heads * b->head_dim, st));
+  if (r != QMOE_OK) return r;
+  r = qmoe_paged_prefill_attention(c, q, o, QMOE_F32, first, count, T, b->n_heads, 0.f, paged_ws, p_bytes, stream);
+  if (r != QMOE_OK) return r;
+  r = launch_status(attn_output(b, X, h1, T, base, L, qkv_tc, false, status, st));
+  if (r != QMOE_OK) return r;
+  g_launches.fetch_add(1);
+  r = launch_status(launch_rmsnorm(h1, b->g2, b->eps, r2, T, b->H, st));
+  if (r != QMOE_OK) return r;
+  return qmoe_moe_forward(&b->moe, r2, h1, nullptr, nullptr, out, T, moe_ws, ws_bytes - (moe_ws - paged_ws), stream);
+}
+
+
 const char* qmoe_status_str(int s) {
   switch (s) {
     case QMOE_OK: return "ok";

@@ -120,7 +120,7 @@ struct PrefillArgs {
   float scale;
   int* status;
   unsigned long long wait_ns;  // bound on a device wait
-  bool fault;                  // test-only: the first CTA never copies its first keys
+  bool fault;                  // test-only: no CTA copies its first keys
   void* ws;
 };
 size_t paged_prefill_ws_bytes(const PagedView& c, int n_rows, int n_heads);

@@ -557,7 +557,7 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
 #pragma unroll 1
     for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
       const int buf = j & 1;
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.s_full[blk][buf], (j >> 1) & 1, abort_flag, lim))) return;
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar.s_full[blk][buf], (j >> 1) & 1, abort_flag, lim))) return;
       tc::tc_fence_after();
       const uint32_t tS = tq + C::s_col(blk, buf);
       uint32_t v[PF_KEYS], w[PF_KEYS / 2];
@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     walk.begin(a.p, cuts);
     int k = 0, q_n = 0;
     bool ok = true;
-    const bool withhold = a.p.a.fault && blockIdx.x == 0;
+    const bool withhold = a.p.a.fault;
     for (int n = 0; ok; ++n) {
       const bool more = walk.next(a.p, a.w, &it);
       if (!more) it.b = -1;
@@ -1071,7 +1071,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
-        ok = tc::mbar_wait_poll(&bar.p_full[blk][buf], (j >> 1) & 1, abort_flag, lim);
+        ok = tc::mbar_wait(&bar.p_full[blk][buf], (j >> 1) & 1, abort_flag, lim);
         if (C::F32) ok = ok && (j == 0 || tc::mbar_wait_poll(&bar.o_read, (j - 1) & 1, abort_flag, lim));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;

@@ -165,3 +165,33 @@ def test_python_names_of_a_rotation():
     for kw in (dict(layout="both"), dict(scaling="log"), dict(frequencies=[1.0] * 3), dict(dims=0), dict(frequencies=[float("nan")] * 32)):
         with pytest.raises(qb.QmoeError):
             qb.Rope(**(dict(dims=64) | kw))
+
+
+def block_desc(**kw):
+    d = qb.BlockDesc(2048, 16, 2, 128, 1e7, 1e-6, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                     qb.MoeDesc(2048, 256, 8, 512, 0, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE))
+    for name, value in kw.items():
+        setattr(d, name, value)
+    return d
+
+
+def prefill(lib, b=None, d=None, X=FAKE, out=2 * FAKE, n_rows=5, first=FAKE, count=FAKE, seq=FAKE, slot=FAKE, pos=FAKE, rope=None,
+            ws=FAKE, ws_bytes=1 << 40):
+    return lib.qmoe_block_prefill_paged(ctypes.byref(b or block_desc()), ctypes.byref(d or desc()), X, out, n_rows, first, count,
+                                        seq, slot, pos, ctypes.byref(rope) if rope else None, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"n_rows": -1}, ARG), ({"X": None}, NULL), ({"out": None}, NULL), ({"first": None}, NULL), ({"count": None}, NULL),
+    ({"seq": None}, NULL), ({"slot": None}, NULL), ({"pos": None}, NULL), ({"ws": None}, NULL), ({"out": FAKE}, ARG),
+    ({"X": FAKE + 8}, ALIGN), ({"out": FAKE + 4}, ALIGN), ({"first": FAKE + 2}, ALIGN), ({"pos": FAKE + 1}, ALIGN),
+    ({"ws": FAKE + 64}, ALIGN), ({"ws_bytes": 4096}, WORKSPACE)])
+def test_block_arguments(lib, kw, status):
+    assert prefill(lib, **kw) == status
+
+
+def test_block_of_another_cache(lib):
+    assert prefill(lib, d=desc(n_kv=4)) == ARG and prefill(lib, d=desc(head_dim=64)) == ARG
+    assert prefill(lib, rope=rope_desc(dims=136)) == ARG and prefill(lib, n_rows=0, ws=None) == 0
+    assert lib.qmoe_block_prefill_paged_workspace_bytes(ctypes.byref(block_desc()), ctypes.byref(desc(n_kv=4)), 5) == 0
+    assert lib.qmoe_block_prefill_paged_workspace_bytes(ctypes.byref(block_desc()), ctypes.byref(desc()), 0) == 0
