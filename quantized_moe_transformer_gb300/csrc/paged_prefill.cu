@@ -11,6 +11,7 @@
 #include <cmath>
 
 #include "paged.cuh"
+#include "rope.cuh"
 #include "tc.cuh"
 
 namespace qmoe {
@@ -90,53 +91,60 @@ __device__ __forceinline__ PfCut pf_cut(const PrefillRows& r, int row, int b, lo
   return PfCut{row, b, (int)t, kb};
 }
 
-// Where this CTA's work begins and ends, by all threads of the CTA.
-template <int THREADS>
-__device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w, PfCut* cuts, long long* sums) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int WARPS = THREADS / 32;
-  const int each = (p.c.n_seqs + THREADS - 1) / THREADS, b0 = min(tid * each, p.c.n_seqs), b1 = min(b0 + each, p.c.n_seqs);
-  long long mine = 0;
-#pragma unroll 1
-  for (int b = b0; b < b1; ++b) {
-    const PrefillRows r = prefill_rows(p, b);
-    if (r.count > 0) mine += pf_cost((r.count + w.span - 1) / w.span, max(r.before, 0), w.span);
-  }
-  long long v = mine;
+// Where this CTA's work begins and ends, by one warp: a lane has a sequence of 32.
+__device__ __forceinline__ long long pf_sequence_cost(const PrefillRows& r, int span) {
+  return r.count > 0 ? pf_cost((r.count + span - 1) / span, max(r.before, 0), span) : 0;
+}
+
+__device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w, PfCut (&cuts)[2]) {
+  const int lane = threadIdx.x & 31;
+  long long total = 0;
+#pragma unroll 4
+  for (int b = lane; b < p.c.n_seqs; b += 32) total += pf_sequence_cost(prefill_rows(p, b), w.span);
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
-  }
-  if (lane == 31) sums[warp] = v;
-  if (tid < 2) cuts[tid] = PfCut{w.head_rows, 0, 0, 0};
-  __syncthreads();
-  long long before = v - mine, total = 0;
-  for (int i = 0; i < WARPS; ++i) {
-    if (i < warp) before += sums[i];
-    total += sums[i];
-  }
+  for (int d = 16; d; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
+  cuts[0] = cuts[1] = PfCut{w.head_rows, 0, 0, 0};
   if (total == 0) return;
   const long long all = total * w.head_rows, per = all / w.ctas, more = all - per * w.ctas;
-#pragma unroll 1
+  long long at[2];
+  int row[2];
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int i = blockIdx.x + k;
-    if (i >= w.ctas) break;
-    const long long x = per * i + min((long long)i, more);
-    int row = (int)((float)x / (float)total);
-    while (row > 0 && row * total > x) --row;
-    while ((row + 1) * total <= x) ++row;
-    long long at = x - row * total - before;
-    if (at < 0 || at >= mine) continue;
-    for (int b = b0; b < b1; ++b) {
-      const PrefillRows r = prefill_rows(p, b);
-      const long long cost = r.count > 0 ? pf_cost((r.count + w.span - 1) / w.span, max(r.before, 0), w.span) : 0;
-      if (at < cost) {
-        cuts[k] = pf_cut(r, row, b, at, w.span);
-        break;
-      }
-      at -= cost;
+    const long long x = i < w.ctas ? per * i + min((long long)i, more) : all;
+    int q = (int)((float)x / (float)total);
+    while (q > 0 && q * total > x) --q;
+    while ((q + 1) * total <= x) ++q;
+    row[k] = q;
+    at[k] = x - q * total;  // inside the sequences' costs
+  }
+  long long before = 0;
+  bool open[2] = {row[0] < w.head_rows, row[1] < w.head_rows};
+  for (int b0 = 0; b0 < p.c.n_seqs && (open[0] || open[1]); b0 += 32) {
+    const PrefillRows mine = b0 + lane < p.c.n_seqs ? prefill_rows(p, b0 + lane) : PrefillRows{0, 0, 0, 0};
+    const long long cost = pf_sequence_cost(mine, w.span);
+    long long end = cost;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long o = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += o;
     }
+    end += before;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      if (!open[k]) continue;
+      const unsigned behind = __ballot_sync(0xffffffffu, end > at[k]);
+      if (behind == 0) continue;
+      const int src = __ffs(behind) - 1;
+      PrefillRows r;
+      r.first = 0;
+      r.count = __shfl_sync(0xffffffffu, mine.count, src);
+      r.len = __shfl_sync(0xffffffffu, mine.len, src);
+      r.before = r.len - r.count;
+      cuts[k] = pf_cut(r, row[k], b0 + src, at[k] - __shfl_sync(0xffffffffu, end - cost, src), w.span);
+      open[k] = false;
+    }
+    before = __shfl_sync(0xffffffffu, end, 31);
   }
 }
 
@@ -180,7 +188,9 @@ struct PfWalk {
     }
     at.b = window + __ffs(left) - 1;
   }
-  __device__ __forceinline__ void begin(const PrefillView& p, const PfCut* cuts) {
+  __device__ __forceinline__ void begin(const PrefillView& p, const PfTiling& w) {
+    PfCut cuts[2];
+    pf_share(p, w, cuts);
     at = cuts[0];
     end = cuts[1];
     look(p, at.b);
@@ -261,8 +271,9 @@ struct PfArgs {
   uint32_t flip;     // the sign bit where the scale is negative
   int box_rows;      // slots of a copy
   int block_pos;     // positions of a block of 128 query rows
-  float2* part_ml;   // [CTAs][2 slots][256 rows]
-  float* part_o;     // [CTAs][2][256][HDP]
+  bool wide;         // rows of out are 32-byte aligned
+  float2* part_ml;   // [CTAs][2 slots][blocks][128 rows]
+  float* part_o;     // as pf_part has it
 };
 
 struct PfBars {
@@ -480,56 +491,29 @@ __device__ __forceinline__ float pf_max(const uint32_t* v) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Four lanes with 64 bytes of a row each exchange 16-byte pieces: then lane q of them has
-// piece q of the four rows, which a store puts side by side (a store of a row's own 16 bytes a
-// lane would touch 32 lines).
-__device__ __forceinline__ void pf_quad(uint32_t* w) {
-  const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-      const uint32_t y = __shfl_xor_sync(0xffffffffu, b0 ? w[4 * k + i] : w[4 * k + 4 + i], 1);
-      if (b0)
-        w[4 * k + i] = y;
-      else
-        w[4 * k + 4 + i] = y;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t y = __shfl_xor_sync(0xffffffffu, b1 ? w[4 * k + i] : w[4 * k + 8 + i], 2);
-      if (b1)
-        w[4 * k + i] = y;
-      else
-        w[4 * k + 8 + i] = y;
-    }
+// 32 or 16 bytes of a row. (A row's bytes in pieces of 32, whole sectors, by its own thread: 8 of
+// them take a warp less time than 16 pieces of 16, and than pieces exchanged between lanes.)
+__device__ __forceinline__ void pf_store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void pf_store16(void* p, const uint32_t* w) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 8 words of a row of which ``bytes`` exist.
+__device__ __forceinline__ void pf_store_row(char* p, const uint32_t* w, int bytes, bool wide) {
+  if (bytes >= 32 && wide) {
+    pf_store32(p, w);
+  } else {
+    if (bytes >= 16) pf_store16(p, w);
+    if (bytes >= 32) pf_store16(p + 16, w + 4);
   }
 }
 
-// Where the rows of four lanes go: element, and whether they exist.
-struct PfQuad {
-  long long at[4];
-  bool valid[4];
-};
-__device__ __forceinline__ PfQuad pf_quad_rows(long long at, bool valid) {
-  PfQuad q;
-  const unsigned all = __ballot_sync(0xffffffffu, valid);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int src = ((int)threadIdx.x & 28) + k;
-    q.at[k] = __shfl_sync(0xffffffffu, at, src);
-    q.valid[k] = (all >> src) & 1u;
-  }
-  return q;
-}
-
-// 16 fp32 columns of each row from ``col`` on, columns from ``n`` on left out.
-__device__ __forceinline__ void pf_store16(float* base, const PfQuad& q, uint32_t* w, int col, int n) {
-  pf_quad(w);
-  const int c = col + 4 * ((int)threadIdx.x & 3);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (q.valid[k] && c < n) *reinterpret_cast<uint4*>(base + q.at[k] + c) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+// A part's O: [part][block][4 columns][128 rows], so that a warp's rows lie side by side.
+__device__ __forceinline__ float4* pf_part(float* base, long long part, int blk, int blocks, int hdp, int col4, int r) {
+  return reinterpret_cast<float4*>(base) + ((part * blocks + blk) * (hdp / 4) + col4) * 128 + r;
 }
 
 // Warps 0-7 of tiles of bf16 rows.
@@ -624,9 +608,9 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
       tc::tc_fence_after();
     }
     const float il = l > 0.f ? 1.f / l : 0.f;
-    const long long part = ((long long)blockIdx.x * 2 + it.slot) * 256 + blk * 128 + r;
-    if (it.slot >= 0 && row.valid) a.part_ml[part] = make_float2(m, l);
-    const PfQuad q = pf_quad_rows(it.slot >= 0 ? part * C::HDP : row.at, row.valid);
+    const long long part = (long long)blockIdx.x * 2 + it.slot;
+    if (it.slot >= 0 && row.valid) a.part_ml[(part * C::BLOCKS + blk) * 128 + r] = make_float2(m, l);
+    char* out = reinterpret_cast<char*>(static_cast<__nv_bfloat16*>(a.p.a.out) + row.at);
 #pragma unroll 1
     for (int i = 0; i < C::HDP / 32; ++i) {
       uint32_t o[32];
@@ -638,20 +622,21 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
       if (it.slot >= 0) {
-        pf_store16(a.part_o, q, o, 32 * i, C::HDP);
-        pf_store16(a.part_o, q, o + 16, 32 * i + 16, C::HDP);
-      } else {
+        if (row.valid) {
+          float4* to = pf_part(a.part_o, part, blk, C::BLOCKS, C::HDP, 8 * i, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            to[128 * e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                      __uint_as_float(o[4 * e + 3]));
+        }
+      } else if (row.valid) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           o[e] = tc::pack_bf16x2(__uint_as_float(o[2 * e]) * il, __uint_as_float(o[2 * e + 1]) * il);
-        pf_quad(o);
-        const int col = 32 * i + 8 * (lane & 3);
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.p.a.out) + col;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (q.valid[k] && col < hd)
-            *reinterpret_cast<uint4*>(out + q.at[k]) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        for (int e = 0; e < 2; ++e) pf_store_row(out + 64 * i + 32 * e, o + 8 * e, 2 * hd - 64 * i - 32 * e, a.wide);
       }
+      __syncwarp();
     }
     tc::tc_fence_before();
   }
@@ -757,7 +742,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
       // last is done and read)
       if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar.pv_done[0][(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, lim))) return;
       factor[j & 3][r] = l > 0.f ? 1.f / l : 0.f;
-      if (it.slot >= 0 && row.valid) a.part_ml[((long long)blockIdx.x * 2 + it.slot) * 256 + r] = make_float2(m, l);
+      if (it.slot >= 0 && row.valid) a.part_ml[((long long)blockIdx.x * 2 + it.slot) * 128 + r] = make_float2(m, l);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar.l_full);
     }
@@ -793,16 +778,23 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
       ++nl;
       il = factor[j & 3][r];
     }
-    const long long part = ((long long)blockIdx.x * 2 + it.slot) * 256 + r;
-    const PfQuad q = pf_quad_rows(it.slot >= 0 ? part * C::HDP : row.at, row.valid);
-    if (it.slot < 0) {
+    if (!row.valid) continue;
+    if (it.slot >= 0) {
+      float4* to = pf_part(a.part_o, (long long)blockIdx.x * 2 + it.slot, 0, 1, C::HDP, 0, r);
 #pragma unroll
-      for (int i = 0; i < C::HDP; ++i) acc[i] = __float_as_uint(__uint_as_float(acc[i]) * il);
+      for (int e = 0; e < C::HDP / 4; ++e)
+        to[128 * e] = make_float4(__uint_as_float(acc[4 * e]), __uint_as_float(acc[4 * e + 1]),
+                                  __uint_as_float(acc[4 * e + 2]), __uint_as_float(acc[4 * e + 3]));
+    } else {
+      char* out = reinterpret_cast<char*>(static_cast<float*>(a.p.a.out) + row.at);
+#pragma unroll
+      for (int e = 0; e < C::HDP / 8; ++e) {
+        uint32_t x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(__uint_as_float(acc[8 * e + k]) * il);
+        pf_store_row(out + 32 * e, x, 4 * hd - 32 * e, a.wide);
+      }
     }
-    float* to = it.slot >= 0 ? a.part_o : static_cast<float*>(a.p.a.out);
-    const int cols = it.slot >= 0 ? C::HDP : hd;
-#pragma unroll
-    for (int i = 0; i < C::HDP; i += 16) pf_store16(to, q, acc + i, i, cols);
   }
 }
 
@@ -811,8 +803,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     prefill_tc_kernel(const PfArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t pf_smem_raw[];
-  __shared__ PfCut cuts[2];
-  __shared__ long long sums[C::THREADS / 32];
   __shared__ PfItem items[PF_ITEMS];
   __shared__ uint32_t there[2 * C::KST];
   __shared__ __align__(8) PfBars bar;
@@ -850,12 +840,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   if (warp == PF_SWARP) tc::tmem_alloc(&tmem_slot, 512);
-  tc::grid_dep_launch();
-  tc::grid_dep_wait();
-  pf_share<C::THREADS>(a.p, a.w, cuts, sums);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
   const uint32_t tmem = tmem_slot;
   const int hd = a.p.c.head_dim;
   const uint32_t leader = pf_leader();
@@ -889,7 +878,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (lane < 2) desc[lane] = make_int4(-1, 0, 0, 0);
     __syncwarp();
     PfWalk walk;
-    walk.begin(a.p, cuts);
+    walk.begin(a.p, a.w);
     int k = 0, q_n = 0;
     bool ok = true;
     const bool withhold = a.p.a.fault;
@@ -1108,21 +1097,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 // ---------------------------------------------------------------- parts of tiles
 // A tile that begins in CTA x and goes on: its parts, in order of the CTAs, joined by
-// their maxima. A warp has a row; the lanes take 32 parts' weights at a time.
-constexpr int PJ_THREADS = 256, PJ_SPLIT = 4;
+// their maxima. A CTA has a quarter of the columns, a lane a row. Few parts: a warp takes them all for 32
+// rows, eight warps eight times 32 rows; many (few rows on a long axis): the warps take the parts of
+// 32 rows in turn, and their sums meet in shared memory.
+constexpr int PJ_THREADS = 256, PJ_WARPS = 8, PJ_SPLIT = 4;
 constexpr int PF_MAX_CTAS = 256;  // the workspace does not depend on the device
 
 struct PfJoin {
   PrefillView p;
   PfTiling w;
-  int block_pos, blocks, hdp;  // positions of a block of 128 rows, blocks of a tile
+  int block_pos;  // positions of a block of 128 rows
   const float2* part_ml;
-  const float* part_o;
+  float* part_o;
 };
 
-template <typename T>
+template <typename T, int HDP, int BLOCKS>
 __global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j) {
+  constexpr int C4 = HDP / 4 / PJ_SPLIT;  // float4s of a row in this CTA
   __shared__ int parts[PF_MAX_CTAS], n_parts;
+  __shared__ float4 sum[PJ_WARPS][C4][32];
+  __shared__ float2 ml[PJ_WARPS][32];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int4 d = j.w.desc[2 * blockIdx.x + 1];
@@ -1147,44 +1141,84 @@ __global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j
     if (lane == 0) n_parts = n;
   }
   __syncthreads();
-  const int n = n_parts, rows_of_kv = j.w.head_rows / j.p.c.n_kv, g = d.z / rows_of_kv;
-  const PrefillRows r = prefill_rows(j.p, d.x);
-  for (int row = blockIdx.y * (PJ_THREADS / 32) + warp; row < 128 * j.blocks; row += PJ_SPLIT * (PJ_THREADS / 32)) {
-    const int in = row & 127, place = in / j.w.row_heads;
-    const int pos = d.y * j.w.span + (row >> 7) * j.block_pos + place;
+  const int n = n_parts, rows_of_kv = j.w.head_rows / j.p.c.n_kv, g = d.z / rows_of_kv, c0 = blockIdx.y * C4;
+  const PrefillRows rr = prefill_rows(j.p, d.x);
+  const bool many = n > PJ_WARPS;
+  for (int group = many ? 0 : warp; group < 4 * BLOCKS; group += many ? 1 : PJ_WARPS) {
+    const int in = 32 * (group & 3) + lane, blk = group >> 2, place = in / j.w.row_heads;
+    const int pos = d.y * j.w.span + blk * j.block_pos + place;
     const int h = (d.z - g * rows_of_kv) * j.w.row_heads + in - place * j.w.row_heads;
-    if (place >= j.block_pos || pos >= r.count || h >= j.p.group) continue;
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, j.part_ml[(long long)parts[i] * 256 + row].x);
+    const bool valid = place < j.block_pos && pos < rr.count && h < j.p.group;
+    if (!__any_sync(0xffffffffu, valid)) continue;  // (the same for all warps of a group)
+    float top = -INFINITY, l = 0.f;
+    float4 acc[C4];
 #pragma unroll
-    for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float wgt = 0.f;
-      if (i0 + lane < n) {
-        const float2 ml = j.part_ml[(long long)parts[i0 + lane] * 256 + row];
-        wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-        l += wgt * ml.y;
-      }
-      const int many = min(32, n - i0);
-#pragma unroll 4
-      for (int i = 0; i < many; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, wgt, i);
-        if (wi == 0.f) continue;
-        const float* o = j.part_o + ((long long)parts[i0 + i] * 256 + row) * j.hdp;
+    for (int e = 0; e < C4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (valid) {
+#pragma unroll 2
+      for (int i = many ? warp : 0; i < n; i += many ? PJ_WARPS : 1) {
+        const float2 x = j.part_ml[((long long)parts[i] * BLOCKS + blk) * 128 + in];
+        const float4* o = pf_part(j.part_o, parts[i], blk, BLOCKS, HDP, c0, in);
+        float4 v[C4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (lane + 32 * e < hd) acc[e] = fmaf(wi, o[lane + 32 * e], acc[e]);
+        for (int e = 0; e < C4; ++e) v[e] = o[128 * e];
+        if (x.x == -INFINITY) continue;
+        const float m = fmaxf(top, x.x), old = exp2f(top - m), w = exp2f(x.x - m);
+        top = m;
+        l = l * old + x.y * w;
+#pragma unroll
+        for (int e = 0; e < C4; ++e) {
+          acc[e].x = acc[e].x * old + v[e].x * w;
+          acc[e].y = acc[e].y * old + v[e].y * w;
+          acc[e].z = acc[e].z * old + v[e].z * w;
+          acc[e].w = acc[e].w * old + v[e].w * w;
+        }
       }
     }
+    if (many) {
+      ml[warp][lane] = make_float2(top, l);
 #pragma unroll
-    for (int o = 16; o; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+      for (int e = 0; e < C4; ++e) sum[warp][e][lane] = acc[e];
+      __syncthreads();
+      float m = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < PJ_WARPS; ++x) m = fmaxf(m, ml[x][lane].x);
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < C4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < PJ_WARPS; ++x) {
+        const float2 y = ml[x][lane];
+        const float w = y.x == -INFINITY ? 0.f : exp2f(y.x - m);
+        l += y.y * w;
+#pragma unroll
+        for (int e = 0; e < C4; ++e) {
+          if (e % PJ_WARPS != warp) continue;  // a warp finishes one in eight of the columns
+          const float4 v = sum[x][e][lane];
+          acc[e].x += v.x * w;
+          acc[e].y += v.y * w;
+          acc[e].z += v.z * w;
+          acc[e].w += v.w * w;
+        }
+      }
+      __syncthreads();
+    }
     const float il = l > 0.f ? 1.f / l : 0.f;
-    T* out = static_cast<T*>(j.p.a.out) + ((long long)(r.first + pos) * j.p.a.n_heads + g * j.p.group + h) * hd;
+    T* out = static_cast<T*>(j.p.a.out) + ((long long)(rr.first + pos) * j.p.a.n_heads + g * j.p.group + h) * hd + 4 * c0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (lane + 32 * e < hd) out[lane + 32 * e] = (T)(acc[e] * il);
+    for (int e = 0; e < C4; ++e) {
+      if (!valid || 4 * (c0 + e) >= hd || (many && e % PJ_WARPS != warp)) continue;
+      *reinterpret_cast<typename Four<T>::raw*>(out + 4 * e) =
+          Four<T>::narrow(make_float4(acc[e].x * il, acc[e].y * il, acc[e].z * il, acc[e].w * il));
+    }
   }
+}
+
+template <typename T, int BLOCKS>
+cudaError_t launch_join(const PfJoin& j, int hdp, cudaStream_t st) {
+  const dim3 grid(j.w.ctas, PJ_SPLIT);
+  return hdp == 64 ? launch_overlapped(prefill_join_kernel<T, 64, BLOCKS>, grid, PJ_THREADS, 0, 0, st, j)
+                   : launch_overlapped(prefill_join_kernel<T, 128, BLOCKS>, grid, PJ_THREADS, 0, 0, st, j);
 }
 
 // ---------------------------------------------------------------- any head size
@@ -1370,15 +1404,14 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
   x.part_o = reinterpret_cast<float*>(ws + pl.o);
   x.block_pos = pl.block_pos;
+  x.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && c.head_dim * (a.f32 ? 4 : 2) % 32 == 0;
   x.scale = fminf(fmaxf(fabsf(p.scale_log2), FLT_MIN), FLT_MAX);
   x.flip = a.scale < 0.f ? 0x80000000u : 0u;
   cudaError_t e = a.f32 ? (pl.hdp == 64 ? launch_tc<PfCfg<64, true>>(x, st) : launch_tc<PfCfg<128, true>>(x, st))
                         : (pl.hdp == 64 ? launch_tc<PfCfg<64, false>>(x, st) : launch_tc<PfCfg<128, false>>(x, st));
   if (e != cudaSuccess || !pl.cuts) return e;
-  PfJoin j{p, x.w, pl.block_pos, pl.blocks, pl.hdp, x.part_ml, x.part_o};
-  const dim3 grid(x.w.ctas, PJ_SPLIT);
-  return a.f32 ? launch_overlapped(prefill_join_kernel<float>, grid, PJ_THREADS, 0, 0, st, j)
-               : launch_overlapped(prefill_join_kernel<__nv_bfloat16>, grid, PJ_THREADS, 0, 0, st, j);
+  const PfJoin j{p, x.w, pl.block_pos, x.part_ml, x.part_o};
+  return a.f32 ? launch_join<float, 1>(j, pl.hdp, st) : launch_join<__nv_bfloat16, 2>(j, pl.hdp, st);
 }
 
 }  // namespace qmoe
