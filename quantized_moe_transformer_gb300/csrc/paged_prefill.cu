@@ -45,15 +45,15 @@ __device__ __forceinline__ PrefillRows prefill_rows(const PrefillView& p, int b)
 // A tile is ``span`` positions of a sequence for the query heads of one "head
 // row" (a KV head's heads, or 128 of them at most). All tiles in order, head row by
 // head row, sequence by sequence, are dealt out evenly over the CTAs by their cost,
-// the entries that they see and PF_TILE_COST more; a cut inside a tile falls between
+// the entries that they see and ``tile_cost`` more; a cut inside a tile falls between
 // key blocks, at least PF_MIN_BLOCKS from its ends. So a CTA has whole tiles, and at
 // most one part of a tile that began in an earlier CTA (slot 0) and one of a tile that
 // goes on in a later one (slot 1); the join kernel puts those together.
-constexpr int PF_KEYS = 64, PF_MIN_BLOCKS = 4, PF_TILE_COST = 256, PF_ITEMS = 4;
+constexpr int PF_KEYS = 64, PF_MIN_BLOCKS = 4, PF_ITEMS = 4;
 
 struct PfTiling {
   int span, head_rows, row_heads;  // positions of a tile; head rows in all, of a KV head's heads row_heads each
-  int ctas;
+  int ctas, tile_cost;
   int4* desc;  // [CTAs][2] a part of a tile: (sequence or -1, tile, head row, 1 if it is the tile's last)
 };
 
@@ -61,8 +61,8 @@ struct PfItem {
   int b, t, row, kb0, kb1, first, count, len, before, slot;  // b -1: no more; slot -1: a whole tile
 };
 
-__device__ __forceinline__ long long pf_cost(long long tiles, long long before, int span) {
-  return tiles * (PF_TILE_COST + before) + span * (tiles * (tiles + 1) / 2);
+__device__ __forceinline__ long long pf_cost(long long tiles, long long each, int span) {
+  return tiles * each + span * (tiles * (tiles + 1) / 2);
 }
 __device__ __forceinline__ int pf_blocks(const PrefillRows& r, int t, int span) {
   const int end = r.before + min((t + 1) * span, r.count);
@@ -74,17 +74,17 @@ struct PfCut {
 };
 
 // The place ``x`` (in units of cost, inside sequence b) cuts the sequence's tiles at.
-__device__ __forceinline__ PfCut pf_cut(const PrefillRows& r, int row, int b, long long x, int span) {
-  const long long before = max(r.before, 0);
+__device__ __forceinline__ PfCut pf_cut(const PrefillRows& r, int row, int b, long long x, int span, int tile_cost) {
+  const long long before = (long long)max(r.before, 0) + tile_cost;
   // the tile whose sum of costs reaches x: near the root of the quadratic, then exactly
-  const float half = (float)PF_TILE_COST + (float)before + 0.5f * span, xf = (float)x;
+  const float half = (float)before + 0.5f * span, xf = (float)x;
   long long t = (long long)(2.f * xf / (half + sqrtf(half * half + 2.f * span * xf)));
   const int tiles = (r.count + span - 1) / span;
   t = max(0ll, min(t, (long long)tiles - 1));
   while (t > 0 && pf_cost(t, before, span) > x) --t;
   while (t + 1 < tiles && pf_cost(t + 1, before, span) <= x) ++t;
   const int blocks = pf_blocks(r, (int)t, span);
-  const long long off = x - pf_cost(t, before, span) - PF_TILE_COST + PF_KEYS / 2;
+  const long long off = x - pf_cost(t, before, span) - tile_cost + PF_KEYS / 2;
   int kb = off > 0 ? (int)(off / PF_KEYS) : 0;
   if (kb < PF_MIN_BLOCKS) kb = 0;
   if (blocks - kb < PF_MIN_BLOCKS && kb > 0) return PfCut{row, b, (int)t + 1, 0};
@@ -92,15 +92,15 @@ __device__ __forceinline__ PfCut pf_cut(const PrefillRows& r, int row, int b, lo
 }
 
 // Where this CTA's work begins and ends, by one warp: a lane has a sequence of 32.
-__device__ __forceinline__ long long pf_sequence_cost(const PrefillRows& r, int span) {
-  return r.count > 0 ? pf_cost((r.count + span - 1) / span, max(r.before, 0), span) : 0;
+__device__ __forceinline__ long long pf_sequence_cost(const PrefillRows& r, int span, int tile_cost) {
+  return r.count > 0 ? pf_cost((r.count + span - 1) / span, (long long)max(r.before, 0) + tile_cost, span) : 0;
 }
 
 __device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w, PfCut (&cuts)[2]) {
   const int lane = threadIdx.x & 31;
   long long total = 0;
 #pragma unroll 4
-  for (int b = lane; b < p.c.n_seqs; b += 32) total += pf_sequence_cost(prefill_rows(p, b), w.span);
+  for (int b = lane; b < p.c.n_seqs; b += 32) total += pf_sequence_cost(prefill_rows(p, b), w.span, w.tile_cost);
 #pragma unroll
   for (int d = 16; d; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
   cuts[0] = cuts[1] = PfCut{w.head_rows, 0, 0, 0};
@@ -122,7 +122,7 @@ __device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w
   bool open[2] = {row[0] < w.head_rows, row[1] < w.head_rows};
   for (int b0 = 0; b0 < p.c.n_seqs && (open[0] || open[1]); b0 += 32) {
     const PrefillRows mine = b0 + lane < p.c.n_seqs ? prefill_rows(p, b0 + lane) : PrefillRows{0, 0, 0, 0};
-    const long long cost = pf_sequence_cost(mine, w.span);
+    const long long cost = pf_sequence_cost(mine, w.span, w.tile_cost);
     long long end = cost;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -130,7 +130,7 @@ __device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w
       if (lane >= d) end += o;
     }
     end += before;
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!open[k]) continue;
       const unsigned behind = __ballot_sync(0xffffffffu, end > at[k]);
@@ -141,7 +141,8 @@ __device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w
       r.count = __shfl_sync(0xffffffffu, mine.count, src);
       r.len = __shfl_sync(0xffffffffu, mine.len, src);
       r.before = r.len - r.count;
-      cuts[k] = pf_cut(r, row[k], b0 + src, at[k] - __shfl_sync(0xffffffffu, end - cost, src), w.span);
+      cuts[k] = pf_cut(r, row[k], b0 + src, at[k] - __shfl_sync(0xffffffffu, end - cost, src), w.span,
+                       w.tile_cost);
       open[k] = false;
     }
     before = __shfl_sync(0xffffffffu, end, 31);
@@ -361,6 +362,26 @@ __device__ __forceinline__ void pf_tma_q(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Waits for an mbarrier's phase; false: given up, after ``limit_ns`` or because another
+// warp has (tc::mbar_wait in fewer instructions: the kernel's loops take turns in the instruction
+// cache, and with it the same loops ran 1 x 16384 in 710 to 910 us, by where the compiler put them).
+__device__ __forceinline__ uint32_t pf_now() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit_ns) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = pf_now();
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if (*abort || pf_now() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // MMAs and their commits by one lane of a whole warp: predicated instead of branched
 // around, so that descriptors stay in uniform registers (in a branch of one lane every operand is moved there
 // first, about 70 cycles an MMA).
@@ -521,7 +542,7 @@ template <class C, class Take>
 __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, const PfItem& it, uint32_t tmem,
                                                   const uint32_t* there, PfBars& bar, volatile int* abort_flag) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hd = a.p.c.head_dim;
-  const uint64_t lim = a.p.a.wait_ns;
+  const uint32_t lim = (uint32_t)min(a.p.a.wait_ns, 4000000000ull);
   const int blk = warp >> 2, r = threadIdx.x & 127;
   const int place = r / a.w.row_heads, head = r - place * a.w.row_heads;
   const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::o_col(blk);
@@ -541,14 +562,14 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
 #pragma unroll 1
     for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
       const int buf = j & 1;
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar.s_full[blk][buf], (j >> 1) & 1, abort_flag, lim))) return;
+      if (!__all_sync(0xffffffffu, pf_wait(&bar.s_full[blk][buf], (j >> 1) & 1, abort_flag, lim))) return;
       tc::tc_fence_after();
       const uint32_t tS = tq + C::s_col(blk, buf);
       uint32_t v[PF_KEYS], w[PF_KEYS / 2];
       const uint32_t exist = there[ring];
       ring = ring + 1 == 2 * C::KST ? 0 : ring + 1;
       pf_ld64(tS, v);
-      if (kb >= whole || exist != 0xFFu) {
+      if (__builtin_expect(kb >= whole || exist != 0xFFu, 0)) {
         if (a.flip) {
 #pragma unroll
           for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
@@ -573,13 +594,13 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
         const float2 la = unpack2(l2[0]), lc = unpack2(l2[1]);
         lb = (la.x + la.y) + (lc.x + lc.y);
         const bool need = mx > m + PF_RESCALE_LOG2;
-        if (!__any_sync(0xffffffffu, need)) break;
+        if (__builtin_expect(!__any_sync(0xffffffffu, need), 1)) break;
         const float alpha = need ? exp2f(m - mx) : 1.f;
         if (need) m = mx;
         l *= alpha;
         if (kb > it.kb0) {
           // O holds P V of the block before once that is done
-          if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][buf ^ 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
+          if (!__all_sync(0xffffffffu, pf_wait(&bar.pv_done[blk][buf ^ 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
             return;
           tc::tc_fence_after();
 #pragma unroll 1
@@ -603,7 +624,7 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
     // out = O / l, or the part's O, m and l
     const bool some = it.kb1 > it.kb0;
     if (some) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[blk][(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
+      if (!__all_sync(0xffffffffu, pf_wait(&bar.pv_done[blk][(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, lim)))
         return;
       tc::tc_fence_after();
     }
@@ -648,7 +669,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
                                                  const uint32_t* there, PfBars& bar, float (*factor)[128],
                                                  volatile int* abort_flag) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127, hd = a.p.c.head_dim;
-  const uint64_t lim = a.p.a.wait_ns;
+  const uint32_t lim = (uint32_t)min(a.p.a.wait_ns, 4000000000ull);
   const int place = r / a.w.row_heads, head = r - place * a.w.row_heads;
   const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::o_col(0);
   const float c = a.scale;
@@ -661,22 +682,30 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
       constexpr int LANES = C::HDP / 4, ROWS = 32 / LANES;
       const int sub = lane / LANES, d = 4 * (lane - sub * LANES);
       // (the S products of the item before are done: this warp has taken their results)
-#pragma unroll 4
-      for (int i = 0; i < 32; i += ROWS) {
-        const long long at = __shfl_sync(0xffffffffu, row.at, i + sub);
-        const bool there_ = __shfl_sync(0xffffffffu, (int)row.valid, i + sub);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (there_ && d < hd) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.p.a.q) + at + d);
-        const int rr = 32 * warp + i + sub, ch = d >> 3;
-        const uint32_t to = (ch >> 3) * C::QHALF + tc::sw128_offset(rr, ch & 7) + 2 * (d & 4);
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32; i0 += 16 * ROWS) {
+        float4 x[16];
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          const uint32_t w0 = tc::pack_bf16x2(x.x, x.y), w1 = tc::pack_bf16x2(x.z, x.w);
-          x.x -= __uint_as_float(w0 << 16);
-          x.y -= __uint_as_float(w0 & 0xFFFF0000u);
-          x.z -= __uint_as_float(w1 << 16);
-          x.w -= __uint_as_float(w1 & 0xFFFF0000u);
-          *reinterpret_cast<uint2*>(sQ + part * C::QTILE + to) = make_uint2(w0, w1);
+        for (int i = 0; i < 16; ++i) {
+          const int src = i0 + i * ROWS + sub;
+          const long long at = __shfl_sync(0xffffffffu, row.at, src);
+          const bool real = __shfl_sync(0xffffffffu, (int)row.valid, src);
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (real && d < hd) x[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.p.a.q) + at + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int rr = 32 * warp + i0 + i * ROWS + sub, ch = d >> 3;
+          const uint32_t to = (ch >> 3) * C::QHALF + tc::sw128_offset(rr, ch & 7) + 2 * (d & 4);
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const uint32_t w0 = tc::pack_bf16x2(x[i].x, x[i].y), w1 = tc::pack_bf16x2(x[i].z, x[i].w);
+            x[i].x -= __uint_as_float(w0 << 16);
+            x[i].y -= __uint_as_float(w0 & 0xFFFF0000u);
+            x[i].z -= __uint_as_float(w1 << 16);
+            x[i].w -= __uint_as_float(w1 & 0xFFFF0000u);
+            *reinterpret_cast<uint2*>(sQ + part * C::QTILE + to) = make_uint2(w0, w1);
+          }
         }
       }
       tc::fence_proxy_async_smem();
@@ -686,7 +715,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
         const int buf = j & 1;
-        if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.s_full[0][buf], (j >> 1) & 1, abort_flag, lim))) return;
+        if (!__all_sync(0xffffffffu, pf_wait(&bar.s_full[0][buf], (j >> 1) & 1, abort_flag, lim))) return;
         tc::tc_fence_after();
         uint32_t v[PF_KEYS];
         pf_ld64(tq + C::s_col(0, buf), v);
@@ -712,7 +741,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         // P's buffer, and the slot of the factor, are free once P V of two blocks before is done
-        if (j > 1 && !__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[0][buf], ((j >> 1) - 1) & 1, abort_flag, lim)))
+        if (j > 1 && !__all_sync(0xffffffffu, pf_wait(&bar.pv_done[0][buf], ((j >> 1) - 1) & 1, abort_flag, lim)))
           return;
         tc::tc_fence_after();
         if (kb > it.kb0) factor[j & 3][r] = alpha;
@@ -738,9 +767,8 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bar.p_full[0][buf]);
       }
-      // 1 / l goes by the slot behind the last block's (the sums have read it when P V of the block before the
-      // last is done and read)
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar.pv_done[0][(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, lim))) return;
+      // 1 / l goes by the slot behind the last block's: the sums have read what lay there when P V of the last but two is
+      // done, which this warp waited for ahead of its last weights
       factor[j & 3][r] = l > 0.f ? 1.f / l : 0.f;
       if (it.slot >= 0 && row.valid) a.part_ml[((long long)blockIdx.x * 2 + it.slot) * 128 + r] = make_float2(m, l);
       __syncwarp();
@@ -756,7 +784,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
     for (int i = 0; i < C::HDP; ++i) acc[i] = 0u;
 #pragma unroll 1
     for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.pv_done[0][j & 1], (j >> 1) & 1, abort_flag, lim))) return;
+      if (!__all_sync(0xffffffffu, pf_wait(&bar.pv_done[0][j & 1], (j >> 1) & 1, abort_flag, lim))) return;
       tc::tc_fence_after();
       const float alpha = kb > it.kb0 ? factor[j & 3][r] : 0.f;
 #pragma unroll
@@ -774,7 +802,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
     }
     float il = 0.f;
     if (it.kb1 > it.kb0) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_poll(&bar.l_full, nl & 1, abort_flag, lim))) return;
+      if (!__all_sync(0xffffffffu, pf_wait(&bar.l_full, nl & 1, abort_flag, lim))) return;
       ++nl;
       il = factor[j & 3][r];
     }
@@ -816,7 +844,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint8_t* sV = sK + C::KST * C::TILE;      // [VST]
   volatile int* abort_flag = &abort_word;
   const int warp = pf_same(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const uint64_t lim = a.p.a.wait_ns;
+  const uint32_t lim = (uint32_t)min(a.p.a.wait_ns, 4000000000ull);
 
   if (threadIdx.x == 0) {
     const auto init = [](uint64_t* b, int n, uint32_t count) {
@@ -852,7 +880,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   // The next item for a consumer warp (n: items taken so far); false: none, or given up.
   PfItem it;
   auto take = [&](int n) -> bool {
-    if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar.it_full[n % PF_ITEMS], (n / PF_ITEMS) & 1, abort_flag, lim))) return false;
+    if (!__all_sync(0xffffffffu, pf_wait(&bar.it_full[n % PF_ITEMS], (n / PF_ITEMS) & 1, abort_flag, lim))) return false;
     it = items[n % PF_ITEMS];
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&bar.it_empty[n % PF_ITEMS]);
@@ -886,7 +914,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const bool more = walk.next(a.p, a.w, &it);
       if (!more) it.b = -1;
       if (n >= PF_ITEMS &&
-          !__all_sync(0xffffffffu, tc::mbar_wait(&bar.it_empty[n % PF_ITEMS], (n / PF_ITEMS - 1) & 1, abort_flag, lim)))
+          !__all_sync(0xffffffffu, pf_wait(&bar.it_empty[n % PF_ITEMS], (n / PF_ITEMS - 1) & 1, abort_flag, lim)))
         break;
       if (lane == 0) {
         items[n % PF_ITEMS] = it;
@@ -907,7 +935,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const auto queries = [&](int blk) -> bool {
         const int qs = q_n % 3;
         if (q_n >= 3 &&
-            !__all_sync(0xffffffffu, tc::mbar_wait(&bar.q_empty[qs], (q_n / 3 - 1) & 1, abort_flag, lim)))
+            !__all_sync(0xffffffffu, pf_wait(&bar.q_empty[qs], (q_n / 3 - 1) & 1, abort_flag, lim)))
           return false;
         ++q_n;
         if (lane == 0) {
@@ -927,14 +955,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const PfPages pg = pf_pages(a, it, kb);
         const int st = k % C::KST;
         if (k >= C::KST &&
-            !__all_sync(0xffffffffu, tc::mbar_wait(&bar.k_empty[st], (k / C::KST - 1) & 1, abort_flag, lim))) {
+            !__all_sync(0xffffffffu, pf_wait(&bar.k_empty[st], (k / C::KST - 1) & 1, abort_flag, lim))) {
           ok = false;
           break;
         }
         if (withhold && k == 0) {
           // test-only: never copied
           volatile int late = 0;
-          tc::mbar_wait(&bar.k_full[0], 0, &late, lim);
+          pf_wait(&bar.k_full[0], 0, &late, lim);
           *abort_flag = 1;
           ok = false;
           break;
@@ -951,10 +979,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // copies in flight land before the CTA leaves
     volatile int never = 0;
 #pragma unroll 1
-    for (int i = max(0, k - C::KST); i < k; ++i) tc::mbar_wait(&bar.k_full[i % C::KST], (i / C::KST) & 1, &never, lim);
+    for (int i = max(0, k - C::KST); i < k; ++i) pf_wait(&bar.k_full[i % C::KST], (i / C::KST) & 1, &never, lim);
     if (!C::F32) {
 #pragma unroll 1
-      for (int i = max(0, q_n - 3); i < q_n; ++i) tc::mbar_wait(&bar.q_full[i % 3], (i / 3) & 1, &never, lim);
+      for (int i = max(0, q_n - 3); i < q_n; ++i) pf_wait(&bar.q_full[i % 3], (i / 3) & 1, &never, lim);
     }
     __syncwarp();
   } else if (warp == PF_VWARP) {
@@ -968,7 +996,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const PfPages pg = pf_pages(a, it, kb);
         const int st = k % C::VST;
         if (k >= C::VST &&
-            !__all_sync(0xffffffffu, tc::mbar_wait(&bar.v_empty[st], (k / C::VST - 1) & 1, abort_flag, lim))) {
+            !__all_sync(0xffffffffu, pf_wait(&bar.v_empty[st], (k / C::VST - 1) & 1, abort_flag, lim))) {
           ok = false;
           break;
         }
@@ -977,7 +1005,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     volatile int never = 0;
 #pragma unroll 1
-    for (int i = max(0, k - C::VST); i < k; ++i) tc::mbar_wait(&bar.v_full[i % C::VST], (i / C::VST) & 1, &never, lim);
+    for (int i = max(0, k - C::VST); i < k; ++i) pf_wait(&bar.v_full[i % C::VST], (i / C::VST) & 1, &never, lim);
     __syncwarp();
   } else if (warp == PF_SWARP || warp == 12) {
     // ------------------------------------------------------------ S = Q K^T
@@ -991,18 +1019,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const int st = k % C::KST, buf = j & 1;
-        ok = tc::mbar_wait(&bar.k_full[st], (k / C::KST) & 1, abort_flag, lim);
+        ok = pf_wait(&bar.k_full[st], (k / C::KST) & 1, abort_flag, lim);
         if (blk >= blocks) {  // no rows in this block: the stage is free as far as this warp goes
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) tc::mbar_arrive(&bar.k_empty[st]);
           continue;
         }
-        if (kb == it.kb0) ok = ok && tc::mbar_wait_poll(&bar.q_full[qs], (C::F32 ? q : q / 3) & 1, abort_flag, lim);
+        if (kb == it.kb0) ok = ok && pf_wait(&bar.q_full[qs], (C::F32 ? q : q / 3) & 1, abort_flag, lim);
         // the buffer is free again: bf16 once P V of two blocks before, which reads P there, is done; fp32 once
         // the softmax has taken S of two blocks before
         uint64_t* free_bar = C::F32 ? &bar.p_full[0][buf] : &bar.pv_done[blk][buf];
-        ok = ok && (j < 2 || tc::mbar_wait(free_bar, ((j >> 1) - 1) & 1, abort_flag, lim));
+        ok = ok && (j < 2 || pf_wait(free_bar, ((j >> 1) - 1) & 1, abort_flag, lim));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++j;
@@ -1027,7 +1055,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     pf_commit(leader, &bar.drain[blk]);
     volatile int never = 0;
-    tc::mbar_wait(&bar.drain[blk], 0, &never, lim);
+    pf_wait(&bar.drain[blk], 0, &never, lim);
     __syncwarp();
   } else if (warp == 11 || warp == 13) {
     // ------------------------------------------------------------ O += P V
@@ -1040,7 +1068,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const int st = k % C::VST, buf = j & 1;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bar.v_full[st], (k / C::VST) & 1, abort_flag, lim));
+        ok = __all_sync(0xffffffffu, pf_wait(&bar.v_full[st], (k / C::VST) & 1, abort_flag, lim));
         if (!ok) break;
         if (blk >= blocks) {
           if (lane == 0) tc::mbar_arrive(&bar.v_empty[st]);
@@ -1060,8 +1088,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
-        ok = tc::mbar_wait(&bar.p_full[blk][buf], (j >> 1) & 1, abort_flag, lim);
-        if (C::F32) ok = ok && (j == 0 || tc::mbar_wait_poll(&bar.o_read, (j - 1) & 1, abort_flag, lim));
+        ok = pf_wait(&bar.p_full[blk][buf], (j >> 1) & 1, abort_flag, lim);
+        if (C::F32) ok = ok && (j == 0 || pf_wait(&bar.o_read, (j - 1) & 1, abort_flag, lim));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++j;
@@ -1083,7 +1111,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     pf_commit(leader, &bar.drain[2 + blk]);
     volatile int never = 0;
-    tc::mbar_wait(&bar.drain[2 + blk], 0, &never, lim);
+    pf_wait(&bar.drain[2 + blk], 0, &never, lim);
     __syncwarp();
   }
 
@@ -1399,6 +1427,9 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.w.span = pl.span;
   x.w.head_rows = c.n_kv * pl.row_tiles;
   x.w.row_heads = pl.row_heads;
+  // in keys' worth of time: the change of tiles (1 x 16384 bf16 with 64 907 us, 256 796, 1152 809; fp32 1 x 4096 with 256
+  // 279 us, 640 223, 1152 227)
+  x.w.tile_cost = a.f32 ? 640 : 256;
   x.w.ctas = device_sm_count() < pl.ctas ? device_sm_count() : pl.ctas;
   x.w.desc = reinterpret_cast<int4*>(ws + pl.desc);
   x.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
