@@ -237,10 +237,10 @@ struct PfWalk {
 // S_j's own columns; S_{j+2} takes them again when P_j V_j is done. While one block's softmax runs, the
 // tensor core has the other's products and the same block's next S.
 // fp32 rows: a tile is one block; q and each probability are three bf16 parts (24 bits), so S and P V
-// take three products each, small parts first. P V of a key block goes into a fresh accumulator; warps 4-7 add
-// it, rounded, to the output in their registers (a thread a row), so nothing is cut off over a long axis.
-// Warps: bf16 0-3 and 4-7 softmax of block 0 and 1, fp32 0-3 softmax, 4-7 sums; 8 walks the CTA's work and
-// copies K (and bf16 Q), 10 copies V; 9 and 11 issue block 0's S and P V, 12 and 13 block 1's. Every wait is bounded.
+// take three products each, small parts first. P V of a key block goes into a fresh accumulator and is added, rounded, to
+// the output in registers, so nothing is cut off over a long axis.
+// Warps: 0-7 the softmax; then one that walks the CTA's work and copies K (and bf16 Q), one that issues S, one that copies V,
+// one that issues P V, and for bf16's second block of rows one more of each of the issuers. Every wait is bounded.
 template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;
@@ -282,7 +282,7 @@ struct PfBars {
   uint64_t it_full[PF_ITEMS], it_empty[PF_ITEMS];
   uint64_t q_full[3], q_empty[3];                      // bf16: of the ring; fp32: q_full[0]
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [block][buffer]
-  uint64_t o_read, l_full, drain[4];
+  uint64_t o_read, drain[4];
 };
 
 __device__ __forceinline__ void pf_tma(uint32_t dst, const CUtensorMap* map, int dim, int row, int head, int page,
@@ -663,39 +663,98 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
   }
 }
 
-// Warps 0-7 of tiles of fp32 rows.
+// What the two warps of 32 fp32 rows (a half of the columns each) tell one another.
+struct PfHalves {
+  uint64_t max_there[4][2], l_there[4];  // [quarter][key block parity]
+  float max[2][2][128], l[2][128];       // [parity][half][row]
+};
+
+// Tiles of fp32 rows: warps w and w + 4 have the same 32 rows, each half of a key block's scores and half
+// of the head dims of their output, which is in registers. The weights are formed by the reference as it is
+// while the partner's maximum is on its way, and again where it moves. P V of a key block is added once the
+// next one's weights are out; a tile's last one, after the next tile's queries.
 template <class C, class Take>
 __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, const PfItem& it, uint32_t tmem, uint8_t* sQ,
-                                                 const uint32_t* there, PfBars& bar, float (*factor)[128],
+                                                 const uint32_t* there, PfBars& bar, PfHalves& halves,
                                                  volatile int* abort_flag) {
+  constexpr int KH = PF_KEYS / 2, DH = C::HDP / 2;  // scores and head dims of a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127, hd = a.p.c.head_dim;
+  const int half = warp >> 2, quarter = warp & 3;
   const uint32_t lim = (uint32_t)min(a.p.a.wait_ns, 4000000000ull);
   const int place = r / a.w.row_heads, head = r - place * a.w.row_heads;
-  const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::o_col(0);
+  const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16), tO = tq + C::o_col(0) + DH * half;
   const float c = a.scale;
-  int j = 0;   // key blocks so far
-  if (warp < 4) {
-    for (int n = 0; take(n); ++n) {
-      if (it.kb1 <= it.kb0) continue;
-      const PfRow row = pf_row(a, it, pf_heads(a, it.row), 0, place, head);
-      // q as three bf16 parts, which hold all its bits: a row's head dims over HDP / 4 lanes
-      constexpr int LANES = C::HDP / 4, ROWS = 32 / LANES;
-      const int sub = lane / LANES, d = 4 * (lane - sub * LANES);
-      // (the S products of the item before are done: this warp has taken their results)
+  const auto wait = [&](uint64_t* b, int phase) -> bool {
+    return __all_sync(0xffffffffu, pf_wait(b, (uint32_t)phase & 1u, abort_flag, lim));
+  };
+  int j = 0, tiles = 0;      // key blocks, and tiles with key blocks, so far
+  float m = -INFINITY, l = 0.f, alpha = 0.f;
+  float acc[DH];
+  PfRow row{}, old{};
+  int slot = -1;
+  bool open = false;         // the tile before waits for its last P V
+  // acc = acc alpha + P V of key block k
+  const auto add = [&](int k) -> bool {
+    if (!wait(&bar.pv_done[0][k & 1], k >> 1)) return false;
+    tc::tc_fence_after();
+#pragma unroll
+    for (int i = 0; i < DH / 32; ++i) {
+      uint32_t o[32];
+      pf_ld32(tO + 32 * i, o);
+      pf_wait_ld(o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[32 * i + e] = fmaf(acc[32 * i + e], alpha, __uint_as_float(o[e]));
+    }
+    tc::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bar.o_read);
+    return true;
+  };
+  const auto store = [&](const PfRow& to, float il) {
+    if (!to.valid) return;
+    if (slot >= 0) {
+      float4* p = pf_part(a.part_o, (long long)blockIdx.x * 2 + slot, 0, 1, C::HDP, DH / 4 * half, r);
+#pragma unroll
+      for (int e = 0; e < DH / 4; ++e)
+        p[128 * e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+    } else {
+      char* p = reinterpret_cast<char*>(static_cast<float*>(a.p.a.out) + to.at + DH * half);
+#pragma unroll
+      for (int e = 0; e < DH / 8; ++e) {
+        uint32_t x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(acc[8 * e + k] * il);
+        pf_store_row(p + 32 * e, x, 4 * (hd - DH * half) - 32 * e, a.wide);
+      }
+    }
+  };
+  for (int n = 0;; ++n) {
+    const bool more = take(n);
+    if (more) row = pf_row(a, it, pf_heads(a, it.row), 0, place, head);
+    if (more && it.kb1 > it.kb0) {
+      // q as three bf16 parts, which hold all its bits, where the S products of the tile before no longer read (this
+      // warp has taken their results): 16 rows of the quarter, a row's head dims over HDP / 4 lanes, the next
+      // rows' loads ahead
+      constexpr int LANES = C::HDP / 4, ROWS = 32 / LANES, STEP = 4;
+      const int sub = lane / LANES, d = 4 * (lane - sub * LANES), r0 = 16 * half;
+      const auto load = [&](int i) {
+        const long long at = __shfl_sync(0xffffffffu, row.at, r0 + (i * ROWS + sub) % 16);
+        const bool real = __shfl_sync(0xffffffffu, (int)row.valid, r0 + (i * ROWS + sub) % 16);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (real && d < hd) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.p.a.q) + at + d);
+        return x;
+      };
+      float4 x[STEP];
+#pragma unroll
+      for (int i = 0; i < STEP; ++i) x[i] = load(i);
 #pragma unroll 1
-      for (int i0 = 0; i0 < 32; i0 += 16 * ROWS) {
-        float4 x[16];
+      for (int i0 = 0; i0 < 16 / ROWS; i0 += STEP) {
+        float4 y[STEP];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int src = i0 + i * ROWS + sub;
-          const long long at = __shfl_sync(0xffffffffu, row.at, src);
-          const bool real = __shfl_sync(0xffffffffu, (int)row.valid, src);
-          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (real && d < hd) x[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.p.a.q) + at + d);
-        }
+        for (int i = 0; i < STEP; ++i) y[i] = load(i0 + STEP + i);  // (behind the last: the first again)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int rr = 32 * warp + i0 + i * ROWS + sub, ch = d >> 3;
+        for (int i = 0; i < STEP; ++i) {
+          const int rr = 32 * quarter + r0 + (i0 + i) * ROWS + sub, ch = d >> 3;
           const uint32_t to = (ch >> 3) * C::QHALF + tc::sw128_offset(rr, ch & 7) + 2 * (d & 4);
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
@@ -706,121 +765,103 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
             x[i].w -= __uint_as_float(w1 & 0xFFFF0000u);
             *reinterpret_cast<uint2*>(sQ + part * C::QTILE + to) = make_uint2(w0, w1);
           }
+          x[i] = y[i];
         }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar.q_full[0]);
-      float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-      for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
-        const int buf = j & 1;
-        if (!__all_sync(0xffffffffu, pf_wait(&bar.s_full[0][buf], (j >> 1) & 1, abort_flag, lim))) return;
-        tc::tc_fence_after();
-        uint32_t v[PF_KEYS];
-        pf_ld64(tq + C::s_col(0, buf), v);
-        if (a.flip) {
+    }
+    if (open) {
+      // the tile before: its last P V, then out = O / l, or the part's O, m and l
+      if (!add(j - 1)) return;
+      halves.l[half][r] = l;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&halves.l_there[quarter]);
+      if (!wait(&halves.l_there[quarter], tiles)) return;
+      ++tiles;
+      l = halves.l[0][r] + halves.l[1][r];
+      if (slot >= 0 && old.valid && half == 0) a.part_ml[((long long)blockIdx.x * 2 + slot) * 128 + r] = make_float2(m, l);
+      store(old, l > 0.f ? 1.f / l : 0.f);
+    }
+    if (!more) return;
 #pragma unroll
-          for (int i = 0; i < PF_KEYS; ++i) v[i] ^= a.flip;
+    for (int i = 0; i < DH; ++i) acc[i] = 0.f;
+    m = -INFINITY;
+    l = alpha = 0.f;
+    slot = it.slot;
+    old = row;
+    open = it.kb1 > it.kb0;
+    if (!open) store(row, 0.f);
+#pragma unroll 1
+    for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
+      const int buf = j & 1;
+      if (!wait(&bar.s_full[0][buf], j >> 1)) return;
+      tc::tc_fence_after();
+      const uint32_t exist = there[j & (2 * C::KST - 1)];
+      uint32_t v[KH];
+      pf_ld32(tq + C::s_col(0, buf) + KH * half, v);
+      pf_wait_ld(v);
+      const int seen = row.vis - kb * PF_KEYS - KH * half;
+      if (__builtin_expect(a.flip || exist != 0xFFu || __any_sync(0xffffffffu, seen < KH), 0)) {
+#pragma unroll
+        for (int i = 0; i < KH; ++i) v[i] = i >= seen || !((exist >> (4 * half + i / 8)) & 1u) ? 0xFF800000u : v[i] ^ a.flip;
+      }
+      float mx = __uint_as_float(v[0]);
+#pragma unroll
+      for (int i = 1; i + 1 < KH; i += 2) mx = pf_max3(mx, v[i], v[i + 1]);
+      mx = fmaxf(mx, __uint_as_float(v[KH - 1])) * c;
+      halves.max[buf][half][r] = mx;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&halves.max_there[quarter][buf]);
+      float p[KH], lb;
+      const float before = alpha;  // the factor that goes with P V of the block before
+      alpha = 1.f;
+      for (bool met = false;;) {
+        const float mref = m == -INFINITY ? 0.f : m;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < KH; ++i) {
+          p[i] = exp2f(fmaf(__uint_as_float(v[i]), c, -mref));
+          l4[i & 3] += p[i];
         }
-        pf_mask(v, row.vis - kb * PF_KEYS, there[j % (2 * C::KST)]);
-        const float mx = pf_max(v) * c;
-        float alpha = 1.f;
-        if (mx > m + PF_RESCALE_LOG2) {
+        lb = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if (met) break;
+        met = true;
+        if (!wait(&halves.max_there[quarter][buf], j >> 1)) return;
+        mx = fmaxf(mx, halves.max[buf][half ^ 1][r]);
+        const bool need = mx > m + PF_RESCALE_LOG2;
+        if (__builtin_expect(!__any_sync(0xffffffffu, need), 1)) break;
+        if (need) {
           alpha = exp2f(m - mx);
           m = mx;
           l *= alpha;
         }
-        const float mref = m == -INFINITY ? 0.f : m;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      }
+      l += lb;
+      // (P's buffer is free: this warp has added P V of two blocks before)
 #pragma unroll
-        for (int i = 0; i < PF_KEYS; ++i) {
-          const float x = exp2f(fmaf(__uint_as_float(v[i]), c, -mref));
-          l4[i & 3] += x;
-          v[i] = __float_as_uint(x);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        // P's buffer, and the slot of the factor, are free once P V of two blocks before is done
-        if (j > 1 && !__all_sync(0xffffffffu, pf_wait(&bar.pv_done[0][buf], ((j >> 1) - 1) & 1, abort_flag, lim)))
-          return;
-        tc::tc_fence_after();
-        if (kb > it.kb0) factor[j & 3][r] = alpha;
+      for (int part = 0; part < 3; ++part) {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < PF_KEYS / 32; ++i) {
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x0 = __uint_as_float(v[32 * i + 2 * e]), x1 = __uint_as_float(v[32 * i + 2 * e + 1]);
-              w[e] = tc::pack_bf16x2(x0, x1);
-              if (part < 2) {
-                v[32 * i + 2 * e] = __float_as_uint(x0 - __uint_as_float(w[e] << 16));
-                v[32 * i + 2 * e + 1] = __float_as_uint(x1 - __uint_as_float(w[e] & 0xFFFF0000u));
-              }
-            }
-            tc::tmem_st16(tq + C::p_col(0, part, buf) + 16 * i, w);
+        for (int e = 0; e < 16; ++e) {
+          w[e] = tc::pack_bf16x2(p[2 * e], p[2 * e + 1]);
+          if (part < 2) {
+            p[2 * e] -= __uint_as_float(w[e] << 16);
+            p[2 * e + 1] -= __uint_as_float(w[e] & 0xFFFF0000u);
           }
         }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar.p_full[0][buf]);
+        tc::tmem_st16(tq + C::p_col(0, part, buf) + KH / 2 * half, w);
       }
-      // 1 / l goes by the slot behind the last block's: the sums have read what lay there when P V of the last but two is
-      // done, which this warp waited for ahead of its last weights
-      factor[j & 3][r] = l > 0.f ? 1.f / l : 0.f;
-      if (it.slot >= 0 && row.valid) a.part_ml[((long long)blockIdx.x * 2 + it.slot) * 128 + r] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar.l_full);
-    }
-    return;
-  }
-  int nl = 0;  // items with key blocks so far
-  for (int n = 0; take(n); ++n) {
-    const PfRow row = pf_row(a, it, pf_heads(a, it.row), 0, place, head);
-    uint32_t acc[C::HDP];
-#pragma unroll
-    for (int i = 0; i < C::HDP; ++i) acc[i] = 0u;
-#pragma unroll 1
-    for (int kb = it.kb0; kb < it.kb1; ++kb, ++j) {
-      if (!__all_sync(0xffffffffu, pf_wait(&bar.pv_done[0][j & 1], (j >> 1) & 1, abort_flag, lim))) return;
-      tc::tc_fence_after();
-      const float alpha = kb > it.kb0 ? factor[j & 3][r] : 0.f;
-#pragma unroll
-      for (int i = 0; i < C::HDP / 32; ++i) {
-        uint32_t o[32];
-        pf_ld32(tO + 32 * i, o);
-        pf_wait_ld(o);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          acc[32 * i + e] = __float_as_uint(fmaf(__uint_as_float(acc[32 * i + e]), alpha, __uint_as_float(o[e])));
-      }
+      tc::tmem_wait_st();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar.o_read);
-    }
-    float il = 0.f;
-    if (it.kb1 > it.kb0) {
-      if (!__all_sync(0xffffffffu, pf_wait(&bar.l_full, nl & 1, abort_flag, lim))) return;
-      ++nl;
-      il = factor[j & 3][r];
-    }
-    if (!row.valid) continue;
-    if (it.slot >= 0) {
-      float4* to = pf_part(a.part_o, (long long)blockIdx.x * 2 + it.slot, 0, 1, C::HDP, 0, r);
-#pragma unroll
-      for (int e = 0; e < C::HDP / 4; ++e)
-        to[128 * e] = make_float4(__uint_as_float(acc[4 * e]), __uint_as_float(acc[4 * e + 1]),
-                                  __uint_as_float(acc[4 * e + 2]), __uint_as_float(acc[4 * e + 3]));
-    } else {
-      char* out = reinterpret_cast<char*>(static_cast<float*>(a.p.a.out) + row.at);
-#pragma unroll
-      for (int e = 0; e < C::HDP / 8; ++e) {
-        uint32_t x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(__uint_as_float(acc[8 * e + k]) * il);
-        pf_store_row(out + 32 * e, x, 4 * hd - 32 * e, a.wide);
+      if (lane == 0) tc::mbar_arrive(&bar.p_full[0][buf]);
+      if (kb > it.kb0) {
+        const float now = alpha;
+        alpha = before;
+        if (!add(j - 1)) return;
+        alpha = now;
       }
     }
   }
@@ -834,7 +875,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __shared__ PfItem items[PF_ITEMS];
   __shared__ uint32_t there[2 * C::KST];
   __shared__ __align__(8) PfBars bar;
-  __shared__ float factor[C::F32 ? 4 : 1][128];  // fp32 rows: O's factor at a key block; at the end 1 / l
+  __shared__ __align__(8) PfHalves halves;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t s0 = tc::smem_u32(pf_smem_raw);
@@ -855,12 +896,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     init(bar.k_empty, 12, C::BLOCKS);      // and v_empty
     init(bar.it_full, PF_ITEMS, 1);
     init(bar.it_empty, PF_ITEMS, 9 + 2 * C::BLOCKS);
-    init(bar.q_full, 3, C::F32 ? 4 : 1);
+    init(bar.q_full, 3, C::F32 ? 8 : 1);
     init(bar.q_empty, 3, 1);
     init(&bar.s_full[0][0], 4, 1);
-    init(&bar.p_full[0][0], 4, 4);
+    init(&bar.p_full[0][0], 4, C::F32 ? 8 : 4);
     init(&bar.pv_done[0][0], 4, 1);
-    init(&bar.o_read, 2, 4);  // and l_full
+    init(&bar.o_read, 1, 8);
+    if constexpr (C::F32) init(&halves.max_there[0][0], 12, 2);  // and l_there
     init(bar.drain, 4, 1);
     abort_word = 0;
     tc::fence_barrier_init();
@@ -897,7 +939,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
   if (warp < 8) {
     if constexpr (C::F32)
-      prefill_f32_rows<C>(a, take, it, tmem, sQ, there, bar, factor, abort_flag);
+      prefill_f32_rows<C>(a, take, it, tmem, sQ, there, bar, halves, abort_flag);
     else
       prefill_bf16_rows<C>(a, take, it, tmem, there, bar, abort_flag);
   } else if (warp == PF_KWARP) {
