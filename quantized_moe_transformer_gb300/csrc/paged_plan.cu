@@ -10,7 +10,9 @@ namespace qmoe {
 
 namespace {
 
-constexpr int PL_THREADS = 1024, PL_WARPS = 32, PF_THREADS = 256, PF_ROWS = 1024, PF_MAX_CTAS = 2048;
+constexpr int PL_THREADS = 1024, PL_WARPS = 32, PF_THREADS = 256, PF_ROWS = 4, PF_MAX_CTAS = 2048;
+constexpr int PL_SEQS = 1024;   // as many sequences' arrays fit in shared memory
+constexpr int PL_ALONE = 1024;  // up to as many rows are written by the kernel that counts
 
 // What the first kernel leaves for the second: the state of the pool before the
 // call, and arrays over the sequences.
@@ -26,8 +28,10 @@ struct PlanWs {
   int32_t *need;      // pages that it asks for (0: none, or refused for its size)
   int32_t *len;       // entries that it keeps
   int32_t *from;      // first table entry without a page
+  int32_t *granted;   // rows that the sequence is granted
   int32_t *back;      // [pages] the pages that came back, in order
 };
+constexpr int PL_ARRAYS = 7;
 
 __host__ __device__ inline size_t plan_up(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -37,7 +41,7 @@ __host__ PlanWs plan_ws(const PagedView& c, void* ws, size_t* total) {
   size_t o = 256;
   PlanWs w{};
   w.head = reinterpret_cast<PlanHead*>(p);
-  int32_t** const arrays[] = {&w.first, &w.back_end, &w.need_end, &w.need, &w.len, &w.from};
+  int32_t** const arrays[] = {&w.first, &w.back_end, &w.need_end, &w.need, &w.len, &w.from, &w.granted};
   for (int32_t** a : arrays) {
     *a = reinterpret_cast<int32_t*>(p + o);
     o += seqs;
@@ -88,11 +92,21 @@ __device__ __forceinline__ bool plan_granted(const PagedView& c, const PlanArgs&
          (w.need[b] == 0 || w.need_end[b] <= h.n_free + h.back);
 }
 
+// The threads with ``mine`` in ``list`` (in any order), and how many; all threads of the CTA.
+__device__ __forceinline__ int plan_list(bool mine, int* list, int* listed) {
+  if (threadIdx.x == 0) *listed = 0;
+  __syncthreads();
+  if (mine) list[atomicAdd(listed, 1)] = threadIdx.x;
+  __syncthreads();
+  return *listed;
+}
+
 // One CTA: each sequence's pages that come back and that it misses, and their sums
-// over the sequences. A thread has a sequence; runs of pages are walked by its warp.
+// over the sequences. A thread has a sequence; long runs of pages are walked and moved by the warps.
 __device__ __forceinline__ void plan_count(const PagedView& c, const PlanArgs& a, const PlanWs& w) {
   __shared__ long long part[3][PL_WARPS];
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ int list[PL_THREADS], one_of[3][PL_THREADS], listed;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long cap = paged_slots(c);
   long long rows0 = 0, back0 = 0, need0 = 0;
   for (int b0 = 0; b0 < c.n_seqs; b0 += PL_THREADS) {
@@ -115,24 +129,44 @@ __device__ __forceinline__ void plan_count(const PagedView& c, const PlanArgs& a
     // how far the sequence's pages go: where they come back all of them, else as far as the rows need
     const int32_t* row = c.table + (long long)(mine ? b : 0) * c.max_pages;
     const int stop = !mine ? 0 : keep >= 0 ? c.max_pages : n > 0 ? want : 0;
-    bool open = mine && have < stop && plan_page(c, row[have]);
-    if (open) ++have;
-    for (unsigned m = __ballot_sync(0xffffffffu, open); m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int32_t* r = c.table + (long long)(b - lane + src) * c.max_pages;
-      int at = __shfl_sync(0xffffffffu, have, src);
-      const int to = __shfl_sync(0xffffffffu, stop, src);
-      while (at < to) {
-        const bool page = at + lane < to && plan_page(c, r[at + lane]);
-        const unsigned gone = __ballot_sync(0xffffffffu, !page);
+    // (most have the page that is begun and none behind it: two entries at once by the thread itself)
+    const bool one = have < stop && plan_page(c, row[have]);
+    const bool two = have + 1 < stop && plan_page(c, row[have + 1]);
+    if (one) have += two ? 2 : 1;
+    const bool open = one && two;
+    const int n_open = plan_list(open, list, &listed);
+    one_of[0][tid] = have;
+    one_of[1][tid] = stop;
+    __syncthreads();
+    for (int i = warp; i < n_open; i += PL_WARPS) {
+      const int src = list[i], to = one_of[1][src];
+      const int32_t* r = c.table + (long long)(b0 + src) * c.max_pages;
+      int at = one_of[0][src];
+      while (at < to) {  // 128 entries at once, the last of them that is a page, and the first that is none
+        int page[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) page[k] = at + 32 * k + lane < to ? r[at + 32 * k + lane] : -1;
+        unsigned gone = 0;
+        int k = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const unsigned g = __ballot_sync(0xffffffffu, !plan_page(c, page[e]));
+          if (gone == 0 && g != 0) {
+            gone = g;
+            k = e;
+          }
+        }
         if (gone) {
-          at += __ffs(gone) - 1;
+          at += 32 * k + __ffs(gone) - 1;
           break;
         }
-        at += 32;
+        at += 128;
       }
-      if (lane == src) have = min(at, to);
+      if (lane == 0) one_of[0][src] = min(at, to);
     }
+    __syncthreads();
+    have = one_of[0][tid];
+    __syncthreads();
     const int back = keep >= 0 ? max(have - cut, 0) : 0;
     const int from = keep >= 0 ? min(have, cut) : have;
     long long v[3] = {n, back, 0}, total[3];
@@ -152,17 +186,32 @@ __device__ __forceinline__ void plan_count(const PagedView& c, const PlanArgs& a
       a.first[b] = plan_int(first);
     }
     // the pages that come back, in order, leave the table
-    for (unsigned m = __ballot_sync(0xffffffffu, back > 0); m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      int32_t* r = const_cast<int32_t*>(c.table) + (long long)(b - lane + src) * c.max_pages +
-                   __shfl_sync(0xffffffffu, cut, src);
-      const int many = __shfl_sync(0xffffffffu, back, src);
-      const long long to = __shfl_sync(0xffffffffu, back_end, src) - many;
-      for (int i = lane; i < many; i += 32) {
-        if (to + i < c.n_pages) w.back[to + i] = r[i];
-        r[i] = -1;
+    const int n_back = plan_list(back > 0, list, &listed);
+    one_of[0][tid] = cut;
+    one_of[1][tid] = back;
+    one_of[2][tid] = (int)min(back_end - back, (long long)c.n_pages);
+    __syncthreads();
+    for (int i = warp; i < n_back; i += PL_WARPS) {
+      const int src = list[i], many = one_of[1][src];
+      int32_t* r = const_cast<int32_t*>(c.table) + (long long)(b0 + src) * c.max_pages + one_of[0][src];
+      const long long to = one_of[2][src];
+      for (int i0 = 0; i0 < many; i0 += 128) {
+        int page[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int x = i0 + 32 * k + lane;
+          if (x < many) page[k] = r[x];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int x = i0 + 32 * k + lane;
+          if (x >= many) continue;
+          if (to + x < c.n_pages) w.back[to + x] = page[k];
+          r[x] = -1;
+        }
       }
     }
+    __syncthreads();
     rows0 += total[0];
     back0 += total[1];
     need0 += need_total[0];
@@ -186,7 +235,7 @@ __device__ __forceinline__ void plan_count(const PagedView& c, const PlanArgs& a
     const int n = max(a.count[b], 0);
     const PlanHead h{n_free, (int)back0, 0, 0};
     const bool ok = plan_granted(c, a, w, h, b, n);
-    a.granted[b] = ok ? n : 0;
+    a.granted[b] = w.granted[b] = ok ? n : 0;
     if (ok && w.need[b] > 0) atomicMax(&taken, w.need_end[b]);
   }
   __syncthreads();
@@ -209,10 +258,9 @@ __device__ __forceinline__ int plan_above(const int32_t* end, int n, int v) {
   return lo;
 }
 
-// Table, stack and row maps, over ``threads`` threads of the grid.
-__device__ __forceinline__ void plan_fill(const PagedView& c, const PlanArgs& a, const PlanWs& w, long long tid,
-                                          long long threads) {
-  const PlanHead h = *w.head;
+// Table, stack and row maps, over ``threads`` threads of the grid (a multiple of 32).
+__device__ __forceinline__ void plan_fill(const PagedView& c, const PlanArgs& a, const PlanWs& w, const PlanHead& h,
+                                          long long tid, long long threads) {
   const int pool = h.n_free + h.back, left = pool - h.taken;
   // pages that came back and that the rows leave are pushed
   for (long long i = tid; h.n_free + i < left; i += threads) a.free_pages[h.n_free + i] = w.back[i];
@@ -227,35 +275,94 @@ __device__ __forceinline__ void plan_fill(const PagedView& c, const PlanArgs& a,
     }
     const_cast<int32_t*>(c.table)[(long long)b * c.max_pages + w.from[b] + (int)i - before] = page;
   }
-  for (long long i = tid; i < a.n_rows; i += threads) {
+  // four rows a thread, 16 bytes of each map where they lie so
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.seq) | reinterpret_cast<uintptr_t>(a.slot) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
+  for (long long i0 = PF_ROWS * tid; i0 < a.n_rows; i0 += PF_ROWS * threads) {
     // the last sequence that begins at or before the row (those without rows begin where the next one does)
-    const int b = plan_above(w.first, c.n_seqs, (int)i) - 1;
-    const int r = (int)i - w.first[b], n = max(a.count[b], 0);
-    const bool somebodys = r < n;
-    a.seq[i] = somebodys ? b : -1;
-    a.slot[i] = somebodys && a.granted[b] > 0 ? w.len[b] + r : -1;
-    a.pos[i] = !somebodys ? 0 : (a.next_pos ? a.next_pos[b] : w.len[b]) + r;
+    int b = plan_above(w.first, c.n_seqs, (int)i0) - 1;
+    int seq[PF_ROWS], slot[PF_ROWS], pos[PF_ROWS];
+    int next = b + 1 < c.n_seqs ? w.first[b + 1] : INT_MAX, r0 = w.first[b], n = max(a.count[b], 0), granted = w.granted[b],
+        len = w.len[b], at = a.next_pos ? a.next_pos[b] : len;
+#pragma unroll
+    for (int k = 0; k < PF_ROWS; ++k) {
+      const int i = (int)i0 + k;
+      if (i >= next) {
+        b = plan_above(w.first, c.n_seqs, i) - 1;
+        next = b + 1 < c.n_seqs ? w.first[b + 1] : INT_MAX;
+        r0 = w.first[b];
+        n = max(a.count[b], 0);
+        granted = w.granted[b];
+        len = w.len[b];
+        at = a.next_pos ? a.next_pos[b] : len;
+      }
+      const int r = i - r0;
+      const bool somebodys = r < n;
+      seq[k] = somebodys ? b : -1;
+      slot[k] = somebodys && granted > 0 ? len + r : -1;
+      pos[k] = somebodys ? at + r : 0;
+    }
+    if (wide && i0 + PF_ROWS <= a.n_rows) {
+      *reinterpret_cast<int4*>(a.seq + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+      *reinterpret_cast<int4*>(a.slot + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < PF_ROWS; ++k) {
+        if (i0 + k >= a.n_rows) break;
+        a.seq[i0 + k] = seq[k];
+        a.slot[i0 + k] = slot[k];
+        a.pos[i0 + k] = pos[k];
+      }
+    }
   }
 }
 
-__global__ void __launch_bounds__(PL_THREADS) plan_count_kernel(const PagedView c, const PlanArgs a, const PlanWs w,
-                                                                bool fill) {
+// The arrays over the sequences in shared memory.
+__device__ __forceinline__ PlanWs plan_shared(PlanWs w, int32_t (*arrays)[PL_SEQS]) {
+  w.first = arrays[0];
+  w.back_end = arrays[1];
+  w.need_end = arrays[2];
+  w.need = arrays[3];
+  w.len = arrays[4];
+  w.from = arrays[5];
+  w.granted = arrays[6];
+  return w;
+}
+
+// The pages are counted by one CTA: sums over the sequences decide who gets which. With few rows it writes all the
+// rest too; a second launch costs 2 us more than 1024 rows do here.
+__global__ void __launch_bounds__(PL_THREADS) plan_count_kernel(const PagedView c, const PlanArgs a, PlanWs w, bool fill) {
+  __shared__ int32_t arrays[PL_ARRAYS][PL_SEQS];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
+  if (fill && c.n_seqs <= PL_SEQS) w = plan_shared(w, arrays);
   plan_count(c, a, w);
   if (!fill) return;
   __syncthreads();
-  plan_fill(c, a, w, threadIdx.x, PL_THREADS);
+  plan_fill(c, a, w, *w.head, threadIdx.x, PL_THREADS);
 }
 
-__global__ void __launch_bounds__(PF_THREADS) plan_fill_kernel(const PagedView c, const PlanArgs a, const PlanWs w) {
+__global__ void __launch_bounds__(PF_THREADS) plan_fill_kernel(const PagedView c, const PlanArgs a, PlanWs w) {
+  __shared__ int32_t arrays[PL_ARRAYS][PL_SEQS];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  plan_fill(c, a, w, (long long)blockIdx.x * PF_THREADS + threadIdx.x, (long long)gridDim.x * PF_THREADS);
+  const PlanHead h = *w.head;
+  if (c.n_seqs <= PL_SEQS) {
+    const PlanWs s = plan_shared(w, arrays);
+    for (int b = threadIdx.x; b < c.n_seqs; b += PF_THREADS) {
+      s.first[b] = w.first[b];
+      s.need_end[b] = w.need_end[b];
+      s.len[b] = w.len[b];
+      s.from[b] = w.from[b];
+      s.granted[b] = w.granted[b];
+    }
+    w = s;
+    __syncthreads();
+  }
+  plan_fill(c, a, w, h, (long long)blockIdx.x * PF_THREADS + threadIdx.x, (long long)gridDim.x * PF_THREADS);
 }
 
-// One CTA does it all where there are few rows.
-bool plan_alone(const PlanArgs& a) { return a.n_rows <= PF_ROWS; }
+bool plan_alone(const PlanArgs& a) { return a.n_rows <= PL_ALONE; }
 
 }  // namespace
 
@@ -272,7 +379,7 @@ cudaError_t launch_paged_plan(const PagedView& c, const PlanArgs& a, cudaStream_
   const PlanWs w = plan_ws(c, a.ws, &total);
   cudaError_t e = launch_overlapped(plan_count_kernel, dim3(1), PL_THREADS, 0, 0, st, c, a, w, plan_alone(a));
   if (e != cudaSuccess || plan_alone(a)) return e;
-  long long ctas = ((long long)a.n_rows + PF_THREADS - 1) / PF_THREADS;
+  long long ctas = ((long long)a.n_rows + PF_ROWS * PF_THREADS - 1) / (PF_ROWS * PF_THREADS);
   if (ctas > PF_MAX_CTAS) ctas = PF_MAX_CTAS;
   return launch_overlapped(plan_fill_kernel, dim3((unsigned)ctas), PF_THREADS, 0, 0, st, c, a, w);
 }

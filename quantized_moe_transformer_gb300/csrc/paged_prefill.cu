@@ -1469,9 +1469,9 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.w.span = pl.span;
   x.w.head_rows = c.n_kv * pl.row_tiles;
   x.w.row_heads = pl.row_heads;
-  // in keys' worth of time: the change of tiles (1 x 16384 bf16 with 64 907 us, 256 796, 1152 809; fp32 1 x 4096 with 256
-  // 279 us, 640 223, 1152 227)
-  x.w.tile_cost = a.f32 ? 640 : 256;
+  // in keys' worth of time: the change of tiles (1 x 16384 bf16 with 64 907 us, 256 796, 1152 809; fp32 1 x 4096 with 320
+  // 167 us, 512 160, 896 168)
+  x.w.tile_cost = a.f32 ? 512 : 256;
   x.w.ctas = device_sm_count() < pl.ctas ? device_sm_count() : pl.ctas;
   x.w.desc = reinterpret_cast<int4*>(ws + pl.desc);
   x.part_ml = reinterpret_cast<float2*>(ws + pl.ml);

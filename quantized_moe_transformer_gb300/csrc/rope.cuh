@@ -62,16 +62,25 @@ __device__ __forceinline__ RopeUnit rope_unit(int u, int dims, bool interleaved)
   return RopeUnit{8 * u, 8 * u + 4, turned};
 }
 
+// The pair (v, w) turned by (cos, sin): the same roundings wherever it is called.
+__device__ __forceinline__ void rope_pair(float& v, float& w, float2 t) {
+  const float a = v, b = w;
+  v = __fmaf_rn(a, t.x, -__fmul_rn(b, t.y));
+  w = __fmaf_rn(b, t.x, __fmul_rn(a, t.y));
+}
+
 // The unit's elements p (from a) and q (from b) turned by the four (cos, sin) at ``t``.
 __device__ __forceinline__ void rope_apply(float4& p, float4& q, const float2* t, bool interleaved) {
-  const float4 v = p, w = q;
-  const float2 t0 = t[0], t1 = t[1], t2 = t[2], t3 = t[3];
   if (interleaved) {
-    p = make_float4(v.x * t0.x - v.y * t0.y, v.y * t0.x + v.x * t0.y, v.z * t1.x - v.w * t1.y, v.w * t1.x + v.z * t1.y);
-    q = make_float4(w.x * t2.x - w.y * t2.y, w.y * t2.x + w.x * t2.y, w.z * t3.x - w.w * t3.y, w.w * t3.x + w.z * t3.y);
+    rope_pair(p.x, p.y, t[0]);
+    rope_pair(p.z, p.w, t[1]);
+    rope_pair(q.x, q.y, t[2]);
+    rope_pair(q.z, q.w, t[3]);
   } else {
-    p = make_float4(v.x * t0.x - w.x * t0.y, v.y * t1.x - w.y * t1.y, v.z * t2.x - w.z * t2.y, v.w * t3.x - w.w * t3.y);
-    q = make_float4(w.x * t0.x + v.x * t0.y, w.y * t1.x + v.y * t1.y, w.z * t2.x + v.z * t2.y, w.w * t3.x + v.w * t3.y);
+    rope_pair(p.x, q.x, t[0]);
+    rope_pair(p.y, q.y, t[1]);
+    rope_pair(p.z, q.z, t[2]);
+    rope_pair(p.w, q.w, t[3]);
   }
 }
 
