@@ -245,14 +245,15 @@ template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;
   static constexpr int HDP = HDP_, NH = HDP / 64;
-  static constexpr int BLOCKS = F32 ? 1 : 2, PARTS = F32 ? 3 : 1;
-  static constexpr int THREADS = F32 ? 384 : 512;  // (bf16: two warps more, so that warps give registers up by fours)
-  static constexpr int QT = 3;                     // bf16: a ring of blocks of queries; fp32: their parts
-  static constexpr int QHALF = 128 * 128;          // 64 head dims of 128 query rows
+  static constexpr int BLOCKS = F32 || HDP == 256 ? 1 : 2, PARTS = F32 ? 3 : 1;
+  static constexpr int SOFT = F32 ? 8 : 4 * BLOCKS;       // warps of the softmax (of 8; the others have none)
+  static constexpr int THREADS = BLOCKS == 1 ? 384 : 512; // (two blocks: two warps more, so that warps give registers up by fours)
+  static constexpr int QT = HDP == 256 ? 1 : 3;           // bf16: a ring of blocks of queries; fp32: their parts
+  static constexpr int QHALF = 128 * 128;                 // 64 head dims of 128 query rows
   static constexpr int QTILE = NH * QHALF;
-  static constexpr int HALF = PF_KEYS * 128;       // 64 head dims of a key block
+  static constexpr int HALF = PF_KEYS * 128;              // 64 head dims of a key block
   static constexpr int TILE = NH * HALF;
-  static constexpr int KST = 4, VST = HDP == 128 ? (F32 ? 3 : 4) : 6;
+  static constexpr int KST = HDP == 256 ? 2 : 4, VST = HDP == 256 ? 2 : HDP == 128 ? (F32 ? 3 : 4) : 6;
   static constexpr int SMEM = 1024 + QT * QTILE + (KST + VST) * TILE;
   static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;
   // tensor memory: S of (block, buffer), P of (block or part, buffer), O of a block
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     init(bar.k_full, 12, 1);               // and v_full
     init(bar.k_empty, 12, C::BLOCKS);      // and v_empty
     init(bar.it_full, PF_ITEMS, 1);
-    init(bar.it_empty, PF_ITEMS, 9 + 2 * C::BLOCKS);
+    init(bar.it_empty, PF_ITEMS, C::SOFT + 1 + 2 * C::BLOCKS);
     init(bar.q_full, 3, C::F32 ? 8 : 1);
     init(bar.q_empty, 3, 1);
     init(&bar.s_full[0][0], 4, 1);
@@ -931,7 +932,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto blocks_of = [&]() { return C::BLOCKS == 2 && it.count - it.t * a.w.span > a.block_pos ? 2 : 1; };
 
   // registers of 512 threads go from the others to the softmax, which holds 64 scores and 32 weights: 256 x 168 + 256 x 80
-  if constexpr (!C::F32) {
+  if constexpr (C::BLOCKS == 2) {
     if (warp < 8)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     else
@@ -940,7 +941,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   if (warp < 8) {
     if constexpr (C::F32)
       prefill_f32_rows<C>(a, take, it, tmem, sQ, there, bar, halves, abort_flag);
-    else
+    else if (warp < C::SOFT)
       prefill_bf16_rows<C>(a, take, it, tmem, there, bar, abort_flag);
   } else if (warp == PF_KWARP) {
     // ------------------------------------------------------------ the CTA's work, copies of K and bf16 Q
@@ -971,13 +972,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (it.kb1 <= it.kb0) continue;
       const PfHeads hs = pf_heads(a, it.row);
       const int blocks = blocks_of();
-      // A block's queries go into the space of the third block before, once S no longer reads that; what lies behind
+      // A block's queries go into the space of the third block before (of the one before, with 256 head dims), once S no longer reads that; what lies behind
       // the rows (other sequences' rows, zeros from n_rows on) is masked. The second block's wait for the item
       // before: it comes behind the first keys.
       const auto queries = [&](int blk) -> bool {
-        const int qs = q_n % 3;
-        if (q_n >= 3 &&
-            !__all_sync(0xffffffffu, pf_wait(&bar.q_empty[qs], (q_n / 3 - 1) & 1, abort_flag, lim)))
+        const int qs = q_n % C::QT;
+        if (q_n >= C::QT &&
+            !__all_sync(0xffffffffu, pf_wait(&bar.q_empty[qs], (q_n / C::QT - 1) & 1, abort_flag, lim)))
           return false;
         ++q_n;
         if (lane == 0) {
@@ -1024,7 +1025,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int i = max(0, k - C::KST); i < k; ++i) pf_wait(&bar.k_full[i % C::KST], (i / C::KST) & 1, &never, lim);
     if (!C::F32) {
 #pragma unroll 1
-      for (int i = max(0, q_n - 3); i < q_n; ++i) pf_wait(&bar.q_full[i % 3], (i / 3) & 1, &never, lim);
+      for (int i = max(0, q_n - C::QT); i < q_n; ++i) pf_wait(&bar.q_full[i % C::QT], (i / C::QT) & 1, &never, lim);
     }
     __syncwarp();
   } else if (warp == PF_VWARP) {
@@ -1057,7 +1058,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     int k = 0, j = 0, q_n = 0;  // j: S products so far; q_n: bf16 blocks of queries (fp32: tiles) of the items before
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int blocks = blocks_of(), q = q_n + blk, qs = C::F32 ? 0 : q % 3;
+      const int blocks = blocks_of(), q = q_n + blk, qs = C::F32 ? 0 : q % C::QT;
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const int st = k % C::KST, buf = j & 1;
@@ -1068,7 +1069,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (lane == 0) tc::mbar_arrive(&bar.k_empty[st]);
           continue;
         }
-        if (kb == it.kb0) ok = ok && pf_wait(&bar.q_full[qs], (C::F32 ? q : q / 3) & 1, abort_flag, lim);
+        if (kb == it.kb0) ok = ok && pf_wait(&bar.q_full[qs], (C::F32 ? q : q / C::QT) & 1, abort_flag, lim);
         // the buffer is free again: bf16 once P V of two blocks before, which reads P there, is done; fp32 once
         // the softmax has taken S of two blocks before
         uint64_t* free_bar = C::F32 ? &bar.p_full[0][buf] : &bar.pv_done[blk][buf];
@@ -1167,10 +1168,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 // ---------------------------------------------------------------- parts of tiles
 // A tile that begins in CTA x and goes on: its parts, in order of the CTAs, joined by
-// their maxima. A CTA has a quarter of the columns, a lane a row. Few parts: a warp takes them all for 32
+// their maxima. A CTA has a part of the columns, a lane a row. Few parts: a warp takes them all for 32
 // rows, eight warps eight times 32 rows; many (few rows on a long axis): the warps take the parts of
 // 32 rows in turn, and their sums meet in shared memory.
-constexpr int PJ_THREADS = 256, PJ_WARPS = 8, PJ_SPLIT = 4;
+constexpr int PJ_THREADS = 256, PJ_WARPS = 8;
+__host__ __device__ constexpr int pj_split(int hdp) { return hdp == 256 ? 8 : 4; }  // CTAs over the columns
 constexpr int PF_MAX_CTAS = 256;  // the workspace does not depend on the device
 
 struct PfJoin {
@@ -1183,7 +1185,7 @@ struct PfJoin {
 
 template <typename T, int HDP, int BLOCKS>
 __global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j) {
-  constexpr int C4 = HDP / 4 / PJ_SPLIT;  // float4s of a row in this CTA
+  constexpr int C4 = HDP / 4 / pj_split(HDP);  // float4s of a row in this CTA
   __shared__ int parts[PF_MAX_CTAS], n_parts;
   __shared__ float4 sum[PJ_WARPS][C4][32];
   __shared__ float2 ml[PJ_WARPS][32];
@@ -1284,11 +1286,9 @@ __global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j
   }
 }
 
-template <typename T, int BLOCKS>
-cudaError_t launch_join(const PfJoin& j, int hdp, cudaStream_t st) {
-  const dim3 grid(j.w.ctas, PJ_SPLIT);
-  return hdp == 64 ? launch_overlapped(prefill_join_kernel<T, 64, BLOCKS>, grid, PJ_THREADS, 0, 0, st, j)
-                   : launch_overlapped(prefill_join_kernel<T, 128, BLOCKS>, grid, PJ_THREADS, 0, 0, st, j);
+template <typename T, int HDP, int BLOCKS>
+cudaError_t launch_join(const PfJoin& j, cudaStream_t st) {
+  return launch_overlapped(prefill_join_kernel<T, HDP, BLOCKS>, dim3(j.w.ctas, pj_split(HDP)), PJ_THREADS, 0, 0, st, j);
 }
 
 // ---------------------------------------------------------------- any head size
@@ -1379,9 +1379,9 @@ size_t pf_up(size_t v) { return (v + 255) & ~size_t(255); }
 PfPlan pf_plan(const PagedView& c, int n_rows, int n_heads, bool f32) {
   PfPlan p{};
   const int group = n_heads / c.n_kv;
-  p.tc = c.head_dim <= 128;
-  p.hdp = c.head_dim <= 64 ? 64 : 128;
-  p.blocks = f32 ? 1 : 2;
+  p.tc = c.head_dim <= 128 || !f32;
+  p.hdp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
+  p.blocks = f32 || p.hdp == 256 ? 1 : 2;
   p.row_tiles = (group + 127) / 128;
   p.row_heads = (group + p.row_tiles - 1) / p.row_tiles;
   p.block_pos = 128 / p.row_heads;
@@ -1480,11 +1480,16 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && c.head_dim * (a.f32 ? 4 : 2) % 32 == 0;
   x.scale = fminf(fmaxf(fabsf(p.scale_log2), FLT_MIN), FLT_MAX);
   x.flip = a.scale < 0.f ? 0x80000000u : 0u;
-  cudaError_t e = a.f32 ? (pl.hdp == 64 ? launch_tc<PfCfg<64, true>>(x, st) : launch_tc<PfCfg<128, true>>(x, st))
-                        : (pl.hdp == 64 ? launch_tc<PfCfg<64, false>>(x, st) : launch_tc<PfCfg<128, false>>(x, st));
+  cudaError_t e = a.f32           ? (pl.hdp == 64 ? launch_tc<PfCfg<64, true>>(x, st) : launch_tc<PfCfg<128, true>>(x, st))
+                  : pl.hdp == 64  ? launch_tc<PfCfg<64, false>>(x, st)
+                  : pl.hdp == 128 ? launch_tc<PfCfg<128, false>>(x, st)
+                                  : launch_tc<PfCfg<256, false>>(x, st);
   if (e != cudaSuccess || !pl.cuts) return e;
   const PfJoin j{p, x.w, pl.block_pos, x.part_ml, x.part_o};
-  return a.f32 ? launch_join<float, 1>(j, pl.hdp, st) : launch_join<__nv_bfloat16, 2>(j, pl.hdp, st);
+  if (a.f32) return pl.hdp == 64 ? launch_join<float, 64, 1>(j, st) : launch_join<float, 128, 1>(j, st);
+  return pl.hdp == 64    ? launch_join<__nv_bfloat16, 64, 2>(j, st)
+         : pl.hdp == 128 ? launch_join<__nv_bfloat16, 128, 2>(j, st)
+                         : launch_join<__nv_bfloat16, 256, 1>(j, st);
 }
 
 }  // namespace qmoe
