@@ -53,7 +53,7 @@ constexpr int PF_KEYS = 64, PF_MIN_BLOCKS = 4, PF_ITEMS = 4;
 
 struct PfTiling {
   int span, head_rows, row_heads;  // positions of a tile; head rows in all, of a KV head's heads row_heads each
-  int ctas, tile_cost;
+  int ctas, tile_cost, v_parts;    // v_parts: head rows that share their query heads, with 128 head dims of the values each
   int4* desc;  // [CTAs][2] a part of a tile: (sequence or -1, tile, head row, 1 if it is the tile's last)
 };
 
@@ -238,30 +238,34 @@ struct PfWalk {
 // tensor core has the other's products and the same block's next S.
 // fp32 rows: a tile is one block; q and each probability are three bf16 parts (24 bits), so S and P V
 // take three products each, small parts first. P V of a key block goes into a fresh accumulator and is added, rounded, to
-// the output in registers, so nothing is cut off over a long axis.
+// the output in registers, so nothing is cut off over a long axis. With more than 128 head dims the three parts of 128 rows do
+// not fit: a block is 64 rows (the instruction's other 64 read what follows in shared memory and are masked), and a tile
+// has half of the values' head dims, so that S is formed twice.
 // Warps: 0-7 the softmax; then one that walks the CTA's work and copies K (and bf16 Q), one that issues S, one that copies V,
 // one that issues P V, and for bf16's second block of rows one more of each of the issuers. Every wait is bounded.
 template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;
-  static constexpr int HDP = HDP_, NH = HDP / 64;
+  static constexpr int HDP = HDP_, NH = HDP / 64;         // head dims of queries and keys, padded
+  static constexpr int HDV = F32 && HDP == 256 ? 128 : HDP;  // of a tile's values: 256 of fp32 rows are two tiles
+  static constexpr int QROWS = F32 && HDP == 256 ? 64 : 128; // rows of a block that are used
   static constexpr int BLOCKS = F32 || HDP == 256 ? 1 : 2, PARTS = F32 ? 3 : 1;
   static constexpr int SOFT = F32 ? 8 : 4 * BLOCKS;       // warps of the softmax (of 8; the others have none)
   static constexpr int THREADS = BLOCKS == 1 ? 384 : 512; // (two blocks: two warps more, so that warps give registers up by fours)
-  static constexpr int QT = HDP == 256 ? 1 : 3;           // bf16: a ring of blocks of queries; fp32: their parts
-  static constexpr int QHALF = 128 * 128;                 // 64 head dims of 128 query rows
+  static constexpr int QT = HDP == 256 && !F32 ? 1 : 3;   // bf16: a ring of blocks of queries; fp32: their parts
+  static constexpr int QHALF = QROWS * 128;               // 64 head dims of the query rows
   static constexpr int QTILE = NH * QHALF;
   static constexpr int HALF = PF_KEYS * 128;              // 64 head dims of a key block
-  static constexpr int TILE = NH * HALF;
-  static constexpr int KST = HDP == 256 ? 2 : 4, VST = HDP == 256 ? 2 : HDP == 128 ? (F32 ? 3 : 4) : 6;
-  static constexpr int SMEM = 1024 + QT * QTILE + (KST + VST) * TILE;
+  static constexpr int TILE = NH * HALF, VTILE = HDV / 64 * HALF;
+  static constexpr int KST = HDP == 256 ? 2 : 4, VST = HDP == 64 ? 6 : F32 ? 3 : HDP == 128 ? 4 : 2;
+  static constexpr int SMEM = 1024 + QT * QTILE + KST * TILE + VST * VTILE;
   static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;
   // tensor memory: S of (block, buffer), P of (block or part, buffer), O of a block
   static __device__ __forceinline__ uint32_t s_col(int blk, int buf) { return 64u * (2 * blk + buf); }
   static __device__ __forceinline__ uint32_t p_col(int blk, int part, int buf) {
     return F32 ? P_COL + 96u * buf + 32u * part : s_col(blk, buf);
   }
-  static __device__ __forceinline__ uint32_t o_col(int blk) { return O_COL + (uint32_t)HDP * blk; }
+  static __device__ __forceinline__ uint32_t o_col(int blk) { return O_COL + (uint32_t)HDV * blk; }
 };
 constexpr int PF_KWARP = 8, PF_SWARP = 9, PF_VWARP = 10;  // 11 P V; block 1's S and P V 12 and 13
 constexpr float PF_RESCALE_LOG2 = 8.f;
@@ -448,28 +452,31 @@ __device__ __forceinline__ PfPages pf_pages(const PfArgs& a, const PfItem& it, i
   return r;
 }
 
-template <class C>
-__device__ __forceinline__ void pf_copy(const PfArgs& a, int g, const PfPages& pg, const CUtensorMap* map, uint8_t* stage,
-                                        uint64_t* bar) {
+template <int NH, int HALF>
+__device__ __forceinline__ void pf_copy(const PfArgs& a, int g, int dim, const PfPages& pg, const CUtensorMap* map,
+                                        uint8_t* stage, uint64_t* bar) {
   const int lane = threadIdx.x & 31, boxes = PF_KEYS / a.box_rows;
-  if (lane == 0) tc::mbar_expect_tx(bar, C::TILE);
+  if (lane == 0) tc::mbar_expect_tx(bar, NH * HALF);
   __syncwarp();
   if (lane < boxes) {
     const uint32_t dst = tc::smem_u32(stage) + lane * a.box_rows * 128;
 #pragma unroll
-    for (int h = 0; h < C::NH; ++h) pf_tma(dst + h * C::HALF, map, 64 * h, pg.row, g, pg.page, bar);
+    for (int h = 0; h < NH; ++h) pf_tma(dst + h * HALF, map, dim + 64 * h, pg.row, g, pg.page, bar);
   }
   __syncwarp();
 }
 
-// The KV head and the first query head of a head row.
+// The KV head of a head row, its first query head and how many there are, and its first head dim of the values.
 struct PfHeads {
-  int g, h0, n;  // n: heads of the row that exist
+  int g, h0, n, dv;
 };
+__host__ __device__ __forceinline__ PfHeads pf_heads(const PfTiling& w, int n_kv, int group, int row) {
+  if (w.head_rows == n_kv) return PfHeads{row, row * group, group, 0};
+  const int rows = w.head_rows / n_kv, g = row / rows, in = row - g * rows, tile = in / w.v_parts, at = tile * w.row_heads;
+  return PfHeads{g, g * group + at, min(w.row_heads, group - at), 128 * (in - tile * w.v_parts)};
+}
 __device__ __forceinline__ PfHeads pf_heads(const PfArgs& a, int row) {
-  if (a.w.head_rows == a.p.c.n_kv) return PfHeads{row, row * a.p.group, a.p.group};
-  const int rows = a.w.head_rows / a.p.c.n_kv, g = row / rows, at = (row - g * rows) * a.w.row_heads;
-  return PfHeads{g, g * a.p.group + at, min(a.w.row_heads, a.p.group - at)};
+  return pf_heads(a.w, a.p.c.n_kv, a.p.group, row);
 }
 
 // Row r of a block of 128: position ``place``, head ``head`` of the block's.
@@ -678,7 +685,7 @@ template <class C, class Take>
 __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, const PfItem& it, uint32_t tmem, uint8_t* sQ,
                                                  const uint32_t* there, PfBars& bar, PfHalves& halves,
                                                  volatile int* abort_flag) {
-  constexpr int KH = PF_KEYS / 2, DH = C::HDP / 2;  // scores and head dims of a warp
+  constexpr int KH = PF_KEYS / 2, DH = C::HDV / 2;  // scores and head dims of a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127, hd = a.p.c.head_dim;
   const int half = warp >> 2, quarter = warp & 3;
   const uint32_t lim = (uint32_t)min(a.p.a.wait_ns, 4000000000ull);
@@ -692,7 +699,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
   float m = -INFINITY, l = 0.f, alpha = 0.f;
   float acc[DH];
   PfRow row{}, old{};
-  int slot = -1;
+  int slot = -1, dv = 0;     // of the tile before
   bool open = false;         // the tile before waits for its last P V
   // acc = acc alpha + P V of key block k
   const auto add = [&](int k) -> bool {
@@ -714,18 +721,18 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
   const auto store = [&](const PfRow& to, float il) {
     if (!to.valid) return;
     if (slot >= 0) {
-      float4* p = pf_part(a.part_o, (long long)blockIdx.x * 2 + slot, 0, 1, C::HDP, DH / 4 * half, r);
+      float4* p = pf_part(a.part_o, (long long)blockIdx.x * 2 + slot, 0, 1, C::HDV, DH / 4 * half, r);
 #pragma unroll
       for (int e = 0; e < DH / 4; ++e)
         p[128 * e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
     } else {
-      char* p = reinterpret_cast<char*>(static_cast<float*>(a.p.a.out) + to.at + DH * half);
+      char* p = reinterpret_cast<char*>(static_cast<float*>(a.p.a.out) + to.at + dv + DH * half);
 #pragma unroll
       for (int e = 0; e < DH / 8; ++e) {
         uint32_t x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(acc[8 * e + k] * il);
-        pf_store_row(p + 32 * e, x, 4 * (hd - DH * half) - 32 * e, a.wide);
+        pf_store_row(p + 32 * e, x, 4 * (hd - dv - DH * half) - 32 * e, a.wide);
       }
     }
   };
@@ -736,11 +743,13 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
       // q as three bf16 parts, which hold all its bits, where the S products of the tile before no longer read (this
       // warp has taken their results): 16 rows of the quarter, a row's head dims over HDP / 4 lanes, the next
       // rows' loads ahead
-      constexpr int LANES = C::HDP / 4, ROWS = 32 / LANES, STEP = 4;
-      const int sub = lane / LANES, d = 4 * (lane - sub * LANES), r0 = 16 * half;
+      constexpr int LANES = C::HDP < 128 ? C::HDP / 4 : 32, ROWS = 32 / LANES, PER = C::HDP / (4 * LANES), STEP = 4;
+      constexpr int STEPS = 16 / ROWS * PER;
+      const int sub = lane / LANES, d0 = 4 * (lane - sub * LANES), r0 = 16 * half;
       const auto load = [&](int i) {
-        const long long at = __shfl_sync(0xffffffffu, row.at, r0 + (i * ROWS + sub) % 16);
-        const bool real = __shfl_sync(0xffffffffu, (int)row.valid, r0 + (i * ROWS + sub) % 16);
+        const int src = r0 + (i % STEPS / PER) * ROWS + sub, d = d0 + 128 * (i % PER);
+        const long long at = __shfl_sync(0xffffffffu, row.at, src);
+        const bool real = __shfl_sync(0xffffffffu, (int)row.valid, src);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (real && d < hd) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.p.a.q) + at + d);
         return x;
@@ -749,13 +758,13 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
 #pragma unroll
       for (int i = 0; i < STEP; ++i) x[i] = load(i);
 #pragma unroll 1
-      for (int i0 = 0; i0 < 16 / ROWS; i0 += STEP) {
+      for (int i0 = 0; i0 < STEPS && 32 * quarter < C::QROWS; i0 += STEP) {
         float4 y[STEP];
 #pragma unroll
         for (int i = 0; i < STEP; ++i) y[i] = load(i0 + STEP + i);  // (behind the last: the first again)
 #pragma unroll
         for (int i = 0; i < STEP; ++i) {
-          const int rr = 32 * quarter + r0 + (i0 + i) * ROWS + sub, ch = d >> 3;
+          const int rr = 32 * quarter + r0 + (i0 + i) / PER * ROWS + sub, d = d0 + 128 * ((i0 + i) % PER), ch = d >> 3;
           const uint32_t to = (ch >> 3) * C::QHALF + tc::sw128_offset(rr, ch & 7) + 2 * (d & 4);
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
@@ -791,6 +800,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
     m = -INFINITY;
     l = alpha = 0.f;
     slot = it.slot;
+    dv = pf_heads(a, it.row).dv;
     old = row;
     open = it.kb1 > it.kb0;
     if (!open) store(row, 0.f);
@@ -1011,7 +1021,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           break;
         }
         if (lane == 0) there[k % (2 * C::KST)] = pg.there;
-        pf_copy<C>(a, hs.g, pg, &kmap, sK + st * C::TILE, &bar.k_full[st]);
+        pf_copy<C::NH, C::HALF>(a, hs.g, 0, pg, &kmap, sK + st * C::TILE, &bar.k_full[st]);
         if (!C::F32 && kb == second && blocks == 2 && !queries(1)) {
           ++k;
           ok = false;
@@ -1033,7 +1043,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     int k = 0;
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int g = pf_heads(a, it.row).g;
+      const PfHeads hs = pf_heads(a, it.row);
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const PfPages pg = pf_pages(a, it, kb);
@@ -1043,7 +1053,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ok = false;
           break;
         }
-        pf_copy<C>(a, g, pg, &vmap, sV + st * C::TILE, &bar.v_full[st]);
+        pf_copy<C::HDV / 64, C::HALF>(a, hs.g, hs.dv, pg, &vmap, sV + st * C::VTILE, &bar.v_full[st]);
       }
     }
     volatile int never = 0;
@@ -1103,11 +1113,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else if (warp == 11 || warp == 13) {
     // ------------------------------------------------------------ O += P V
     const int blk = C::BLOCKS == 2 && warp == 13 ? 1 : 0;
-    const uint32_t idesc = tc::idesc_bf16_f32(128, (hd + 15) / 16 * 16) | (1u << 16);  // B (V) MN-major
     int k = 0, j = 0;  // j: P V products so far
     bool ok = true;
     for (int n = 0; ok && take(n); ++n) {
-      const int blocks = blocks_of();
+      const int blocks = blocks_of(), dims = min(hd - pf_heads(a, it.row).dv, C::HDV);
+      const uint32_t idesc = tc::idesc_bf16_f32(128, (dims + 15) / 16 * 16) | (1u << 16);  // B (V) MN-major
 #pragma unroll 1
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++k) {
         const int st = k % C::VST, buf = j & 1;
@@ -1117,7 +1127,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (lane == 0) tc::mbar_arrive(&bar.v_empty[st]);
           continue;
         }
-        uint8_t* vs = sV + st * C::TILE;
+        uint8_t* vs = sV + st * C::VTILE;
         // rows behind the sequence's last entry may hold anything, NaN too: zero weights need zero values (both
         // blocks' warps write the zeros, each ahead of its own products)
         if (it.len - kb * PF_KEYS < PF_KEYS) {
@@ -1125,7 +1135,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
           for (int i = 8 * r0 + lane; i < 8 * PF_KEYS; i += 32) {
 #pragma unroll
-            for (int h = 0; h < C::NH; ++h)
+            for (int h = 0; h < C::HDV / 64; ++h)
               *reinterpret_cast<uint4*>(vs + h * C::HALF + 16 * i) = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async_smem();
@@ -1137,7 +1147,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!ok) break;
         ++j;
         tc::tc_fence_after();
-        const uint32_t vd = pf_same(pf_desc(tc::smem_u32(sV) + (uint32_t)(st * C::TILE), C::HALF));
+        const uint32_t vd = pf_same(pf_desc(tc::smem_u32(sV) + (uint32_t)(st * C::VTILE), C::HALF));
         const uint32_t d = pf_same(tmem + C::o_col(blk));
         const bool first = !C::F32 && kb == it.kb0;
 #pragma unroll
@@ -1213,14 +1223,15 @@ __global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j
     if (lane == 0) n_parts = n;
   }
   __syncthreads();
-  const int n = n_parts, rows_of_kv = j.w.head_rows / j.p.c.n_kv, g = d.z / rows_of_kv, c0 = blockIdx.y * C4;
+  const int n = n_parts, c0 = blockIdx.y * C4;
+  const PfHeads hs = pf_heads(j.w, j.p.c.n_kv, j.p.group, d.z);
   const PrefillRows rr = prefill_rows(j.p, d.x);
   const bool many = n > PJ_WARPS;
   for (int group = many ? 0 : warp; group < 4 * BLOCKS; group += many ? 1 : PJ_WARPS) {
     const int in = 32 * (group & 3) + lane, blk = group >> 2, place = in / j.w.row_heads;
     const int pos = d.y * j.w.span + blk * j.block_pos + place;
-    const int h = (d.z - g * rows_of_kv) * j.w.row_heads + in - place * j.w.row_heads;
-    const bool valid = place < j.block_pos && pos < rr.count && h < j.p.group;
+    const int h = in - place * j.w.row_heads;
+    const bool valid = place < j.block_pos && pos < rr.count && h < hs.n;
     if (!__any_sync(0xffffffffu, valid)) continue;  // (the same for all warps of a group)
     float top = -INFINITY, l = 0.f;
     float4 acc[C4];
@@ -1276,10 +1287,10 @@ __global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j
       __syncthreads();
     }
     const float il = l > 0.f ? 1.f / l : 0.f;
-    T* out = static_cast<T*>(j.p.a.out) + ((long long)(rr.first + pos) * j.p.a.n_heads + g * j.p.group + h) * hd + 4 * c0;
+    T* out = static_cast<T*>(j.p.a.out) + ((long long)(rr.first + pos) * j.p.a.n_heads + hs.h0 + h) * hd + hs.dv + 4 * c0;
 #pragma unroll
     for (int e = 0; e < C4; ++e) {
-      if (!valid || 4 * (c0 + e) >= hd || (many && e % PJ_WARPS != warp)) continue;
+      if (!valid || hs.dv + 4 * (c0 + e) >= hd || (many && e % PJ_WARPS != warp)) continue;
       *reinterpret_cast<typename Four<T>::raw*>(out + 4 * e) =
           Four<T>::narrow(make_float4(acc[e].x * il, acc[e].y * il, acc[e].z * il, acc[e].w * il));
     }
@@ -1291,85 +1302,9 @@ cudaError_t launch_join(const PfJoin& j, cudaStream_t st) {
   return launch_overlapped(prefill_join_kernel<T, HDP, BLOCKS>, dim3(j.w.ctas, pj_split(HDP)), PJ_THREADS, 0, 0, st, j);
 }
 
-// ---------------------------------------------------------------- any head size
-constexpr int PP_THREADS = 128, PP_WARPS = 4;
-
-// A warp has one row and head: a lane scores one key of 32 at a time, then all
-// lanes add the 32 values, a part of the head dims each.
-template <typename T>
-__global__ void __launch_bounds__(PP_THREADS) prefill_rows_kernel(const PrefillView p) {
-  __shared__ float sq[PP_WARPS][256];
-  tc::grid_dep_launch();
-  tc::grid_dep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hd = p.c.head_dim;
-  const PrefillRows r = prefill_rows(p, blockIdx.y);
-  const int32_t* table = p.c.table + (long long)blockIdx.y * p.c.max_pages;
-  for (long long it = (long long)blockIdx.x * PP_WARPS + warp; it < (long long)r.count * p.a.n_heads;
-       it += (long long)gridDim.x * PP_WARPS) {
-    const int i = (int)(it / p.a.n_heads), h = (int)(it - (long long)i * p.a.n_heads), g = h / p.group;
-    const long long at = ((long long)(r.first + i) * p.a.n_heads + h) * hd;
-    const T* q = static_cast<const T*>(p.a.q) + at;
-    __syncwarp();
-    for (int d = lane; d < hd; d += 32) sq[warp][d] = (float)q[d];
-    __syncwarp();
-    const int n = max(r.before + i + 1, 0);
-    float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      const int j = j0 + lane;
-      long long off = -1;
-      float s = -INFINITY;
-      if (j < n) {
-        const int page = table[j >> p.c.page_log2];
-        if ((unsigned)page < (unsigned)p.c.n_pages)
-          off = (long long)page * p.c.page_stride + (long long)(j & ((1 << p.c.page_log2) - 1)) * p.c.slot_stride +
-                g * p.c.head_stride;
-        else
-          record_status(p.a.status, QMOE_ERR_DEVICE_ARG);
-      }
-      if (off >= 0) {
-        s = 0.f;
-        for (int d = 0; d < hd; d += 8) {
-          const uint4 k = *reinterpret_cast<const uint4*>(p.c.k + off + d);
-          const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s = fmaf(sq[warp][d + 2 * e], __uint_as_float(w[e] << 16), s);
-            s = fmaf(sq[warp][d + 2 * e + 1], __uint_as_float(w[e] & 0xFFFF0000u), s);
-          }
-        }
-        s *= p.scale_log2;
-      }
-      float top = s;
-#pragma unroll
-      for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      if (top == -INFINITY) continue;
-      const float m2 = fmaxf(m, top), alpha = exp2f(m - m2), w = s == -INFINITY ? 0.f : exp2f(s - m2);
-      m = m2;
-      l = l * alpha + w;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] *= alpha;
-      for (int k = 0; k < 32; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const long long ok = __shfl_sync(0xffffffffu, off, k);
-        if (ok < 0) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (lane + 32 * e < hd) o[e] = fmaf(wk, __bfloat162float(p.c.v[ok + lane + 32 * e]), o[e]);
-      }
-    }
-#pragma unroll
-    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-    T* out = static_cast<T*>(p.a.out) + at;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (lane + 32 * e < hd) out[lane + 32 * e] = (T)(l > 0.f ? o[e] / l : 0.f);
-  }
-}
-
 // ---------------------------------------------------------------- host
 struct PfPlan {
-  bool tc;          // on the tensor cores
-  int hdp, row_heads, row_tiles, block_pos, blocks, span, ctas;
+  int hdp, row_heads, row_tiles, v_parts, block_pos, blocks, span, ctas;
   bool cuts;        // tiles may be cut between CTAs
   size_t desc, ml, o, total;
 };
@@ -1379,15 +1314,16 @@ size_t pf_up(size_t v) { return (v + 255) & ~size_t(255); }
 PfPlan pf_plan(const PagedView& c, int n_rows, int n_heads, bool f32) {
   PfPlan p{};
   const int group = n_heads / c.n_kv;
-  p.tc = c.head_dim <= 128 || !f32;
   p.hdp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   p.blocks = f32 || p.hdp == 256 ? 1 : 2;
-  p.row_tiles = (group + 127) / 128;
+  const int block = f32 && p.hdp == 256 ? 64 : 128;  // query rows
+  p.v_parts = 128 / block;
+  p.row_tiles = (group + block - 1) / block;
   p.row_heads = (group + p.row_tiles - 1) / p.row_tiles;
-  p.block_pos = 128 / p.row_heads;
+  p.block_pos = block / p.row_heads;
   p.span = p.blocks * p.block_pos;
   const long long seqs = c.n_seqs < n_rows ? c.n_seqs : n_rows;
-  const long long tiles = ((long long)n_rows / p.span + seqs) * c.n_kv * p.row_tiles;
+  const long long tiles = ((long long)n_rows / p.span + seqs) * c.n_kv * p.row_tiles * p.v_parts;
   const long long keys = (paged_slots(c) + PF_KEYS - 1) / PF_KEYS;
   p.cuts = keys >= 2 * PF_MIN_BLOCKS;
   const long long pieces = tiles * (p.cuts ? keys / PF_MIN_BLOCKS : 1);
@@ -1396,7 +1332,7 @@ PfPlan pf_plan(const PagedView& c, int n_rows, int n_heads, bool f32) {
   p.desc = o; o += pf_up(sizeof(int4) * 2 * (size_t)p.ctas);
   p.ml = o;   o += p.cuts ? pf_up(sizeof(float2) * 512 * (size_t)p.ctas) : 0;
   p.o = o;    o += p.cuts ? pf_up(sizeof(float) * 512 * (size_t)p.hdp * p.ctas) : 0;
-  p.total = p.tc ? o : 256;
+  p.total = o;
   return p;
 }
 
@@ -1450,24 +1386,18 @@ size_t paged_prefill_ws_bytes(const PagedView& c, int n_rows, int n_heads) {
 
 int paged_prefill_launches(const PagedView& c, const PrefillArgs& a) {
   const PfPlan pl = pf_plan(c, a.n_rows, a.n_heads, a.f32);
-  return pl.tc && pl.cuts ? 2 : 1;
+  return pl.cuts ? 2 : 1;
 }
 
 cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaStream_t st) {
   const PfPlan pl = pf_plan(c, a.n_rows, a.n_heads, a.f32);
   PrefillView p{c, a, a.scale * 1.4426950408889634f, a.n_heads / c.n_kv};
-  if (!pl.tc) {
-    long long ctas = ((long long)a.n_rows * a.n_heads + PP_WARPS - 1) / PP_WARPS;
-    if (ctas > 16384) ctas = 16384;
-    const dim3 grid((unsigned)ctas, (unsigned)c.n_seqs);
-    return a.f32 ? launch_overlapped(prefill_rows_kernel<float>, grid, PP_THREADS, 0, 0, st, p)
-                 : launch_overlapped(prefill_rows_kernel<__nv_bfloat16>, grid, PP_THREADS, 0, 0, st, p);
-  }
   char* ws = static_cast<char*>(a.ws);
   PfArgs x{};
   x.p = p;
   x.w.span = pl.span;
-  x.w.head_rows = c.n_kv * pl.row_tiles;
+  x.w.head_rows = c.n_kv * pl.row_tiles * pl.v_parts;
+  x.w.v_parts = pl.v_parts;
   x.w.row_heads = pl.row_heads;
   // in keys' worth of time: the change of tiles (1 x 16384 bf16 with 64 907 us, 256 796, 1152 809; fp32 1 x 4096 with 320
   // 167 us, 512 160, 896 168)
@@ -1480,10 +1410,15 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && c.head_dim * (a.f32 ? 4 : 2) % 32 == 0;
   x.scale = fminf(fmaxf(fabsf(p.scale_log2), FLT_MIN), FLT_MAX);
   x.flip = a.scale < 0.f ? 0x80000000u : 0u;
-  cudaError_t e = a.f32           ? (pl.hdp == 64 ? launch_tc<PfCfg<64, true>>(x, st) : launch_tc<PfCfg<128, true>>(x, st))
-                  : pl.hdp == 64  ? launch_tc<PfCfg<64, false>>(x, st)
-                  : pl.hdp == 128 ? launch_tc<PfCfg<128, false>>(x, st)
-                                  : launch_tc<PfCfg<256, false>>(x, st);
+  cudaError_t e;
+  if (a.f32)
+    e = pl.hdp == 64    ? launch_tc<PfCfg<64, true>>(x, st)
+        : pl.hdp == 128 ? launch_tc<PfCfg<128, true>>(x, st)
+                        : launch_tc<PfCfg<256, true>>(x, st);
+  else
+    e = pl.hdp == 64    ? launch_tc<PfCfg<64, false>>(x, st)
+        : pl.hdp == 128 ? launch_tc<PfCfg<128, false>>(x, st)
+                        : launch_tc<PfCfg<256, false>>(x, st);
   if (e != cudaSuccess || !pl.cuts) return e;
   const PfJoin j{p, x.w, pl.block_pos, x.part_ml, x.part_o};
   if (a.f32) return pl.hdp == 64 ? launch_join<float, 64, 1>(j, st) : launch_join<float, 128, 1>(j, st);
