@@ -105,13 +105,15 @@ __device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w
   for (int d = 16; d; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
   cuts[0] = cuts[1] = PfCut{w.head_rows, 0, 0, 0};
   if (total == 0) return;
-  const long long all = total * w.head_rows, per = all / w.ctas, more = all - per * w.ctas;
+  // (where the shares are cut need not be exact, only the same in both CTAs and in order; fp32 products are)
+  const long long all = total * w.head_rows;
+  const float per = (float)all / (float)w.ctas;
   long long at[2];
   int row[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int i = blockIdx.x + k;
-    const long long x = i < w.ctas ? per * i + min((long long)i, more) : all;
+    const long long x = i < w.ctas ? min((long long)(per * (float)i), all - 1) : all;
     int q = (int)((float)x / (float)total);
     while (q > 0 && q * total > x) --q;
     while ((q + 1) * total <= x) ++q;
@@ -1177,12 +1179,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 }
 
 // ---------------------------------------------------------------- parts of tiles
-// A tile that begins in CTA x and goes on: its parts, in order of the CTAs, joined by
-// their maxima. A CTA has a part of the columns, a lane a row. Few parts: a warp takes them all for 32
-// rows, eight warps eight times 32 rows; many (few rows on a long axis): the warps take the parts of
-// 32 rows in turn, and their sums meet in shared memory.
-constexpr int PJ_THREADS = 256, PJ_WARPS = 8;
-__host__ __device__ constexpr int pj_split(int hdp) { return hdp == 256 ? 8 : 4; }  // CTAs over the columns
+// A tile over several CTAs: its parts, in order of the CTAs, joined by their maxima. As many CTAs of this kernel as
+// the tile has parts share its groups of 32 rows, each with a part of the columns; a lane has a row. Few parts: a warp
+// takes them all for its group; many (few rows on a long axis): eight warps take the parts of a group
+// in turn, and their sums meet in shared memory.
+constexpr int PJ_THREADS = 256, PJ_WARPS = 8, PJ_C4 = 8;  // PJ_C4 float4s of a row in a CTA
 constexpr int PF_MAX_CTAS = 256;  // the workspace does not depend on the device
 
 struct PfJoin {
@@ -1193,113 +1194,142 @@ struct PfJoin {
   float* part_o;
 };
 
+__device__ __forceinline__ bool pj_same(int4 a, int4 b) { return a.x == b.x && a.y == b.y && a.z == b.z; }
+
 template <typename T, int HDP, int BLOCKS>
 __global__ void __launch_bounds__(PJ_THREADS) prefill_join_kernel(const PfJoin j) {
-  constexpr int C4 = HDP / 4 / pj_split(HDP);  // float4s of a row in this CTA
-  __shared__ int parts[PF_MAX_CTAS], n_parts;
-  __shared__ float4 sum[PJ_WARPS][C4][32];
+  __shared__ int parts[PF_MAX_CTAS], n_parts, rank_here;
+  __shared__ float4 sum[PJ_WARPS][PJ_C4][32];
   __shared__ float2 ml[PJ_WARPS][32];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  const int4 d = j.w.desc[2 * blockIdx.x + 1];
-  if (d.x < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hd = j.p.c.head_dim;
-  if (warp == 0) {
-    int n = 1;
-    if (lane == 0) parts[0] = 2 * blockIdx.x + 1;
-    bool open = true;
-    for (int x = blockIdx.x + 1; open && x < j.w.ctas; x += 32) {
-      const int4 e = x + lane < j.w.ctas ? j.w.desc[2 * (x + lane)] : make_int4(-1, 0, 0, 0);
-      const bool mine = e.x == d.x && e.y == d.y && e.z == d.z;
-      unsigned have = __ballot_sync(0xffffffffu, mine);
-      const unsigned last = __ballot_sync(0xffffffffu, mine && e.w);
-      if (last) {
-        have &= 0xffffffffu >> (32 - __ffs(last));
-        open = false;
-      }
-      if ((have >> lane) & 1u) parts[n + __popc(have & ((1u << lane) - 1u))] = 2 * (x + lane);
-      n += __popc(have);
-    }
-    if (lane == 0) n_parts = n;
-  }
-  __syncthreads();
-  const int n = n_parts, c0 = blockIdx.y * C4;
-  const PfHeads hs = pf_heads(j.w, j.p.c.n_kv, j.p.group, d.z);
-  const PrefillRows rr = prefill_rows(j.p, d.x);
-  const bool many = n > PJ_WARPS;
-  for (int group = many ? 0 : warp; group < 4 * BLOCKS; group += many ? 1 : PJ_WARPS) {
-    const int in = 32 * (group & 3) + lane, blk = group >> 2, place = in / j.w.row_heads;
-    const int pos = d.y * j.w.span + blk * j.block_pos + place;
-    const int h = in - place * j.w.row_heads;
-    const bool valid = place < j.block_pos && pos < rr.count && h < hs.n;
-    if (!__any_sync(0xffffffffu, valid)) continue;  // (the same for all warps of a group)
-    float top = -INFINITY, l = 0.f;
-    float4 acc[C4];
-#pragma unroll
-    for (int e = 0; e < C4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (valid) {
-#pragma unroll 2
-      for (int i = many ? warp : 0; i < n; i += many ? PJ_WARPS : 1) {
-        const float2 x = j.part_ml[((long long)parts[i] * BLOCKS + blk) * 128 + in];
-        const float4* o = pf_part(j.part_o, parts[i], blk, BLOCKS, HDP, c0, in);
-        float4 v[C4];
-#pragma unroll
-        for (int e = 0; e < C4; ++e) v[e] = o[128 * e];
-        if (x.x == -INFINITY) continue;
-        const float m = fmaxf(top, x.x), old = exp2f(top - m), w = exp2f(x.x - m);
-        top = m;
-        l = l * old + x.y * w;
-#pragma unroll
-        for (int e = 0; e < C4; ++e) {
-          acc[e].x = acc[e].x * old + v[e].x * w;
-          acc[e].y = acc[e].y * old + v[e].y * w;
-          acc[e].z = acc[e].z * old + v[e].z * w;
-          acc[e].w = acc[e].w * old + v[e].w * w;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hd = j.p.c.head_dim, c0 = blockIdx.y * PJ_C4;
+#pragma unroll 1
+  for (int slot = 0; slot < 2; ++slot) {
+    // this CTA's part: of a tile that began in an earlier CTA, of one that begins here
+    const int4 d = j.w.desc[2 * blockIdx.x + slot];
+    if (d.x < 0) continue;
+    __syncthreads();
+    if (warp == 0) {
+      int x0 = blockIdx.x;
+      if (slot == 0) {  // back to the CTA that the tile begins in
+        x0 = -1;
+        for (int x = (int)blockIdx.x - 1; x0 < 0 && x >= 0; x -= 32) {
+          const int4 e = x - lane >= 0 ? j.w.desc[2 * (x - lane) + 1] : make_int4(-1, 0, 0, 0);
+          const unsigned begins = __ballot_sync(0xffffffffu, pj_same(e, d));
+          if (begins) x0 = x - (__ffs(begins) - 1);
         }
       }
+      int n = x0 >= 0 ? 1 : 0, rank = 0;  // (a CTA that gave up may have left no beginning)
+      if (lane == 0) parts[0] = 2 * x0 + 1;
+      bool open = x0 >= 0;
+      for (int x = x0 + 1; open && x < j.w.ctas; x += 32) {
+        const int4 e = x + lane < j.w.ctas ? j.w.desc[2 * (x + lane)] : make_int4(-1, 0, 0, 0);
+        const bool mine = pj_same(e, d);
+        unsigned have = __ballot_sync(0xffffffffu, mine);
+        const unsigned last = __ballot_sync(0xffffffffu, mine && e.w);
+        if (last) {
+          have &= 0xffffffffu >> (32 - __ffs(last));
+          open = false;
+        }
+        if ((have >> lane) & 1u) parts[n + __popc(have & ((1u << lane) - 1u))] = 2 * (x + lane);
+        if (slot == 0 && (int)blockIdx.x >= x && (int)blockIdx.x < x + 32)
+          rank = n + __popc(have & ((1u << (blockIdx.x - x)) - 1u));
+        n += __popc(have);
+      }
+      if (lane == 0) {
+        n_parts = n;
+        rank_here = rank;
+      }
     }
-    if (many) {
-      ml[warp][lane] = make_float2(top, l);
+    __syncthreads();
+    const int n = n_parts, rank = rank_here;
+    if (n == 0) continue;
+    const PfHeads hs = pf_heads(j.w, j.p.c.n_kv, j.p.group, d.z);
+    const PrefillRows rr = prefill_rows(j.p, d.x);
+    const bool many = n > PJ_WARPS;
+    for (int group = many ? rank : rank + n * warp; group < 4 * BLOCKS; group += many ? n : n * PJ_WARPS) {
+      const int in = 32 * (group & 3) + lane, blk = group >> 2, place = in / j.w.row_heads;
+      const int pos = d.y * j.w.span + blk * j.block_pos + place, h = in - place * j.w.row_heads;
+      const bool valid = place < j.block_pos && pos < rr.count && h < hs.n;
+      if (!__any_sync(0xffffffffu, valid)) continue;  // (the same for all warps of a group)
+      float top = -INFINITY, l = 0.f;
+      float4 acc[PJ_C4];
 #pragma unroll
-      for (int e = 0; e < C4; ++e) sum[warp][e][lane] = acc[e];
-      __syncthreads();
-      float m = -INFINITY;
+      for (int e = 0; e < PJ_C4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      constexpr int U = 2;
+      const int step = many ? PJ_WARPS : 1;
+      for (int i0 = many ? warp : 0; valid && i0 < n; i0 += U * step) {
+        float2 x[U];
+        float4 v[U][PJ_C4];
 #pragma unroll
-      for (int x = 0; x < PJ_WARPS; ++x) m = fmaxf(m, ml[x][lane].x);
-      l = 0.f;
+        for (int u = 0; u < U; ++u) {
+          x[u] = make_float2(-INFINITY, 0.f);
+          if (i0 + u * step >= n) continue;
+          const int part = parts[i0 + u * step];
+          x[u] = j.part_ml[((long long)part * BLOCKS + blk) * 128 + in];
+          const float4* o = pf_part(j.part_o, part, blk, BLOCKS, HDP, c0, in);
 #pragma unroll
-      for (int e = 0; e < C4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int e = 0; e < PJ_C4; ++e) v[u][e] = o[128 * e];
+        }
 #pragma unroll
-      for (int x = 0; x < PJ_WARPS; ++x) {
-        const float2 y = ml[x][lane];
-        const float w = y.x == -INFINITY ? 0.f : exp2f(y.x - m);
-        l += y.y * w;
+        for (int u = 0; u < U; ++u) {
+          if (x[u].x == -INFINITY) continue;
+          const float m = fmaxf(top, x[u].x), old = exp2f(top - m), w = exp2f(x[u].x - m);
+          top = m;
+          l = l * old + x[u].y * w;
 #pragma unroll
-        for (int e = 0; e < C4; ++e) {
-          if (e % PJ_WARPS != warp) continue;  // a warp finishes one in eight of the columns
-          const float4 v = sum[x][e][lane];
-          acc[e].x += v.x * w;
-          acc[e].y += v.y * w;
-          acc[e].z += v.z * w;
-          acc[e].w += v.w * w;
+          for (int e = 0; e < PJ_C4; ++e) {
+            acc[e].x = acc[e].x * old + v[u][e].x * w;
+            acc[e].y = acc[e].y * old + v[u][e].y * w;
+            acc[e].z = acc[e].z * old + v[u][e].z * w;
+            acc[e].w = acc[e].w * old + v[u][e].w * w;
+          }
         }
       }
-      __syncthreads();
-    }
-    const float il = l > 0.f ? 1.f / l : 0.f;
-    T* out = static_cast<T*>(j.p.a.out) + ((long long)(rr.first + pos) * j.p.a.n_heads + hs.h0 + h) * hd + hs.dv + 4 * c0;
+      if (many) {
+        ml[warp][lane] = make_float2(top, l);
 #pragma unroll
-    for (int e = 0; e < C4; ++e) {
-      if (!valid || hs.dv + 4 * (c0 + e) >= hd || (many && e % PJ_WARPS != warp)) continue;
-      *reinterpret_cast<typename Four<T>::raw*>(out + 4 * e) =
-          Four<T>::narrow(make_float4(acc[e].x * il, acc[e].y * il, acc[e].z * il, acc[e].w * il));
+        for (int e = 0; e < PJ_C4; ++e) sum[warp][e][lane] = acc[e];
+        __syncthreads();
+        // a warp finishes one float4
+        float m = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < PJ_WARPS; ++x) m = fmaxf(m, ml[x][lane].x);
+        l = 0.f;
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (warp < PJ_C4) {
+#pragma unroll
+          for (int x = 0; x < PJ_WARPS; ++x) {
+            const float2 y = ml[x][lane];
+            const float w = y.x == -INFINITY ? 0.f : exp2f(y.x - m);
+            const float4 v = sum[x][warp][lane];
+            l += y.y * w;
+            acc[0].x += v.x * w;
+            acc[0].y += v.y * w;
+            acc[0].z += v.z * w;
+            acc[0].w += v.w * w;
+          }
+        }
+        __syncthreads();
+      }
+      const float il = l > 0.f ? 1.f / l : 0.f;
+      T* out = static_cast<T*>(j.p.a.out) + ((long long)(rr.first + pos) * j.p.a.n_heads + hs.h0 + h) * hd + hs.dv;
+      const int e0 = many ? warp : 0;
+#pragma unroll
+      for (int e = 0; e < PJ_C4; ++e) {
+        const int col = 4 * (c0 + e0 + e);
+        if (!valid || hs.dv + col >= hd || (many && (e > 0 || warp >= PJ_C4))) continue;
+        *reinterpret_cast<typename Four<T>::raw*>(out + col) =
+            Four<T>::narrow(make_float4(acc[e].x * il, acc[e].y * il, acc[e].z * il, acc[e].w * il));
+      }
     }
   }
 }
 
 template <typename T, int HDP, int BLOCKS>
 cudaError_t launch_join(const PfJoin& j, cudaStream_t st) {
-  return launch_overlapped(prefill_join_kernel<T, HDP, BLOCKS>, dim3(j.w.ctas, pj_split(HDP)), PJ_THREADS, 0, 0, st, j);
+  return launch_overlapped(prefill_join_kernel<T, HDP, BLOCKS>, dim3(j.w.ctas, HDP / (4 * PJ_C4)), PJ_THREADS, 0, 0, st, j);
 }
 
 // ---------------------------------------------------------------- host
@@ -1421,7 +1451,7 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
                         : launch_tc<PfCfg<256, false>>(x, st);
   if (e != cudaSuccess || !pl.cuts) return e;
   const PfJoin j{p, x.w, pl.block_pos, x.part_ml, x.part_o};
-  if (a.f32) return pl.hdp == 64 ? launch_join<float, 64, 1>(j, st) : launch_join<float, 128, 1>(j, st);
+  if (a.f32) return pl.hdp == 64 ? launch_join<float, 64, 1>(j, st) : launch_join<float, 128, 1>(j, st);  // (of values)
   return pl.hdp == 64    ? launch_join<__nv_bfloat16, 64, 2>(j, st)
          : pl.hdp == 128 ? launch_join<__nv_bfloat16, 128, 2>(j, st)
                          : launch_join<__nv_bfloat16, 256, 1>(j, st);
