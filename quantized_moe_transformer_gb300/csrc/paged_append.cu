@@ -28,6 +28,9 @@ enum AppendTurn { AP_AS_IS = 0, AP_THETA = 1, AP_ROPE = 2 };
 // One row takes 3.1 us (the launch, the page look-up, one read and one write); 16372
 // bf16 rows of two KV heads of 128 6.5 us, 4.9 TB/s of reads and writes. Angles are
 // exact to 2^-33 turns; a sine or cosine is single precision, off by 2^-21 at most.
+// By a descriptor: 64 fp32 rows 3.0 us; 16372 bf16 rows with 16 query heads, 166 MB, 40 us, 4.1 TB/s. (Units of 16 bytes with
+// places divided out for each, as in rope.cu, and CTAs in 1, 3 or 6 waves took 40 to 44 us; all threads busy with 320 units a
+// row 46 us; the time is not the instructions'.)
 template <typename T, int ROT>
 __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedView c, const AppendArgs a, int rows,
                                                             const __grid_constant__ qmoe_rope_desc fr) {

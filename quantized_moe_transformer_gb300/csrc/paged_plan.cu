@@ -101,6 +101,9 @@ __device__ __forceinline__ int plan_list(bool mine, int* list, int* listed) {
   return *listed;
 }
 
+// What bounds it: a chain of dependent loads and barriers in one CTA (lengths, table entries, sums, pages), 8 us for 96
+// sequences with a row each; 256 sequences, 256 thousand rows and 13 thousand pages given back and handed out 17 us, of which
+// the second kernel's maps take 4 (3 MB).
 // One CTA: each sequence's pages that come back and that it misses, and their sums
 // over the sequences. A thread has a sequence; long runs of pages are walked and moved by the warps.
 __device__ __forceinline__ void plan_count(const PagedView& c, const PlanArgs& a, const PlanWs& w) {

