@@ -527,7 +527,7 @@ int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, in
  * types of qmoe_paged_attention. Rows of no sequence are not written.
  *   q, out [n_rows][n_heads][hd] of type dtype; out may be q. fp32 rows are taken with all
  *   their bits and fp32 accuracy is kept; for bf16 rows, which are exact as they are,
- *   probabilities are rounded to bf16 (2^-9) before they weigh the values, sums are fp32,
+ *   probabilities are rounded to bf16 (2^-8) before they weigh the values, sums are fp32,
  *   and the result is rounded once.
  *   first, count [n_seqs] int32; the sequences' rows must not overlap. Rows out of range
  *   are recorded as QMOE_ERR_DEVICE_ARG and the sequence has none.

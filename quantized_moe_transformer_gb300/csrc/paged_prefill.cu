@@ -1346,7 +1346,7 @@ cudaError_t launch_join(const PfJoin& j, cudaStream_t st) {
 struct PfPlan {
   int hdp, row_heads, row_tiles, v_parts, block_pos, blocks, span, ctas;
   bool cuts;        // tiles may be cut between CTAs
-  size_t desc, ml, o, total;
+  size_t desc, ml, o, q, total;
 };
 
 size_t pf_up(size_t v) { return (v + 255) & ~size_t(255); }
@@ -1372,6 +1372,8 @@ PfPlan pf_plan(const PagedView& c, int n_rows, int n_heads, bool f32) {
   p.desc = o; o += pf_up(sizeof(int4) * 2 * (size_t)p.ctas);
   p.ml = o;   o += p.cuts ? pf_up(sizeof(float2) * 512 * (size_t)p.ctas) : 0;
   p.o = o;    o += p.cuts ? pf_up(sizeof(float) * 512 * (size_t)p.hdp * p.ctas) : 0;
+  // two tiles of fp32 rows with more than 128 head dims read the same queries: where out is q, they read a copy
+  p.q = o;    o += p.v_parts == 2 ? pf_up(sizeof(float) * (size_t)n_rows * n_heads * c.head_dim) : 0;
   p.total = o;
   return p;
 }
@@ -1432,6 +1434,12 @@ int paged_prefill_launches(const PagedView& c, const PrefillArgs& a) {
 cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaStream_t st) {
   const PfPlan pl = pf_plan(c, a.n_rows, a.n_heads, a.f32);
   PrefillView p{c, a, a.scale * 1.4426950408889634f, a.n_heads / c.n_kv};
+  if (pl.v_parts == 2 && a.out == a.q) {
+    p.a.q = static_cast<char*>(a.ws) + pl.q;
+    const size_t bytes = sizeof(float) * (size_t)a.n_rows * a.n_heads * c.head_dim;
+    const cudaError_t e = cudaMemcpyAsync(const_cast<void*>(p.a.q), a.q, bytes, cudaMemcpyDeviceToDevice, st);
+    if (e != cudaSuccess) return e;
+  }
   char* ws = static_cast<char*>(a.ws);
   PfArgs x{};
   x.p = p;

@@ -239,3 +239,45 @@ def test_agrees_with_the_decoding_call():
     _, mean, bound = ref.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], c["first"], c["count"], 64)
     tol = 2 * (2 * 136 * 2.0 ** -24 * bound + 2.0 ** -16) * mean[:5]
     assert bool(((got - want).abs().double() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads,kv,hd", [(8, 2, 256), (6, 2, 200), (300, 2, 64), (40, 1, 144)])
+def test_in_place_where_tiles_share_their_queries(heads, kv, hd, dtype):
+    """Heads of more than 128 dims, or groups of more than a block's rows, are several tiles of the same rows."""
+    c = make([150, 33], [700, 40], heads, kv, hd, 32, dtype, seed=4)
+    want = run(c)
+    cache = qb.PagedCache(c["k"], c["v"], c["table"], c["lens"])
+    for _ in range(3):
+        q = c["q"].clone()
+        qb.paged_prefill_attention(cache, q, c["first"], c["count"], out=q)
+        n = int(c["count"].sum())
+        assert torch.equal(q[:n], want[:n]) and torch.equal(q[n:], c["q"][n:])
+    q = c["q"].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qb.paged_prefill_attention(cache, q, c["first"], c["count"], out=q)
+    for _ in range(3):
+        q.copy_(c["q"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(q[:n], want[:n]) and torch.equal(q[n:], c["q"][n:])
+
+
+def test_two_streams_at_once():
+    a = make([400, 90], [900, 90], 16, 2, 128, 64, torch.bfloat16)
+    b = make([300], [3000], 16, 2, 128, 32, torch.float32, seed=9)
+    want = [run(c) for c in (a, b)]
+    caches = [qb.PagedCache(c["k"], c["v"], c["table"], c["lens"]) for c in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for c, h, st in zip((a, b), caches, streams):
+            with torch.cuda.stream(st):
+                out = torch.full_like(c["q"], 7.0)
+            outs.append(qb.paged_prefill_attention(h, c["q"], c["first"], c["count"], out=out, stream=st))
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert qb.query_status() == 0
