@@ -91,63 +91,62 @@ __device__ __forceinline__ PfCut pf_cut(const PrefillRows& r, int row, int b, lo
   return PfCut{row, b, (int)t, kb};
 }
 
-// Where this CTA's work begins and ends, by one warp: a lane has a sequence of 32.
 __device__ __forceinline__ long long pf_sequence_cost(const PrefillRows& r, int span, int tile_cost) {
   return r.count > 0 ? pf_cost((r.count + span - 1) / span, (long long)max(r.before, 0) + tile_cost, span) : 0;
 }
-
-__device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w, PfCut (&cuts)[2]) {
-  const int lane = threadIdx.x & 31;
-  long long total = 0;
-#pragma unroll 4
-  for (int b = lane; b < p.c.n_seqs; b += 32) total += pf_sequence_cost(prefill_rows(p, b), w.span, w.tile_cost);
+__device__ __forceinline__ long long pf_warp_sum(long long v) {  // inclusive, over the lanes
 #pragma unroll
-  for (int d = 16; d; d /= 2) total += __shfl_xor_sync(0xffffffffu, total, d);
+  for (int d = 1; d < 32; d *= 2) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if ((int)(threadIdx.x & 31) >= d) v += o;
+  }
+  return v;
+}
+
+// Where this CTA's work begins and ends, by one warp: a lane sums a run of sequences, the run that a cut falls
+// into is looked at again, a lane a sequence.
+__device__ __forceinline__ void pf_share(const PrefillView& p, const PfTiling& w, PfCut (&cuts)[2]) {
+  const int lane = threadIdx.x & 31, run = (p.c.n_seqs + 31) / 32;
+  long long mine = 0;
+#pragma unroll 4
+  for (int i = 0; i < run; ++i) {
+    const int b = lane * run + i;
+    if (b < p.c.n_seqs) mine += pf_sequence_cost(prefill_rows(p, b), w.span, w.tile_cost);
+  }
+  const long long end = pf_warp_sum(mine), total = __shfl_sync(0xffffffffu, end, 31);
   cuts[0] = cuts[1] = PfCut{w.head_rows, 0, 0, 0};
   if (total == 0) return;
   // (where the shares are cut need not be exact, only the same in both CTAs and in order; fp32 products are)
   const long long all = total * w.head_rows;
   const float per = (float)all / (float)w.ctas;
-  long long at[2];
-  int row[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int i = blockIdx.x + k;
-    const long long x = i < w.ctas ? min((long long)(per * (float)i), all - 1) : all;
-    int q = (int)((float)x / (float)total);
-    while (q > 0 && q * total > x) --q;
-    while ((q + 1) * total <= x) ++q;
-    row[k] = q;
-    at[k] = x - q * total;  // inside the sequences' costs
-  }
-  long long before = 0;
-  bool open[2] = {row[0] < w.head_rows, row[1] < w.head_rows};
-  for (int b0 = 0; b0 < p.c.n_seqs && (open[0] || open[1]); b0 += 32) {
-    const PrefillRows mine = b0 + lane < p.c.n_seqs ? prefill_rows(p, b0 + lane) : PrefillRows{0, 0, 0, 0};
-    const long long cost = pf_sequence_cost(mine, w.span, w.tile_cost);
-    long long end = cost;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long long o = __shfl_up_sync(0xffffffffu, end, d);
-      if (lane >= d) end += o;
+    if (i >= w.ctas) break;
+    const long long x = min((long long)(per * (float)i), all - 1);
+    int row = (int)((float)x / (float)total);
+    while (row > 0 && row * total > x) --row;
+    while ((row + 1) * total <= x) ++row;
+    long long at = x - row * total;  // inside the sequences' costs
+    const int src = __ffs(__ballot_sync(0xffffffffu, end > at)) - 1;
+    at -= __shfl_sync(0xffffffffu, end - mine, src);
+    const int first = src * run, behind = min(first + run, p.c.n_seqs);
+    for (int b0 = first; b0 < behind; b0 += 32) {
+      const PrefillRows r = b0 + lane < behind ? prefill_rows(p, b0 + lane) : PrefillRows{0, 0, 0, 0};
+      const long long cost = pf_sequence_cost(r, w.span, w.tile_cost), sum = pf_warp_sum(cost);
+      const unsigned over = __ballot_sync(0xffffffffu, sum > at);
+      if (over) {
+        const int l = __ffs(over) - 1;
+        PrefillRows s;
+        s.first = 0;
+        s.count = __shfl_sync(0xffffffffu, r.count, l);
+        s.len = __shfl_sync(0xffffffffu, r.len, l);
+        s.before = s.len - s.count;
+        cuts[k] = pf_cut(s, row, b0 + l, at - __shfl_sync(0xffffffffu, sum - cost, l), w.span, w.tile_cost);
+        break;
+      }
+      at -= __shfl_sync(0xffffffffu, sum, 31);
     }
-    end += before;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!open[k]) continue;
-      const unsigned behind = __ballot_sync(0xffffffffu, end > at[k]);
-      if (behind == 0) continue;
-      const int src = __ffs(behind) - 1;
-      PrefillRows r;
-      r.first = 0;
-      r.count = __shfl_sync(0xffffffffu, mine.count, src);
-      r.len = __shfl_sync(0xffffffffu, mine.len, src);
-      r.before = r.len - r.count;
-      cuts[k] = pf_cut(r, row[k], b0 + src, at[k] - __shfl_sync(0xffffffffu, end - cost, src), w.span,
-                       w.tile_cost);
-      open[k] = false;
-    }
-    before = __shfl_sync(0xffffffffu, end, 31);
   }
 }
 

@@ -265,6 +265,14 @@ def test_in_place_where_tiles_share_their_queries(heads, kv, hd, dtype):
         assert torch.equal(q[:n], want[:n]) and torch.equal(q[n:], c["q"][n:])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seqs", [33, 600, 1100])
+def test_a_batch_of_single_rows(seqs, dtype):
+    """More sequences than lanes, than SMs and than 32 a lane, some without rows."""
+    lens = [1 + (53 * i) % 90 for i in range(seqs)]
+    check(make([0 if i % 7 == 3 else 1 for i in range(seqs)], lens, 4, 2, 64, 32, dtype), 32)
+
+
 def test_two_streams_at_once():
     a = make([400, 90], [900, 90], 16, 2, 128, 64, torch.bfloat16)
     b = make([300], [3000], 16, 2, 128, 32, torch.float32, seed=9)
