@@ -22,10 +22,16 @@ __host__ __device__ __forceinline__ long long paged_slots(const PagedView& c) {
   return (long long)c.max_pages << c.page_log2;
 }
 
+// An entry of the page table. A plan may write the table while the kernel that reads it is already launched and waits
+// for it, so it is no read-only data to that kernel: no __ldg.
+__device__ __forceinline__ int paged_entry(const PagedView& c, int seq, int slot) {
+  return c.table[(long long)seq * c.max_pages + (slot >> c.page_log2)];
+}
+
 // Element offset of (sequence, slot, KV head 0), -1 if the table has no valid
 // page there. ``slot`` is below the table's capacity.
 __device__ __forceinline__ long long paged_offset(const PagedView& c, int seq, int slot) {
-  const int page = __ldg(c.table + (long long)seq * c.max_pages + (slot >> c.page_log2));
+  const int page = paged_entry(c, seq, slot);
   if ((unsigned)page >= (unsigned)c.n_pages) return -1;
   return (long long)page * c.page_stride + (long long)(slot & ((1 << c.page_log2) - 1)) * c.slot_stride;
 }

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
     const int n_in = min(KT, w.len - w.t * KT), slot = w.t * KT + piece * p.box_rows;
     const bool want = some && piece < pieces && piece * p.box_rows < n_in;
     int page = -1;
-    if (want) page = __ldg(c.table + (long long)w.b * c.max_pages + (slot >> c.page_log2));
+    if (want) page = paged_entry(c, w.b, slot);
     load_q(seg);
     const bool there = want && (unsigned)page < (unsigned)c.n_pages;
     if (want && !there) record_status(p.status, QMOE_ERR_DEVICE_ARG);
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(32 * (C::WARPS + 1), 1)
       for (int i = 0; i < PIECES; ++i) {
         const int slot = w.t * KT + i * p.box_rows;
         pages[i] = left > 0 && i < pieces && slot < w.len
-                       ? __ldg(c.table + (long long)w.b * c.max_pages + (slot >> c.page_log2)) : -1;
+                       ? paged_entry(c, w.b, slot) : -1;
       }
     };
     pages_of();

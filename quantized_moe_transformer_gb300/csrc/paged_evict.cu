@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_select_kernel(const PagedVie
     const unsigned mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
     if (hole || mover) {
       int2* to = hole ? ls.hole + holes + __popc(mh & lower) : ls.mover + movers + __popc(mm & lower);
-      to[lb] = make_int2(j, __ldg(table + (j >> c.page_log2)));
+      to[lb] = make_int2(j, table[j >> c.page_log2]);
     }
     holes += __popc(mh);
     movers += __popc(mm);

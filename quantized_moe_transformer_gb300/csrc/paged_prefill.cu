@@ -446,7 +446,7 @@ __device__ __forceinline__ PfPages pf_pages(const PfArgs& a, const PfItem& it, i
   PfPages r{c.n_pages, 0, 0xFFu};
   bool ok = true;
   if (lane < boxes && slot < it.len) {
-    const int page = __ldg(c.table + (long long)it.b * c.max_pages + (slot >> c.page_log2));
+    const int page = paged_entry(c, it.b, slot);
     ok = (unsigned)page < (unsigned)c.n_pages;
     if (ok)
       r.page = page;
