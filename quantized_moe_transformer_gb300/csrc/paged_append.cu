@@ -158,13 +158,13 @@ template <typename T>
 cudaError_t append_rows(const PagedView& c, const AppendArgs& a, const qmoe_rope_desc& fr, cudaStream_t st) {
   // all CTAs at once on the SMs, as few rows in each as that allows
   const int fit = AP_CTAS_PER_SM * device_sm_count();
-  int rows = (a.n_rows + fit - 1) / fit;
+  int rows = (int)(((long long)a.n_rows + fit - 1) / fit);
   if (rows > AP_ROWS) rows = AP_ROWS;
   // one row of many heads: a thread for each of its units
   const int units = (a.n_heads + 2 * c.n_kv) * (c.head_dim / 8);
   int threads = AP_THREADS;
   while (rows == 1 && threads < AP_MAX_THREADS && threads < units) threads += 32;
-  const int ctas = (a.n_rows + rows - 1) / rows;
+  const int ctas = (int)(((long long)a.n_rows + rows - 1) / rows);
   if (a.rope) return launch_overlapped(append_kernel<T, AP_ROPE>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
   if (a.rotate) return launch_overlapped(append_kernel<T, AP_THETA>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);
   return launch_overlapped(append_kernel<T, AP_AS_IS>, dim3(ctas), threads, 0, 0, st, c, a, rows, fr);

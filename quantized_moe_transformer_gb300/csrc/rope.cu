@@ -115,9 +115,9 @@ cudaError_t rope_rows(const qmoe_rope_desc& r, const RopeArgs& a, cudaStream_t s
   // several CTAs after one another on an SM, so that some form their angles while others move rows (16384 rows in one wave
   // 30.3 us, in 3 28.1, in 6 27.1)
   const int fit = RO_WAVES * RO_CTAS_PER_SM * device_sm_count();
-  int rows = (a.n_rows + fit - 1) / fit;
+  int rows = (int)(((long long)a.n_rows + fit - 1) / fit);
   if (rows > 2 * RO_TURNS / r.dims) rows = 2 * RO_TURNS / r.dims;
-  const dim3 grid((a.n_rows + rows - 1) / rows);
+  const dim3 grid((unsigned)(((long long)a.n_rows + rows - 1) / rows));
   return r.layout == QMOE_ROPE_INTERLEAVED
              ? launch_overlapped(rope_kernel<T, N, true>, grid, RO_THREADS, 0, 0, st, a, rows, r)
              : launch_overlapped(rope_kernel<T, N, false>, grid, RO_THREADS, 0, 0, st, a, rows, r);

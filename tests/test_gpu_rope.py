@@ -138,3 +138,16 @@ def test_append_as_theta_does():
     q = [qb.paged_append(qb.PagedCache.empty(1, 64, 2, 128), k, v, pos, q=k, seq=seq, slot=slot, **kw)
          for kw in (dict(rope_theta=1e7), dict(rope=qb.Rope(128, 1e7)))]
     assert float((q[0] - q[1]).abs().max()) <= 2.0 ** -19 * 2 * float(k.abs().max())
+
+
+@pytest.mark.parametrize("n", [2 ** 29 + 5, 2 ** 31 - 1])
+def test_offsets_and_rows_past_32_bits(n):
+    """More elements than 32 bits count, and as many rows as they do: the last rows equal a small call's."""
+    turn = qb.Rope(8, theta=100.0)
+    y = torch.empty(n, 1, 8, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(1, 1, 8, device="cuda").to(torch.bfloat16)
+    pos = torch.full((n,), 7, dtype=torch.int32, device="cuda")
+    pos[-4:] = torch.tensor([1, 2, 3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    qb.rope(turn, pos, x.expand(n, 1, 8), q_out=y)
+    few = qb.rope(turn, pos[-9:].contiguous(), x.repeat(9, 1, 1))
+    assert torch.equal(y[-9:], few) and torch.equal(y[n // 2:n // 2 + 4], few[:4]) and torch.equal(y[:4], few[:4])
