@@ -484,10 +484,12 @@ int qmoe_paged_append_rope(const qmoe_paged_cache *c, const void *q, void *q_out
  *      (next_pos NULL: lens[b]). Rows behind the last: seq -1, slot -1, pos 0.
  * lens does not grow: qmoe_paged_append does that, with these maps (a slot of -1 is its padding).
  *   count, first, granted [n_seqs]; keep, next_pos [n_seqs] or NULL; seq, slot, pos
- *   [n_rows], may be NULL where n_rows is 0; all int32, no two of them the same array. The call
+ *   [n_rows], may be NULL where n_rows is 0; all int32, no two of them the same array, and none
+ *   the cache's own (QMOE_ERR_ARG), but for keep and next_pos, which may be lens: all of a
+ *   sequence kept, positions that are slots. The call
  *   writes the cache's table. A page belongs to one sequence alone. A count of free pages out
- *   of range, a free page's number out of range (its entry becomes -1) and pages that come back
- *   more than once are recorded as QMOE_ERR_DEVICE_ARG.
+ *   of range, a free page's number out of range (its entry becomes -1) and more pages, free or
+ *   come back, than there are (some page came back twice) are recorded as QMOE_ERR_DEVICE_ARG.
  *   ws: qmoe_paged_plan_workspace_bytes(c) bytes, 256-byte aligned.
  */
 size_t qmoe_paged_plan_workspace_bytes(const qmoe_paged_cache *c);
@@ -525,13 +527,15 @@ int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, in
  *   j < lens[b] - count[b] + i + 1
  * (none where that is 0 or less: its output is zeros), with the scores, scale, heads and
  * types of qmoe_paged_attention. Rows of no sequence are not written.
- *   q, out [n_rows][n_heads][hd] of type dtype; out may be q. fp32 rows are taken with all
+ *   q, out [n_rows][n_heads][hd] of type dtype; out may be q (fp32 rows of more than 128 head dims
+ *   are then copied to ws first). fp32 rows are taken with all
  *   their bits and fp32 accuracy is kept; for bf16 rows, which are exact as they are,
  *   probabilities are rounded to bf16 (2^-8) before they weigh the values, sums are fp32,
  *   and the result is rounded once.
  *   first, count [n_seqs] int32; the sequences' rows must not overlap. Rows out of range
  *   are recorded as QMOE_ERR_DEVICE_ARG and the sequence has none.
  *   What the cache holds outside the entries is never used; queries and entries are finite.
+ *   The entries' weights do not grow.
  *   ws: qmoe_paged_prefill_attention_workspace_bytes(c, n_rows, n_heads) bytes, 256-byte
  *   aligned. The sums are taken in a fixed order: the same call gives the same bits. A call whose wait runs
  *   out (QMOE_ERR_TIMEOUT) leaves out undefined.

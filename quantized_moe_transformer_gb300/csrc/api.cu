@@ -703,6 +703,13 @@ int qmoe_paged_plan(const qmoe_paged_cache* c, int32_t* free_pages, int32_t* n_f
     if (!aligned(p, 4)) return QMOE_ERR_ALIGN;
   if (!aligned(ws, 256)) return QMOE_ERR_ALIGN;
   if (ws_bytes < paged_plan_ws_bytes(view)) return QMOE_ERR_WORKSPACE;
+  // what is written is no other array of the call; keep and next_pos are read by a sequence's own thread ahead of its
+  // length or in full behind it, so they may be the lengths
+  const void* const arrays[] = {free_pages, n_free, first, granted, n_rows > 0 ? seq : nullptr, n_rows > 0 ? slot : nullptr,
+                                n_rows > 0 ? pos : nullptr, c->lens, c->table, count, keep, next_pos};
+  for (int i = 0; i < 9; ++i)
+    for (int j = i + 1; j < 12; ++j)
+      if (arrays[i] && arrays[i] == arrays[j] && !(i == 7 && j >= 10)) return QMOE_ERR_ARG;
   PlanArgs a{};
   r = device_ready(&a.status);
   if (r != QMOE_OK) return r;

@@ -128,3 +128,18 @@ def test_pages_that_come_back_twice_are_reported():
     qb.paged_plan(cache, pool, i32([0, 0, 0]), keep=i32([0, 0, 0]), n_rows=0)
     torch.cuda.synchronize()
     assert qb.query_status() == -8 and int(pool.n_free) == 3 and cache.table.tolist() == [[-1, -1]] * 3
+
+
+def test_the_lengths_as_keep_and_positions():
+    """keep = lens returns the pages that hold nothing; positions that are slots."""
+    table, lens = [[5, 2, 7, -1], [0, 1, -1, -1], [-1] * 4], [9, 0, 0]
+    k = torch.zeros(9, 8, 1, 8, dtype=torch.bfloat16, device="cuda")
+    cache = qb.PagedCache(k, torch.zeros_like(k), i32(table), i32(lens))
+    pool = qb.PagePool(i32([3, 4, 6, 8, 99, 99, 99, 99, 99]), i32([4]))
+    got = qb.paged_plan(cache, pool, i32([2, 0, 3]), keep=cache.lens, next_pos=cache.lens, n_rows=6)
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0
+    want, kept, left, *maps = ref.plan(table, lens, [3, 4, 6, 8], [2, 0, 3], lens, lens, 6, 8, 9)
+    assert cache.table.tolist() == want and cache.lens.tolist() == kept == lens
+    assert pool.free[:len(left)].tolist() == left and int(pool.n_free) == len(left)
+    assert [t.tolist() for t in got] == maps

@@ -195,3 +195,27 @@ def test_block_of_another_cache(lib):
     assert prefill(lib, rope=rope_desc(dims=136)) == ARG and prefill(lib, n_rows=0, ws=None) == 0
     assert lib.qmoe_block_prefill_paged_workspace_bytes(ctypes.byref(block_desc()), ctypes.byref(desc(n_kv=4)), 5) == 0
     assert lib.qmoe_block_prefill_paged_workspace_bytes(ctypes.byref(block_desc()), ctypes.byref(desc()), 0) == 0
+
+
+@pytest.mark.parametrize("kw", [{"granted": 3}, {"count": 3}, {"keep": 3}, {"nxt": 3}, {"free": 3}, {"seq": 3}, {"slot": 3},
+                                {"first": "lens"}, {"granted": "lens"}, {"pos": "table"}, {"n_free": "lens"}, {"count": "lens"}])
+def test_a_plan_does_not_write_what_it_reads(lib, kw):
+    """Two arrays of a plan in one place: ``first`` with another, or one with the cache's own."""
+    names = ["free", "n_free", "count", "keep", "nxt", "first", "granted", "seq", "slot", "pos"]
+    apart = {n: FAKE + 4096 * (i + 1) for i, n in enumerate(names)}
+    own = desc()
+    own.lens, own.table = FAKE + 4096 * 20, FAKE + 4096 * 21
+    (name, where), = kw.items()
+    at = {"lens": own.lens, "table": own.table}.get(where, apart["first"])
+    assert plan(lib, own, **{**apart, name: at}) == ARG
+
+
+@pytest.mark.parametrize("name", ["keep", "nxt"])
+def test_a_plan_may_read_the_lengths(lib, name):
+    names = ["free", "n_free", "count", "keep", "nxt", "first", "granted", "seq", "slot", "pos"]
+    apart = {n: FAKE + 4096 * (i + 1) for i, n in enumerate(names)}
+    own = desc()
+    own.lens, own.table = FAKE + 4096 * 20, FAKE + 4096 * 21
+    if torch.cuda.is_available():
+        pytest.skip("the call would run")
+    assert plan(lib, own, **{**apart, name: own.lens}) not in (0, NULL, ARG, ALIGN, WORKSPACE)
