@@ -289,3 +289,27 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
     assert qb.query_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """Rows and pages whose elements lie behind the first 2^31: as the same rows and pages at the front."""
+    heads, kv, hd, page, many = 16, 2, 128, 64, 2 ** 17 + 9
+    c = make([70, 5], [300, 5], heads, kv, hd, page, torch.bfloat16)
+    want = run(c)
+    rows = 2 ** 20 + 100
+    shift, pages = rows - c["q"].shape[0], c["k"].shape[0]
+    pools = [torch.empty(many + pages, page, kv, hd, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    for big, small in zip(pools, (c["k"], c["v"])):
+        big[many:] = small
+    table = torch.where(c["table"] < pages, c["table"] + many, c["table"])
+    q = torch.zeros(rows, heads, hd, dtype=torch.bfloat16, device="cuda")
+    q[shift:] = c["q"]
+    assert q.numel() > 2 ** 31 and pools[0].numel() > 2 ** 31
+    out = qb.paged_prefill_attention(qb.PagedCache(*pools, table, c["lens"]), q, c["first"] + shift, c["count"])
+    n = int(c["count"].sum())
+    assert torch.equal(out[shift:shift + n], want[:n]) and not bool(out[:shift].any()) and not bool(out[shift + n:].any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_pages_of_4096(dtype):
+    check(make([200, 4097], [9000, 4097], 4, 2, 64, 4096, dtype), 4096)
