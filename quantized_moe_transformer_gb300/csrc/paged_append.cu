@@ -28,9 +28,10 @@ enum AppendTurn { AP_AS_IS = 0, AP_THETA = 1, AP_ROPE = 2 };
 // One row takes 3.1 us (the launch, the page look-up, one read and one write); 16372
 // bf16 rows of two KV heads of 128 6.5 us, 4.9 TB/s of reads and writes. Angles are
 // exact to 2^-33 turns; a sine or cosine is single precision, off by 2^-21 at most.
-// By a descriptor: 64 fp32 rows 3.0 us; 16372 bf16 rows with 16 query heads, 166 MB, 40 us, 4.1 TB/s. (Units of 16 bytes with
-// places divided out for each, as in rope.cu, and CTAs in 1, 3 or 6 waves took 40 to 44 us; all threads busy with 320 units a
-// row 46 us; the time is not the instructions'.)
+// By a descriptor: 64 fp32 rows 3.0 us; 16372 bf16 rows with 16 query heads, 166 MB, 33.7 us, 4.9 TB/s, 0.72 of the copy
+// rate: the CTAs begin together with angles and end together, and stores of 8 bytes a lane. (40 us with a lane's four angles
+// side by side in shared memory, four lanes to a bank, and the 64 of 320 units that are left over by one thread in four; two
+// and four waves of CTAs 34 and 38, 96 bytes of a thread in flight 36.)
 template <typename T, int ROT>
 __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedView c, const AppendArgs a, int rows,
                                                             const __grid_constant__ qmoe_rope_desc fr) {
@@ -42,23 +43,24 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, threads = blockDim.x, hd = c.head_dim, half = (ROT == AP_ROPE ? fr.dims : hd) / 2;
-  if (ROT == AP_ROPE) {
-    for (int i = tid; i < n * half; i += threads) {
-      const int r = i / half;
-      turn[i] = rope_turn(a.pos[n0 + r], fr.turns[i - r * half], fr.scale);
-    }
-  }
-  if (ROT == AP_THETA) {
-    for (int i = tid; i < n * half; i += threads) {
+  // a unit's four angles lie ``quarter`` apart, so that the lanes, unit by unit, read side by side (four of one
+  // lane side by side would be four lanes to a bank)
+  const int quarter = half / 4;
+  const auto angles = [&]() {
+    for (int i = tid; ROT && i < n * half; i += threads) {
       const int r = i / half, d = i - r * half;
-      const uint64_t frac = (uint64_t)(long long)a.pos[n0 + r] * fr.turns[d];
-      // the upper 32 bits as a signed part of a turn: |error| <= 2^-33 turns, then one rounding to fp32
-      const float x = (float)(int)((frac + 0x80000000ull) >> 32) * (6.283185307179586f / 4294967296.f);
-      float s, k;
-      sincosf(x, &s, &k);
-      turn[i] = make_float2(k, s);
+      float2 t;
+      if (ROT == AP_ROPE) {
+        t = rope_turn(a.pos[n0 + r], fr.turns[d], fr.scale);
+      } else {
+        const uint64_t frac = (uint64_t)(long long)a.pos[n0 + r] * fr.turns[d];
+        // the upper 32 bits as a signed part of a turn: |error| <= 2^-33 turns, then one rounding to fp32
+        const float x = (float)(int)((frac + 0x80000000ull) >> 32) * (6.283185307179586f / 4294967296.f);
+        sincosf(x, &t.y, &t.x);
+      }
+      turn[r * half + (d & 3) * quarter + (d >> 2)] = t;
     }
-  }
+  };
   if (tid < 32) {
     int seq = -1, slot = -1;
     long long o = -1;
@@ -84,19 +86,19 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
   using raw = typename F::raw;
   const bool inter = ROT == AP_ROPE && fr.layout == QMOE_ROPE_INTERLEAVED;
   const int per_head = hd / 8, units = (a.n_heads + 2 * c.n_kv) * per_head;
-  // a thread keeps its unit and walks rows; where a row has fewer units than the CTA threads, groups of threads take
-  // rows side by side
-  const int groups = units < threads ? threads / units : 1, group = units < threads ? tid / units : 0;
+  // a thread keeps its unit and walks rows; where a row has fewer units (or fewer left) than the CTA threads, groups of
+  // threads take rows side by side
   constexpr int U = 64 / (int)sizeof(raw) / 2;  // 64 bytes of a thread in flight
   bool looked_up = false;
   for (int u0 = 0; u0 < units; u0 += threads) {
-    const int u = u0 + tid - group * units;
-    const bool mine = u < units && group < groups;
+    const int here = min(units - u0, threads), groups = threads / here, group = tid / here;
+    const int u = u0 + tid - group * here;
+    const bool mine = group < groups;
     const int h = u / per_head, g = h - a.n_heads;
     // the unit's two places and its first angle (values never turn: any two places do)
     const RopeUnit at_ = ROT == AP_ROPE ? rope_unit(u - h * per_head, fr.dims, inter)
                                         : RopeUnit{4 * (u - h * per_head), 4 * (u - h * per_head) + hd / 2, true};
-    const int d = at_.a, apart = at_.b - at_.a, angle = 4 * (u - h * per_head);
+    const int d = at_.a, apart = at_.b - at_.a, angle = u - h * per_head;
     const T* src = nullptr;
     long long step = 0;  // elements between a tensor's rows
     if (mine) {
@@ -116,7 +118,10 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
           y[k] = *reinterpret_cast<const raw*>(src + r * step + apart);
         }
       }
-      if (!looked_up) __syncthreads();  // the first reads go on while the pages are looked up
+      if (!looked_up) {  // the first reads go on while the pages are looked up and the angles formed
+        angles();
+        __syncthreads();
+      }
       looked_up = true;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
@@ -125,10 +130,11 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
         const long long o = off[r];
         if (g >= 0 && o < 0) continue;
         float4 p = F::wide(x[k]), q = F::wide(y[k]);
-        if (ROT == AP_ROPE && g < c.n_kv && at_.turned) rope_apply(p, q, turn + r * half + angle, inter);
+        const float2* t = turn + r * half + angle;
+        if (ROT == AP_ROPE && g < c.n_kv && at_.turned)
+          rope_apply(p, q, t[0], t[quarter], t[2 * quarter], t[3 * quarter], inter);
         if (ROT == AP_THETA && g < c.n_kv) {
-          const float2* t = turn + r * half + d;
-          const float2 t0 = t[0], t1 = t[1], t2 = t[2], t3 = t[3];
+          const float2 t0 = t[0], t1 = t[quarter], t2 = t[2 * quarter], t3 = t[3 * quarter];
           const float4 v = p, w = q;
           p = make_float4(v.x * t0.x - w.x * t0.y, v.y * t1.x - w.y * t1.y, v.z * t2.x - w.z * t2.y,
                           v.w * t3.x - w.w * t3.y);

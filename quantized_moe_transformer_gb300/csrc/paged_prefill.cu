@@ -253,7 +253,10 @@ struct PfWalk {
 // cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37 11.3 us.
 // Tried and not kept: key blocks of 128 with one score buffer (the block waits for its scores to be read: 1 x 8192 362 against
 // 325 us at that stage); one warp issuing both blocks' products (222 against 216); four groups of softmax warps that take a
-// block's key blocks in turn and pass the reference on (308 against 214).
+// block's key blocks in turn and pass the reference on (308 against 214); sixteen warps of 16 rows, four lanes a row, 80
+// registers each (all of a block's warps wait for the same scores, so the chain wait - load - weights - store of 1500
+// cycles stays as long: 746 against 703); the next key block's scores fetched by halves while this one's are worked on (886
+// against 703); waits voted on at once and predicated arrivals of the softmax (within 1 %).
 template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;

@@ -69,18 +69,19 @@ __device__ __forceinline__ void rope_pair(float& v, float& w, float2 t) {
   w = __fmaf_rn(b, t.x, __fmul_rn(a, t.y));
 }
 
-// The unit's elements p (from a) and q (from b) turned by the four (cos, sin) at ``t``.
-__device__ __forceinline__ void rope_apply(float4& p, float4& q, const float2* t, bool interleaved) {
+// The unit's elements p (from a) and q (from b) turned by the four (cos, sin) t0 .. t3.
+__device__ __forceinline__ void rope_apply(float4& p, float4& q, float2 t0, float2 t1, float2 t2, float2 t3,
+                                           bool interleaved) {
   if (interleaved) {
-    rope_pair(p.x, p.y, t[0]);
-    rope_pair(p.z, p.w, t[1]);
-    rope_pair(q.x, q.y, t[2]);
-    rope_pair(q.z, q.w, t[3]);
+    rope_pair(p.x, p.y, t0);
+    rope_pair(p.z, p.w, t1);
+    rope_pair(q.x, q.y, t2);
+    rope_pair(q.z, q.w, t3);
   } else {
-    rope_pair(p.x, q.x, t[0]);
-    rope_pair(p.y, q.y, t[1]);
-    rope_pair(p.z, q.z, t[2]);
-    rope_pair(p.w, q.w, t[3]);
+    rope_pair(p.x, q.x, t0);
+    rope_pair(p.y, q.y, t1);
+    rope_pair(p.z, q.z, t2);
+    rope_pair(p.w, q.w, t3);
   }
 }
 
