@@ -245,18 +245,23 @@ struct PfWalk {
 // Warps: 0-7 the softmax; then one that walks the CTA's work and copies K (and bf16 Q), one that issues S, one that copies V,
 // one that issues P V, and for bf16's second block of rows one more of each of the issuers. Every wait is bounded.
 //
-// What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 710 us, 1550 TFLOP/s, 0.80 of cuBLAS' bf16 rate: the tensor pipe
-// is busy 78 % of the time (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of
-// 32), the softmax takes 1500 cycles a key block of both blocks of rows, issue slots are 48 % used, MUFU 32 %. fp32 rows, 1 x
-// 4096: 160 us, 430 TFLOP/s of the attention's own and 1290 of the three products', tensor pipe 73 %. 64 head dims, 256 rows behind 65000
-// entries: 89 us, tensor pipe 47 %: as many exponentials for half the products. Short calls wait on the chain launch - lengths -
-// cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37 11.3 us.
+// What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 680 us, 1620 TFLOP/s, 0.83 of cuBLAS' bf16 rate: the tensor pipe
+// is busy 83 % of the time (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of
+// 32), the softmax takes 1400 cycles a key block of both blocks of rows, issue slots are 47 % used, MUFU 33 %. fp32 rows, 1 x
+// 4096: 160 us, 430 TFLOP/s of the attention's own and 1290 of the three products', tensor pipe 73 %. 64 head dims, 256 rows
+// behind 65000 entries: 88 us, tensor pipe 48 %: as many exponentials for half the products, and the softmax of a block of
+// rows is one chain in each of its warps: see the scores 150 cycles, load them 100, weights 900, store 150, arrive 100. Short
+// calls wait on the chain launch - lengths - cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37
+// 11.6 us.
+// bf16 rows: the maximum of a key block ahead of its weights. Formed together, and the weights again where the reference moved,
+// the scores stay in registers beside all the weights, and a warp has too few left for exponentials in flight (1 x 16384
+// 704 us, 32 sequences 181 against 172).
 // Tried and not kept: key blocks of 128 with one score buffer (the block waits for its scores to be read: 1 x 8192 362 against
 // 325 us at that stage); one warp issuing both blocks' products (222 against 216); four groups of softmax warps that take a
 // block's key blocks in turn and pass the reference on (308 against 214); sixteen warps of 16 rows, four lanes a row, 80
-// registers each (all of a block's warps wait for the same scores, so the chain wait - load - weights - store of 1500
-// cycles stays as long: 746 against 703); the next key block's scores fetched by halves while this one's are worked on (886
-// against 703); waits voted on at once and predicated arrivals of the softmax (within 1 %).
+// registers each (the chain stays as long: 746 against 703); the next key block's scores fetched by halves while this one's are
+// worked on (886 against 703); the two warps of an SM partition forming weights in turn (679 against 684, the others 1 to 3 %
+// slower); seeing the next scores ahead, waits voted on at once, predicated arrivals (none faster by 1 %).
 template <int HDP_, bool F32_>
 struct PfCfg {
   static constexpr bool F32 = F32_;
@@ -598,25 +603,9 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
         }
         pf_mask(v, row.vis - kb * PF_KEYS, exist);
       }
-      // p = exp2(c s - m) as bf16, their sum in fp32. Most blocks do not move the reference: the weights are formed while
-      // the maximum is sought, and again where it does (as in a tile's first block).
-      float lb;
-      for (;;) {
-        const float mref = m == -INFINITY ? 0.f : m;
-        const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
-        const float mx = pf_max(v) * c;
-        uint64_t l2[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < PF_KEYS / 2; ++i) {
-          const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
-          const float p0 = exp2f(d.x), p1 = exp2f(d.y);
-          l2[i & 1] = ffma2(pack2(__float_as_uint(p0), __float_as_uint(p1)), one2, l2[i & 1]);
-          w[i] = tc::pack_bf16x2(p0, p1);
-        }
-        const float2 la = unpack2(l2[0]), lc = unpack2(l2[1]);
-        lb = (la.x + la.y) + (lc.x + lc.y);
-        const bool need = mx > m + PF_RESCALE_LOG2;
-        if (__builtin_expect(!__any_sync(0xffffffffu, need), 1)) break;
+      const float mx = pf_max(v) * c;
+      const bool need = mx > m + PF_RESCALE_LOG2;
+      if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
         const float alpha = need ? exp2f(m - mx) : 1.f;
         if (need) m = mx;
         l *= alpha;
@@ -635,6 +624,19 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
           }
         }
       }
+      // p = exp2(c s - m) as bf16, their sum in fp32
+      const float mref = m == -INFINITY ? 0.f : m;
+      const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
+      uint64_t l2[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < PF_KEYS / 2; ++i) {
+        const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
+        const float p0 = exp2f(d.x), p1 = exp2f(d.y);
+        l2[i & 1] = ffma2(pack2(__float_as_uint(p0), __float_as_uint(p1)), one2, l2[i & 1]);
+        w[i] = tc::pack_bf16x2(p0, p1);
+      }
+      const float2 la = unpack2(l2[0]), lc = unpack2(l2[1]);
+      const float lb = (la.x + la.y) + (lc.x + lc.y);
       l += lb;
       tc::tmem_st16(tS, w);
       tc::tmem_st16(tS + 16, w + 16);
