@@ -610,19 +610,21 @@ class Rope:
 
 def _rope_rows(x, y, what, rows, hd, dtype, dev):
     """One array of rows of ``rope`` and where it goes: on this device, of this
-    type, [rows][heads][hd] with elements one after the other."""
-    shape = (rows, _size(x, 1, what), hd)
+    type, [rows][heads][hd] with elements one after the other (one condition where all
+    is well, as in _need)."""
+    heads = _size(x, 1, what)
+    shape, xs, ys = (rows, heads, hd), x.stride(), y.stride()
+    if (x.shape == shape and y.shape == shape and x.dtype is dtype and y.dtype is dtype and x.get_device() == dev
+            and y.get_device() == dev and xs[2] == 1 and ys[2] == 1):
+        return RopeRows(x.data_ptr(), y.data_ptr(), heads, xs[0], xs[1], ys[0], ys[1])
     for t, name in ((x, what), (y, f"{what}_out")):
-        if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or t.stride(2) != 1:
-            if not t.is_cuda or t.get_device() != dev:
-                raise QmoeError(f"{name} must be on cuda:{dev}, as pos is")
-            if t.dtype is not dtype:
-                raise QmoeError(f"{name} has type {t.dtype}, not {dtype}")
-            if t.shape != shape:
-                raise QmoeError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-            raise QmoeError(f"the elements of a head of {name} must be one after the other")
-    xs, ys = x.stride(), y.stride()
-    return RopeRows(x.data_ptr(), y.data_ptr(), shape[1], xs[0], xs[1], ys[0], ys[1])
+        if not t.is_cuda or t.get_device() != dev:
+            raise QmoeError(f"{name} must be on cuda:{dev}, as pos is")
+        if t.dtype is not dtype:
+            raise QmoeError(f"{name} has type {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            raise QmoeError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    raise QmoeError(f"the elements of a head of {what} or {what}_out must be one after the other")
 
 
 def rope(rope: Rope, pos, q, k=None, q_out=None, k_out=None, transpose: bool = False, stream=None):
@@ -631,7 +633,8 @@ def rope(rope: Rope, pos, q, k=None, q_out=None, k_out=None, transpose: bool = F
     by their positions ``pos`` [rows] int32; ``transpose``: turned back (times the
     scale), which takes gradients of the results to those of the rows. Returns q_out
     and k_out, new tensors by default; they may be q and k."""
-    dtype, dev, rows, hd = q.dtype, pos.get_device(), _size(q, 0, "q"), _size(q, 2, "q")
+    dtype, dev, hd = q.dtype, pos.get_device(), _size(q, 2, "q")
+    rows = q.shape[0]
     if dtype not in _DTYPE:
         raise QmoeError(f"q has type {dtype}, not fp32 or bf16")
     at = _need(pos, "pos", (rows,), torch.int32, dev)
@@ -774,7 +777,7 @@ def paged_plan(cache: PagedCache, pool: PagePool, count, keep=None, next_pos=Non
             raise QmoeError("a plan needs n_rows or an array of that length for seq")
         n_rows = _size(seq, 0, "seq")
     rows = (n_rows,)
-    if any(t is None for t in (first, granted, seq, slot, pos, ws)):
+    if first is None or granted is None or seq is None or slot is None or pos is None or ws is None:
         if n_rows < 0:
             raise QmoeError("n_rows is below 0")
         with _allocating(stream):
