@@ -219,3 +219,9 @@ def test_a_plan_may_read_the_lengths(lib, name):
     if torch.cuda.is_available():
         pytest.skip("the call would run")
     assert plan(lib, own, **{**apart, name: own.lens}) not in (0, NULL, ARG, ALIGN, WORKSPACE)
+
+
+@pytest.mark.parametrize("kw,n_rows", [({"y_row_stride": 0}, 2), ({"y_head_stride": 0}, 1)])
+def test_rows_that_would_be_written_over_one_another(lib, kw, n_rows):
+    assert rope(lib, q=rows(**kw), n_rows=n_rows) == ARG
+    assert rope(lib, k=rows(**kw), n_rows=n_rows) == ARG
