@@ -248,11 +248,11 @@ struct PfWalk {
 // What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 680 us, 1620 TFLOP/s, 0.83 of cuBLAS' bf16 rate: the tensor pipe
 // is busy 83 % of the time (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of
 // 32), the softmax takes 1400 cycles a key block of both blocks of rows, issue slots are 47 % used, MUFU 33 %. fp32 rows, 1 x
-// 4096: 160 us, 430 TFLOP/s of the attention's own and 1290 of the three products', tensor pipe 73 %. 64 head dims, 256 rows
+// 4096: 157 us, 440 TFLOP/s of the attention's own and 1310 of the three products', tensor pipe 74 %. 64 head dims, 256 rows
 // behind 65000 entries: 88 us, tensor pipe 48 %: as many exponentials for half the products, and the softmax of a block of
 // rows is one chain in each of its warps: see the scores 150 cycles, load them 100, weights 900, store 150, arrive 100. Short
 // calls wait on the chain launch - lengths - cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37
-// 11.6 us.
+// 11.5 us.
 // bf16 rows: the maximum of a key block ahead of its weights. Formed together, and the weights again where the reference moved,
 // the scores stay in registers beside all the weights, and a warp has too few left for exponentials in flight (1 x 16384
 // 704 us, 32 sequences 181 against 172).
@@ -636,8 +636,7 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
         w[i] = tc::pack_bf16x2(p0, p1);
       }
       const float2 la = unpack2(l2[0]), lc = unpack2(l2[1]);
-      const float lb = (la.x + la.y) + (lc.x + lc.y);
-      l += lb;
+      l += (la.x + la.y) + (lc.x + lc.y);
       tc::tmem_st16(tS, w);
       tc::tmem_st16(tS + 16, w + 16);
       tc::tmem_wait_st();
@@ -694,9 +693,10 @@ struct PfHalves {
 };
 
 // Tiles of fp32 rows: warps w and w + 4 have the same 32 rows, each half of a key block's scores and half
-// of the head dims of their output, which is in registers. The weights are formed by the reference as it is
-// while the partner's maximum is on its way, and again where it moves. P V of a key block is added once the
-// next one's weights are out; a tile's last one, after the next tile's queries.
+// of the head dims of their output, which is in registers. The reference is settled with the partner's maximum
+// ahead of the weights (formed while that is on its way, and again where the reference moves, they need registers beside
+// the scores: 1 x 4096 163 against 157 us, 256 head dims 488 against 456). P V of a key block is added once
+// the next one's weights are out; a tile's last one, after the next tile's queries.
 template <class C, class Take>
 __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, const PfItem& it, uint32_t tmem, uint8_t* sQ,
                                                  const uint32_t* there, PfBars& bar, PfHalves& halves,
@@ -841,31 +841,23 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
       halves.max[buf][half][r] = mx;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&halves.max_there[quarter][buf]);
-      float p[KH], lb;
       const float before = alpha;  // the factor that goes with P V of the block before
       alpha = 1.f;
-      for (bool met = false;;) {
-        const float mref = m == -INFINITY ? 0.f : m;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < KH; ++i) {
-          p[i] = exp2f(fmaf(__uint_as_float(v[i]), c, -mref));
-          l4[i & 3] += p[i];
-        }
-        lb = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        if (met) break;
-        met = true;
-        if (!wait(&halves.max_there[quarter][buf], j >> 1)) return;
-        mx = fmaxf(mx, halves.max[buf][half ^ 1][r]);
-        const bool need = mx > m + PF_RESCALE_LOG2;
-        if (__builtin_expect(!__any_sync(0xffffffffu, need), 1)) break;
-        if (need) {
-          alpha = exp2f(m - mx);
-          m = mx;
-          l *= alpha;
-        }
+      if (!wait(&halves.max_there[quarter][buf], j >> 1)) return;
+      mx = fmaxf(mx, halves.max[buf][half ^ 1][r]);
+      if (mx > m + PF_RESCALE_LOG2) {
+        alpha = exp2f(m - mx);
+        m = mx;
+        l *= alpha;
       }
-      l += lb;
+      const float mref = m == -INFINITY ? 0.f : m;
+      float p[KH], l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KH; ++i) {
+        p[i] = exp2f(fmaf(__uint_as_float(v[i]), c, -mref));
+        l4[i & 3] += p[i];
+      }
+      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
       // (P's buffer is free: this warp has added P V of two blocks before)
 #pragma unroll
       for (int part = 0; part < 3; ++part) {
