@@ -248,7 +248,7 @@ struct PfWalk {
 // What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 680 us, 1620 TFLOP/s, 0.83 of cuBLAS' bf16 rate: the tensor pipe
 // is busy 83 % of the time (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of
 // 32), the softmax takes 1400 cycles a key block of both blocks of rows, issue slots are 47 % used, MUFU 33 %. fp32 rows, 1 x
-// 4096: 157 us, 440 TFLOP/s of the attention's own and 1310 of the three products', tensor pipe 74 %. 64 head dims, 256 rows
+// 4096: 155 us, 440 TFLOP/s of the attention's own and 1310 of the three products', tensor pipe 74 %. 64 head dims, 256 rows
 // behind 65000 entries: 88 us, tensor pipe 48 %: as many exponentials for half the products, and the softmax of a block of
 // rows is one chain in each of its warps: see the scores 150 cycles, load them 100, weights 900, store 150, arrive 100. Short
 // calls wait on the chain launch - lengths - cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37
@@ -1443,9 +1443,9 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.w.head_rows = c.n_kv * pl.row_tiles * pl.v_parts;
   x.w.v_parts = pl.v_parts;
   x.w.row_heads = pl.row_heads;
-  // in keys' worth of time: the change of tiles (1 x 16384 bf16 with 64 907 us, 256 796, 1152 809; fp32 1 x 4096 with 320
-  // 167 us, 512 160, 896 168)
-  x.w.tile_cost = a.f32 ? 512 : 256;
+  // in keys' worth of time: the change of tiles (bf16: 32 sequences of 1..1000 behind 0..3000 with 192 178 us, 256 172.5, 320
+  // 171.3, 448 175, 8 of 300..2048 and 64 head dims 45.0, 44.9, 45.8, 48; fp32 1 x 4096 with 384 154.7 us, 512 156.5, 768 159)
+  x.w.tile_cost = a.f32 ? 384 : 256;
   x.w.ctas = device_sm_count() < pl.ctas ? device_sm_count() : pl.ctas;
   x.w.desc = reinterpret_cast<int4*>(ws + pl.desc);
   x.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
