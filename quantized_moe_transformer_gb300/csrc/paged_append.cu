@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(AP_MAX_THREADS, 2) append_kernel(const PagedVi
   __shared__ int2 at[AP_ROWS];  // (sequence, slot), slot -1: the row is not cached
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, threads = blockDim.x, hd = c.head_dim, half = (ROT == AP_ROPE ? fr.dims : hd) / 2;
+  const int n0 = blockIdx.x * rows, n = min(rows, a.n_rows - n0), tid = threadIdx.x, threads = blockDim.x;
+  const int hd = c.head_dim, half = (ROT == AP_ROPE ? fr.dims : hd) / 2;
   // a unit's four angles lie ``quarter`` apart, so that the lanes, unit by unit, read side by side (four of one
   // lane side by side would be four lanes to a bank)
   const int quarter = half / 4;

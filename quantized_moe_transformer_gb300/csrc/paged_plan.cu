@@ -279,7 +279,8 @@ __device__ __forceinline__ void plan_fill(const PagedView& c, const PlanArgs& a,
     const_cast<int32_t*>(c.table)[(long long)b * c.max_pages + w.from[b] + (int)i - before] = page;
   }
   // four rows a thread, 16 bytes of each map where they lie so
-  const bool wide = ((reinterpret_cast<uintptr_t>(a.seq) | reinterpret_cast<uintptr_t>(a.slot) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.seq) | reinterpret_cast<uintptr_t>(a.slot) |
+                      reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
   for (long long i0 = PF_ROWS * tid; i0 < a.n_rows; i0 += PF_ROWS * threads) {
     // the last sequence that begins at or before the row (those without rows begin where the next one does)
     int b = plan_above(w.first, c.n_seqs, (int)i0) - 1;

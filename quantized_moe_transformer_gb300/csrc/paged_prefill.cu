@@ -334,7 +334,10 @@ __device__ __forceinline__ void pf_ld32(uint32_t ta, uint32_t* v) {
 // are (loads and wait apart, with the registers passing through the wait, cost a move each).
 __device__ __forceinline__ void pf_ld64(uint32_t ta, uint32_t* v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
+      "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,"
+      "%60,%61,%62,%63}, [%64];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
@@ -990,9 +993,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (it.kb1 <= it.kb0) continue;
       const PfHeads hs = pf_heads(a, it.row);
       const int blocks = blocks_of();
-      // A block's queries go into the space of the third block before (of the one before, with 256 head dims), once S no longer reads that; what lies behind
-      // the rows (other sequences' rows, zeros from n_rows on) is masked. The second block's wait for the item
-      // before: it comes behind the first keys.
+      // A block's queries go into the space of the third block before (of the one before, with 256 head dims), once S
+      // no longer reads that; what lies behind the rows (other sequences' rows, zeros from n_rows on) is masked. The
+      // second block's wait for the item before: it comes behind the first keys.
       const auto queries = [&](int blk) -> bool {
         const int qs = q_n % C::QT;
         if (q_n >= C::QT &&
