@@ -531,7 +531,7 @@ int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, in
  *   q, out [n_rows][n_heads][hd] of type dtype; out may be q (fp32 rows of more than 128 head dims
  *   are then copied to ws first). fp32 rows are taken with all
  *   their bits and fp32 accuracy is kept; for bf16 rows, which are exact as they are,
- *   probabilities are rounded to bf16 (2^-8) before they weigh the values, sums are fp32,
+ *   each probability is held as two bf16 parts (2^-17 of it is left out), sums are fp32,
  *   and the result is rounded once.
  *   first, count [n_seqs] int32; the sequences' rows must not overlap. Rows out of range
  *   are recorded as QMOE_ERR_DEVICE_ARG and the sequence has none.

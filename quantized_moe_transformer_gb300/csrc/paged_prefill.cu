@@ -234,9 +234,10 @@ struct PfWalk {
 //   P_j             exp2(s - m), a thread a row, back to tensor memory: the A operand of
 //   O += P_j V_j    V_j as an MN-major operand, fp32 O in tensor memory.
 // m is a reference: O and l are rescaled only where a row's maximum exceeds it by more than 2^8.
-// bf16 rows: a tile is two blocks of rows that share the copies of K and V. P_j, rounded to bf16, lies in
-// S_j's own columns; S_{j+2} takes them again when P_j V_j is done. While one block's softmax runs, the
-// tensor core has the other's products and the same block's next S.
+// bf16 rows: a tile is two blocks of rows that share the copies of K and V. P_j, two bf16 parts that leave 2^-17 of a
+// probability (one part would leave 2^-8: outputs 2.1e-3 to 2.4e-3 of their norm off 64 bits, of which their own rounding is
+// 1.65e-3; 1 x 16384 674 us), lies in S_j's own columns; S_{j+2} takes them again when P_j V_j is done. While one block's
+// softmax runs, the tensor core has the other's products and the same block's next S.
 // fp32 rows: a tile is one block; q and each probability are three bf16 parts (24 bits), so S and P V
 // take three products each, small parts first. P V of a key block goes into a fresh accumulator and is added, rounded, to
 // the output in registers, so nothing is cut off over a long axis. With more than 128 head dims the three parts of 128 rows do
@@ -245,18 +246,17 @@ struct PfWalk {
 // Warps: 0-7 the softmax; then one that walks the CTA's work and copies K (and bf16 Q), one that issues S, one that copies V,
 // one that issues P V, and for bf16's second block of rows one more of each of the issuers. Every wait is bounded.
 //
-// What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 680 us, 1620 TFLOP/s, 0.83 of cuBLAS' bf16 rate: the tensor pipe
-// is busy 83 % of the time (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of
-// 32), the softmax takes 1400 cycles a key block of both blocks of rows, issue slots are 47 % used, MUFU 33 %. fp32 rows, 1 x
+// What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 838 us, 1310 TFLOP/s, 1970 with both parts' products: the tensor
+// pipe (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of 32). fp32 rows, 1 x
 // 4096: 155 us, 440 TFLOP/s of the attention's own and 1310 of the three products', tensor pipe 74 %. 64 head dims, 256 rows
-// behind 65000 entries: 88 us, tensor pipe 48 %: as many exponentials for half the products, and the softmax of a block of
-// rows is one chain in each of its warps: see the scores 150 cycles, load them 100, weights 900, store 150, arrive 100. Short
+// behind 65000 entries: 104 us: as many exponentials for half the products, and the softmax of a block of
+// rows is one chain in each of its warps: see the scores, load them, form weights, store them, arrive. Short
 // calls wait on the chain launch - lengths - cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37
 // 11.5 us.
 // bf16 rows: the maximum of a key block ahead of its weights. Formed together, and the weights again where the reference moved,
-// the scores stay in registers beside all the weights, and a warp has too few left for exponentials in flight (1 x 16384
-// 704 us, 32 sequences 181 against 172).
-// Tried and not kept: key blocks of 128 with one score buffer (the block waits for its scores to be read: 1 x 8192 362 against
+// the scores stay in registers beside all the weights, and a warp has too few left for exponentials in flight (with one
+// part of a probability 1 x 16384 704 us against 680, 32 sequences 181 against 172).
+// Tried and not kept, with one part: key blocks of 128 with one score buffer (the block waits for its scores to be read: 1 x 8192 362 against
 // 325 us at that stage); one warp issuing both blocks' products (222 against 216); four groups of softmax warps that take a
 // block's key blocks in turn and pass the reference on (308 against 214); sixteen warps of 16 rows, four lanes a row, 80
 // registers each (the chain stays as long: 746 against 703); the next key block's scores fetched by halves while this one's are
@@ -268,7 +268,8 @@ struct PfCfg {
   static constexpr int HDP = HDP_, NH = HDP / 64;         // head dims of queries and keys, padded
   static constexpr int HDV = F32 && HDP == 256 ? 128 : HDP;  // of a tile's values: 256 of fp32 rows are two tiles
   static constexpr int QROWS = F32 && HDP == 256 ? 64 : 128; // rows of a block that are used
-  static constexpr int BLOCKS = F32 || HDP == 256 ? 1 : 2, PARTS = F32 ? 3 : 1;
+  static constexpr int BLOCKS = F32 || HDP == 256 ? 1 : 2;
+  static constexpr int PARTS = F32 ? 3 : 1, P_PARTS = F32 ? 3 : 2;  // bf16 parts of a query and of a probability
   static constexpr int SOFT = F32 ? 8 : 4 * BLOCKS;       // warps of the softmax (of 8; the others have none)
   static constexpr int THREADS = BLOCKS == 1 ? 384 : 512; // (two blocks: two warps more, so that warps give registers up by fours)
   static constexpr int QT = HDP == 256 && !F32 ? 1 : 3;   // bf16: a ring of blocks of queries; fp32: their parts
@@ -279,10 +280,10 @@ struct PfCfg {
   static constexpr int KST = HDP == 256 ? 2 : 4, VST = HDP == 64 ? 6 : F32 ? 3 : HDP == 128 ? 4 : 2;
   static constexpr int SMEM = 1024 + QT * QTILE + KST * TILE + VST * VTILE;
   static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;
-  // tensor memory: S of (block, buffer), P of (block or part, buffer), O of a block
+  // tensor memory: S of (block, buffer), P of (block, part, buffer), O of a block
   static __device__ __forceinline__ uint32_t s_col(int blk, int buf) { return 64u * (2 * blk + buf); }
   static __device__ __forceinline__ uint32_t p_col(int blk, int part, int buf) {
-    return F32 ? P_COL + 96u * buf + 32u * part : s_col(blk, buf);
+    return F32 ? P_COL + 96u * buf + 32u * part : s_col(blk, buf) + 32u * part;
   }
   static __device__ __forceinline__ uint32_t o_col(int blk) { return O_COL + (uint32_t)HDV * blk; }
 };
@@ -577,7 +578,8 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
   const int place = r / a.w.row_heads, head = r - place * a.w.row_heads;
   const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tq + C::o_col(blk);
   const float c = a.scale;
-  const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c)), one2 = pack2(0x3F800000u, 0x3F800000u);
+  const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c)), one2 = pack2(0x3F800000u, 0x3F800000u),
+                 minus2 = pack2(0xBF800000u, 0xBF800000u);
   int j = 0;   // key blocks of this block of rows so far
   int ring = 0;  // the key block's place in the ring of ``there``
   for (int n = 0; take(n); ++n) {
@@ -627,7 +629,7 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
           }
         }
       }
-      // p = exp2(c s - m) as bf16, their sum in fp32
+      // p = exp2(c s - m) as two bf16 parts, their sum in fp32
       const float mref = m == -INFINITY ? 0.f : m;
       const uint64_t negm2 = pack2(__float_as_uint(-mref), __float_as_uint(-mref));
       uint64_t l2[2] = {0, 0};
@@ -635,13 +637,19 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
       for (int i = 0; i < PF_KEYS / 2; ++i) {
         const float2 d = unpack2(ffma2(pack2(v[2 * i], v[2 * i + 1]), c2, negm2));
         const float p0 = exp2f(d.x), p1 = exp2f(d.y);
-        l2[i & 1] = ffma2(pack2(__float_as_uint(p0), __float_as_uint(p1)), one2, l2[i & 1]);
-        w[i] = tc::pack_bf16x2(p0, p1);
+        const uint64_t p = pack2(__float_as_uint(p0), __float_as_uint(p1));
+        l2[i & 1] = ffma2(p, one2, l2[i & 1]);
+        const uint32_t hi = tc::pack_bf16x2(p0, p1);
+        const float2 rest = unpack2(ffma2(pack2(hi << 16, hi & 0xFFFF0000u), minus2, p));
+        w[i & 15] = hi;
+        w[16 + (i & 15)] = tc::pack_bf16x2(rest.x, rest.y);
+        if ((i & 15) == 15) {
+          tc::tmem_st16(tS + (i - 15), w);
+          tc::tmem_st16(tS + 32 + (i - 15), w + 16);
+        }
       }
       const float2 la = unpack2(l2[0]), lc = unpack2(l2[1]);
       l += (la.x + la.y) + (lc.x + lc.y);
-      tc::tmem_st16(tS, w);
-      tc::tmem_st16(tS + 16, w + 16);
       tc::tmem_wait_st();
       tc::tc_fence_before();
       __syncwarp();
@@ -1162,12 +1170,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const uint32_t d = pf_same(tmem + C::o_col(blk));
         const bool first = !C::F32 && kb == it.kb0;
 #pragma unroll
-        for (int part = C::PARTS - 1; part >= 0; --part) {
+        for (int part = C::P_PARTS - 1; part >= 0; --part) {
           const uint32_t pa = pf_same(tmem + C::p_col(blk, part, buf));
 #pragma unroll
           for (int kk = 0; kk < PF_KEYS / 16; ++kk)
             pf_mma_ts(leader, d, pa + 8u * kk, vd + (uint32_t)(2048 / 16 * kk), idesc,
-                      part != C::PARTS - 1 || kk != 0 || (!C::F32 && !first));
+                      part != C::P_PARTS - 1 || kk != 0 || (!C::F32 && !first));
         }
         pf_commit(leader, &bar.pv_done[blk][buf]);
         pf_commit(leader, &bar.v_empty[st]);
