@@ -506,6 +506,12 @@ bool rope_ok(const qmoe_rope_desc& r, int head_dim) {
          r.dims <= head_dim && std::isfinite(r.scale);
 }
 
+// Rows and heads of attention of packed rows. (The kernels count a sequence's rows, rounded up to whole tiles, in 32
+// bits: at most 2^30 rows, as there are slots.)
+bool prefill_shape_ok(const qmoe_paged_cache& c, int n_rows, int n_heads) {
+  return n_rows >= 0 && n_rows <= 1 << 30 && n_heads >= 1 && n_heads <= 65535 && n_heads % c.n_kv == 0;
+}
+
 // One array of rows of qmoe_rope.
 int rope_rows(const qmoe_rope_rows& t, RopeRows* out) {
   if (t.n_heads < 1 || t.n_heads > 65535) return QMOE_ERR_ARG;
@@ -765,7 +771,7 @@ int qmoe_paged_attention(const qmoe_paged_cache* c, const void* q, void* out, in
 
 size_t qmoe_paged_prefill_attention_workspace_bytes(const qmoe_paged_cache* c, int n_rows, int n_heads) {
   PagedView view;
-  if (paged_view(c, &view) != QMOE_OK || n_rows < 0 || n_heads < 1 || n_heads > 65535 || n_heads % c->n_kv != 0) return 0;
+  if (paged_view(c, &view) != QMOE_OK || !prefill_shape_ok(*c, n_rows, n_heads)) return 0;
   return paged_prefill_ws_bytes(view, n_rows, n_heads);
 }
 
@@ -775,9 +781,7 @@ int qmoe_paged_prefill_attention(const qmoe_paged_cache* c, const void* q, void*
   PagedView view;
   int r = paged_view(c, &view);
   if (r != QMOE_OK) return r;
-  if (!dtype_ok(dtype) || n_rows < 0 || n_heads < 1 || n_heads > 65535 || n_heads % c->n_kv != 0 ||
-      !std::isfinite(scale))
-    return QMOE_ERR_ARG;
+  if (!dtype_ok(dtype) || !prefill_shape_ok(*c, n_rows, n_heads) || !std::isfinite(scale)) return QMOE_ERR_ARG;
   if (n_rows == 0) return QMOE_OK;
   if (!q || !out || !first || !count || !ws) return QMOE_ERR_NULL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(first, 4) || !aligned(count, 4) || !aligned(ws, 256))

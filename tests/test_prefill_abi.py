@@ -225,3 +225,13 @@ def test_a_plan_may_read_the_lengths(lib, name):
 def test_rows_that_would_be_written_over_one_another(lib, kw, n_rows):
     assert rope(lib, q=rows(**kw), n_rows=n_rows) == ARG
     assert rope(lib, k=rows(**kw), n_rows=n_rows) == ARG
+
+
+@pytest.mark.parametrize("n_rows", [2 ** 30 + 1, 2 ** 31 - 256, 2 ** 31 - 1])
+def test_more_rows_than_32_bits_count(lib, n_rows):
+    """A sequence's rows rounded up to whole tiles, and a tile's last place, have to stay below 2^31."""
+    assert attend(lib, n_rows=n_rows) == ARG and attend(lib, n_rows=n_rows, dtype=1, d=desc(n_kv=2), heads=6) == ARG
+    assert lib.qmoe_paged_prefill_attention_workspace_bytes(ctypes.byref(desc()), n_rows, 16) == 0
+    assert lib.qmoe_paged_prefill_attention_workspace_bytes(ctypes.byref(desc()), 2 ** 30, 16) > 0
+    assert lib.qmoe_block_prefill_paged_workspace_bytes(ctypes.byref(block_desc()), ctypes.byref(desc()), n_rows) == 0
+    assert prefill(lib, n_rows=n_rows, ws_bytes=1 << 62) == ARG
