@@ -278,6 +278,11 @@ struct PfCfg {
   static constexpr int HALF = PF_KEYS * 128;              // 64 head dims of a key block
   static constexpr int TILE = NH * HALF, VTILE = HDV / 64 * HALF;
   static constexpr int KST = HDP == 256 ? 2 : 4, VST = HDP == 64 ? 6 : F32 ? 3 : HDP == 128 ? 4 : 2;
+  // Key blocks' words on missing pages. A word is read by the softmax of both blocks of rows, but where a tile has rows in
+  // the first block alone, only the rings bound how far the copies run ahead of the second block's softmax: it
+  // holds back the values of VST blocks on, those hold back S of two more, and that the keys of KST more.
+  static constexpr int RING = 16;
+  static_assert(RING > KST + VST + 1, "a word may be overwritten before it is read");
   static constexpr int SMEM = 1024 + QT * QTILE + KST * TILE + VST * VTILE;
   static constexpr uint32_t P_COL = 128, O_COL = F32 ? 320 : 256;
   // tensor memory: S of (block, buffer), P of (block, part, buffer), O of a block
@@ -584,7 +589,7 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
   int ring = 0;  // the key block's place in the ring of ``there``
   for (int n = 0; take(n); ++n) {
     if (blk * a.block_pos >= it.count - it.t * a.w.span) {  // no rows in this block
-      ring = (ring + it.kb1 - it.kb0) % (2 * C::KST);
+      ring = (ring + it.kb1 - it.kb0) % C::RING;
       continue;
     }
     const PfRow row = pf_row(a, it, pf_heads(a, it.row), blk, place, head);
@@ -599,7 +604,7 @@ __device__ __forceinline__ void prefill_bf16_rows(const PfArgs& a, Take& take, c
       const uint32_t tS = tq + C::s_col(blk, buf);
       uint32_t v[PF_KEYS], w[PF_KEYS / 2];
       const uint32_t exist = there[ring];
-      ring = ring + 1 == 2 * C::KST ? 0 : ring + 1;
+      ring = (ring + 1) % C::RING;
       pf_ld64(tS, v);
       if (__builtin_expect(kb >= whole || exist != 0xFFu, 0)) {
         if (a.flip) {
@@ -836,7 +841,7 @@ __device__ __forceinline__ void prefill_f32_rows(const PfArgs& a, Take& take, co
       const int buf = j & 1;
       if (!wait(&bar.s_full[0][buf], j >> 1)) return;
       tc::tc_fence_after();
-      const uint32_t exist = there[j & (2 * C::KST - 1)];
+      const uint32_t exist = there[j % C::RING];
       uint32_t v[KH];
       pf_ld32(tq + C::s_col(0, buf) + KH * half, v);
       pf_wait_ld(v);
@@ -903,7 +908,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                       const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t pf_smem_raw[];
   __shared__ PfItem items[PF_ITEMS];
-  __shared__ uint32_t there[2 * C::KST];
+  __shared__ uint32_t there[C::RING];
   __shared__ __align__(8) PfBars bar;
   __shared__ __align__(8) PfHalves halves;
   __shared__ uint32_t tmem_slot;
@@ -1039,7 +1044,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ok = false;
           break;
         }
-        if (lane == 0) there[k % (2 * C::KST)] = pg.there;
+        if (lane == 0) there[k % C::RING] = pg.there;
         pf_copy<C::NH, C::HALF>(a, hs.g, 0, pg, &kmap, sK + st * C::TILE, &bar.k_full[st]);
         if (!C::F32 && kb == second && blocks == 2 && !queries(1)) {
           ++k;
