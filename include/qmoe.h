@@ -467,7 +467,8 @@ int qmoe_paged_append_rope(const qmoe_paged_cache *c, const void *q, void *q_out
  * A step's plan: which pages and slots the new rows of all sequences take. The pool
  * is a stack: free_pages [n_pages] int32, of which the first *n_free are the numbers of
  * free pages, the last of them the next to go. A sequence's pages are its table
- * entries up to the first that is no page number (-1, say). In this order:
+ * entries up to the first that is no page number (-1, say); those in front of the page that entry
+ * lens[b] (keep[b] where that is less) lies in are taken to be there and not looked at. In this order:
  *   1. keep not NULL, keep[b] >= 0: sequence b is cut to its first keep[b] entries,
  *      lens[b] = min(lens[b], keep[b]), and its pages from the first that holds none of
  *      them on go back: their table entries become -1, and they are pushed onto the stack in
@@ -489,7 +490,8 @@ int qmoe_paged_append_rope(const qmoe_paged_cache *c, const void *q, void *q_out
  *   the cache's own (QMOE_ERR_ARG), but for keep and next_pos, which may be lens: all of a
  *   sequence kept, positions that are slots. The call
  *   writes the cache's table. A page belongs to one sequence alone. A count of free pages out
- *   of range, a free page's number out of range (its entry becomes -1) and more pages, free or
+ *   of range, a number on the stack that is no page where a sequence asks for it (neither it nor what lies
+ *   below it is handed out, as if the pool ended there) and more pages, free or
  *   come back, than there are (some page came back twice) are recorded as QMOE_ERR_DEVICE_ARG.
  *   ws: qmoe_paged_plan_workspace_bytes(c) bytes, 256-byte aligned.
  */

@@ -85,11 +85,11 @@ __device__ __forceinline__ void plan_scan(long long (&v)[3], long long (&total)[
 
 __device__ __forceinline__ int plan_int(long long v) { return v > INT_MAX ? INT_MAX : (int)v; }
 
-// The sequence ``b``'s rows are granted: they fit, and its pages are there.
-__device__ __forceinline__ bool plan_granted(const PagedView& c, const PlanArgs& a, const PlanWs& w, const PlanHead& h,
-                                             int b, int n) {
+// The sequence ``b``'s rows are granted: they fit, and its pages are among the first ``pages`` off the stack.
+__device__ __forceinline__ bool plan_granted(const PagedView& c, const PlanArgs& a, const PlanWs& w, int pages, int b,
+                                             int n) {
   return n > 0 && (long long)w.first[b] + n <= a.n_rows && (long long)w.len[b] + n <= paged_slots(c) &&
-         (w.need[b] == 0 || w.need_end[b] <= h.n_free + h.back);
+         (w.need[b] == 0 || w.need_end[b] <= pages);
 }
 
 // The threads with ``mine`` in ``list`` (in any order), and how many; all threads of the CTA.
@@ -229,22 +229,31 @@ __device__ __forceinline__ void plan_count(const PagedView& c, const PlanArgs& a
     if (tid == 0) record_status(a.status, QMOE_ERR_DEVICE_ARG);
     n_free = n_free < 0 ? 0 : (int)(c.n_pages - back0);
   }
-  __syncthreads();  // everybody has read the pool's count
-  const long long pool = n_free + back0;
-  __shared__ int taken;
-  if (tid == 0) taken = 0;
+  __shared__ int taken, pages;
+  const int pool = (int)(n_free + back0);
+  if (tid == 0) {
+    taken = 0;
+    pages = pool;
+  }
+  __syncthreads();  // (everybody has read the pool's count too)
+  // a number on the stack that is no page ends what can be handed out: a sequence's pages have no hole
+  const int asked = (int)min(need0, (long long)pool);
+  for (int i = (int)back0 + tid; i < asked; i += PL_THREADS) {
+    if (plan_page(c, a.free_pages[pool - 1 - i])) continue;
+    record_status(a.status, QMOE_ERR_DEVICE_ARG);
+    atomicMin(&pages, i);
+  }
   __syncthreads();
   for (int b = tid; b < c.n_seqs; b += PL_THREADS) {
     const int n = max(a.count[b], 0);
-    const PlanHead h{n_free, (int)back0, 0, 0};
-    const bool ok = plan_granted(c, a, w, h, b, n);
+    const bool ok = plan_granted(c, a, w, pages, b, n);
     a.granted[b] = w.granted[b] = ok ? n : 0;
     if (ok && w.need[b] > 0) atomicMax(&taken, w.need_end[b]);
   }
   __syncthreads();
   if (tid == 0) {
     *w.head = PlanHead{n_free, (int)back0, taken, 0};
-    *a.n_free = (int)pool - taken;
+    *a.n_free = pool - taken;
   }
 }
 
@@ -271,12 +280,8 @@ __device__ __forceinline__ void plan_fill(const PagedView& c, const PlanArgs& a,
   for (long long i = tid; i < h.taken; i += threads) {
     const int b = plan_above(w.need_end, c.n_seqs, (int)i);
     const int before = b ? w.need_end[b - 1] : 0, from = pool - 1 - (int)i;
-    int page = from >= h.n_free ? w.back[from - h.n_free] : a.free_pages[from];
-    if (!plan_page(c, page)) {
-      record_status(a.status, QMOE_ERR_DEVICE_ARG);
-      page = -1;
-    }
-    const_cast<int32_t*>(c.table)[(long long)b * c.max_pages + w.from[b] + (int)i - before] = page;
+    const_cast<int32_t*>(c.table)[(long long)b * c.max_pages + w.from[b] + (int)i - before] =
+        from >= h.n_free ? w.back[from - h.n_free] : a.free_pages[from];
   }
   // four rows a thread, 16 bytes of each map where they lie so
   const bool wide = ((reinterpret_cast<uintptr_t>(a.seq) | reinterpret_cast<uintptr_t>(a.slot) |

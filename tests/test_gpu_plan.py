@@ -143,3 +143,44 @@ def test_the_lengths_as_keep_and_positions():
     assert cache.table.tolist() == want and cache.lens.tolist() == kept == lens
     assert pool.free[:len(left)].tolist() == left and int(pool.n_free) == len(left)
     assert [t.tolist() for t in got] == maps
+
+
+def test_a_bad_number_on_the_stack_ends_what_is_handed_out():
+    """A sequence that asks for it gets none of its pages, nor do those behind it that need pages: no page is
+    lost and no sequence's table has a hole. It is reported where it is asked for."""
+    k = torch.zeros(5, 8, 1, 8, dtype=torch.bfloat16, device="cuda")
+    cache = qb.PagedCache(k, torch.zeros_like(k), i32([[-1] * 3, [-1] * 3, [4, -1, -1], [-1] * 3]), i32([0, 0, 5, 0]))
+    pool = qb.PagePool(i32([0, 77, 2, 3, 99]), i32([4]))
+    _, granted, _, slot, _ = qb.paged_plan(cache, pool, i32([8, 16, 3, 1]), n_rows=28)
+    torch.cuda.synchronize()
+    assert qb.query_status() == -8
+    assert granted.tolist() == [8, 0, 3, 0] and slot.tolist() == list(range(8)) + [-1] * 16 + [5, 6, 7, -1]
+    assert cache.table.tolist() == [[3, -1, -1], [-1] * 3, [4, -1, -1], [-1] * 3]
+    assert int(pool.n_free) == 3 and pool.free[:3].tolist() == [0, 77, 2]
+    # all are given up, and one asks for pages that came back and the one above the bad number
+    cache.lens[0] = 8
+    _, granted, *_ = qb.paged_plan(cache, pool, i32([0, 24, 0, 0]), keep=i32([0, 0, 0, 0]), n_rows=24)
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0 and granted.tolist() == [0, 24, 0, 0]
+    assert cache.table.tolist() == [[-1] * 3, [4, 3, 2], [-1] * 3, [-1] * 3]
+    assert int(pool.n_free) == 2 and pool.free[:2].tolist() == [0, 77]
+
+
+@pytest.mark.parametrize("n_rows", [8 * 2000, 8])
+def test_a_bad_number_deep_in_a_long_stack(n_rows):
+    """2500 free pages, more than a CTA has threads; the numbers 1100 and 1700 from the top are none."""
+    n, width = 2600, 2000
+    k = torch.zeros(n, 8, 1, 8, dtype=torch.bfloat16, device="cuda")
+    cache = qb.PagedCache(k, torch.zeros_like(k), torch.full((3, width), -1, dtype=torch.int32, device="cuda"), i32([0, 0, 0]))
+    free = torch.arange(n, dtype=torch.int32, device="cuda")
+    free[2500 - 1 - 1100], free[2500 - 1 - 1700] = -5, n
+    pool = qb.PagePool(free.clone(), i32([2500]))
+    _, granted, *_ = qb.paged_plan(cache, pool, i32([8 * 1100, 8, 8 * 600]), n_rows=8 * 1100 + n_rows)
+    torch.cuda.synchronize()
+    assert qb.query_status() == -8 and granted.tolist() == [8 * 1100, 0, 0]
+    assert cache.table[0, :1100].tolist() == list(range(2499, 1399, -1)) and bool((cache.table[1:] == -1).all())
+    assert int(pool.n_free) == 1400 and torch.equal(pool.free, free)
+    # what is not asked for is not looked at
+    _, granted, *_ = qb.paged_plan(cache, qb.PagePool(free.clone(), i32([2500])), i32([0, 8 * 1100, 0]), n_rows=8 * 1100)
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0 and granted.tolist() == [0, 8 * 1100, 0]
