@@ -23,15 +23,14 @@ struct PlanHead {
 struct PlanWs {
   PlanHead* head;
   int32_t *first;     // the rows before the sequence
-  int32_t *back_end;  // pages that came back up to and with the sequence
   int32_t *need_end;  // pages asked for up to and with it
-  int32_t *need;      // pages that it asks for (0: none, or refused for its size)
   int32_t *len;       // entries that it keeps
   int32_t *from;      // first table entry without a page
   int32_t *granted;   // rows that the sequence is granted
+  int32_t *need;      // pages that it asks for (0: none, or refused for its size); for the first kernel alone
   int32_t *back;      // [pages] the pages that came back, in order
 };
-constexpr int PL_ARRAYS = 7;
+constexpr int PL_ARRAYS = 6, PF_ARRAYS = 5;
 
 __host__ __device__ inline size_t plan_up(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -41,7 +40,7 @@ __host__ PlanWs plan_ws(const PagedView& c, void* ws, size_t* total) {
   size_t o = 256;
   PlanWs w{};
   w.head = reinterpret_cast<PlanHead*>(p);
-  int32_t** const arrays[] = {&w.first, &w.back_end, &w.need_end, &w.need, &w.len, &w.from, &w.granted};
+  int32_t** const arrays[PL_ARRAYS] = {&w.first, &w.need_end, &w.len, &w.from, &w.granted, &w.need};
   for (int32_t** a : arrays) {
     *a = reinterpret_cast<int32_t*>(p + o);
     o += seqs;
@@ -181,7 +180,6 @@ __device__ __forceinline__ void plan_count(const PagedView& c, const PlanArgs& a
     plan_scan(u, need_total, part);
     if (mine) {
       w.first[b] = plan_int(first);
-      w.back_end[b] = plan_int(back_end);
       w.need_end[b] = plan_int(need0 + u[0]);
       w.need[b] = need;
       w.len[b] = len;
@@ -326,15 +324,13 @@ __device__ __forceinline__ void plan_fill(const PagedView& c, const PlanArgs& a,
   }
 }
 
-// The arrays over the sequences in shared memory.
+// The arrays over the sequences in shared memory (all but ``need``).
 __device__ __forceinline__ PlanWs plan_shared(PlanWs w, int32_t (*arrays)[PL_SEQS]) {
   w.first = arrays[0];
-  w.back_end = arrays[1];
-  w.need_end = arrays[2];
-  w.need = arrays[3];
-  w.len = arrays[4];
-  w.from = arrays[5];
-  w.granted = arrays[6];
+  w.need_end = arrays[1];
+  w.len = arrays[2];
+  w.from = arrays[3];
+  w.granted = arrays[4];
   return w;
 }
 
@@ -344,7 +340,10 @@ __global__ void __launch_bounds__(PL_THREADS) plan_count_kernel(const PagedView 
   __shared__ int32_t arrays[PL_ARRAYS][PL_SEQS];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  if (fill && c.n_seqs <= PL_SEQS) w = plan_shared(w, arrays);
+  if (fill && c.n_seqs <= PL_SEQS) {
+    w = plan_shared(w, arrays);
+    w.need = arrays[PF_ARRAYS];
+  }
   plan_count(c, a, w);
   if (!fill) return;
   __syncthreads();
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(PL_THREADS) plan_count_kernel(const PagedView 
 }
 
 __global__ void __launch_bounds__(PF_THREADS) plan_fill_kernel(const PagedView c, const PlanArgs a, PlanWs w) {
-  __shared__ int32_t arrays[PL_ARRAYS][PL_SEQS];
+  __shared__ int32_t arrays[PF_ARRAYS][PL_SEQS];
   tc::grid_dep_launch();
   tc::grid_dep_wait();
   const PlanHead h = *w.head;

@@ -235,3 +235,11 @@ def test_more_rows_than_32_bits_count(lib, n_rows):
     assert lib.qmoe_paged_prefill_attention_workspace_bytes(ctypes.byref(desc()), 2 ** 30, 16) > 0
     assert lib.qmoe_block_prefill_paged_workspace_bytes(ctypes.byref(block_desc()), ctypes.byref(desc()), n_rows) == 0
     assert prefill(lib, n_rows=n_rows, ws_bytes=1 << 62) == ARG
+
+
+@pytest.mark.parametrize("seqs,pages", [(1, 1), (96, 12000), (5000, 77)])
+def test_plan_workspace(lib, seqs, pages):
+    """Six numbers a sequence and one a page, each array to 256 bytes, and a head."""
+    up = lambda n: -(-n // 256) * 256
+    d = desc(n_seqs=seqs, n_pages=pages)
+    assert lib.qmoe_paged_plan_workspace_bytes(ctypes.byref(d)) == 256 + 6 * up(4 * seqs) + up(4 * pages)
