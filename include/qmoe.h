@@ -260,13 +260,16 @@ int qmoe_moe_forward_noalloc(const qmoe_moe_desc *d, const float *X, const float
  *                          softmax warps' last wait runs out;
  *   QMOE_FAULT_PAGED_COPY  paged attention: the first CTA's first warp never
  *                          copies its first tile;
- *   QMOE_FAULT_PREFILL_COPY attention of packed rows on the tensor cores: no CTA
- *                          copies its first keys.
+ *   QMOE_FAULT_PREFILL_COPY attention of packed rows: no CTA copies its first keys;
+ *   QMOE_FAULT_PREFILL_FINAL attention of packed rows, bf16 of up to 128 head dims: P V
+ *                          of a tile's second block of rows is never marked done, so that its
+ *                          softmax warps' wait runs out behind those of the first block.
  * Returns QMOE_ERR_ARG for an unknown site or a negative wait. Not for use
  * outside tests; set QMOE_FAULT_NONE afterwards.
  */
 enum { QMOE_FAULT_NONE = 0, QMOE_FAULT_DECODE_COPY = 1, QMOE_FAULT_TC_ARRIVE = 2, QMOE_FAULT_ATTN_FINAL = 3,
-       QMOE_FAULT_PAGED_COPY = 4, QMOE_FAULT_PREFILL_COPY = 5 };
+       QMOE_FAULT_PAGED_COPY = 4, QMOE_FAULT_PREFILL_COPY = 5,
+       QMOE_FAULT_PREFILL_FINAL = 6 };
 int qmoe_test_inject(int site, int wait_us);
 
 /* Number of kernels this library has enqueued since it was loaded (a CUDA

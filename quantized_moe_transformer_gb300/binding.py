@@ -203,7 +203,8 @@ def moe_forward(layer: MoeLayer, X: torch.Tensor, R: torch.Tensor | None = None,
     return out
 
 
-FAULT_SITES = {"none": 0, "decode_copy": 1, "tc_arrive": 2, "attn_final": 3, "paged_copy": 4, "prefill_copy": 5}
+FAULT_SITES = {"none": 0, "decode_copy": 1, "tc_arrive": 2, "attn_final": 3, "paged_copy": 4, "prefill_copy": 5,
+               "prefill_final": 6}
 
 
 def test_inject(site: str, wait_us: int = 0):

@@ -799,7 +799,8 @@ int qmoe_paged_prefill_attention(const qmoe_paged_cache* c, const void* q, void*
   a.f32 = dtype == QMOE_F32;
   a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)c->head_dim);
   a.wait_ns = wait_limit_ns();
-  a.fault = g_fault_site.load() == QMOE_FAULT_PREFILL_COPY;
+  const int site = g_fault_site.load();
+  a.fault = site == QMOE_FAULT_PREFILL_COPY ? 1 : site == QMOE_FAULT_PREFILL_FINAL ? 2 : 0;
   a.ws = ws;
   g_launches.fetch_add(paged_prefill_launches(view, a));
   return launch_status(launch_paged_prefill(view, a, reinterpret_cast<cudaStream_t>(stream)));
@@ -1444,7 +1445,7 @@ int qmoe_moe_forward_host(const qmoe_moe_desc* d, const float* X_host, const flo
 long long qmoe_launch_count(void) { return g_launches.load(); }
 
 int qmoe_test_inject(int site, int wait_us) {
-  if (site < 0 || site > QMOE_FAULT_PREFILL_COPY || wait_us < 0) return QMOE_ERR_ARG;
+  if (site < 0 || site > QMOE_FAULT_PREFILL_FINAL || wait_us < 0) return QMOE_ERR_ARG;
   g_fault_wait_us.store(wait_us);
   g_fault_site.store(site);
   return QMOE_OK;

@@ -126,7 +126,7 @@ struct PrefillArgs {
   float scale;
   int* status;
   unsigned long long wait_ns;  // bound on a device wait
-  bool fault;                  // test-only: no CTA copies its first keys
+  int fault;                   // test-only: 1 no CTA copies its first keys, 2 a second block's P V is never marked done
   void* ws;
 };
 size_t paged_prefill_ws_bytes(const PagedView& c, int n_rows, int n_heads);

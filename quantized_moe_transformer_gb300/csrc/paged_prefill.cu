@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     walk.begin(a.p, a.w);
     int k = 0, q_n = 0;
     bool ok = true;
-    const bool withhold = a.p.a.fault;
+    const bool withhold = a.p.a.fault == 1;
     for (int n = 0; ok; ++n) {
       const bool more = walk.next(a.p, a.w, &it);
       if (!more) it.b = -1;
@@ -1182,7 +1182,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             pf_mma_ts(leader, d, pa + 8u * kk, vd + (uint32_t)(2048 / 16 * kk), idesc,
                       part != C::P_PARTS - 1 || kk != 0 || (!C::F32 && !first));
         }
-        pf_commit(leader, &bar.pv_done[blk][buf]);
+        if (C::BLOCKS == 1 || blk == 0 || a.p.a.fault != 2) pf_commit(leader, &bar.pv_done[blk][buf]);
         pf_commit(leader, &bar.v_empty[st]);
       }
     }
@@ -1193,10 +1193,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
 
   __syncwarp();
-  if (*abort_flag && threadIdx.x == 0) record_status(a.p.a.status, QMOE_ERR_TIMEOUT);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  // (behind the barrier: a wait may run out when the first warps have long left)
+  if (*abort_flag && threadIdx.x == 0) record_status(a.p.a.status, QMOE_ERR_TIMEOUT);
   if (warp == PF_SWARP) tc::tmem_dealloc(tmem, 512);
 }
 

@@ -246,3 +246,27 @@ def test_withheld_copy_times_out(dtype):
         qb.test_inject("none")
     got = qb.paged_prefill_attention(*args)
     assert qb.query_status() == 0 and torch.equal(got, want)
+
+
+def test_a_wait_that_runs_out_behind_the_first_warp_is_reported():
+    """The second block of rows of a tile gives up when the first block's warps have stored theirs and left."""
+    cache = qb.PagedCache.empty(1, 1024, 2, 128)
+    cache.k.normal_()
+    cache.v.normal_()
+    cache.lens[:] = i32([32])
+    q = torch.randn(32, 16, 128, device="cuda").to(torch.bfloat16)
+    args = (cache, q, i32([0]), i32([32]))
+    want = qb.paged_prefill_attention(*args)
+    torch.cuda.synchronize()
+    assert qb.query_status() == 0
+    qb.test_inject("prefill_final", 2000)
+    try:
+        t0 = time.perf_counter()
+        got = qb.paged_prefill_attention(*args)
+        assert qb.query_status() == -7
+        assert time.perf_counter() - t0 < 5.0
+    finally:
+        qb.test_inject("none")
+    assert torch.equal(got[:16], want[:16])
+    got = qb.paged_prefill_attention(*args)
+    assert qb.query_status() == 0 and torch.equal(got, want)
