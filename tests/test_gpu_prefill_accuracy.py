@@ -29,31 +29,59 @@ def built():
 HEADS = [(16, 2, 128), (8, 8, 64), (12, 4, 96), (8, 2, 256), (3, 1, 200), (2, 2, 8)]
 
 
+def make_exact(counts, lens, heads, kv, hd, page):
+    """bf16 rows and keys of one non-zero head dim, at most 2 there: a score is one exact product of 4 at most,
+    5.8 in units of log2."""
+    c = make(counts, lens, heads, kv, hd, page, torch.bfloat16, spread=1.0)
+    c["k"][..., 1:] = torch.where(torch.isnan(c["k"][..., 1:]), c["k"][..., 1:], 0.0)
+    c["k"].clamp_(-2, 2)
+    c["q"].clamp_(-2, 2)
+    return c
+
+
+def before_rounding(longest):
+    """What an output is off before it is rounded, in parts of the sum of p |v|: a
+    probability's two bf16 parts 2^-17; its argument 4 roundings of 2^-24 times 5.8, in numerator and denominator; n / 8
+    products of 16 entries that the tensor cores cut off at 2^-23, and 64 more of those for the exponential,
+    the denominator's sums, rescaling, joining parts and the division."""
+    return 2.0 ** -17 + 8 * 5.8 * 2.0 ** -24 + (longest / 8 + 64) * 2.0 ** -23
+
+
 @pytest.mark.parametrize("heads,kv,hd", HEADS)
 @pytest.mark.parametrize("counts,lens", [
     ([37], [37]), ([63, 64, 65], [63, 64, 65]), ([300], [300]), ([5, 9, 7], [255, 256, 257]), ([3, 6, 20], [511, 512, 513]),
     ([16], [1000]), ([200], [1100])])
 def test_bf16_rows_are_rounded_once(counts, lens, heads, kv, hd):
-    """Keys of one non-zero head dim, at most 2 like the queries there: a score is one exact product of 4 at
-    most, 5.8 in units of log2. What an output is off before it is rounded, in parts of the sum of p |v|: a
-    probability's two bf16 parts 2^-17; its argument 4 roundings of 2^-24 times 5.8, in numerator and denominator; n / 8
-    products of 16 entries that the tensor cores cut off at 2^-23, and 64 more of those for the exponential,
-    the denominator's sums, rescaling, joining parts and the division. The rounding to bf16 takes the nearest: the output
-    is off by what the right one's rounding is, and twice the rest. Probabilities of one bf16 part
-    are off by up to 2^-8, at random: 2^-10 / sqrt(n) of the sum, 2^-13 at 100 entries."""
+    """The rounding to bf16 takes the nearest: an output is off by what the right one's rounding is, and twice
+    what it was off before. Probabilities of one bf16 part would be off by up to 2^-8, at random: 2^-10 / sqrt(n) of the
+    sum of p |v|, 2^-13 at 100 entries."""
     page = 32
-    c = make(counts, lens, heads, kv, hd, page, torch.bfloat16, spread=1.0)
-    c["k"][..., 1:] = torch.where(torch.isnan(c["k"][..., 1:]), c["k"][..., 1:], 0.0)
-    c["k"].clamp_(-2, 2)
-    c["q"].clamp_(-2, 2)
+    c = make_exact(counts, lens, heads, kv, hd, page)
     out = run(c, scale=1.0)
     assert qb.query_status() == 0
     want, mean, _ = ref.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], c["first"], c["count"], page, 1.0)
     mine = ~torch.isnan(want)
     got, want, mean = out.double()[mine], want[mine], mean[mine]
-    before = (2.0 ** -17 + 8 * 5.8 * 2.0 ** -24 + (max(lens) / 8 + 64) * 2.0 ** -23) * mean
-    tol = (want.to(torch.bfloat16).double() - want).abs() + 2 * before
+    tol = (want.to(torch.bfloat16).double() - want).abs() + 2 * before_rounding(max(lens)) * mean
     assert bool(((got - want).abs() <= tol + 1e-30).all()), float(((got - want).abs() / (tol + 1e-30)).max())
+
+
+@pytest.mark.parametrize("heads,kv,hd", [(16, 2, 128), (8, 8, 64), (8, 2, 256)])
+def test_bf16_single_rows_are_the_decoding_calls(heads, kv, hd):
+    """One row of each sequence: the same as of paged_attention, but where the right output is so near to
+    the middle between two bf16 numbers that what may be lost before the rounding decides. Of 1000 entries, the longest
+    here, that is 2^-15 of the sum of p |v| to each side; an output is about 1 / sqrt(700) of it and a step 2^-7.5 of that:
+    a quarter of the outputs, and less than half of all."""
+    lens = [1, 64, 300, 1000, 77, 513]
+    c = make_exact([1] * len(lens), lens, heads, kv, hd, 64)
+    got = run(c, scale=1.0)[:len(lens)]
+    cache = qb.PagedCache(c["k"], c["v"], c["table"], c["lens"])
+    decoded = qb.paged_attention(cache, c["q"][:len(lens)].contiguous(), scale=1.0)
+    want, mean, _ = ref.attention(c["q"], c["k"], c["v"], c["table"], c["lens"], c["first"], c["count"], 64, 1.0)
+    want, e = want[:len(lens)], before_rounding(max(lens)) * mean[:len(lens)]
+    clear = (want - e).to(torch.bfloat16) == (want + e).to(torch.bfloat16)
+    assert float(clear.double().mean()) > 0.5
+    assert torch.equal(got[clear], decoded[clear])
 
 
 def parts(x, n):
