@@ -430,7 +430,8 @@ int qmoe_paged_append(const qmoe_paged_cache *c, const void *q, void *q_out, con
  *   x, y [n_rows][heads][head_dim] of type dtype, element (n, h, d) at
  *   n * row_stride + h * head_stride + d of its array (strides of at least 0, multiples of 8; the
  *   elements of y must not overlap: a stride of 0 where there is more than one is QMOE_ERR_ARG, more
- *   is not checked). y may be x with the same strides.
+ *   is not checked). y may be x with the same strides; with others, or as the other array's x or y,
+ *   it is QMOE_ERR_ARG.
  *   pos [n_rows] int32. transpose != 0: by the negative angles (times scale): the
  *   transpose of the map, which takes the gradient of y to that of x.
  *   A position times turns[i] is reduced to less than a turn exactly, in integers; sines and

@@ -675,8 +675,13 @@ int qmoe_rope(const qmoe_rope_desc* r, const qmoe_rope_rows* q, const qmoe_rope_
   int e = rope_rows(*q, &a.q);
   if (e == QMOE_OK && k) e = rope_rows(*k, &a.k);
   if (e != QMOE_OK) return e;
-  for (const RopeRows* t : {&a.q, &a.k})  // (x may be one row for all)
+  for (const RopeRows* t : {&a.q, &a.k}) {  // (x may be one row for all)
     if (t->heads > 0 && ((n_rows > 1 && t->y_row == 0) || (t->heads > 1 && t->y_head == 0))) return QMOE_ERR_ARG;
+    if (t->heads > 0 && t->x == t->y && ((n_rows > 1 && t->x_row != t->y_row) || (t->heads > 1 && t->x_head != t->y_head)))
+      return QMOE_ERR_ARG;
+  }
+  // rows are read and written in no order: none where the other array's are written
+  if (k && (a.q.y == a.k.y || a.q.y == a.k.x || a.k.y == a.q.x)) return QMOE_ERR_ARG;
   if (!pos) return QMOE_ERR_NULL;
   if (!aligned(pos, 4)) return QMOE_ERR_ALIGN;
   int* status = nullptr;

@@ -243,3 +243,24 @@ def test_plan_workspace(lib, seqs, pages):
     up = lambda n: -(-n // 256) * 256
     d = desc(n_seqs=seqs, n_pages=pages)
     assert lib.qmoe_paged_plan_workspace_bytes(ctypes.byref(d)) == 256 + 6 * up(4 * seqs) + up(4 * pages)
+
+
+A, B, C, D = (FAKE + (1 << 20) * i for i in range(4))
+
+
+@pytest.mark.parametrize("q,k", [
+    (dict(x=A, y=A, y_row_stride=4096), None), (dict(x=A, y=A, y_head_stride=256), None), (dict(x=A, y=A, x_row_stride=0), None),
+    (dict(x=A, y=B), dict(x=C, y=C, x_head_stride=0)), (dict(x=A, y=B), dict(x=C, y=B)), (dict(x=A, y=B), dict(x=B, y=C)),
+    (dict(x=A, y=B), dict(x=C, y=A)), (dict(x=A, y=A), dict(x=A, y=A))])
+def test_rows_that_are_written_while_they_are_read(lib, q, k):
+    """In place with other strides, or one array's rows where the other's lie."""
+    assert rope(lib, q=rows(**q), k=rows(**k) if k else None) == ARG
+
+
+@pytest.mark.parametrize("q,k", [
+    (dict(x=A, y=A), dict(x=B, y=B)), (dict(x=A, y=B), dict(x=A, y=C)), (dict(x=A, y=A, n_heads=1, y_head_stride=64), None),
+    (dict(x=A, y=B, x_row_stride=0), dict(x=C, y=D, n_heads=2))])
+def test_rows_in_place_and_apart_are_taken(lib, q, k):
+    if torch.cuda.is_available():
+        pytest.skip("the call would run")
+    assert rope(lib, q=rows(**q), k=rows(**k) if k else None) not in (0, NULL, ARG, ALIGN)
