@@ -423,7 +423,9 @@ int qmoe_paged_append(const qmoe_paged_cache *c, const void *q, void *q_out, con
  *     QMOE_ROPE_PARTS    f_i (g + (1 - g) / factor), g = (r_i - low) / (high - low)
  *                        cut to 0..1, r_i = context f_i / (2 pi): pairs that turn high times and
  *                        more within the first ``context`` positions keep their frequency, those
- *                        that turn low times and less are stretched.
+ *                        that turn low times and less are stretched. The blend is linear in how often a
+ *                        pair turns. Models whose blend is linear in the pair's number i, between
+ *                        two rounded ones, have other frequencies: fill in turns for those.
  *   1 <= theta <= 1e30, 1 <= factor <= 1e6, 0 < context <= 2^30, 0 <= low < high <= 2^30 (what the
  *   scaling does not read is not looked at), scale finite.
  * qmoe_rope turns rows of queries and, with k not NULL, of keys:

@@ -586,8 +586,9 @@ class Rope:
     of them apart ("half") or of neighbours ("interleaved"), by theta^(-2i/dims) a
     position, scaled for long contexts ("linear": divided by ``factor``; "parts":
     only where a pair turns less than ``high`` times within ``context`` positions,
-    in full below ``low``), the result times ``scale``. ``frequencies`` (an angle
-    of one position for each pair) take the place of theta and the scaling."""
+    in full below ``low``, and between them by how often it turns; models that blend by
+    the pair's number need ``frequencies``), the result times ``scale``. ``frequencies``
+    (an angle of one position for each pair) take the place of theta and the scaling."""
 
     def __init__(self, dims, theta=1e7, layout="half", scaling=None, factor=1.0, context=0.0, low=0.0, high=0.0,
                  scale=1.0, frequencies=None):
