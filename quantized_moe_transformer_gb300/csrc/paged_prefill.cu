@@ -246,16 +246,18 @@ struct PfWalk {
 // Warps: 0-7 the softmax; then one that walks the CTA's work and copies K (and bf16 Q), one that issues S, one that copies V,
 // one that issues P V, and for bf16's second block of rows one more of each of the issuers. Every wait is bounded.
 //
-// What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 838 us, 1310 TFLOP/s, 1970 with both parts' products: the tensor
-// pipe (64-key products read the queries' 4 KB for each 2 KB of keys, which holds it at 40 cycles an MMA of 32). fp32 rows, 1 x
-// 4096: 155 us, 440 TFLOP/s of the attention's own and 1310 of the three products', tensor pipe 74 %. 64 head dims, 256 rows
-// behind 65000 entries: 104 us: as many exponentials for half the products, and the softmax of a block of
-// rows is one chain in each of its warps: see the scores, load them, form weights, store them, arrive. Short
+// What bounds it. bf16, 16 heads on 2 of 128, 1 x 16384: 859 us at burst clocks (933 under the power cap of a warm GPU), 1280
+// TFLOP/s, 1920 with both parts' products: the tensor pipe is busy 90 % of the time (64-key products read the queries' 4 KB for
+// each 2 KB of keys, which holds it at 40 cycles an MMA of 32), issue slots are 54 % used, MUFU 28 %. fp32 rows, 1 x
+// 4096: 156 us (171 warm), 440 TFLOP/s of the attention's own and 1310 of the three products', tensor pipe 73 %. 64 head dims,
+// 256 rows behind 65000 entries: 104 us, tensor pipe 55 %: as many exponentials for half the products, and the softmax of a
+// block of rows is one chain in each of its warps: see the scores, load them, form weights, store them, arrive. Short
 // calls wait on the chain launch - lengths - cut - pages - copies - S - softmax - P V - store, and on code that runs once: 1 x 37
 // 11.5 us.
 // bf16 rows: the maximum of a key block ahead of its weights. Formed together, and the weights again where the reference moved,
-// the scores stay in registers beside all the weights, and a warp has too few left for exponentials in flight (with one
-// part of a probability 1 x 16384 704 us against 680, 32 sequences 181 against 172).
+// the scores stay in registers beside all the weights, and a warp has too few left for exponentials in flight (1 x 16384
+// 943 us against 862, 32 sequences 220 against 205, 256 head dims 1 x 4096 99 against 94; with one part of a probability
+// 704 against 680, 181 against 172, and 256 head dims, whose four warps have registers enough, 80 against 84).
 // Tried and not kept, with one part: key blocks of 128 with one score buffer (the block waits for its scores to be read: 1 x 8192 362 against
 // 325 us at that stage); one warp issuing both blocks' products (222 against 216); four groups of softmax warps that take a
 // block's key blocks in turn and pass the reference on (308 against 214); sixteen warps of 16 rows, four lanes a row, 80
@@ -1460,8 +1462,9 @@ cudaError_t launch_paged_prefill(const PagedView& c, const PrefillArgs& a, cudaS
   x.w.head_rows = c.n_kv * pl.row_tiles * pl.v_parts;
   x.w.v_parts = pl.v_parts;
   x.w.row_heads = pl.row_heads;
-  // in keys' worth of time: the change of tiles (bf16: 32 sequences of 1..1000 behind 0..3000 with 192 178 us, 256 172.5, 320
-  // 171.3, 448 175, 8 of 300..2048 and 64 head dims 45.0, 44.9, 45.8, 48; fp32 1 x 4096 with 384 154.7 us, 512 156.5, 768 159)
+  // in keys' worth of time: the change of tiles (bf16: 32 sequences of 1..1000 behind 0..3000 with 192 205 us, 256 201, 320 204,
+  // 448 208, 8 of 300..2048 and 64 head dims 51.9, 52.0, 53.2, 56, 1 x 4096 and 256 head dims the same with all four within
+  // its 4 % of spread; fp32 1 x 4096 with 256 175 us, 384 156, 512 157; of fp32 rows with 256 head dims not measured)
   x.w.tile_cost = a.f32 ? 384 : 256;
   x.w.ctas = device_sm_count() < pl.ctas ? device_sm_count() : pl.ctas;
   x.w.desc = reinterpret_cast<int4*>(ws + pl.desc);
