@@ -537,7 +537,7 @@ int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, in
  * (none where that is 0 or less: its output is zeros), with the scores, scale, heads and
  * types of qmoe_paged_attention. Rows of no sequence are not written.
  *   q, out [n_rows][n_heads][hd] of type dtype, n_rows at most 2^30; out may be q (fp32 rows of more than 128 head dims
- *   are then copied to ws first). fp32 rows are taken with all
+ *   are then copied to ws first), and a part of it is QMOE_ERR_ARG. fp32 rows are taken with all
  *   their bits and fp32 accuracy is kept; for bf16 rows, which are exact as they are,
  *   each probability is held as two bf16 parts (2^-17 of it is left out), sums are fp32,
  *   and the result is rounded once.
@@ -595,7 +595,7 @@ int qmoe_block_decode_paged(const qmoe_block_desc *b, const qmoe_paged_cache *c,
 
 /*
  * The block for packed rows of prompts, parts of prompts and single new tokens of
- * c->n_seqs sequences at once: rows X, out [n_rows][H] fp32, n_rows at most 2^30 (out may not alias X). The
+ * c->n_seqs sequences at once: rows X, out [n_rows][H] fp32, n_rows at most 2^30 (out may not overlap X). The
  * rows' keys and values are appended (seq, slot, pos as in qmoe_paged_append, a slot below 0
  * padding), then row first[b] + i of sequence b attends as in
  * qmoe_paged_prefill_attention, then O, residual, norm and MoE. qmoe_paged_plan

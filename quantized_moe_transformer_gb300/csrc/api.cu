@@ -506,6 +506,12 @@ bool rope_ok(const qmoe_rope_desc& r, int head_dim) {
          r.dims <= head_dim && std::isfinite(r.scale);
 }
 
+// Two arrays of ``bytes`` lie over one another in part.
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x != y && (x < y ? y - x : x - y) < bytes;
+}
+
 // Rows and heads of attention of packed rows. (The kernels count a sequence's rows, rounded up to whole tiles, in 32
 // bits: at most 2^30 rows, as there are slots.)
 bool prefill_shape_ok(const qmoe_paged_cache& c, int n_rows, int n_heads) {
@@ -791,6 +797,7 @@ int qmoe_paged_prefill_attention(const qmoe_paged_cache* c, const void* q, void*
   if (!q || !out || !first || !count || !ws) return QMOE_ERR_NULL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(first, 4) || !aligned(count, 4) || !aligned(ws, 256))
     return QMOE_ERR_ALIGN;
+  if (overlap(q, out, (size_t)n_rows * n_heads * c->head_dim * (dtype == QMOE_F32 ? 4 : 2))) return QMOE_ERR_ARG;
   if (ws_bytes < paged_prefill_ws_bytes(view, n_rows, n_heads)) return QMOE_ERR_WORKSPACE;
   PrefillArgs a{};
   r = device_ready(&a.status);
@@ -922,6 +929,7 @@ int qmoe_block_prefill_paged(const qmoe_block_desc* b, const qmoe_paged_cache* c
   if (!aligned(X, 16) || !aligned(out, 16) || !aligned(first, 4) || !aligned(count, 4) || !aligned(seq, 4) ||
       !aligned(slot, 4) || !aligned(pos, 4) || !aligned(ws, 256))
     return QMOE_ERR_ALIGN;
+  if (overlap(X, out, sizeof(float) * (size_t)n_rows * b->H)) return QMOE_ERR_ARG;
   const size_t need = qmoe_block_prefill_paged_workspace_bytes(b, c, n_rows);
   if (need == 0) return QMOE_ERR_ARG;
   if (ws_bytes < need) return QMOE_ERR_WORKSPACE;

@@ -264,3 +264,23 @@ def test_rows_in_place_and_apart_are_taken(lib, q, k):
     if torch.cuda.is_available():
         pytest.skip("the call would run")
     assert rope(lib, q=rows(**q), k=rows(**k) if k else None) not in (0, NULL, ARG, ALIGN)
+
+
+@pytest.mark.parametrize("dtype,size", [(0, 4), (1, 2)])
+def test_outputs_over_a_part_of_the_rows(lib, dtype, size):
+    """Rows are read and written in no order: out is q, or apart from it."""
+    total = 5 * 16 * 128 * size
+    for off in (16, total // 5, total - 16):
+        assert attend(lib, q=A, out=A + off, dtype=dtype) == ARG and attend(lib, q=A + off, out=A, dtype=dtype) == ARG
+    total = 5 * 2048 * 4
+    for off in (16, total - 16):
+        assert prefill(lib, X=A, out=A + off) == ARG and prefill(lib, X=A + off, out=A) == ARG
+
+
+@pytest.mark.parametrize("dtype,size", [(0, 4), (1, 2)])
+def test_outputs_in_place_and_apart_are_taken(lib, dtype, size):
+    if torch.cuda.is_available():
+        pytest.skip("the call would run")
+    total = 5 * 16 * 128 * size
+    for out in (A, A + total, A - total):
+        assert attend(lib, q=A, out=out, dtype=dtype) not in (0, NULL, ARG, ALIGN, WORKSPACE)
