@@ -539,8 +539,8 @@ int qmoe_paged_attention(const qmoe_paged_cache *c, const void *q, void *out, in
  *   q, out [n_rows][n_heads][hd] of type dtype, n_rows at most 2^30; out may be q (fp32 rows of more than 128 head dims
  *   are then copied to ws first), and a part of it is QMOE_ERR_ARG. fp32 rows are taken with all
  *   their bits and fp32 accuracy is kept; for bf16 rows, which are exact as they are,
- *   each probability is held as two bf16 parts (2^-17 of it is left out), sums are fp32,
- *   and the result is rounded once.
+ *   each probability is held as two bf16 parts (2^-17 of it is left out), sums are fp32 (cut off at each 16
+ *   entries, 2^-23), and the result is rounded once.
  *   first, count [n_seqs] int32; the sequences' rows must not overlap. Rows out of range
  *   are recorded as QMOE_ERR_DEVICE_ARG and the sequence has none.
  *   What the cache holds outside the entries is never used; queries and entries are finite.
